@@ -22,6 +22,8 @@ DLRM_OPT_ADAGRAD, DLRM_OPT_SGD = 0, 1
 DLRM_ACT_NONE, DLRM_ACT_RELU = 0, 1
 DLRM_FLAG_CHECK_INDICES = 1
 DLRM_GRAM_AUTO, DLRM_GRAM_MFMA, DLRM_GRAM_VALU = 0, 1, 2
+DLRM_F8_E4M3 = 2
+DLRM_SEQ_MAX_BUCKETS = 128
 
 _lib = None
 
@@ -30,6 +32,24 @@ class DlrmError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
         super().__init__(f"{what}: {status_string(status)} (status {status})")
+
+
+class _SeqAttn(ctypes.Structure):
+    """dlrm_seq_attn (dlrm_seq.h)."""
+    _fields_ = [("B", ctypes.c_int64), ("Nq", ctypes.c_int64), ("Nkv", ctypes.c_int64), ("Hq", ctypes.c_int32),
+                ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32), ("index_type", ctypes.c_int32),
+                ("q_offsets", ctypes.c_void_p), ("kv_begin", ctypes.c_void_p), ("kv_end", ctypes.c_void_p),
+                ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q_row", ctypes.c_int64),
+                ("q_head", ctypes.c_int64), ("k_row", ctypes.c_int64), ("k_head", ctypes.c_int64),
+                ("v_row", ctypes.c_int64), ("v_head", ctypes.c_int64), ("window", ctypes.c_int32),
+                ("sinks", ctypes.c_int32), ("scale", ctypes.c_float), ("buckets", ctypes.c_int32),
+                ("bias", ctypes.c_void_p), ("bounds", ctypes.c_void_p)]
+
+
+class _Dropout(ctypes.Structure):
+    """dlrm_dropout_spec (dlrm_seq.h)."""
+    _fields_ = [("p", ctypes.c_float), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64),
+                ("offset_dev", ctypes.c_void_p)]
 
 
 def lib() -> ctypes.CDLL:
@@ -69,6 +89,21 @@ def lib() -> ctypes.CDLL:
         L.dlrm_cast_rows.argtypes = [p, i32, i64, i64, i32, p, i32, i32, p]
         for f in (L.dlrm_linear_fwd, L.dlrm_linear_bwd, L.dlrm_bce_head, L.dlrm_sgd_dense, L.dlrm_cast_rows):
             f.restype = ctypes.c_int
+        L.dlrm_seq_attn_fwd.argtypes = [p, p, p, p, p]
+        L.dlrm_seq_attn_bwd_workspace_size.argtypes = [i64, i64, i32, i32]
+        L.dlrm_seq_attn_bwd.argtypes = [p, p, p, p, p, p, p, p, p, p, sz, p]
+        L.dlrm_seq_attn_decode_workspace_size.argtypes = [i64, i32, i32, i32, i32, i32, i64]
+        L.dlrm_seq_attn_decode.argtypes = [p, i64, p, p, sz, p]
+        L.dlrm_dropout.argtypes = [p, i32, i64, p, p, p]
+        L.dlrm_add_rmsnorm_fwd.argtypes = [p, i32, p, i32, p, f32, p, i64, i32, p, p, i32, p, p, p]
+        L.dlrm_add_rmsnorm_bwd_workspace_size.argtypes = [i64, i32]
+        L.dlrm_add_rmsnorm_bwd.argtypes = [p, i32, p, p, i32, p, p, p, i64, i32, p, i32, p, p, p, sz, p]
+        for f in (L.dlrm_seq_attn_fwd, L.dlrm_seq_attn_bwd, L.dlrm_seq_attn_decode, L.dlrm_dropout, L.dlrm_add_rmsnorm_fwd,
+                  L.dlrm_add_rmsnorm_bwd):
+            f.restype = ctypes.c_int
+        for f in (L.dlrm_seq_attn_bwd_workspace_size, L.dlrm_seq_attn_decode_workspace_size,
+                  L.dlrm_add_rmsnorm_bwd_workspace_size):
+            f.restype = sz
         L.dlrm_status_string.argtypes = [ctypes.c_int]
         L.dlrm_status_string.restype = ctypes.c_char_p
         L.dlrm_synth_fill_table.argtypes = [p, i32, i64, i32, i32, u64, f32, p]
@@ -726,6 +761,301 @@ def dlrm_cast_rows(src: torch.Tensor, cols: int, dst_cols: int, dst_dtype: torch
     _check(lib().dlrm_cast_rows(_ptr(src), _TORCH_CODE[src.dtype], src.stride(0), M, cols, _ptr(dst),
                                 _TORCH_CODE[dst.dtype], dst_cols, _stream(dev)), "dlrm_cast_rows")
     return dst
+
+
+# ---------------------------------------------------------------- user histories (dlrm_seq.h)
+
+def dlrm_seq_bucket_bounds(buckets: int, reach: int) -> List[int]:
+    """First distances of `buckets` distance buckets for dlrm_seq_attn_*: one distance a bucket for the
+    first half, then growing by an equal factor up to `reach`; the last bucket is open."""
+    if buckets < 1 or buckets > DLRM_SEQ_MAX_BUCKETS:
+        raise ValueError(f"buckets must be 1 to {DLRM_SEQ_MAX_BUCKETS}, got {buckets}")
+    half = max(1, buckets // 2)
+    out = list(range(half))
+    for i in range(half, buckets):
+        f = (i - half) / max(1, buckets - 1 - half)
+        out.append(max(out[-1] + 1, int(round(half * (max(reach, half + 1) / half) ** f))))
+    return out
+
+
+def _head_rows(t, name: str, heads: Optional[int] = None, d: Optional[int] = None) -> torch.Tensor:
+    """[rows, heads, d] bf16 whose heads are packed and whose row and head strides are free (a part
+    of a joint projection, for instance)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or (d is not None and t.shape[2] != d):
+        raise ValueError(f"{name} must be [rows, heads={heads}, d={d}], got {tuple(t.shape)}")
+    if t.shape[1] < 1 or t.shape[2] < 1:
+        raise ValueError(f"{name} must have heads and columns, got {tuple(t.shape)}")
+    if t.numel() and t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name} must have packed heads (stride 1 in the last dimension)")
+    return t
+
+
+def _head_strides(t: torch.Tensor) -> Tuple[int, int]:
+    """Row and head strides; those of a dimension of one entry are of no account."""
+    rows, heads, d = t.shape
+    head = t.stride(1) if heads > 1 and rows else d
+    return (t.stride(0) if rows > 1 else max(heads * head, d)), head
+
+
+def _offsets(t, name: str, n: Optional[int] = None) -> torch.Tensor:
+    _need(t, name, (torch.int64, torch.int32))
+    if t.dim() != 1 or t.numel() < 1 or (n is not None and t.numel() != n):
+        raise ValueError(f"{name} must be 1-D with {n if n is not None else 'B+1'} entries, got {tuple(t.shape)}")
+    return t
+
+
+def _count(v, name: str) -> int:
+    v = int(v)
+    if not 0 <= v < 1 << 31:
+        raise ValueError(f"{name} must be 0 or more and below 2^31, got {v}")
+    return v
+
+
+def _seq_attn(q, k, v, q_offsets, begin, end, B, window, sinks, scale, bias, bounds):
+    """The checked description of an attention call; returns (struct, what it points to, device)."""
+    _head_rows(q, "q")
+    Hq, d = q.shape[1], q.shape[2]
+    _head_rows(k, "k", None, d)
+    Hkv = k.shape[1]
+    _head_rows(v, "v", Hkv, d)
+    if v.shape[0] != k.shape[0]:
+        raise ValueError(f"k and v must have the same rows, got {k.shape[0]} and {v.shape[0]}")
+    if Hq % Hkv:
+        raise ValueError(f"q's heads must be a multiple of k's, got {Hq} and {Hkv}")
+    if d % 8 or d > 128:
+        raise ValueError(f"a head must have a multiple of 8 columns, at most 128, got {d}")
+    if q_offsets is not None and begin.dtype != q_offsets.dtype or end.dtype != begin.dtype:
+        raise ValueError("all offsets must have one type")
+    if (bias is None) != (bounds is None):
+        raise ValueError("bias and bounds go together")
+    n, edges = 0, None
+    if bias is not None:
+        n = len(bounds)
+        if not 1 <= n <= DLRM_SEQ_MAX_BUCKETS or bounds[0] != 0 or any(b <= a for a, b in zip(bounds, bounds[1:])):
+            raise ValueError(f"bounds must be 1 to {DLRM_SEQ_MAX_BUCKETS} strictly increasing distances from 0 on")
+        if bounds[-1] >= 1 << 31:
+            raise ValueError("bounds must be below 2^31")
+        _need(bias, "bias", torch.float32, (Hq, n))
+        edges = (ctypes.c_int32 * n)(*bounds)
+    dev = _device(q, k, v, q_offsets, begin, end, bias)
+    a = _SeqAttn(B, q.shape[0], k.shape[0], Hq, Hkv, d, DLRM_INDEX_I32 if begin.dtype == torch.int32 else DLRM_INDEX_I64,
+                 None if q_offsets is None else q_offsets.data_ptr(), begin.data_ptr(), end.data_ptr(),
+                 q.data_ptr(), k.data_ptr(), v.data_ptr(), *_head_strides(q), *_head_strides(k), *_head_strides(v),
+                 _count(window, "window"), _count(sinks, "sinks"), 1.0 / d ** 0.5 if scale is None else float(scale), n,
+                 None if bias is None else bias.data_ptr(), None if edges is None else ctypes.addressof(edges))
+    return a, edges, dev
+
+
+def _kv_ranges(kv_offsets, B: int):
+    """(begin, end) of B sequences' keys, from offsets [B+1] or from such a pair."""
+    if isinstance(kv_offsets, (tuple, list)):
+        begin, end = kv_offsets
+        return _offsets_b(begin, "kv_begin", B), _offsets_b(end, "kv_end", B)
+    _offsets(kv_offsets, "kv_offsets", B + 1)
+    return kv_offsets[:-1], kv_offsets[1:]
+
+
+def _offsets_b(t, name: str, B: int) -> torch.Tensor:
+    return _need(t, name, (torch.int64, torch.int32), (B,))
+
+
+def dlrm_seq_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: torch.Tensor, kv_offsets=None, *,
+                      window: int = 0, sinks: int = 0, scale: Optional[float] = None,
+                      bias: Optional[torch.Tensor] = None, bounds: Optional[Sequence[int]] = None,
+                      for_backward: bool = False, out: Optional[torch.Tensor] = None,
+                      out_lo: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None):
+    """Causal attention over jagged sequences (C: dlrm_seq_attn_fwd): o [Nq, Hq, d] bf16, or with
+    for_backward (o, o_lo, lse).  q is [Nq, Hq, d], k and v [Nkv, Hkv, d]; the queries are the last
+    events of their sequence.  kv_offsets: offsets [B+1], a (begin, end) pair of [B], or None: the
+    queries' own.  scale: None is 1 / sqrt(d).  bias [Hq, buckets] with bounds, the first distance
+    of each bucket (dlrm_seq_bucket_bounds)."""
+    _offsets(q_offsets, "q_offsets")
+    B = q_offsets.numel() - 1
+    begin, end = _kv_ranges(q_offsets if kv_offsets is None else kv_offsets, B)
+    a, edges, dev = _seq_attn(q, k, v, q_offsets, begin, end, B, window, sinks, scale, bias, bounds)
+    shape = tuple(q.shape)
+    out = _opt(out, "out", torch.bfloat16, shape)
+    if out_lo is not None or lse is not None:
+        for_backward = True
+    out_lo = _opt(out_lo, "out_lo", torch.float32, shape)
+    lse = _opt(lse, "lse", torch.float32, shape[:2])
+    _device(q, out, out_lo, lse)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    if for_backward:
+        out_lo = torch.empty(shape, dtype=torch.float32, device=dev) if out_lo is None else out_lo
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=dev) if lse is None else lse
+    _check(lib().dlrm_seq_attn_fwd(ctypes.byref(a), _ptr(out), _ptr(out_lo), _ptr(lse), _stream(dev)), "dlrm_seq_attn_fwd")
+    return (out, out_lo, lse) if for_backward else out
+
+
+def dlrm_seq_attn_bwd_workspace_size(B: int, Nq: int, Hq: int, buckets: int) -> int:
+    return int(lib().dlrm_seq_attn_bwd_workspace_size(B, Nq, Hq, buckets))
+
+
+def dlrm_seq_attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
+                      o_lo: torch.Tensor, lse: torch.Tensor, q_offsets: torch.Tensor,
+                      kv_offsets: Optional[torch.Tensor] = None, *, window: int = 0, sinks: int = 0,
+                      scale: Optional[float] = None, bias: Optional[torch.Tensor] = None,
+                      bounds: Optional[Sequence[int]] = None, dq: Optional[torch.Tensor] = None,
+                      dk: Optional[torch.Tensor] = None, dv: Optional[torch.Tensor] = None,
+                      dbias: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """(dq, dk, dv, dbias or None) of dlrm_seq_attn_fwd (C: dlrm_seq_attn_bwd); o, o_lo and lse are what
+    it gave with for_backward, the other arguments its own; kv_offsets is None or offsets [B+1]."""
+    _offsets(q_offsets, "q_offsets")
+    B = q_offsets.numel() - 1
+    if isinstance(kv_offsets, (tuple, list)):
+        raise ValueError("the backward takes kv_offsets [B+1]: every key row in one sequence")
+    begin, end = _kv_ranges(q_offsets if kv_offsets is None else kv_offsets, B)
+    a, edges, dev = _seq_attn(q, k, v, q_offsets, begin, end, B, window, sinks, scale, bias, bounds)
+    qs, ks = tuple(q.shape), tuple(k.shape)
+    _need(dout, "dout", torch.bfloat16, qs)
+    _need(o, "o", torch.bfloat16, qs)
+    _need(o_lo, "o_lo", torch.float32, qs)
+    _need(lse, "lse", torch.float32, qs[:2])
+    dq, dk, dv = (_opt(t, name, torch.bfloat16, s) for t, name, s in ((dq, "dq", qs), (dk, "dk", ks), (dv, "dv", ks)))
+    if bias is None and dbias is not None:
+        raise ValueError("dbias without a bias")
+    dbias = _opt(dbias, "dbias", torch.float32, None if bias is None else tuple(bias.shape))
+    _device(q, dout, o, o_lo, lse, dq, dk, dv, dbias)
+    bf = dict(dtype=torch.bfloat16, device=dev)
+    dq = torch.empty(qs, **bf) if dq is None else dq
+    dk = torch.empty(ks, **bf) if dk is None else dk
+    dv = torch.empty(ks, **bf) if dv is None else dv
+    if bias is not None and dbias is None:
+        dbias = torch.empty_like(bias)
+    ws = _ws(dlrm_seq_attn_bwd_workspace_size(B, qs[0], qs[1], a.buckets), dev, workspace)
+    _check(lib().dlrm_seq_attn_bwd(ctypes.byref(a), _ptr(dout), _ptr(o), _ptr(o_lo), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),
+                                   _ptr(dbias), _ptr(ws), ws.numel(), _stream(dev)), "dlrm_seq_attn_bwd")
+    return dq, dk, dv, dbias
+
+
+def dlrm_seq_attn_decode_workspace_size(B: int, Hq: int, Hkv: int, d: int, window: int, sinks: int, max_kv_len: int) -> int:
+    return int(lib().dlrm_seq_attn_decode_workspace_size(B, Hq, Hkv, d, window, sinks, max_kv_len))
+
+
+def dlrm_seq_attn_decode(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_begin: torch.Tensor, kv_end: torch.Tensor, *,
+                         window: int = 0, sinks: int = 0, scale: Optional[float] = None,
+                         bias: Optional[torch.Tensor] = None, bounds: Optional[Sequence[int]] = None,
+                         max_kv_len: Optional[int] = None, out: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Attention of one new event a sequence over its cached keys (C: dlrm_seq_attn_decode): o [B, Hq, d]
+    bf16.  q is [B, Hq, d]; sequence b's keys are the rows kv_begin[b] .. kv_end[b] - 1 of k and v
+    [rows, Hkv, d], the event's own the last.  max_kv_len (the sequences' longest, None: k's rows)
+    only chooses how far a sequence is split."""
+    _head_rows(q, "q")
+    B = q.shape[0]
+    begin, end = _offsets_b(kv_begin, "kv_begin", B), _offsets_b(kv_end, "kv_end", B)
+    a, edges, dev = _seq_attn(q, k, v, None, begin, end, B, window, sinks, scale, bias, bounds)
+    longest = k.shape[0] if max_kv_len is None else int(max_kv_len)
+    if longest < 0:
+        raise ValueError(f"max_kv_len must not be negative, got {longest}")
+    out = _opt(out, "out", torch.bfloat16, tuple(q.shape))
+    _device(q, out)
+    if out is None:
+        out = torch.empty(tuple(q.shape), dtype=torch.bfloat16, device=dev)
+    ws = _ws(dlrm_seq_attn_decode_workspace_size(B, a.Hq, a.Hkv, a.d, a.window, a.sinks, longest), dev, workspace)
+    _check(lib().dlrm_seq_attn_decode(ctypes.byref(a), longest, _ptr(out), _ptr(ws), ws.numel(), _stream(dev)),
+           "dlrm_seq_attn_decode")
+    return out
+
+
+def _drop_spec(p: float, seed: int, offset: int, offset_dev: Optional[torch.Tensor]) -> _Dropout:
+    if not 0.0 <= p <= 1.0:
+        raise ValueError(f"p must be between 0 and 1, got {p}")
+    for x, name in ((seed, "seed"), (offset, "offset")):
+        if not 0 <= x < 1 << 64:
+            raise ValueError(f"{name} must be 0 or more and below 2^64, got {x}")
+    _opt(offset_dev, "offset_dev", torch.int64, min_numel=1)
+    return _Dropout(p, seed, offset, None if offset_dev is None else offset_dev.data_ptr())
+
+
+def dlrm_dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0, *, offset_dev: Optional[torch.Tensor] = None,
+                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Dropout by counter-based random numbers, no mask stored; its derivative is the same call on
+    the gradient (C: dlrm_dropout).  out may be x; offset_dev: one int64 on the device, added."""
+    _need(x, "x", (torch.float32, torch.bfloat16))
+    out = _opt(out, "out", x.dtype, tuple(x.shape))
+    spec = _drop_spec(p, seed, offset, offset_dev)
+    dev = _device(x, out, offset_dev)
+    if out is None:
+        out = torch.empty_like(x)
+    _check(lib().dlrm_dropout(_ptr(x), _TORCH_CODE[x.dtype], x.numel(), ctypes.byref(spec), _ptr(out), _stream(dev)),
+           "dlrm_dropout")
+    return out
+
+
+def dlrm_add_rmsnorm_fwd(x: torch.Tensor, residual: Optional[torch.Tensor], w: torch.Tensor, eps: float = 1e-6, *,
+                         p: float = 0.0, seed: int = 0, offset: int = 0, offset_dev: Optional[torch.Tensor] = None,
+                         y_dtype: torch.dtype = torch.bfloat16, res_dtype: Optional[torch.dtype] = None,
+                         s: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                         rstd: Optional[torch.Tensor] = None, y_scale: Optional[torch.Tensor] = None):
+    """(s, y, rstd, y_scale or None): s = residual + dropout(x), y = s * rstd * w (C:
+    dlrm_add_rmsnorm_fwd).  x and residual are [M, D]; y_dtype float8_e4m3fn gives 8-bit values to be
+    multiplied by y_scale [M].  s may be the residual.  res_dtype is for a residual of None."""
+    _mat(x, "x", (torch.float32, torch.bfloat16))
+    M, D = x.shape
+    rt = residual.dtype if isinstance(residual, torch.Tensor) else res_dtype or x.dtype
+    _opt(residual, "residual", (torch.float32, torch.bfloat16), (M, D))
+    if rt not in _TORCH_CODE:
+        raise ValueError(f"res_dtype must be float32 or bfloat16, got {rt}")
+    _need(w, "w", torch.float32, (D,))
+    yt = y_dtype if y is None else y.dtype
+    codes = {**_TORCH_CODE, torch.float8_e4m3fn: DLRM_F8_E4M3}
+    if yt not in codes:
+        raise ValueError(f"y_dtype must be float32, bfloat16 or float8_e4m3fn, got {yt}")
+    s, y = _opt(s, "s", rt, (M, D)), _opt(y, "y", yt, (M, D))
+    rstd, y_scale = _opt(rstd, "rstd", torch.float32, (M,)), _opt(y_scale, "y_scale", torch.float32, (M,))
+    spec = _drop_spec(p, seed, offset, offset_dev)
+    dev = _device(x, residual, w, s, y, rstd, y_scale, offset_dev)
+    s = torch.empty((M, D), dtype=rt, device=dev) if s is None else s
+    y = torch.empty((M, D), dtype=yt, device=dev) if y is None else y
+    rstd = torch.empty(M, dtype=torch.float32, device=dev) if rstd is None else rstd
+    if yt == torch.float8_e4m3fn and y_scale is None:
+        y_scale = torch.empty(M, dtype=torch.float32, device=dev)
+    _check(lib().dlrm_add_rmsnorm_fwd(_ptr(x), _TORCH_CODE[x.dtype], _ptr(residual), _TORCH_CODE[rt], _ptr(w), float(eps),
+                                      ctypes.byref(spec), M, D, _ptr(s), _ptr(y), codes[yt], _ptr(y_scale), _ptr(rstd),
+                                      _stream(dev)), "dlrm_add_rmsnorm_fwd")
+    return s, y, rstd, (y_scale if yt == torch.float8_e4m3fn else None)
+
+
+def dlrm_add_rmsnorm_bwd_workspace_size(M: int, D: int) -> int:
+    return int(lib().dlrm_add_rmsnorm_bwd_workspace_size(M, D))
+
+
+def dlrm_add_rmsnorm_bwd(dy: torch.Tensor, ds: Optional[torch.Tensor], s: torch.Tensor, w: torch.Tensor, rstd: torch.Tensor, *,
+                         x_dtype: torch.dtype = torch.bfloat16, p: float = 0.0, seed: int = 0, offset: int = 0,
+                         offset_dev: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                         dresidual: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None):
+    """(dx, dresidual, dw) of dlrm_add_rmsnorm_fwd, given dy and (or None) ds, the gradient that reaches
+    s past the norm; s, w, rstd and the dropout arguments are the forward's (C: dlrm_add_rmsnorm_bwd).
+    dresidual may be ds."""
+    _mat(s, "s", (torch.float32, torch.bfloat16))
+    M, D = s.shape
+    _need(dy, "dy", (torch.float32, torch.bfloat16), (M, D))
+    _opt(ds, "ds", s.dtype, (M, D))
+    _need(w, "w", torch.float32, (D,))
+    _need(rstd, "rstd", torch.float32, (M,))
+    xt = x_dtype if dx is None else dx.dtype
+    if xt not in _TORCH_CODE:
+        raise ValueError(f"x_dtype must be float32 or bfloat16, got {xt}")
+    dx, dresidual = _opt(dx, "dx", xt, (M, D)), _opt(dresidual, "dresidual", s.dtype, (M, D))
+    dw = _opt(dw, "dw", torch.float32, (D,))
+    spec = _drop_spec(p, seed, offset, offset_dev)
+    dev = _device(dy, ds, s, w, rstd, dx, dresidual, dw, offset_dev)
+    dx = torch.empty((M, D), dtype=xt, device=dev) if dx is None else dx
+    dresidual = torch.empty_like(s) if dresidual is None else dresidual
+    dw = torch.empty(D, dtype=torch.float32, device=dev) if dw is None else dw
+    ws = _ws(dlrm_add_rmsnorm_bwd_workspace_size(M, D), dev, workspace)
+    _check(lib().dlrm_add_rmsnorm_bwd(_ptr(dy), _TORCH_CODE[dy.dtype], _ptr(ds), _ptr(s), _TORCH_CODE[s.dtype], _ptr(w),
+                                      _ptr(rstd), ctypes.byref(spec), M, D, _ptr(dx), _TORCH_CODE[xt], _ptr(dresidual),
+                                      _ptr(dw), _ptr(ws), ws.numel(), _stream(dev)), "dlrm_add_rmsnorm_bwd")
+    return dx, dresidual, dw
 
 
 def dlrm_trace_enable(on: bool = True) -> None:

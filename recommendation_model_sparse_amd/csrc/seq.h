@@ -1,0 +1,219 @@
+// Shared by the attention kernels over jagged sequences (dlrm_seq.h): arguments, the map from
+// workgroups to tiles of sequences, LDS tiles and matrix-core fragments.
+#pragma once
+
+#include "common.h"
+#include "dlrm_seq.h"
+
+namespace dlrm {
+namespace seq {
+
+constexpr int kBK = 64;  // rows of a staged tile (keys; queries in the backward over keys)
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kInf = __builtin_inff();
+// Above this a maximum or log-sum of the logits is rounded by more than 2^-4, and exp(z - m) is
+// taken from the difference itself instead of from one fused multiply-add in base 2: a row whose
+// every visible bias is -1e9, or the type's lowest value, still has z - m = 0.
+constexpr float kHuge = 0x1p20f;
+
+struct Args {
+    const uint16_t *q, *k, *v;
+    int64_t q_row, q_head, k_row, k_head, v_row, v_head;
+    const void *q_off, *kv_begin, *kv_end;
+    int64_t Nq, Nkv;
+    int32_t B, Hq, Hkv, group, d;
+    int32_t idx32;
+    int32_t window, sinks;
+    float scale;       // of <q, k>
+    float scale_log2;  // scale * log2(e): the softmax is computed in base 2
+    const float *bias;
+    int32_t buckets;   // 0 without a bias
+    int32_t last;      // first distance of the last bucket: from there on the bias is one value
+    int32_t bounds[DLRM_SEQ_MAX_BUCKETS];
+};
+
+// Checks the description and fills Args (host).
+int check_attn(const dlrm_seq_attn *a, bool need_q_offsets, Args *out);
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+union Frag {  // eight bf16 values: one lane's share of an MFMA operand
+    uint32_t w[4];
+    u32x4 q;
+    s16x4 h[2];
+    bf16x8 b;
+};
+
+// Two fp32 -> two bf16, round to nearest even.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const f32x2 v = {lo, hi};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+}
+
+__device__ __forceinline__ int64_t offset_at(const Args &a, const void *p, int64_t i, int64_t limit) {
+    const int64_t x = a.idx32 ? static_cast<const int32_t *>(p)[i] : static_cast<const int64_t *>(p)[i];
+    return x < 0 ? 0 : (x > limit ? limit : x);
+}
+
+// Tiles of T rows over B jagged sequences without a table of them: sequence b owns the slots from
+// off[b] / T + b on.  It needs ceil(len / T) <= off[b+1] / T - off[b] / T + 1 of them, so no two
+// sequences meet; rows / T + B slots cover all, and those a sequence does not need end at once.
+__host__ __device__ __forceinline__ int64_t slot_count(int64_t rows, int64_t B, int T) { return rows / T + B; }
+
+// The sequence that owns a slot: a 64-ary search by one wavefront (two rounds up to 4096
+// sequences), as every probe waits for memory.
+__device__ __forceinline__ int find_sequence(const Args &a, const void *off, int64_t limit, int64_t slot, int T) {
+    int lo = 0, n = a.B;
+    while (n > 1) {
+        const int step = (n + 63) / 64;
+        const int at = static_cast<int>(__lane_id()) * step;
+        bool below = false;
+        if (at < n) below = offset_at(a, off, lo + at, limit) / T + lo + at <= slot;
+        const int c = __popcll(__ballot(below));
+        if (c == 0) return lo;  // offsets that are not in order: any sequence does
+        lo += (c - 1) * step;
+        n = min(step, n - (c - 1) * step);
+    }
+    return __builtin_amdgcn_readfirstlane(lo);
+}
+
+struct Span {  // one sequence
+    int64_t q0, k0;  // first rows
+    int qlen, klen;
+    int shift;       // position of query 0
+};
+
+__device__ __forceinline__ Span span_of(const Args &a, int b) {
+    Span s;
+    s.q0 = offset_at(a, a.q_off, b, a.Nq);
+    const int64_t q1 = offset_at(a, a.q_off, b + 1, a.Nq);
+    s.k0 = offset_at(a, a.kv_begin, b, a.Nkv);
+    const int64_t k1 = offset_at(a, a.kv_end, b, a.Nkv);
+    s.qlen = q1 > s.q0 ? static_cast<int>(q1 - s.q0) : 0;
+    s.klen = k1 > s.k0 ? static_cast<int>(k1 - s.k0) : 0;
+    s.shift = s.klen - s.qlen;
+    return s;
+}
+
+// ---------------------------------------------------------------- LDS tiles
+//
+// A tile holds 64 rows of LP elements (LP = 32, 64 or 128: the head's width rounded up) in 16-byte
+// chunks.  Chunk c of row r is kept at c ^ mix(r): the rows that one read instruction touches at
+// the same c then lie in different banks.
+
+template <int LP>
+__device__ __forceinline__ int chunk_at(int r, int c) {
+    constexpr int CH = LP / 8;
+    const int mix = CH >= 16 ? r : r / (16 / CH);
+    return r * CH + (c ^ (mix & (CH - 1)));
+}
+
+// One lane's 8 bf16 of row r from column 8 * c on.
+template <int LP>
+__device__ __forceinline__ void read_row(Frag &f, const uint16_t *tile, int r, int c) {
+    f.q = *reinterpret_cast<const u32x4 *>(tile + chunk_at<LP>(r, c) * 8);
+}
+
+// Transposed operand of v_mfma_f32_32x32x16_bf16 from a row-major tile: lane l gets column
+// col0 + (l & 31) of the rows row0 + 4 * (l >> 5) + {0..3} and those 8 further on.  That is the
+// order in which the accumulator of the product before holds its rows, so that its values are this
+// product's other operand as they stand.  Within 16 lanes ds_read_b64_tr_b16 takes 4 rows of 16
+// columns, lane i reading 4 columns of row i / 4, and gives lane i column i of the 4 rows.
+template <int LP>
+__device__ __forceinline__ void read_columns(Frag &f, const uint16_t *tile, int row0, int col0, int lane) {
+    const int i = lane & 15;
+    const int col = col0 + (lane & 16) + 4 * (i & 3);
+    const int row = row0 + 4 * (lane >> 5) + (i >> 2);
+    typedef __attribute__((address_space(3))) s16x4 *lds_t;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        const uint16_t *p = tile + chunk_at<LP>(row + 8 * g, col >> 3) * 8 + (col & 7);
+        f.h[g] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t)(p));
+    }
+}
+
+// 64 rows of a [rows][d] bf16 matrix on their way to LDS, through registers: `load` issues the
+// reads for a tile (rows outside [first, end), but for those below `sinks`, are zeros, as are
+// columns from d on), `store` writes it.
+template <int LP, int THREADS>
+struct Stage {
+    static constexpr int CH = LP / 8;
+    static constexpr int N = kBK * CH / THREADS;  // chunks a thread
+    u32x4 r[N];
+
+    __device__ __forceinline__ void load(const uint16_t *base, int64_t row_stride, int d, int row0, int first, int end,
+                                         int sinks) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int at = i * THREADS + static_cast<int>(threadIdx.x);
+            const int row = row0 + at / CH, c = at % CH;
+            r[i] = u32x4{0, 0, 0, 0};
+            if (row < end && (row >= first || row < sinks) && c * 8 < d)
+                r[i] = *(const DLRM_GLOBAL u32x4 *)(base + row * row_stride + c * 8);
+        }
+    }
+    __device__ __forceinline__ void store(uint16_t *tile) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int at = i * THREADS + static_cast<int>(threadIdx.x);
+            *reinterpret_cast<u32x4 *>(tile + chunk_at<LP>(at / CH, at % CH) * 8) = r[i];
+        }
+    }
+};
+
+// Two bf16 with infinities and NaN replaced by zeros.
+__device__ __forceinline__ uint32_t only_finite(uint32_t x) {
+    const uint32_t lo = (x & 0x7f80u) == 0x7f80u ? 0u : x & 0xffffu;
+    const uint32_t hi = (x & 0x7f800000u) == 0x7f800000u ? 0u : x & 0xffff0000u;
+    return lo | hi;
+}
+
+// Orders one wavefront's LDS writes before its lanes' reads of each other's.
+__device__ __forceinline__ void wave_lds_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// The maximum (sum) of a value over the two lanes l and l ^ 32.
+__device__ __forceinline__ float max_halves(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float add_halves(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// ---------------------------------------------------------------- bias by distance
+
+// The bucket of distance n >= 0: the last t with bounds[t] <= n.
+__device__ __forceinline__ int bucket_of(const int *bounds, int buckets, int n) {
+    int lo = 0, hi = buckets;  // bounds[lo] <= n < bounds[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (bounds[mid] <= n) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// What a tile's table adds to the logits at distance n: the bias, or -infinity where it is not visible
+// (`sink_tile`: the window is left to the caller, who knows which keys are first ones).
+// bounds_s and bias_s are in LDS.
+__device__ __forceinline__ float table_entry(const Args &a, const int *bounds_s, const float *bias_s, int n, bool sink_tile,
+                                             int *bucket) {
+    const int t = n > 0 && a.buckets ? bucket_of(bounds_s, a.buckets, n) : 0;
+    *bucket = t;
+    if (n < 0 || (a.window && n >= a.window && !sink_tile)) return -kInf;
+    return a.buckets ? bias_s[t] : 0.f;
+}
+
+}  // namespace seq
+}  // namespace dlrm

@@ -1,0 +1,315 @@
+// Attention of one new event a sequence over its cached keys and values (dlrm_seq.h).
+//
+// Bound by reading the cache once.  A workgroup takes one key/value head of one sequence, or a run
+// of its visible keys where there are too few of them to fill the GPU, and up to 16 query heads
+// that share it: each byte of the cache is read by one wavefront.  Each of the four wavefronts walks
+// chunks of 32 keys with its own running maximum and sum; their results are joined at the end, those
+// of several runs by a second kernel.  The products are 16x16x32 matrix instructions on transposed
+// tiles, as in the forward: K goes from memory straight into the first operand, P^T stays in
+// registers, and V passes through LDS, each wavefront's own, for the transposed read.
+#include "seq.h"
+
+namespace dlrm {
+namespace seq {
+namespace {
+
+constexpr int kHeads = 16;  // query heads a workgroup: the columns of a product
+constexpr int kWaves = 4;
+constexpr int kChunk = 32;  // keys a wavefront takes at once
+
+__device__ __forceinline__ float max_quarters(float x) {  // over lanes l, l ^ 16, l ^ 32, l ^ 48
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return max_halves(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+}
+__device__ __forceinline__ float add_quarters(float x) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return add_halves(__uint_as_float(r[0]) + __uint_as_float(r[1]));
+}
+
+// part: [B][Hq][splits] rows of d floats; ml: their (maximum, sum)
+template <int DP>
+__global__ __launch_bounds__(kWaves * 64) void k_seq_attn_decode(const Args a, const int splits, const int head_groups,
+                                                                 uint16_t *o_out, float *part, float2 *ml) {
+    constexpr int LP = DP, CH = LP / 8, STEPS = DP / 32, MB = DP / 16, VN = kChunk * CH / 64;
+    union Lds {
+        uint16_t v[kWaves][kChunk * LP];
+        float o[kWaves][kHeads][DP];
+    };
+    __shared__ __attribute__((aligned(16))) Lds lds;
+    __shared__ __attribute__((aligned(16))) int ids[kWaves][kChunk];
+    __shared__ float top_s[kWaves][kHeads], sum_s[kWaves][kHeads];
+    __shared__ float bias_s[kHeads * DLRM_SEQ_MAX_BUCKETS];
+    __shared__ int bounds_s[DLRM_SEQ_MAX_BUCKETS];
+
+    int64_t id = blockIdx.x;
+    const int split = static_cast<int>(id % splits);
+    id /= splits;
+    const int hg = static_cast<int>(id % head_groups);
+    id /= head_groups;
+    const int kvh = static_cast<int>(id % a.Hkv), b = static_cast<int>(id / a.Hkv);
+    const int h0 = kvh * a.group + hg * kHeads, heads = min(kHeads, a.group - hg * kHeads);
+    const int tid = threadIdx.x, lane = tid & 63, ln = lane & 15, quad = lane >> 4;
+    const int w = static_cast<int>(wave_id());
+
+    const int64_t row0 = offset_at(a, a.kv_begin, b, a.Nkv), row1 = offset_at(a, a.kv_end, b, a.Nkv);
+    const int klen = row1 > row0 ? static_cast<int>(row1 - row0) : 0;
+    // the visible keys in a row: the first `skip` ones, then those from `start` on
+    const int start = a.window ? max(0, klen - a.window) : 0;
+    const int skip = min(a.sinks, start);
+    const int seen = skip + klen - start;
+    const int per = ((seen + kChunk - 1) / kChunk + splits - 1) / splits * kChunk;
+    const int v0 = min(static_cast<int64_t>(split) * per, static_cast<int64_t>(seen)), v1 = min(v0 + per, seen);
+
+    for (int i = tid; i < a.buckets; i += kWaves * 64) bounds_s[i] = a.bounds[i];
+    for (int i = tid; i < a.buckets * heads; i += kWaves * 64) bias_s[i] = a.bias[static_cast<int64_t>(h0) * a.buckets + i];
+    __syncthreads();
+    const float *my_bias = bias_s + (ln < heads ? ln * a.buckets : 0);
+    const float far = a.buckets ? my_bias[a.buckets - 1] : 0.f;
+
+    Frag qf[STEPS];
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+        qf[s].q = u32x4{0, 0, 0, 0};
+        const int c = 32 * s + 8 * quad;
+        if (ln < heads && c < a.d) qf[s].q = *(const DLRM_GLOBAL u32x4 *)(a.q + b * a.q_row + (h0 + ln) * a.q_head + c);
+    }
+    const uint16_t *kb = a.k + row0 * a.k_row + kvh * a.k_head;
+    const uint16_t *vb = a.v + row0 * a.v_row + kvh * a.v_head;
+
+    floatx4 o[MB];
+#pragma unroll
+    for (int m = 0; m < MB; ++m) o[m] = floatx4{0.f, 0.f, 0.f, 0.f};
+    float top = -kInf, sum = 0.f;
+
+    u32x4 kr[2][STEPS], vr[VN];
+    const auto load = [&](int c) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const int v = c + 16 * g + ln;
+            const int64_t key = v < skip ? v : start + v - skip;
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                kr[g][s] = u32x4{0, 0, 0, 0};
+                const int col = 32 * s + 8 * quad;
+                if (v < v1 && col < a.d) kr[g][s] = *(const DLRM_GLOBAL u32x4 *)(kb + key * a.k_row + col);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < VN; ++i) {
+            const int at = i * 64 + lane, v = c + at / CH, col = at % CH * 8;
+            const int64_t key = v < skip ? v : start + v - skip;
+            vr[i] = u32x4{0, 0, 0, 0};
+            if (v < v1 && col < a.d) vr[i] = *(const DLRM_GLOBAL u32x4 *)(vb + key * a.v_row + col);
+        }
+    };
+
+    int c = v0 + w * kChunk;
+    if (c < v1) load(c);
+    for (; c < v1; c += kWaves * kChunk) {
+        uint16_t *vt = lds.v[w];
+        floatx4 s[2];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            s[g] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < STEPS; ++i) {
+                Frag k;
+                k.q = kr[g][i];
+                s[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k.b, qf[i].b, s[g], 0, 0, 0);
+            }
+        }
+        wave_lds_sync();  // the chunk before has been read
+#pragma unroll
+        for (int i = 0; i < VN; ++i) {
+            const int at = i * 64 + lane;
+            *reinterpret_cast<u32x4 *>(vt + chunk_at<LP>(at / CH, at % CH) * 8) = vr[i];
+        }
+        const int next = c + kWaves * kChunk;
+        if (next < v1) load(next);
+
+        // register r of block g: key c + 16 g + 4 quad + r (of those in a row)
+        const int last_v = min(c + kChunk, v1) - 1;
+        const int nearest = klen - 1 - (last_v < skip ? last_v : start + last_v - skip);
+        if (!a.buckets || nearest >= a.last) {
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) s[g][r] = fmaf(s[g][r], a.scale, far);
+        } else {
+            if (lane < kChunk) {
+                const int v = c + lane;
+                ids[w][lane] = bucket_of(bounds_s, a.buckets, max(0, klen - 1 - (v < skip ? v : start + v - skip)));
+            }
+            wave_lds_sync();
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) s[g][r] = fmaf(s[g][r], a.scale, my_bias[ids[w][16 * g + 4 * quad + r]]);
+        }
+        if (c + kChunk > v1) {
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (c + 16 * g + 4 * quad + r >= v1) s[g][r] = -kInf;
+        }
+        float mx = s[0][0];
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) mx = fmaxf(mx, s[g][r]);
+        mx = fmaxf(max_quarters(mx), top);
+        if (__any(mx > top)) {
+            const float f = mx == -kInf ? 1.f : __builtin_amdgcn_exp2f((top - mx) * kLog2e);
+            sum *= f;
+#pragma unroll
+            for (int m = 0; m < MB; ++m)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) o[m][r] *= f;
+            top = mx;
+        }
+        const float ref = top == -kInf ? 0.f : top;
+        Frag p;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                s[g][r] = __builtin_amdgcn_exp2f((s[g][r] - ref) * kLog2e);
+                sum += s[g][r];
+            }
+            p.w[2 * g] = pack_bf16(s[g][0], s[g][1]);
+            p.w[2 * g + 1] = pack_bf16(s[g][2], s[g][3]);
+        }
+        wave_lds_sync();
+#pragma unroll
+        for (int m = 0; m < MB; ++m) {
+            // column 16 m + ln of the keys 4 quad + {0..3} and those 16 further on
+            typedef __attribute__((address_space(3))) s16x4 *lds_t;
+            Frag v;
+            const int col = 16 * m + 4 * (ln & 3), row = 4 * quad + (ln >> 2);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const uint16_t *at = vt + chunk_at<LP>(row + 16 * g, col >> 3) * 8 + (col & 7);
+                v.h[g] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t)(at));
+            }
+            o[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v.b, p.b, o[m], 0, 0, 0);
+        }
+    }
+    sum = add_quarters(sum);
+
+    // join the wavefronts
+    __syncthreads();
+    if (quad == 0) top_s[w][ln] = top, sum_s[w][ln] = sum;
+#pragma unroll
+    for (int m = 0; m < MB; ++m) *reinterpret_cast<floatx4 *>(&lds.o[w][ln][16 * m + 4 * quad]) = o[m];
+    __syncthreads();
+    for (int i = tid; i < heads * (DP / 4); i += kWaves * 64) {
+        const int hd = i / (DP / 4), col = i % (DP / 4) * 4;
+        if (col >= a.d) continue;
+        float mx = top_s[0][hd];
+#pragma unroll
+        for (int v = 1; v < kWaves; ++v) mx = fmaxf(mx, top_s[v][hd]);
+        float total = 0.f;
+        floatx4 x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int v = 0; v < kWaves; ++v) {
+            const float t = top_s[v][hd];
+            const float f = t == -kInf ? 0.f : __builtin_amdgcn_exp2f((t - mx) * kLog2e);
+            const floatx4 y = *reinterpret_cast<const floatx4 *>(&lds.o[v][hd][col]);
+            total += f * sum_s[v][hd];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] += f * y[e];
+        }
+        const int64_t row = static_cast<int64_t>(b) * a.Hq + h0 + hd;
+        if (splits == 1) {
+            const float inv = total == 0.f ? 0.f : 1.f / total;
+            *(DLRM_GLOBAL u32x2 *)(o_out + row * a.d + col) =
+                u32x2{pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv)};
+        } else {
+            *(DLRM_GLOBAL floatx4 *)(part + (row * splits + split) * a.d + col) = x;
+            if (col == 0) ml[row * splits + split] = make_float2(mx, total);
+        }
+    }
+}
+
+// Joins the runs of a row: one wavefront a row, two columns a lane.
+__global__ __launch_bounds__(256) void k_seq_decode_join(const float *part, const float2 *ml, int64_t rows, int splits, int d,
+                                                         uint16_t *o) {
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
+    if (row >= rows) return;
+    float mx = -kInf;
+    for (int s = 0; s < splits; ++s) mx = fmaxf(mx, ml[row * splits + s].x);
+    float total = 0.f, x = 0.f, y = 0.f;
+    for (int s = 0; s < splits; ++s) {
+        const float2 t = ml[row * splits + s];
+        const float f = t.x == -kInf ? 0.f : __builtin_amdgcn_exp2f((t.x - mx) * kLog2e);
+        total += f * t.y;
+        if (2 * lane < d) {
+            const float2 v = *reinterpret_cast<const float2 *>(part + (row * splits + s) * d + 2 * lane);
+            x += f * v.x, y += f * v.y;
+        }
+    }
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+    if (2 * lane < d) *reinterpret_cast<uint32_t *>(o + row * d + 2 * lane) = pack_bf16(x * inv, y * inv);
+}
+
+// Runs a sequence's keys are split into: enough workgroups for four a CU, at least 256 keys each.
+int split_count(int64_t B, int32_t Hq, int32_t Hkv, int32_t window, int32_t sinks, int64_t max_kv_len) {
+    const int64_t blocks = B * Hkv * ((Hq / Hkv + kHeads - 1) / kHeads);
+    int64_t seen = max_kv_len;
+    if (window > 0 && static_cast<int64_t>(window) + sinks < seen) seen = static_cast<int64_t>(window) + sinks;
+    int64_t s = blocks > 0 ? (1024 + blocks - 1) / blocks : 1;
+    const int64_t most = (seen + 255) / 256;
+    s = s < most ? s : most;
+    return static_cast<int>(s < 1 ? 1 : s > 256 ? 256 : s);
+}
+
+template <int DP>
+int launch(const Args &a, int splits, uint16_t *o, void *ws, hipStream_t stream) {
+    const int head_groups = (a.group + kHeads - 1) / kHeads;
+    const int64_t rows = static_cast<int64_t>(a.B) * a.Hq, blocks = static_cast<int64_t>(a.B) * a.Hkv * head_groups * splits;
+    if (blocks >= (int64_t(1) << 31)) return DLRM_ERR_UNSUPPORTED;
+    float *part = static_cast<float *>(ws);
+    float2 *ml = reinterpret_cast<float2 *>(part ? part + rows * splits * a.d : nullptr);
+    DLRM_LAUNCH("seq_attn_decode", (k_seq_attn_decode<DP>), dim3(static_cast<uint32_t>(blocks)), dim3(kWaves * 64), 0, stream, a,
+                splits, head_groups, o, part, ml);
+    if (splits > 1)
+        DLRM_LAUNCH("seq_decode_join", k_seq_decode_join, dim3(static_cast<uint32_t>((rows + 3) / 4)), dim3(256), 0, stream,
+                    static_cast<const float *>(part), static_cast<const float2 *>(ml), rows, splits, a.d, o);
+    return launch_status();
+}
+
+}  // namespace
+}  // namespace seq
+}  // namespace dlrm
+
+extern "C" size_t dlrm_seq_attn_decode_workspace_size(int64_t B, int32_t Hq, int32_t Hkv, int32_t d, int32_t window,
+                                                      int32_t sinks, int64_t max_kv_len) {
+    using namespace dlrm::seq;
+    if (B < 0 || B >= (1 << 24) || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Hq > 4096 || d < 1 || d > 128 || window < 0 || sinks < 0 ||
+        max_kv_len < 0)
+        return 0;
+    const int splits = split_count(B, Hq, Hkv, window, sinks, max_kv_len);
+    return 256 + (splits > 1 ? static_cast<size_t>(B) * Hq * splits * (d + 2) * 4 : 0);
+}
+
+extern "C" int dlrm_seq_attn_decode(const dlrm_seq_attn *desc, int64_t max_kv_len, uint16_t *o, void *workspace,
+                                    size_t workspace_bytes, dlrm_stream_t stream_) {
+    using namespace dlrm;
+    using namespace dlrm::seq;
+    Args a;
+    const int rc = check_attn(desc, false, &a);
+    if (rc != DLRM_OK) return rc;
+    if (a.Nq != a.B || max_kv_len < 0) return DLRM_ERR_INVALID_ARG;
+    if (a.B == 0) return DLRM_OK;
+    if (!o || !aligned(o, 16)) return DLRM_ERR_INVALID_ARG;
+    const int splits = split_count(a.B, a.Hq, a.Hkv, a.window, a.sinks, max_kv_len);
+    if (splits > 1 && (!workspace || !aligned(workspace, 256) ||
+                       workspace_bytes < dlrm_seq_attn_decode_workspace_size(a.B, a.Hq, a.Hkv, a.d, a.window, a.sinks, max_kv_len)))
+        return DLRM_ERR_WORKSPACE;
+    hipStream_t stream = reinterpret_cast<hipStream_t>(stream_);
+    if (a.d <= 32) return launch<32>(a, splits, o, workspace, stream);
+    if (a.d <= 64) return launch<64>(a, splits, o, workspace, stream);
+    return launch<128>(a, splits, o, workspace, stream);
+}

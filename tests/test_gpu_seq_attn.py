@@ -1,0 +1,388 @@
+"""GPU parity of attention over jagged histories (dlrm_seq.h; needs an MI355X) against oracle/seq.py.
+
+Error measure: |gpu - oracle| over the sum of the absolute values of the terms (the oracle's scales).
+Gates, from the arithmetic, with e = (d + 8) 2^-24 z_s a bound of a logit's error (fp32 products and
+sums; z_s the largest sum of a logit's terms), which is a relative error of P:
+  - o of the forward alone: P rounded to bf16 (8 significant bits: 2^-8), o too, and e twice (P and
+    its sum): 2^-7 + 2 e + 2^-16 for exp2 and the fp32 sums;
+  - o + o_lo with for_backward: held to 2^-15 + 2 e, which two pieces of 8 bits each would meet;
+  - lse: an absolute error of e + 2^-21 z_s + 2^-20;
+  - dq, dk: ds rounded to bf16, the result too: 2^-7, and P and dP - delta in fp32 from o + o_lo:
+    2^-14 + 4 e;  dv: P and the result rounded: the same;
+  - dbias: no rounding to bf16: 2^-14 + 4 e.
+Inputs are bf16 values, so both sides start from the same numbers.
+"""
+import zlib
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import seq
+from recommendation_model_sparse_amd import (DlrmError, dlrm_seq_attn_bwd, dlrm_seq_attn_decode, dlrm_seq_attn_fwd,
+                                             dlrm_seq_bucket_bounds, synth)
+
+from gpu_util import DEV, rel_err, say, to_dev
+
+pytestmark = pytest.mark.gpu
+
+
+def rng_of(*a):
+    return np.random.default_rng(zlib.crc32("-".join(map(str, a)).encode()))
+
+
+def bf16(rng, *shape):
+    """(device bf16 tensor, host fp64 values)."""
+    bits = synth.f32_to_bf16_bits(rng.standard_normal(shape).astype(np.float32))
+    return to_dev(bits), synth.bf16_bits_to_f32(bits).astype(np.float64)
+
+
+def host(t):
+    return t.float().cpu().numpy().astype(np.float64)
+
+
+def offsets(lens, dtype=np.int64):
+    return np.cumsum([0] + list(lens)).astype(dtype)
+
+
+def e_of(d, ref):
+    return (d + 8) * 2.0 ** -24 * ref["z_s"]
+
+
+def check_lse(got, ref, e):
+    dead = np.isinf(ref["lse"])
+    assert np.array_equal(np.isinf(got), dead) and (got[dead] < 0).all()
+    if (~dead).any():
+        assert np.abs(got[~dead] - ref["lse"][~dead]).max() <= e + 2.0 ** -21 * ref["z_s"] + 2.0 ** -20
+
+
+LENS = {
+    "one": ([1], [1]),
+    "few": ([3, 0, 1, 2, 0], [3, 0, 1, 2, 0]),
+    "tiles": ([31, 32, 33, 63, 64, 65, 1], [31, 32, 33, 63, 64, 65, 1]),
+    "blocks": ([127, 128, 129, 200], [127, 128, 129, 200]),
+    "long": ([700, 5, 391], [700, 5, 391]),
+    "later": ([3, 64, 130, 1, 40], [90, 200, 131, 77, 40]),     # the queries are the last events
+    "blind": ([70, 5, 140, 3], [3, 0, 65, 3]),                  # more queries than keys: the first see none
+}
+SHAPES = [
+    # lens, Hq, Hkv, d, window, sinks, buckets, reach
+    ("one", 1, 1, 8, 0, 0, 0, 0), ("one", 4, 2, 64, 1, 1, 8, 20), ("few", 2, 1, 16, 0, 0, 1, 5), ("few", 3, 3, 128, 2, 1, 32, 128),
+    ("tiles", 2, 2, 32, 0, 0, 32, 128), ("tiles", 4, 1, 64, 0, 0, 0, 0), ("tiles", 2, 1, 40, 10, 0, 8, 64),
+    ("tiles", 2, 2, 128, 33, 3, 33, 40), ("blocks", 2, 2, 64, 0, 0, 32, 64), ("blocks", 4, 2, 96, 64, 70, 64, 150),
+    ("blocks", 1, 1, 128, 0, 0, 128, 300), ("long", 2, 1, 64, 100, 4, 32, 128), ("long", 2, 2, 32, 0, 0, 8, 30),
+    ("long", 6, 2, 128, 0, 0, 32, 4096), ("long", 1, 1, 64, 1, 0, 4, 4), ("long", 2, 2, 64, 130, 200, 16, 100),
+    ("later", 4, 2, 64, 0, 0, 32, 128), ("later", 2, 1, 128, 50, 3, 16, 64), ("later", 2, 2, 32, 64, 64, 0, 0),
+    ("blind", 2, 1, 64, 0, 0, 16, 64), ("blind", 4, 4, 32, 20, 2, 8, 16),
+]
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,d,window,sinks,buckets,reach", SHAPES)
+@pytest.mark.parametrize("itype", [np.int64, np.int32])
+def test_forward_backward(lens, Hq, Hkv, d, window, sinks, buckets, reach, itype):
+    if itype is np.int32 and lens not in ("few", "later"):
+        pytest.skip("int32 offsets on two sets of lengths")
+    rng = rng_of("seq", lens, Hq, Hkv, d, window, sinks, buckets)
+    q_lens, k_lens = LENS[lens]
+    qo, ko = offsets(q_lens, itype), offsets(k_lens, itype)
+    q_d, q = bf16(rng, qo[-1], Hq, d)
+    k_d, k = bf16(rng, ko[-1], Hkv, d)
+    v_d, v = bf16(rng, ko[-1], Hkv, d)
+    g_d, g = bf16(rng, qo[-1], Hq, d)
+    scale = float(np.float32(1.0 / np.sqrt(d)))
+    bias = bounds = None
+    how = dict(window=window, sinks=sinks, scale=scale)
+    if buckets:
+        bias, bounds = rng.standard_normal((Hq, buckets)).astype(np.float32), dlrm_seq_bucket_bounds(buckets, reach)
+        how.update(bias=to_dev(bias), bounds=bounds)
+        bias = bias.astype(np.float64)
+    ref = seq.seq_attn(q, k, v, qo, ko[:-1], ko[1:], window, sinks, scale, bias, bounds, g)
+    e = e_of(d, ref)
+    qo_d, ko_d = to_dev(qo), to_dev(ko)
+    say(f"[seq] {lens} Hq={Hq} Hkv={Hkv} d={d} window={window} sinks={sinks} buckets={buckets} {itype.__name__}")
+    o1 = dlrm_seq_attn_fwd(q_d, k_d, v_d, qo_d, ko_d, **how)
+    torch.cuda.synchronize()
+    assert rel_err(host(o1), ref["o"], ref["o_s"]) <= 2.0 ** -7 + 2 * e + 2.0 ** -16
+    o, lo, lse = dlrm_seq_attn_fwd(q_d, k_d, v_d, qo_d, ko_d, for_backward=True, **how)
+    torch.cuda.synchronize()
+    err = rel_err(host(o) + host(lo), ref["o"], ref["o_s"])
+    say(f"   o + o_lo {err:.2e} (gate {2.0 ** -15 + 2 * e:.2e})")
+    assert err <= 2.0 ** -15 + 2 * e
+    check_lse(lse.cpu().numpy().astype(np.float64), ref, e)
+    got = dlrm_seq_attn_bwd(g_d, q_d, k_d, v_d, o, lo, lse, qo_d, ko_d, **how)
+    again = dlrm_seq_attn_bwd(g_d, q_d, k_d, v_d, o, lo, lse, qo_d, ko_d, **how)
+    torch.cuda.synchronize()
+    for name, x, y in zip(("dq", "dk", "dv", "dbias"), got, again):
+        if x is None:
+            assert name == "dbias" and not buckets
+            continue
+        assert torch.equal(x.view(torch.int16 if x.dtype == torch.bfloat16 else torch.int32),
+                           y.view(torch.int16 if x.dtype == torch.bfloat16 else torch.int32)), name
+        err, gate = rel_err(host(x), ref[name], ref[name + "_s"]), (2.0 ** -7 if name != "dbias" else 0) + 2.0 ** -14 + 4 * e
+        say(f"   {name} {err:.2e} (gate {gate:.2e})")
+        assert err <= gate, name
+
+
+def test_bias_gradient_against_differences():
+    """The loss <do, o> along a direction of the bias: fp32 in, o + o_lo out, so that a central
+    difference of step h is off by the third derivative (O(h^2)) and by the outputs' independent errors
+    of 2^-15 of their terms, six times their root sum of squares, over h."""
+    rng = rng_of("seq-diff")
+    lens = [50, 130, 7]
+    qo = offsets(lens)
+    q_d, q = bf16(rng, qo[-1], 2, 32)
+    k_d, k = bf16(rng, qo[-1], 1, 32)
+    v_d, v = bf16(rng, qo[-1], 1, 32)
+    g_d, g = bf16(rng, qo[-1], 2, 32)
+    bounds = dlrm_seq_bucket_bounds(16, 64)
+    bias, step = rng.standard_normal((2, 16)), rng.standard_normal((2, 16))
+    qo_d = to_dev(qo)
+
+    def loss(b):
+        o, lo, _ = dlrm_seq_attn_fwd(q_d, k_d, v_d, qo_d, bias=to_dev(b.astype(np.float32)), bounds=bounds, for_backward=True)
+        return float(((host(o) + host(lo)) * g).sum())
+
+    h = 1 / 64
+    slope = (loss(bias + h * step) - loss(bias - h * step)) / (2 * h)
+    o, lo, lse = dlrm_seq_attn_fwd(q_d, k_d, v_d, qo_d, bias=to_dev(bias.astype(np.float32)), bounds=bounds, for_backward=True)
+    dbias = dlrm_seq_attn_bwd(g_d, q_d, k_d, v_d, o, lo, lse, qo_d, bias=to_dev(bias.astype(np.float32)), bounds=bounds)[3]
+    want = float((host(dbias) * step).sum())
+    size = np.abs(host(dbias) * step).sum()
+    # third derivatives of a softmax along a step of |step| <= 3.5: below 6 * 3.5^2 times the terms
+    o_s = seq.seq_attn(q, k, v, qo, qo[:-1], qo[1:], scale=32 ** -0.5, bias=bias, bounds=bounds)["o_s"]
+    assert abs(slope - want) <= size * h * h * 3.5 ** 2 + 6 * np.sqrt(((g * o_s) ** 2).sum()) * 2.0 ** -15 / h
+
+
+def test_strided_views_of_a_joint_projection():
+    rng = rng_of("seq-strided")
+    lens, Hq, Hkv, d = [40, 90, 3], 4, 2, 32
+    qo = offsets(lens)
+    joint_d, joint = bf16(rng, qo[-1], Hq + 2 * Hkv, d)
+    qkv = joint_d[:, :Hq], joint_d[:, Hq:Hq + Hkv], joint_d[:, Hq + Hkv:]
+    packed = [t.contiguous() for t in qkv]
+    g_d, _ = bf16(rng, qo[-1], Hq, d)
+    a = dlrm_seq_attn_fwd(*qkv, to_dev(qo), for_backward=True, window=30, sinks=2)
+    b = dlrm_seq_attn_fwd(*packed, to_dev(qo), for_backward=True, window=30, sinks=2)
+    c = dlrm_seq_attn_bwd(g_d, *qkv, *a, to_dev(qo), window=30, sinks=2)[:3]
+    e = dlrm_seq_attn_bwd(g_d, *packed, *b, to_dev(qo), window=30, sinks=2)[:3]
+    heads_first = [t.transpose(0, 1).contiguous().transpose(0, 1) for t in packed]  # head stride above the row stride
+    f = dlrm_seq_attn_fwd(*heads_first, to_dev(qo), for_backward=True, window=30, sinks=2)
+    torch.cuda.synchronize()
+    for x, y in list(zip(a, b)) + list(zip(c, e)) + list(zip(f, b)):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("d", [32, 128])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (40, 0), (40, 3)])
+def test_what_hidden_keys_hold(d, window, sinks):
+    """NaN and infinities in a key change nothing for the queries that do not see it, and everything
+    for those that do; in the gradient too for keys that no query sees."""
+    rng = rng_of("seq-hidden", d, window, sinks)
+    n = 150
+    qo = to_dev(offsets([n]))
+    q_d, _ = bf16(rng, n, 2, d)
+    k_d, _ = bf16(rng, n, 1, d)
+    v_d, _ = bf16(rng, n, 1, d)
+    bias, bounds = to_dev(rng.standard_normal((2, 8)).astype(np.float32)), dlrm_seq_bucket_bounds(8, 32)
+    how = dict(window=window, sinks=sinks, bias=bias, bounds=bounds)
+    clean = dlrm_seq_attn_fwd(q_d, k_d, v_d, qo, for_backward=True, **how)
+    for j, what in ((70, float("nan")), (100, float("inf")), (20, float("-inf")), (149, float("nan"))):
+        for hurt_k in (False, True):
+            k2, v2 = k_d.clone(), v_d.clone()
+            (k2 if hurt_k else v2)[j, 0, 3] = what
+            o, lo, lse = dlrm_seq_attn_fwd(q_d, k2, v2, qo, for_backward=True, **how)
+            o1 = dlrm_seq_attn_fwd(q_d, k2, v2, qo, **how)
+            torch.cuda.synchronize()
+            i = np.arange(n)
+            sees = torch.from_numpy((i >= j) & ((window == 0) | (i - j < window) | (j < sinks)))
+            for x, y in ((o, clean[0]), (lo, clean[1])):
+                assert torch.equal(x.cpu()[~sees], y.cpu()[~sees]), (j, what, hurt_k)
+            assert torch.isfinite(o1.cpu()[~sees].float()).all()
+            if not hurt_k:
+                col = o.cpu()[sees][:, :, 3].float()
+                assert (torch.isnan(col) if what != what else col == what).all()
+                assert torch.equal(lse.cpu(), clean[2].cpu())
+            elif what != what:
+                assert torch.isnan(o.cpu()[sees].float()).all()
+    if window and not sinks:  # only the last 30 events ask: keys before the window are seen by none
+        m = 30
+        new = to_dev(offsets([m]))
+        ko = to_dev(offsets([n]))
+        k2, v2 = k_d.clone(), v_d.clone()
+        k2[:n - m - window + 1] = float("nan")
+        v2[:n - m - window + 1] = float("inf")
+        g_d, _ = bf16(rng, m, 2, d)
+        res = []
+        for kk, vv in ((k_d, v_d), (k2, v2)):
+            o, lo, lse = dlrm_seq_attn_fwd(q_d[n - m:], kk, vv, new, ko, for_backward=True, **how)
+            res.append((o, lo, lse) + dlrm_seq_attn_bwd(g_d, q_d[n - m:], kk, vv, o, lo, lse, new, ko, **how))
+        torch.cuda.synchronize()
+        for x, y in zip(*res):
+            assert torch.equal(x, y)
+        assert (res[0][4][:n - m - window + 1] == 0).all()
+
+
+@pytest.mark.parametrize("low", [-1e9, float(torch.finfo(torch.float32).min), -float("inf")])
+def test_bias_that_masks(low):
+    """A bucket at a mask's usual values: no weight beside other keys; a query whose every key has it
+    attends to them evenly (-infinity: to none)."""
+    rng = rng_of("seq-mask")
+    n, d = 100, 64
+    qo = to_dev(offsets([n]))
+    q_d, q = bf16(rng, n, 1, d)
+    k_d, k = bf16(rng, n, 1, d)
+    v_d, v = bf16(rng, n, 1, d)
+    g_d, g = bf16(rng, n, 1, d)
+    bounds = [0, 1, 20]  # a key's own event is masked: the first query sees nothing else
+    bias = np.array([[low, 0.5, -0.25]], np.float32)
+    o, lo, lse = dlrm_seq_attn_fwd(q_d, k_d, v_d, qo, bias=to_dev(bias), bounds=bounds, for_backward=True)
+    got = dlrm_seq_attn_bwd(g_d, q_d, k_d, v_d, o, lo, lse, qo, bias=to_dev(bias), bounds=bounds)
+    torch.cuda.synchronize()
+    whole = host(o) + host(lo)
+    ref = seq.seq_attn(q, k, v, [0, n], [0], [n], 0, 0, float(np.float32(d ** -0.5)), bias.astype(np.float64), bounds, g)
+    e = (d + 8) * 2.0 ** -24 * 60  # the unmasked logits' terms
+    if low == -float("inf"):
+        assert (whole[0] == 0).all() and lse[0, 0].item() == low
+    else:
+        assert np.abs(whole[0] - v[0]).max() <= 2.0 ** -15 * np.abs(v[0]).max() and lse[0, 0].item() == np.float32(low)
+    assert rel_err(whole[1:], ref["o"][1:], ref["o_s"][1:]) <= 2.0 ** -15 + 2 * e
+    for name, x in zip(("dq", "dk", "dv"), got):
+        assert rel_err(host(x), ref[name], ref[name + "_s"]) <= 2.0 ** -7 + 2.0 ** -14 + 4 * e, name
+
+
+def test_cache_regions_with_gaps():
+    """begin and end apart from each other: each user's keys fill the front of a region of its own, the
+    rest of which holds NaN."""
+    rng = rng_of("seq-gaps")
+    lens, cap, d = [100, 0, 37, 64], 128, 64
+    begin = np.arange(4) * cap
+    end = begin + lens
+    new = [5, 2, 37, 1]
+    qo = offsets(new)
+    q_d, q = bf16(rng, qo[-1], 4, d)
+    k_d, k = bf16(rng, 4 * cap, 2, d)
+    v_d, v = bf16(rng, 4 * cap, 2, d)
+    for b in range(4):
+        k_d[end[b]:begin[b] + cap] = float("nan")
+        v_d[end[b]:begin[b] + cap] = float("nan")
+    scale = float(np.float32(d ** -0.5))
+    ref = seq.seq_attn(q, k, v, qo, begin, end, 20, 2, scale)
+    o = dlrm_seq_attn_fwd(q_d, k_d, v_d, to_dev(qo), (to_dev(begin), to_dev(end)), window=20, sinks=2)
+    last = torch.from_numpy(qo[1:] - 1).to(DEV)
+    o1 = dlrm_seq_attn_decode(q_d[last], k_d, v_d, to_dev(begin), to_dev(end), window=20, sinks=2)
+    torch.cuda.synchronize()
+    gate = 2.0 ** -7 + 2 * e_of(d, ref) + 2.0 ** -16
+    assert rel_err(host(o), ref["o"], ref["o_s"]) <= gate
+    assert rel_err(host(o1), ref["o"][qo[1:] - 1], ref["o_s"][qo[1:] - 1]) <= gate
+
+
+DECODE = [
+    # lens, Hq, Hkv, d, window, sinks, buckets, reach
+    ([1], 1, 1, 8, 0, 0, 0, 0), ([0, 1, 2, 31, 32, 33], 4, 4, 32, 0, 0, 32, 128), ([5, 0, 700], 8, 2, 64, 0, 0, 32, 128),
+    ([3000], 4, 1, 128, 0, 0, 32, 512), ([127, 128, 129, 4000], 16, 1, 64, 0, 0, 8, 2000), ([900, 40], 20, 1, 40, 0, 0, 33, 300),
+    ([2500, 90, 10], 8, 2, 128, 100, 4, 32, 64), ([2500, 300], 2, 2, 96, 513, 70, 16, 1000), ([600], 2, 1, 64, 1, 0, 4, 9),
+    ([5000, 1], 33, 1, 16, 0, 0, 0, 0),
+]
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,d,window,sinks,buckets,reach", DECODE)
+def test_decode(lens, Hq, Hkv, d, window, sinks, buckets, reach):
+    rng = rng_of("dec", lens, Hq, Hkv, d, window)
+    B, ko = len(lens), offsets(lens)
+    q_d, q = bf16(rng, B, Hq, d)
+    k_d, k = bf16(rng, ko[-1], Hkv, d)
+    v_d, v = bf16(rng, ko[-1], Hkv, d)
+    scale = float(np.float32(0.7 / np.sqrt(d)))
+    bias = bounds = None
+    how = dict(window=window, sinks=sinks, scale=scale)
+    if buckets:
+        bias, bounds = rng.standard_normal((Hq, buckets)).astype(np.float32), dlrm_seq_bucket_bounds(buckets, reach)
+        how.update(bias=to_dev(bias), bounds=bounds)
+        bias = bias.astype(np.float64)
+    ref = seq.seq_attn(q, k, v, np.arange(B + 1), ko[:-1], ko[1:], window, sinks, scale, bias, bounds)
+    gate = 2.0 ** -7 + 2 * e_of(d, ref) + 2.0 ** -16
+    for itype in (np.int64, np.int32):
+        off = to_dev(ko.astype(itype))
+        for longest in (None, 1, max(lens)):  # the split changes; the answer does not, but for rounding
+            say(f"[seq] decode {lens} Hq={Hq} Hkv={Hkv} d={d} window={window} longest={longest} {itype.__name__}")
+            o = dlrm_seq_attn_decode(q_d, k_d, v_d, off[:-1], off[1:], max_kv_len=longest, **how)
+            torch.cuda.synchronize()
+            assert rel_err(host(o), ref["o"], ref["o_s"]) <= gate
+    # the forward's one-query case is the same operator
+    o = dlrm_seq_attn_fwd(q_d, k_d, v_d, to_dev(np.arange(B + 1)), to_dev(ko), **how)
+    torch.cuda.synchronize()
+    assert rel_err(host(o), ref["o"], ref["o_s"]) <= gate
+
+
+def test_another_stream():
+    rng = rng_of("seq-stream")
+    lens = [300, 200]
+    qo = to_dev(offsets(lens))
+    q_d, _ = bf16(rng, 500, 2, 64)
+    k_d, _ = bf16(rng, 500, 2, 64)
+    v_d, _ = bf16(rng, 500, 2, 64)
+    g_d, _ = bf16(rng, 500, 2, 64)
+    bias, bounds = to_dev(rng.standard_normal((2, 8)).astype(np.float32)), dlrm_seq_bucket_bounds(8, 32)
+
+    def both():
+        o, lo, lse = dlrm_seq_attn_fwd(q_d, k_d, v_d, qo, bias=bias, bounds=bounds, for_backward=True)
+        return (o, lo, lse) + dlrm_seq_attn_bwd(g_d, q_d, k_d, v_d, o, lo, lse, qo, bias=bias, bounds=bounds)
+
+    here = both()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        there = both()
+    side.synchronize()
+    for x, y in zip(here, there):
+        assert torch.equal(x, y)
+
+
+def test_nothing_to_do():
+    q = torch.empty((0, 2, 32), dtype=torch.bfloat16, device=DEV)
+    zero = torch.zeros(1, dtype=torch.int64, device=DEV)
+    bias = torch.ones((2, 4), device=DEV)
+    o, lo, lse = dlrm_seq_attn_fwd(q, q, q, zero, bias=bias, bounds=[0, 1, 2, 3], for_backward=True)
+    dq, dk, dv, db = dlrm_seq_attn_bwd(q, q, q, q, o, lo, lse, zero, bias=bias, bounds=[0, 1, 2, 3])
+    assert o.shape == q.shape and (db == 0).all()
+    three = torch.zeros(4, dtype=torch.int64, device=DEV)  # three empty sequences
+    o, lo, lse = dlrm_seq_attn_fwd(q, q, q, three, bias=bias, bounds=[0, 1, 2, 3], for_backward=True)
+    assert (dlrm_seq_attn_bwd(q, q, q, q, o, lo, lse, three, bias=bias, bounds=[0, 1, 2, 3])[3] == 0).all()
+    q1 = torch.ones((3, 2, 32), dtype=torch.bfloat16, device=DEV)
+    assert (dlrm_seq_attn_decode(q1, q, q, three[:3], three[1:]) == 0).all()
+    assert dlrm_seq_attn_decode(q, q, q, zero[:0], zero[:0]).shape == (0, 2, 32)
+
+
+def test_refusals():
+    rng = rng_of("seq-refuse")
+    q, _ = bf16(rng, 10, 4, 32)
+    k, _ = bf16(rng, 10, 2, 32)
+    off = to_dev(offsets([4, 6]))
+    bias = torch.zeros((4, 3), device=DEV)
+    ok = dict(q=q, k=k, v=k, q_offsets=off)
+    dlrm_seq_attn_fwd(**ok)
+    wide, _ = bf16(rng, 10, 1, 136)
+    odd, _ = bf16(rng, 10, 2, 12)
+    for bad in (dict(q=q.float()), dict(q=q.cpu()), dict(k=k[:9]), dict(k=k[:, :, :16]), dict(v=k[:, :1]),
+                dict(q=q[:, :3]), dict(q_offsets=off.float()), dict(q_offsets=off.cpu()), dict(kv_offsets=off[:2]),
+                dict(kv_offsets=off.int()), dict(window=-1), dict(sinks=-2), dict(bias=bias), dict(bounds=[0, 1, 2]),
+                dict(bias=bias, bounds=[0, 2, 2]), dict(bias=bias, bounds=[1, 2, 3]), dict(bias=bias, bounds=[0, 1]),
+                dict(bias=bias[:2], bounds=[0, 1, 2]), dict(out=q[:5]), dict(out=q.float()), dict(q=wide, k=wide, v=wide),
+                dict(q=odd, k=odd, v=odd), dict(q=q.transpose(1, 2).contiguous().transpose(1, 2)), dict(lse=bias)):
+        with pytest.raises(ValueError):
+            dlrm_seq_attn_fwd(**{**ok, **bad})
+    flat = torch.zeros(10 * 4 * 32 + 8, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(DlrmError):  # 8-byte aligned rows
+        dlrm_seq_attn_fwd(**{**ok, "q": flat[4:4 + 1280].view(10, 4, 32)})
+    o, lo, lse = dlrm_seq_attn_fwd(**ok, for_backward=True)
+    good = dict(dout=q, **ok, o=o, o_lo=lo, lse=lse)
+    dlrm_seq_attn_bwd(**good)
+    for bad in (dict(dout=q[:5]), dict(o=o.float()), dict(lse=lse[:, :2]), dict(dbias=bias), dict(dk=q), dict(dq=k),
+                dict(kv_offsets=(off[:-1], off[1:])), dict(workspace=torch.zeros(4, device=DEV))):
+        with pytest.raises(ValueError):
+            dlrm_seq_attn_bwd(**{**good, **bad})
+    one = dict(q=q[:2], k=k, v=k, kv_begin=off[:-1], kv_end=off[1:])
+    dlrm_seq_attn_decode(**one)
+    for bad in (dict(q=q[:3]), dict(kv_begin=off), dict(kv_end=off[1:].int()), dict(max_kv_len=-1), dict(out=q)):
+        with pytest.raises(ValueError):
+            dlrm_seq_attn_decode(**{**one, **bad})
