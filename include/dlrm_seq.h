@@ -54,12 +54,12 @@ enum { DLRM_F8_E4M3 = 2 };
  *              in elements, multiples of 8, >= d; 16-byte aligned
  *   q_offsets  [B+1];  kv_begin, kv_end [B] (a CSR array of B+1 offsets gives both: it, and it + 1);
  *              int64 (DLRM_INDEX_I64) or int32; non-decreasing, within [0, Nq] and [0, Nkv].
- *              Offsets outside are taken as the nearest inside: no foreign memory is read.
+ *              Offsets outside are brought inside: no foreign memory is read.
  *   window     0: none; sinks: how many first keys every later query sees (only with a window)
  *   bias       [Hq][buckets] fp32, or NULL: no bias;  bounds (host) [buckets], bounds[0] == 0,
  *              strictly increasing: the first distance of each bucket, the last bucket open
- *   Limits: d % 8 == 0, 8 <= d <= 128; 1 <= Hq <= 4096; B < 2^24; a sequence < 2^30 rows;
- *   1 <= buckets <= DLRM_SEQ_MAX_BUCKETS.
+ *   Limits: d % 8 == 0, 8 <= d <= 128; 1 <= Hq <= 4096; B < 2^24; Nq, Nkv < 2^31; row strides
+ *   < 2^24 elements; a sequence < 2^30 rows; 1 <= buckets <= DLRM_SEQ_MAX_BUCKETS.
  */
 typedef struct {
     int64_t B, Nq, Nkv;
@@ -75,18 +75,20 @@ typedef struct {
     const int32_t *bounds; /* (host) */
 } dlrm_seq_attn;
 
+/* Entries of the forward's `tiles` (0 on invalid sizes). */
+size_t dlrm_seq_attn_tiles(int64_t B, int64_t Nq);
+
 /*
  * Forward.  o [Nq][Hq][d] bf16; rows outside every sequence are not written.
- *   o_lo, lse: NULL, or both given for a backward pass: lse [Nq][Hq] fp32, and o_lo [Nq][Hq][d]
- *   fp32, what o's rounding left over.  The bias's gradient sums P (dP - <do, o>) over up to every
- *   pair, where much cancels: it needs <do, o> in fp32, so with these outputs P goes into the
- *   product with V in full as well (three bf16 pieces), not rounded to bf16.
+ *   lse, tiles: NULL, or both given for a backward pass: lse [Nq][Hq] fp32, and tiles, int32
+ *   [dlrm_seq_attn_tiles(B, Nq)]: the sequence that each tile of queries belongs to, which the
+ *   backward would have to search for again.
  */
-int dlrm_seq_attn_fwd(const dlrm_seq_attn *a, uint16_t *o, float *o_lo, float *lse,
+int dlrm_seq_attn_fwd(const dlrm_seq_attn *a, uint16_t *o, float *lse, int32_t *tiles,
                       dlrm_stream_t stream);
 
-/* Bytes of workspace dlrm_seq_attn_bwd needs (0 on invalid sizes). */
-size_t dlrm_seq_attn_bwd_workspace_size(int64_t B, int64_t Nq, int32_t Hq, int32_t buckets);
+/* Bytes of workspace dlrm_seq_attn_bwd needs for this description (0 on an invalid one). */
+size_t dlrm_seq_attn_bwd_workspace_size(const dlrm_seq_attn *a);
 
 /*
  * Backward.  With P = exp(z - lse) on the visible pairs, dP[i][j] = <do_i, v_j> and
@@ -95,13 +97,16 @@ size_t dlrm_seq_attn_bwd_workspace_size(int64_t B, int64_t Nq, int32_t Hq, int32
  *     dv_j = sum_i P do_i;  dk_j = scale sum_i ds q_i;  dq_i = scale sum_j ds k_j;
  *     dbias[h][t] = sum over the pairs of bucket t of ds
  *
- *   kv_begin must be a CSR array of B+1 offsets (kv_end is not read)
- *   dout [Nq][Hq][d] bf16; o, o_lo, lse as the forward wrote them
+ *   a: the forward's, with kv_begin a CSR array of B+1 offsets (kv_end == kv_begin + 1)
+ *   dout [Nq][Hq][d] bf16; o, lse, tiles as the forward wrote them (o is read without a bias only:
+ *   with one, <do, o> is summed again in fp32, as dbias needs it)
  *   dq [Nq][Hq][d], dk, dv [Nkv][Hkv][d] bf16 (rows of every sequence are written in full);
  *   dbias [Hq][buckets] fp32 (with a bias; else NULL)
+ *   Infinities and NaN in a key that a query does not see have no effect on its dq, and a key that
+ *   no query sees has gradients of zero; those of q and dout reach every key near by.
  */
 int dlrm_seq_attn_bwd(const dlrm_seq_attn *a, const uint16_t *dout, const uint16_t *o,
-                      const float *o_lo, const float *lse, uint16_t *dq, uint16_t *dk,
+                      const float *lse, const int32_t *tiles, uint16_t *dq, uint16_t *dk,
                       uint16_t *dv, float *dbias, void *workspace, size_t workspace_bytes,
                       dlrm_stream_t stream);
 

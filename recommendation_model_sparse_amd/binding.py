@@ -90,7 +90,8 @@ def lib() -> ctypes.CDLL:
         for f in (L.dlrm_linear_fwd, L.dlrm_linear_bwd, L.dlrm_bce_head, L.dlrm_sgd_dense, L.dlrm_cast_rows):
             f.restype = ctypes.c_int
         L.dlrm_seq_attn_fwd.argtypes = [p, p, p, p, p]
-        L.dlrm_seq_attn_bwd_workspace_size.argtypes = [i64, i64, i32, i32]
+        L.dlrm_seq_attn_bwd_workspace_size.argtypes = [p]
+        L.dlrm_seq_attn_tiles.argtypes = [i64, i64]
         L.dlrm_seq_attn_bwd.argtypes = [p, p, p, p, p, p, p, p, p, p, sz, p]
         L.dlrm_seq_attn_decode_workspace_size.argtypes = [i64, i32, i32, i32, i32, i32, i64]
         L.dlrm_seq_attn_decode.argtypes = [p, i64, p, p, sz, p]
@@ -101,7 +102,7 @@ def lib() -> ctypes.CDLL:
         for f in (L.dlrm_seq_attn_fwd, L.dlrm_seq_attn_bwd, L.dlrm_seq_attn_decode, L.dlrm_dropout, L.dlrm_add_rmsnorm_fwd,
                   L.dlrm_add_rmsnorm_bwd):
             f.restype = ctypes.c_int
-        for f in (L.dlrm_seq_attn_bwd_workspace_size, L.dlrm_seq_attn_decode_workspace_size,
+        for f in (L.dlrm_seq_attn_bwd_workspace_size, L.dlrm_seq_attn_tiles, L.dlrm_seq_attn_decode_workspace_size,
                   L.dlrm_add_rmsnorm_bwd_workspace_size):
             f.restype = sz
         L.dlrm_status_string.argtypes = [ctypes.c_int]
@@ -867,44 +868,41 @@ def dlrm_seq_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offse
                       window: int = 0, sinks: int = 0, scale: Optional[float] = None,
                       bias: Optional[torch.Tensor] = None, bounds: Optional[Sequence[int]] = None,
                       for_backward: bool = False, out: Optional[torch.Tensor] = None,
-                      out_lo: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None):
+                      tiles: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None):
     """Causal attention over jagged sequences (C: dlrm_seq_attn_fwd): o [Nq, Hq, d] bf16, or with
-    for_backward (o, o_lo, lse).  q is [Nq, Hq, d], k and v [Nkv, Hkv, d]; the queries are the last
-    events of their sequence.  kv_offsets: offsets [B+1], a (begin, end) pair of [B], or None: the
-    queries' own.  scale: None is 1 / sqrt(d).  bias [Hq, buckets] with bounds, the first distance
-    of each bucket (dlrm_seq_bucket_bounds)."""
+    for_backward (o, tiles, lse), what dlrm_seq_attn_bwd takes.  q is [Nq, Hq, d], k and v
+    [Nkv, Hkv, d]; the queries are the last events of their sequence.  kv_offsets: offsets [B+1], a
+    (begin, end) pair of [B], or None: the queries' own.  scale: None is 1 / sqrt(d).
+    bias [Hq, buckets] with bounds, the first distance of each bucket (dlrm_seq_bucket_bounds)."""
     _offsets(q_offsets, "q_offsets")
     B = q_offsets.numel() - 1
     begin, end = _kv_ranges(q_offsets if kv_offsets is None else kv_offsets, B)
     a, edges, dev = _seq_attn(q, k, v, q_offsets, begin, end, B, window, sinks, scale, bias, bounds)
     shape = tuple(q.shape)
+    for_backward = for_backward or tiles is not None or lse is not None
     out = _opt(out, "out", torch.bfloat16, shape)
-    if out_lo is not None or lse is not None:
-        for_backward = True
-    out_lo = _opt(out_lo, "out_lo", torch.float32, shape)
-    lse = _opt(lse, "lse", torch.float32, shape[:2])
-    _device(q, out, out_lo, lse)
+    if for_backward:
+        n = int(lib().dlrm_seq_attn_tiles(B, shape[0]))
+        tiles, lse = _opt(tiles, "tiles", torch.int32, (n,)), _opt(lse, "lse", torch.float32, shape[:2])
+        _device(q, out, tiles, lse)
+        tiles = torch.empty(n, dtype=torch.int32, device=dev) if tiles is None else tiles
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=dev) if lse is None else lse
+    elif out is not None:
+        _device(q, out)
     if out is None:
         out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    if for_backward:
-        out_lo = torch.empty(shape, dtype=torch.float32, device=dev) if out_lo is None else out_lo
-        lse = torch.empty(shape[:2], dtype=torch.float32, device=dev) if lse is None else lse
-    _check(lib().dlrm_seq_attn_fwd(ctypes.byref(a), _ptr(out), _ptr(out_lo), _ptr(lse), _stream(dev)), "dlrm_seq_attn_fwd")
-    return (out, out_lo, lse) if for_backward else out
-
-
-def dlrm_seq_attn_bwd_workspace_size(B: int, Nq: int, Hq: int, buckets: int) -> int:
-    return int(lib().dlrm_seq_attn_bwd_workspace_size(B, Nq, Hq, buckets))
+    _check(lib().dlrm_seq_attn_fwd(ctypes.byref(a), _ptr(out), _ptr(lse), _ptr(tiles), _stream(dev)), "dlrm_seq_attn_fwd")
+    return (out, tiles, lse) if for_backward else out
 
 
 def dlrm_seq_attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
-                      o_lo: torch.Tensor, lse: torch.Tensor, q_offsets: torch.Tensor,
+                      tiles: torch.Tensor, lse: torch.Tensor, q_offsets: torch.Tensor,
                       kv_offsets: Optional[torch.Tensor] = None, *, window: int = 0, sinks: int = 0,
                       scale: Optional[float] = None, bias: Optional[torch.Tensor] = None,
                       bounds: Optional[Sequence[int]] = None, dq: Optional[torch.Tensor] = None,
                       dk: Optional[torch.Tensor] = None, dv: Optional[torch.Tensor] = None,
                       dbias: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
-    """(dq, dk, dv, dbias or None) of dlrm_seq_attn_fwd (C: dlrm_seq_attn_bwd); o, o_lo and lse are what
+    """(dq, dk, dv, dbias or None) of dlrm_seq_attn_fwd (C: dlrm_seq_attn_bwd); o, tiles and lse are what
     it gave with for_backward, the other arguments its own; kv_offsets is None or offsets [B+1]."""
     _offsets(q_offsets, "q_offsets")
     B = q_offsets.numel() - 1
@@ -915,21 +913,21 @@ def dlrm_seq_attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: t
     qs, ks = tuple(q.shape), tuple(k.shape)
     _need(dout, "dout", torch.bfloat16, qs)
     _need(o, "o", torch.bfloat16, qs)
-    _need(o_lo, "o_lo", torch.float32, qs)
+    _need(tiles, "tiles", torch.int32, (int(lib().dlrm_seq_attn_tiles(B, qs[0])),))
     _need(lse, "lse", torch.float32, qs[:2])
     dq, dk, dv = (_opt(t, name, torch.bfloat16, s) for t, name, s in ((dq, "dq", qs), (dk, "dk", ks), (dv, "dv", ks)))
     if bias is None and dbias is not None:
         raise ValueError("dbias without a bias")
     dbias = _opt(dbias, "dbias", torch.float32, None if bias is None else tuple(bias.shape))
-    _device(q, dout, o, o_lo, lse, dq, dk, dv, dbias)
+    _device(q, dout, o, tiles, lse, dq, dk, dv, dbias)
     bf = dict(dtype=torch.bfloat16, device=dev)
     dq = torch.empty(qs, **bf) if dq is None else dq
     dk = torch.empty(ks, **bf) if dk is None else dk
     dv = torch.empty(ks, **bf) if dv is None else dv
     if bias is not None and dbias is None:
         dbias = torch.empty_like(bias)
-    ws = _ws(dlrm_seq_attn_bwd_workspace_size(B, qs[0], qs[1], a.buckets), dev, workspace)
-    _check(lib().dlrm_seq_attn_bwd(ctypes.byref(a), _ptr(dout), _ptr(o), _ptr(o_lo), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),
+    ws = _ws(int(lib().dlrm_seq_attn_bwd_workspace_size(ctypes.byref(a))), dev, workspace)
+    _check(lib().dlrm_seq_attn_bwd(ctypes.byref(a), _ptr(dout), _ptr(o), _ptr(lse), _ptr(tiles), _ptr(dq), _ptr(dk), _ptr(dv),
                                    _ptr(dbias), _ptr(ws), ws.numel(), _stream(dev)), "dlrm_seq_attn_bwd")
     return dq, dk, dv, dbias
 

@@ -9,6 +9,7 @@ namespace dlrm {
 namespace seq {
 
 constexpr int kBK = 64;  // rows of a staged tile (keys; queries in the backward over keys)
+constexpr int kQT = 64;  // queries of a workgroup
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kInf = __builtin_inff();
@@ -56,9 +57,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
 
-__device__ __forceinline__ int64_t offset_at(const Args &a, const void *p, int64_t i, int64_t limit) {
-    const int64_t x = a.idx32 ? static_cast<const int32_t *>(p)[i] : static_cast<const int64_t *>(p)[i];
-    return x < 0 ? 0 : (x > limit ? limit : x);
+// Entry i of an offset array, brought into [0, limit] (limit < 2^31; what is negative is limit).
+__device__ __forceinline__ int offset_at(const Args &a, const void *p, int64_t i, int64_t limit) {
+    if (a.idx32) {
+        const uint32_t x = static_cast<const uint32_t *>(p)[i];
+        return static_cast<int>(min(x, static_cast<uint32_t>(limit)));
+    }
+    const uint64_t x = static_cast<const uint64_t *>(p)[i];
+    return static_cast<int>(x < static_cast<uint64_t>(limit) ? static_cast<uint32_t>(x) : static_cast<uint32_t>(limit));
 }
 
 // Tiles of T rows over B jagged sequences without a table of them: sequence b owns the slots from
@@ -66,17 +72,16 @@ __device__ __forceinline__ int64_t offset_at(const Args &a, const void *p, int64
 // sequences meet; rows / T + B slots cover all, and those a sequence does not need end at once.
 __host__ __device__ __forceinline__ int64_t slot_count(int64_t rows, int64_t B, int T) { return rows / T + B; }
 
-// The sequence that owns a slot: a 64-ary search by one wavefront (two rounds up to 4096
-// sequences), as every probe waits for memory.
-__device__ __forceinline__ int find_sequence(const Args &a, const void *off, int64_t limit, int64_t slot, int T) {
+// The sequence that owns a slot, by one wavefront, as every probe waits for memory: 64 probes at
+// once, twice for up to 4096 sequences.
+__device__ __forceinline__ int find_sequence(const Args &a, const void *off, int64_t limit, int slot, int T) {
     int lo = 0, n = a.B;
     while (n > 1) {
         const int step = (n + 63) / 64;
         const int at = static_cast<int>(__lane_id()) * step;
         bool below = false;
-        if (at < n) below = offset_at(a, off, lo + at, limit) / T + lo + at <= slot;
-        const int c = __popcll(__ballot(below));
-        if (c == 0) return lo;  // offsets that are not in order: any sequence does
+        if (at < n) below = offset_at(a, off, lo + at, limit) / static_cast<uint32_t>(T) + lo + at <= static_cast<uint32_t>(slot);
+        const int c = max(1, __popcll(__ballot(below)));  // none: offsets that are not in order
         lo += (c - 1) * step;
         n = min(step, n - (c - 1) * step);
     }
@@ -90,34 +95,33 @@ struct Span {  // one sequence
 };
 
 __device__ __forceinline__ Span span_of(const Args &a, int b) {
+    const int q0 = offset_at(a, a.q_off, b, a.Nq), q1 = offset_at(a, a.q_off, b + 1, a.Nq);
+    const int k0 = offset_at(a, a.kv_begin, b, a.Nkv), k1 = offset_at(a, a.kv_end, b, a.Nkv);
     Span s;
-    s.q0 = offset_at(a, a.q_off, b, a.Nq);
-    const int64_t q1 = offset_at(a, a.q_off, b + 1, a.Nq);
-    s.k0 = offset_at(a, a.kv_begin, b, a.Nkv);
-    const int64_t k1 = offset_at(a, a.kv_end, b, a.Nkv);
-    s.qlen = q1 > s.q0 ? static_cast<int>(q1 - s.q0) : 0;
-    s.klen = k1 > s.k0 ? static_cast<int>(k1 - s.k0) : 0;
+    s.q0 = q0, s.k0 = k0;
+    s.qlen = max(q1 - q0, 0), s.klen = max(k1 - k0, 0);
     s.shift = s.klen - s.qlen;
     return s;
 }
 
 // ---------------------------------------------------------------- LDS tiles
 //
-// A tile holds 64 rows of LP elements (LP = 32, 64 or 128: the head's width rounded up) in 16-byte
-// chunks.  Chunk c of row r is kept at c ^ mix(r): the rows that one read instruction touches at
-// the same c then lie in different banks.
+// A tile holds 64 rows of LP elements (LP = 32, 64 or 128: the head's width rounded up), 16 elements
+// apart: the rows that one read instruction touches (8 of 16 bytes, or 4 of 32 in the transposing
+// read) lie in different banks, and every address is a lane's base plus a constant.
 
 template <int LP>
-__device__ __forceinline__ int chunk_at(int r, int c) {
-    constexpr int CH = LP / 8;
-    const int mix = CH >= 16 ? r : r / (16 / CH);
-    return r * CH + (c ^ (mix & (CH - 1)));
+constexpr int kPitch = LP + 16;
+
+// A lane's place in a tile for read_row: row `row`, columns from 8 * half on.
+template <int LP>
+__device__ __forceinline__ int row_base(int row, int half) {
+    return row * kPitch<LP> + 8 * half;
 }
 
-// One lane's 8 bf16 of row r from column 8 * c on.
-template <int LP>
-__device__ __forceinline__ void read_row(Frag &f, const uint16_t *tile, int r, int c) {
-    f.q = *reinterpret_cast<const u32x4 *>(tile + chunk_at<LP>(r, c) * 8);
+// One lane's 8 bf16 at step i (16 columns a step).
+__device__ __forceinline__ void read_row(Frag &f, const uint16_t *at, int i) {
+    f.q = *reinterpret_cast<const u32x4 *>(at + 16 * i);
 }
 
 // Transposed operand of v_mfma_f32_32x32x16_bf16 from a row-major tile: lane l gets column
@@ -126,16 +130,17 @@ __device__ __forceinline__ void read_row(Frag &f, const uint16_t *tile, int r, i
 // product's other operand as they stand.  Within 16 lanes ds_read_b64_tr_b16 takes 4 rows of 16
 // columns, lane i reading 4 columns of row i / 4, and gives lane i column i of the 4 rows.
 template <int LP>
-__device__ __forceinline__ void read_columns(Frag &f, const uint16_t *tile, int row0, int col0, int lane) {
+__device__ __forceinline__ int column_base(int lane) {
     const int i = lane & 15;
-    const int col = col0 + (lane & 16) + 4 * (i & 3);
-    const int row = row0 + 4 * (lane >> 5) + (i >> 2);
+    return (4 * (lane >> 5) + (i >> 2)) * kPitch<LP> + (lane & 16) + 4 * (i & 3);
+}
+
+template <int LP>
+__device__ __forceinline__ void read_columns(Frag &f, const uint16_t *at, int row0, int col0) {
     typedef __attribute__((address_space(3))) s16x4 *lds_t;
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-        const uint16_t *p = tile + chunk_at<LP>(row + 8 * g, col >> 3) * 8 + (col & 7);
-        f.h[g] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t)(p));
-    }
+    for (int g = 0; g < 2; ++g)
+        f.h[g] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t)(at + (row0 + 8 * g) * kPitch<LP> + col0));
 }
 
 // 64 rows of a [rows][d] bf16 matrix on their way to LDS, through registers: `load` issues the
@@ -144,26 +149,38 @@ __device__ __forceinline__ void read_columns(Frag &f, const uint16_t *tile, int 
 template <int LP, int THREADS>
 struct Stage {
     static constexpr int CH = LP / 8;
-    static constexpr int N = kBK * CH / THREADS;  // chunks a thread
+    static constexpr int N = kBK * CH / THREADS;  // 16-byte pieces a thread
+    static constexpr int R = THREADS / CH;        // rows that are read at once
     u32x4 r[N];
+    int row, lds;
+    uint32_t at;
+    bool col;
 
-    __device__ __forceinline__ void load(const uint16_t *base, int64_t row_stride, int d, int row0, int first, int end,
-                                         int sinks) {
+    __device__ __forceinline__ Stage(int64_t stride, int d) {
+        const int c = threadIdx.x % CH;
+        row = threadIdx.x / CH;
+        lds = row * kPitch<LP> + 8 * c;
+        at = static_cast<uint32_t>(row) * static_cast<uint32_t>(stride) * 2 + 16 * c;
+        col = 8 * c < d;
+    }
+    __device__ __forceinline__ void load(const uint16_t *base, int64_t stride, int d, int row0, int first, int end, int sinks) {
+        const char *p = reinterpret_cast<const char *>(base + row0 * stride);
+        const int64_t step = R * stride * 2;
+        if (d == LP && row0 >= first && row0 + kBK <= end) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int at = i * THREADS + static_cast<int>(threadIdx.x);
-            const int row = row0 + at / CH, c = at % CH;
+            for (int i = 0; i < N; ++i, p += step) r[i] = *(const DLRM_GLOBAL u32x4 *)(p + at);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i, p += step) {
+            const int x = row0 + i * R + row;
             r[i] = u32x4{0, 0, 0, 0};
-            if (row < end && (row >= first || row < sinks) && c * 8 < d)
-                r[i] = *(const DLRM_GLOBAL u32x4 *)(base + row * row_stride + c * 8);
+            if (col && x < end && (x >= first || x < sinks)) r[i] = *(const DLRM_GLOBAL u32x4 *)(p + at);
         }
     }
     __device__ __forceinline__ void store(uint16_t *tile) const {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int at = i * THREADS + static_cast<int>(threadIdx.x);
-            *reinterpret_cast<u32x4 *>(tile + chunk_at<LP>(at / CH, at % CH) * 8) = r[i];
-        }
+        for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4 *>(tile + lds + i * R * kPitch<LP>) = r[i];
     }
 };
 

@@ -1,15 +1,23 @@
 // Attention over jagged sequences, backward (dlrm_seq.h).
 //
-//   P = exp(z - lse);  dP = dO V^T;  ds = P (dP - <dO, o>)
+//   P = exp(z - lse);  dP = dO V^T;  ds = P (dP - delta), delta = sum_j P dP = <dO, o>
 //   dQ = scale ds K;  dK = scale ds^T Q;  dV = P^T dO;  dbias[t] = sum of ds over bucket t
 //
 // P is computed again from Q, K and the saved log-sums.  Two kernels, so that every sum has an owner
-// and no gradient is added to by atomics: one over blocks of queries (dQ, dbias and <dO, o>), one
-// over blocks of keys (dK, dV; it walks the query heads that share the key head one after the
-// other).  That computes S and dP twice: 7 products of Q x K x d instead of the 5 that one kernel
-// with atomic dQ would need.  Both work on the tiles of the forward: the accumulator of S and dP
-// becomes the next product's operand in registers, and the transposed operands (K^T; Q^T and dO^T)
-// are read from row-major tiles by transposing LDS loads.
+// and no gradient is added to by atomics: one over blocks of queries (delta, dQ, dbias), one over
+// blocks of keys (dK, dV; it walks the query heads that share the key head one after the other).
+// That computes S and dP twice: 7 products of Q x K x d instead of the 5 that one kernel with atomic
+// dQ would need.  Both work on the tiles of the forward: the accumulator of S and dP becomes the
+// next product's operand in registers, and the transposed operands (K^T; Q^T and dO^T) are read from
+// row-major tiles by transposing LDS loads.
+//
+// delta.  Without a bias it is <dO, o> from the forward's output.  That o is rounded to bf16, which
+// the gradients, rounded to bf16 too, bear; dbias does not: it sums ds over up to every pair, where
+// most cancels, and would be 1e-3 off.  With a bias the first kernel therefore goes over its keys
+// twice, first for delta = sum P dP in fp32.  The other way, an output kept in 24 bits by a forward
+// that multiplies P in three bf16 pieces, was measured: 6 more bytes an element to write and read
+// and as much arithmetic (1024 sequences of up to 512, two heads of 64: 0.62 against 0.46 ms for
+// forward and backward).
 #include <type_traits>
 
 #include "seq.h"
@@ -18,13 +26,21 @@ namespace dlrm {
 namespace seq {
 namespace {
 
-// Rows of one slot table of partial bias gradients: [head][slot][bucket].
+constexpr int kFarChunk = 256;  // queries of a workgroup of the far part, below
+constexpr int kFarMost = 128;   // most first keys that have a far part of their own
+
 struct Grads {
     const uint16_t *dout, *o;
-    const float *o_lo, *lse;
-    float *delta;    // [Nq][Hq]
-    float *partial;  // [Hq][slots][buckets]
+    const float *lse;
+    const int32_t *tiles;  // the sequence of each 64-query tile, from the forward
+    float *delta;          // [Nq][Hq]
+    float *partial;        // [Hq][slots][buckets]: dbias of each workgroup
     uint16_t *dq, *dk, *dv;
+    float *split;          // [splits][2][Nkv][Hkv][d]: dk and dv, where a key block's queries are split
+    int splits;
+    // first keys under a window: their gradients from the queries past it, [slot][Hkv][far_rows][2][d]
+    float *far;
+    int far_sinks, far_rows;
 };
 
 template <int CTRL, int ROWS>
@@ -48,69 +64,38 @@ __device__ __forceinline__ void add_by_bucket(float *sums, float x, int t, int l
     wave_lds_sync();
 }
 
-template <int DP, int LP, int NW>
-__global__ __launch_bounds__(NW * 64) void k_seq_attn_bwd_q(const Args a, const Grads gr, const int64_t slots) {
-    constexpr int QT = NW * 32, STEPS = DP / 16, MB = DP / 32, THREADS = NW * 64;
-    constexpr int TAB = QT + kBK, PITCH = 36;
-    __shared__ __attribute__((aligned(16))) uint16_t Ks[2][kBK * LP], Vs[2][kBK * LP];
+// WQ wavefronts of 32 queries, by WK that take one half each of a tile's 64 keys.
+template <int DP, int LP, int WQ, int WK, int OCC>
+__global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_bwd_q(const Args a, const Grads gr) {
+    constexpr int QT = WQ * 32, STEPS = DP / 16, MB = DP / 32, THREADS = WQ * WK * 64, NW = WQ * WK;
+    constexpr int TAB = QT + kBK, TILE = kBK * kPitch<LP>, PITCH = 36;
+    static_assert(QT == kQT, "the forward's tiles");
+    __shared__ __attribute__((aligned(16))) uint16_t tiles_s[2 * TILE];
     __shared__ __attribute__((aligned(16))) float skew[NW][32 * PITCH];
-    __shared__ float tab[2][TAB], bias_s[DLRM_SEQ_MAX_BUCKETS], sums[NW][DLRM_SEQ_MAX_BUCKETS];
+    __shared__ float tab[2][TAB], bias_s[DLRM_SEQ_MAX_BUCKETS], sums[NW][DLRM_SEQ_MAX_BUCKETS], half_s[WQ][32];
     __shared__ int bounds_s[DLRM_SEQ_MAX_BUCKETS];
     __shared__ uint8_t btab[2][TAB];
+    uint16_t *const Ks = tiles_s, *const Vs = tiles_s + TILE;
 
-    const int64_t id = xcd_contiguous(blockIdx.x, gridDim.x);
-    if (id >= slots * a.Hq) return;
-    const int h = static_cast<int>(id / slots);
-    const int64_t slot = id - h * slots;
-    const int b = find_sequence(a, a.q_off, a.Nq, slot, QT);
+    const int slots = static_cast<int>(slot_count(a.Nq, a.B, QT));
+    const int slot = static_cast<int>(xcd_contiguous(blockIdx.x, gridDim.x));
+    if (slot >= slots) return;
+    const int h = blockIdx.y;
+    const int64_t id = static_cast<int64_t>(h) * slots + slot;
+    const int b = min(max(gr.tiles[slot], 0), a.B - 1);
     const Span sp = span_of(a, b);
-    const int64_t t = slot - (sp.q0 / QT + b);
+    const int t = slot - (static_cast<int>(sp.q0) / QT + b);
     const int tiles = (sp.qlen + QT - 1) / QT;
     const int tid = threadIdx.x, lane = tid & 63, ln = lane & 31, half = lane >> 5;
     if (t < 0 || t >= tiles) {
         for (int i = tid; i < a.buckets; i += THREADS) gr.partial[id * a.buckets + i] = 0.f;
         return;
     }
-    const int q0 = (tiles - 1 - static_cast<int>(t)) * QT;
-    const int w = static_cast<int>(wave_id());
+    const int q0 = (tiles - 1 - t) * QT;
+    const int wave = static_cast<int>(wave_id()), w = wave % WQ, wk = wave / WQ;
     const int kvh = h / a.group;
     const uint16_t *kb = a.k + sp.k0 * a.k_row + kvh * a.k_head;
     const uint16_t *vb = a.v + sp.k0 * a.v_row + kvh * a.v_head;
-
-    for (int i = tid; i < a.buckets; i += THREADS) {
-        bounds_s[i] = a.bounds[i];
-        bias_s[i] = a.bias[static_cast<int64_t>(h) * a.buckets + i];
-    }
-    const int ql = q0 + w * 32 + ln;
-    const bool live = ql < sp.qlen;
-    const int64_t orow = ((sp.q0 + ql) * a.Hq + h) * static_cast<int64_t>(a.d);
-    Frag qf[STEPS], df[STEPS];
-    float delta = 0.f, lse = kInf;  // a query that sees nothing: P = exp(z - infinity) = 0
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-        qf[s].q = df[s].q = u32x4{0, 0, 0, 0};
-        const int c = 16 * s + 8 * half;
-        if (live && c < a.d) {
-            qf[s].q = *(const DLRM_GLOBAL u32x4 *)(a.q + (sp.q0 + ql) * a.q_row + h * a.q_head + c);
-            df[s].q = *(const DLRM_GLOBAL u32x4 *)(gr.dout + orow + c);
-            const u32x4 hi = *(const DLRM_GLOBAL u32x4 *)(gr.o + orow + c);
-            uint32_t lo[8];
-            gload_words<8>(gr.o_lo + orow + c, lo);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                delta = fmaf(bf16_lo(df[s].w[e]), bf16_lo(hi[e]) + __uint_as_float(lo[2 * e]), delta);
-                delta = fmaf(bf16_hi(df[s].w[e]), bf16_hi(hi[e]) + __uint_as_float(lo[2 * e + 1]), delta);
-            }
-        }
-    }
-    delta = add_halves(delta);
-    if (live) {
-        const float x = gr.lse[(sp.q0 + ql) * a.Hq + h];
-        if (x != -kInf) lse = x;
-        if (half == 0) gr.delta[(sp.q0 + ql) * a.Hq + h] = delta;
-    }
-    const bool huge = __any(fabsf(lse) > kHuge && fabsf(lse) < kInf);
-    const float lse2 = lse * kLog2e;
 
     const int pmin = q0 + sp.shift, pmax = min(q0 + QT, sp.qlen) - 1 + sp.shift;
     const int end = min(sp.klen, pmax + 1);
@@ -120,72 +105,99 @@ __global__ __launch_bounds__(NW * 64) void k_seq_attn_bwd_q(const Args a, const 
     const int nsink = min((a.sinks + kBK - 1) / kBK, t0);
     const int n = nsink + t1 - t0;
 
-    Stage<LP, THREADS> ks, vs;
+    Stage<LP, THREADS> ks(a.k_row, a.d), vs(a.v_row, a.d);
     const auto key0 = [&](int it) { return (it < nsink ? it : t0 + it - nsink) * kBK; };
     const auto load = [&](int it) {
         ks.load(kb, a.k_row, a.d, key0(it), first, end, a.sinks);
         vs.load(vb, a.v_row, a.d, key0(it), first, end, a.sinks);
     };
-    const auto whole = [&](int k0) {
-        return pmin - (k0 + kBK - 1) >= 0 && (!a.window || q0 + QT - 1 + sp.shift - k0 < a.window || k0 + kBK <= a.sinks);
+    const auto even = [&](int k0) {
+        const int nearest = pmin - (k0 + kBK - 1);
+        return nearest >= a.last && (!a.window || q0 + QT - 1 + sp.shift - k0 < a.window || k0 + kBK <= a.sinks);
     };
-    const auto even = [&](int k0) { return whole(k0) && pmin - (k0 + kBK - 1) >= a.last; };
-    const auto fill = [&](int it) {
-        const int k0 = key0(it), buf = it & 1;
-        ks.store(Ks[buf]);
-        vs.store(Vs[buf]);
-        if (!even(k0)) {
-            const int n0 = pmin - (k0 + kBK - 1);
-            for (int i = tid; i < TAB - 1; i += THREADS) {
-                int bucket;
-                tab[buf][i] = table_entry(a, bounds_s, bias_s, n0 + i, k0 < a.sinks, &bucket);
-                btab[buf][i] = static_cast<uint8_t>(bucket);
-            }
+    const auto table = [&](int it) {
+        const int k0 = key0(it), n0 = pmin - (k0 + kBK - 1);
+        if (even(k0)) return;
+        for (int i = tid; i < TAB - 1; i += THREADS) {
+            int bucket;
+            tab[it & 1][i] = table_entry(a, bounds_s, bias_s, n0 + i, k0 < a.sinks, &bucket);
+            btab[it & 1][i] = static_cast<uint8_t>(bucket);
         }
     };
 
-    f32x16 dq[MB];
-    float far = 0.f;           // ds summed over the pairs of the last bucket, where a tile has only those
-    float carry = 0.f;         // see below
-    int carry_key = -1;        // the tile that it goes on in
-    const auto drop_carry = [&] {  // distances pmin + 32 w - carry_key + ln
-        if (carry_key < 0) return;
-        const int dist = pmin + 32 * w - carry_key + ln;
-        const float x = add_halves(carry);
-        const int bt = half ? a.buckets - 1 : bucket_of(bounds_s, a.buckets, max(dist, 0));
-        add_by_bucket(sums[w], half ? 0.f : x, bt, lane);
-        carry = 0.f, carry_key = -1;
-    };
-
-    const auto pass = [&](auto is_wild) {  // WILD: a second pass, as in the forward
-    constexpr bool WILD = decltype(is_wild)::value;
-#pragma unroll
-    for (int m = 0; m < MB; ++m) dq[m] = f32x16{};
-    far = carry = 0.f, carry_key = -1;
-    for (int i = tid; i < NW * DLRM_SEQ_MAX_BUCKETS; i += THREADS) sums[0][i] = 0.f;
+    const int ql = q0 + w * 32 + ln;
+    const bool live = ql < sp.qlen;
+    const int64_t orow = ((sp.q0 + ql) * a.Hq + h) * static_cast<int64_t>(a.d);
     if (n > 0) load(0);
-    __syncthreads();
-    if (n > 0) fill(0);
-    for (int it = 0; it < n; ++it) {
-        const int k0 = key0(it), buf = it & 1;
-        if (it + 1 < n) load(it + 1);
-        __syncthreads();
-        const int wpos = pmin + w * 32;
-        const bool none = wpos + 31 < k0 || q0 + w * 32 >= sp.qlen ||
-                          (a.window && wpos - (k0 + kBK - 1) >= a.window && k0 >= a.sinks);
-        if (!none) {
-            const bool flat = even(k0);
-            const bool near = a.buckets && !flat;
-            float hi[2], lo[2];
+    Frag qf[STEPS], df[STEPS];
+    float delta = 0.f, lse = kInf;  // a query that sees nothing: P = exp(z - infinity) = 0
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
+    for (int s = 0; s < STEPS; ++s) {
+        qf[s].q = df[s].q = u32x4{0, 0, 0, 0};
+        const int c = 16 * s + 8 * half;
+        if (live && c < a.d) {
+            qf[s].q = *(const DLRM_GLOBAL u32x4 *)(a.q + (sp.q0 + ql) * a.q_row + h * a.q_head + c);
+            df[s].q = *(const DLRM_GLOBAL u32x4 *)(gr.dout + orow + c);
+            if (!a.buckets) {
+                const u32x4 x = *(const DLRM_GLOBAL u32x4 *)(gr.o + orow + c);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    delta = fmaf(bf16_lo(df[s].w[e]), bf16_lo(x[e]), delta);
+                    delta = fmaf(bf16_hi(df[s].w[e]), bf16_hi(x[e]), delta);
+                }
+            }
+        }
+    }
+    if (live) {
+        const float x = gr.lse[(sp.q0 + ql) * a.Hq + h];
+        if (x != -kInf) lse = x;
+    }
+    delta = add_halves(delta);
+    const bool huge = __any(fabsf(lse) > kHuge && fabsf(lse) < kInf);
+    const float lse2 = lse * kLog2e;
+    for (int i = tid; i < a.buckets; i += THREADS) {
+        bounds_s[i] = a.bounds[i];
+        bias_s[i] = a.bias[static_cast<int64_t>(h) * a.buckets + i];
+    }
+
+    f32x16 dq[MB];
+    float far = 0.f;  // ds summed over the pairs of the last bucket, where a tile has only those
+    const uint16_t *const krow = Ks + row_base<LP>(ln, half), *const vrow = Vs + row_base<LP>(ln, half);
+    const uint16_t *const kcol = Ks + column_base<LP>(lane);
+    const float *const tb0 = tab[0] + w * 32 + ln + kBK - 1 - 4 * half;
+
+    // One pass over the keys: for delta alone, or for the gradients.  WILD as in the forward.
+    const auto sweep = [&](auto is_wild, auto is_delta, bool staged) {
+        constexpr bool WILD = decltype(is_wild)::value, DELTA = decltype(is_delta)::value;
+        if (!staged) __syncthreads();
+        if (n > 0 && !staged) table(0);
+        for (int it = 0; it < n; ++it) {
+            const int k0 = key0(it);
+            if (!staged) {
+                if (it > 0) __syncthreads();
+                ks.store(Ks);
+                vs.store(Vs);
+                __syncthreads();
+            }
+            if (it + 1 < n) {
+                load(it + 1);
+                table(it + 1);
+            }
+            const int wpos = pmin + w * 32;
+            const bool flat = even(k0);
+#pragma unroll 1
+            for (int g = WK == 2 ? wk : 0; g < (WK == 2 ? wk + 1 : 2); ++g) {
+                const int k1 = k0 + 32 * g;
+                if (wpos + 31 < k1 || q0 + w * 32 >= sp.qlen || (a.window && wpos - (k1 + 31) >= a.window && k1 >= a.sinks))
+                    continue;
+                const int at = 32 * g * kPitch<LP>;
                 f32x16 s = f32x16{}, dp = f32x16{};
 #pragma unroll
                 for (int i = 0; i < STEPS; ++i) {
                     Frag k, v;
-                    read_row<LP>(k, Ks[buf], 32 * g + ln, 2 * i + half);
+                    read_row(k, krow + at, i);
                     s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k.b, qf[i].b, s, 0, 0, 0);
-                    read_row<LP>(v, Vs[buf], 32 * g + ln, 2 * i + half);
+                    read_row(v, vrow + at, i);
                     dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v.b, df[i].b, dp, 0, 0, 0);
                 }
                 if (flat) {
@@ -193,7 +205,7 @@ __global__ __launch_bounds__(NW * 64) void k_seq_attn_bwd_q(const Args a, const 
 #pragma unroll
                     for (int r = 0; r < 16; ++r) s[r] = fmaf(s[r], a.scale, c);
                 } else {
-                    const float *tb = tab[buf] + w * 32 + ln + kBK - 1 - 4 * half - 32 * g;
+                    const float *tb = tb0 + (it & 1) * TAB - 32 * g;
 #pragma unroll
                     for (int r = 0; r < 16; ++r) s[r] = fmaf(s[r], a.scale, tb[-(8 * (r / 4) + r % 4)]);
                     if constexpr (WILD) {
@@ -204,7 +216,7 @@ __global__ __launch_bounds__(NW * 64) void k_seq_attn_bwd_q(const Args a, const 
                     if (k0 < a.sinks) {
 #pragma unroll
                         for (int r = 0; r < 16; ++r) {
-                            const int key = k0 + 32 * g + 8 * (r / 4) + 4 * half + r % 4;
+                            const int key = k1 + 8 * (r / 4) + 4 * half + r % 4;
                             if (wpos + ln - key >= a.window && key >= a.sinks) s[r] = -kInf;
                         }
                     }
@@ -216,13 +228,18 @@ __global__ __launch_bounds__(NW * 64) void k_seq_attn_bwd_q(const Args a, const 
 #pragma unroll
                     for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], kLog2e, -lse2));
                 }
-#pragma unroll
-                for (int r = 0; r < 16; ++r) dp[r] = s[r] * (dp[r] - delta);
                 if constexpr (WILD) {  // a hidden key's dP may be NaN
 #pragma unroll
                     for (int r = 0; r < 16; ++r)
-                        if (s[r] == 0.f) dp[r] = 0.f;
+                        if (s[r] == 0.f) dp[r] = delta;
                 }
+                if constexpr (DELTA) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) far = fmaf(s[r], dp[r], far);
+                    continue;
+                }
+#pragma unroll
+                for (int r = 0; r < 16; ++r) dp[r] = s[r] * (dp[r] - delta);
                 Frag ds[2];
 #pragma unroll
                 for (int r = 0; r < 16; r += 2) ds[r / 8].w[r / 2 % 4] = pack_bf16(dp[r], dp[r + 1]);
@@ -231,7 +248,7 @@ __global__ __launch_bounds__(NW * 64) void k_seq_attn_bwd_q(const Args a, const 
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         Frag k;
-                        read_columns<LP>(k, Ks[buf], 32 * g + 16 * u, 32 * m, lane);
+                        read_columns<LP>(k, kcol + at, 16 * u, 32 * m);
                         if constexpr (WILD) {
 #pragma unroll
                             for (int e = 0; e < 4; ++e) k.w[e] = only_finite(k.w[e]);
@@ -245,60 +262,96 @@ __global__ __launch_bounds__(NW * 64) void k_seq_attn_bwd_q(const Args a, const 
                 } else {
                     // the block's sums along its diagonals: through LDS as rows of queries, of which
                     // lane ln then takes key q - ln (mod 32) of query q.  Those with q >= ln are at
-                    // distance D + ln, the others at D + ln - 32, D = wpos - k0 - 32 g.
-                    float *sk = skew[w];
+                    // distance D + ln, the others at D + ln - 32, D = wpos - k1.
+                    float *sk = skew[wave];
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         *reinterpret_cast<floatx4 *>(sk + ln * PITCH + 8 * j + 4 * half) =
                             floatx4{dp[4 * j], dp[4 * j + 1], dp[4 * j + 2], dp[4 * j + 3]};
                     wave_lds_sync();
-                    hi[g] = lo[g] = 0.f;
+                    float upper = 0.f, lower = 0.f;
                     const int edge = ln - 16 * half;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const int q = 16 * half + i;
                         const float x = sk[q * PITCH + ((q - ln) & 31)];
-                        hi[g] += i >= edge ? x : 0.f;
-                        lo[g] += i >= edge ? 0.f : x;
+                        upper += i >= edge ? x : 0.f;
+                        lower += i >= edge ? 0.f : x;
                     }
                     wave_lds_sync();
+                    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(lower), __float_as_uint(upper), false, false);
+                    const float x = __uint_as_float(r[0]) + __uint_as_float(r[1]);  // distance D - 32 + lane
+                    add_by_bucket(sums[wave], x, btab[it & 1][w * 32 + 31 - 32 * g + lane], lane);
                 }
             }
-            if (near) {
-                // distances of the two blocks' sums, with D = wpos - k0: hi[0] D + ln; lo[0] and hi[1]
-                // D + ln - 32; lo[1] D + ln - 64, which is hi[0]'s place in the next tile
-                if (carry_key != k0) drop_carry();
-                const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(lo[0] + hi[1]),
-                                                                __float_as_uint(carry + hi[0]), false, false);
-                const float x = __uint_as_float(r[0]) + __uint_as_float(r[1]);  // distance D - 32 + lane
-                add_by_bucket(sums[w], x, btab[buf][w * 32 + 31 + lane], lane);
-                carry = lo[1], carry_key = k0 + kBK;
+        }
+    };
+    const auto both = [&](auto is_wild, bool staged) {
+        if (a.buckets) {
+            far = delta = 0.f;
+            sweep(is_wild, std::true_type(), staged);
+            staged = n == 1;  // its only tile is still there
+            if (n > 1) load(0);
+            delta = add_halves(far);
+            if constexpr (WK == 2) {
+                __syncthreads();
+                if (wk == 1 && half == 0) half_s[w][ln] = delta;
+                __syncthreads();
+                const float x = half_s[w][ln];
+                if (wk == 0) delta += x;
+                __syncthreads();
+                if (wk == 0 && half == 0) half_s[w][ln] = delta;
+                __syncthreads();
+                delta = half_s[w][ln];
             }
         }
-        if (it + 1 < n) fill(it + 1);
-    }
+        far = 0.f;
+#pragma unroll
+        for (int m = 0; m < MB; ++m) dq[m] = f32x16{};
+        for (int i = lane; i < a.buckets; i += 64) sums[wave][i] = 0.f;
+        wave_lds_sync();
+        sweep(is_wild, std::false_type(), staged);
     };
-    pass(std::false_type());
+    both(std::false_type(), false);
     float any = 0.f;
 #pragma unroll
     for (int m = 0; m < MB; ++m)
 #pragma unroll
         for (int r = 0; r < 16; ++r) any += dq[m][r];
-    if (__syncthreads_or(any != any)) pass(std::true_type());
+    if (__syncthreads_or(any != any)) {
+        if (n > 0) load(0);
+        both(std::true_type(), false);
+    }
     if (a.buckets) {
-        drop_carry();
 #pragma unroll
         for (int i = 1; i < 64; i <<= 1) far += __shfl_xor(far, i);
-        if (lane == 0) sums[w][a.buckets - 1] += far;
-        __syncthreads();
-        for (int i = tid; i < a.buckets; i += THREADS) {
-            float x = 0.f;
+        if (lane == 0) sums[wave][a.buckets - 1] += far;
+    }
+    __syncthreads();
+    for (int i = tid; i < a.buckets; i += THREADS) {
+        float x = 0.f;
 #pragma unroll
-            for (int v = 0; v < NW; ++v) x += sums[v][i];
-            gr.partial[id * a.buckets + i] = x;
+        for (int v = 0; v < NW; ++v) x += sums[v][i];
+        gr.partial[id * a.buckets + i] = x;
+    }
+    if constexpr (WK == 2) {
+        float *const part = reinterpret_cast<float *>(tiles_s) + w * MB * 16 * 64 + lane;
+        static_assert(WQ * MB * 16 * 64 * 4 <= 2 * TILE * 2, "the tiles' room holds the halves' results");
+        if (wk == 1) {
+#pragma unroll
+            for (int m = 0; m < MB; ++m)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) part[(m * 16 + r) * 64] = dq[m][r];
         }
+        __syncthreads();
+        if (wk == 1) return;
+#pragma unroll
+        for (int m = 0; m < MB; ++m)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) dq[m][r] += part[(m * 16 + r) * 64];
     }
     if (!live) return;
+    if (half == 0) gr.delta[(sp.q0 + ql) * a.Hq + h] = delta;
 #pragma unroll
     for (int m = 0; m < MB; ++m)
 #pragma unroll
@@ -311,30 +364,91 @@ __global__ __launch_bounds__(NW * 64) void k_seq_attn_bwd_q(const Args a, const 
         }
 }
 
-template <int DP, int LP, int NW>
-__global__ __launch_bounds__(NW * 64) void k_seq_attn_bwd_kv(const Args a, const Grads gr, const int64_t slots) {
-    constexpr int KT = NW * 32, STEPS = DP / 16, MB = DP / 32, THREADS = NW * 64;
-    constexpr int TAB = KT + kBK;
-    __shared__ __attribute__((aligned(16))) uint16_t Qs[2][kBK * LP], Ds[2][kBK * LP];
-    __shared__ __attribute__((aligned(16))) float lse_s[2][kBK], delta_s[2][kBK];
-    __shared__ float tab[2][TAB], bias_s[DLRM_SEQ_MAX_BUCKETS];
-    __shared__ int bounds_s[DLRM_SEQ_MAX_BUCKETS], huge_s[2];
+// WY wavefronts of 32 keys, by WX that take one half each of a tile's 64 queries.  blockIdx.y: the
+// key head, and which run of the queries (of all heads that share it) where they are split.
+//
+// FAR: the few first keys that every later query sees, and only the queries past the window: a key
+// block of its own would walk all queries of a long sequence after the others are done.  A workgroup
+// takes kFarChunk queries; the block that owns the keys adds their sums in order.
+template <int DP, int LP, int WY, int WX, int OCC, bool FAR>
+__global__ __launch_bounds__(WY * WX * 64, OCC) void k_seq_attn_bwd_kv(const Args a, const Grads gr) {
+    constexpr int KT = WY * 32, STEPS = DP / 16, MB = DP / 32, THREADS = WY * WX * 64;
+    constexpr int TAB = KT + kBK, TILE = kBK * kPitch<LP>;
+    __shared__ __attribute__((aligned(16))) uint16_t tiles_s[2 * TILE];
+    __shared__ __attribute__((aligned(16))) float lse_s[kBK], delta_s[kBK];
+    __shared__ float tab[2][TAB], bias_s[2][DLRM_SEQ_MAX_BUCKETS];
+    __shared__ int bounds_s[DLRM_SEQ_MAX_BUCKETS];
+    uint16_t *const Qs = tiles_s, *const Ds = tiles_s + TILE;
 
-    const int64_t id = xcd_contiguous(blockIdx.x, gridDim.x);
-    if (id >= slots * a.Hkv) return;
-    const int kvh = static_cast<int>(id / slots);
-    const int64_t slot = id - kvh * slots;
-    const int b = find_sequence(a, a.kv_begin, a.Nkv, slot, KT);
+    const int slot = static_cast<int>(xcd_contiguous(blockIdx.x, gridDim.x));
+    const int b = FAR ? find_sequence(a, a.q_off, a.Nq, slot, kFarChunk) : find_sequence(a, a.kv_begin, a.Nkv, slot, KT);
     const Span sp = span_of(a, b);
-    const int64_t t = slot - (sp.k0 / KT + b);
-    const int tiles = (sp.klen + KT - 1) / KT;
-    if (t < 0 || t >= tiles) return;
-    const int k0 = static_cast<int>(t) * KT;  // the first keys are seen by the most queries: first
+    int kvh, run = 0, k0, qlo, qhi;
+    if constexpr (FAR) {
+        const int blocks = gr.far_rows / KT, c = slot - (static_cast<int>(sp.q0) / kFarChunk + b);
+        kvh = blockIdx.y / blocks, k0 = blockIdx.y % blocks * KT;
+        qlo = max(c * kFarChunk, k0 + a.window - sp.shift);
+        qhi = min((c + 1) * kFarChunk, sp.qlen);
+        if (c < 0 || k0 >= sp.klen || qlo >= qhi) return;
+    } else {
+        kvh = blockIdx.y / gr.splits, run = blockIdx.y % gr.splits;
+        const int t = slot - (static_cast<int>(sp.k0) / KT + b);
+        if (t < 0 || t * KT >= sp.klen) return;
+        k0 = t * KT;  // the first keys are seen by the most queries: first
+        qlo = max(0, k0 - sp.shift);
+        const int64_t reach = static_cast<int64_t>(k0) + KT - 1 + a.window - sp.shift;
+        qhi = !a.window || k0 < a.sinks || reach > sp.qlen ? sp.qlen : static_cast<int>(max(reach, int64_t(0)));
+    }
 
     const int tid = threadIdx.x, lane = tid & 63, ln = lane & 31, half = lane >> 5;
-    const int w = static_cast<int>(wave_id());
+    const int wave = static_cast<int>(wave_id()), w = wave % WY, wx = wave / WY;
     const int kl = k0 + w * 32 + ln;
     const bool live = kl < sp.klen;
+    const int t0 = qlo / kBK, nq = qhi > qlo ? (qhi + kBK - 1) / kBK - t0 : 0;
+    // the tiles of every head in a row, and this workgroup's run of them
+    const int all = nq * a.group;
+    const int i0 = static_cast<int>(static_cast<int64_t>(all) * run / (FAR ? 1 : gr.splits));
+    const int i1 = static_cast<int>(static_cast<int64_t>(all) * (run + 1) / (FAR ? 1 : gr.splits));
+
+    Stage<LP, THREADS> qs(a.q_row, a.d), ds(static_cast<int64_t>(a.Hq) * a.d, a.d);
+    float lse_r = kInf, delta_r = 0.f;
+    const auto load = [&](int it) {
+        const int h = kvh * a.group + it / nq, r0 = (t0 + it % nq) * kBK;
+        qs.load(a.q + sp.q0 * a.q_row + h * a.q_head, a.q_row, a.d, r0, 0, sp.qlen, 0);
+        ds.load(gr.dout + (sp.q0 * a.Hq + h) * static_cast<int64_t>(a.d), static_cast<int64_t>(a.Hq) * a.d, a.d, r0, 0, sp.qlen, 0);
+        if (tid < kBK) {
+            const int q = r0 + tid;
+            lse_r = kInf, delta_r = 0.f;
+            if (q < sp.qlen && (!FAR || (q >= qlo && q < qhi))) {
+                const int64_t at = (sp.q0 + q) * a.Hq + h;
+                const float x = gr.lse[at];
+                if (x != -kInf) lse_r = x;
+                delta_r = gr.delta[at];
+            }
+        }
+    };
+    const auto row_of_bias = [&](int it) {
+        const int h = it / nq;
+        for (int i = tid; i < a.buckets; i += THREADS)
+            bias_s[h & 1][i] = a.bias[static_cast<int64_t>(kvh * a.group + h) * a.buckets + i];
+    };
+    const auto even = [&](int r0) {
+        const int nearest = r0 + sp.shift - (k0 + KT - 1);
+        if (FAR) return nearest >= a.last && nearest >= a.window && k0 + KT <= a.sinks;
+        return nearest >= a.last && (!a.window || r0 + sp.shift + kBK - 1 - k0 < a.window || k0 + KT <= a.sinks);
+    };
+    const auto table = [&](int it) {
+        const int r0 = (t0 + it % nq) * kBK, n0 = r0 + sp.shift - (k0 + KT - 1);
+        if (even(r0)) return;
+        for (int i = tid; i < TAB - 1; i += THREADS) {
+            int bucket;
+            float x = table_entry(a, bounds_s, bias_s[it / nq & 1], n0 + i, k0 < a.sinks, &bucket);
+            if (FAR && n0 + i < a.window) x = -kInf;
+            tab[it & 1][i] = x;
+        }
+    };
+
+    if (i1 > i0) load(i0);
     Frag kf[STEPS], vf[STEPS];
     bool odd = false;
 #pragma unroll
@@ -345,206 +459,275 @@ __global__ __launch_bounds__(NW * 64) void k_seq_attn_bwd_kv(const Args a, const
             kf[s].q = *(const DLRM_GLOBAL u32x4 *)(a.k + (sp.k0 + kl) * a.k_row + kvh * a.k_head + c);
             vf[s].q = *(const DLRM_GLOBAL u32x4 *)(a.v + (sp.k0 + kl) * a.v_row + kvh * a.v_head + c);
         }
+    }
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             odd |= only_finite(kf[s].w[e]) != kf[s].w[e] || only_finite(vf[s].w[e]) != vf[s].w[e];
-    }
     const bool wild = __any(odd);  // a hidden key that is not finite keeps its gradients of zero
-
-    // the queries that see one of the block's keys
-    const int qlo = max(0, k0 - sp.shift);
-    const int64_t reach = static_cast<int64_t>(k0) + KT - 1 + a.window - sp.shift;
-    const int qhi = !a.window || k0 < a.sinks || reach > sp.qlen ? sp.qlen : static_cast<int>(max(reach, int64_t(0)));
-    const int t0 = qlo / kBK, t1 = (qhi + kBK - 1) / kBK;
-    const int nq = qhi > qlo ? t1 - t0 : 0;
-    const int n = nq * a.group;
-
-    Stage<LP, THREADS> qs, ds;
-    float lse_r = kInf, delta_r = 0.f;
-    const auto load = [&](int it) {
-        const int h = kvh * a.group + it / nq, r0 = (t0 + it % nq) * kBK;
-        qs.load(a.q + sp.q0 * a.q_row + h * a.q_head, a.q_row, a.d, r0, 0, sp.qlen, 0);
-        ds.load(gr.dout + (sp.q0 * a.Hq + h) * static_cast<int64_t>(a.d), static_cast<int64_t>(a.Hq) * a.d, a.d, r0, 0, sp.qlen, 0);
-        if (tid < kBK) {
-            const int q = r0 + tid;
-            lse_r = kInf, delta_r = 0.f;
-            if (q < sp.qlen) {
-                const int64_t at = (sp.q0 + q) * a.Hq + h;
-                const float x = gr.lse[at];
-                if (x != -kInf) lse_r = x;
-                delta_r = gr.delta[at];
-            }
-        }
-    };
-    const auto whole = [&](int r0) {
-        const int p = r0 + sp.shift;
-        return p - (k0 + KT - 1) >= 0 && (!a.window || p + kBK - 1 - k0 < a.window || k0 + KT <= a.sinks);
-    };
-    const auto even = [&](int r0) { return whole(r0) && r0 + sp.shift - (k0 + KT - 1) >= a.last; };
-    const auto fill = [&](int it) {
-        const int buf = it & 1, r0 = (t0 + it % nq) * kBK;
-        if (a.buckets && it > 0 && it % nq == 0) {  // another head: its row of the bias
-            __syncthreads();
-            const int h = kvh * a.group + it / nq;
-            for (int i = tid; i < a.buckets; i += THREADS) bias_s[i] = a.bias[static_cast<int64_t>(h) * a.buckets + i];
-            __syncthreads();
-        }
-        qs.store(Qs[buf]);
-        ds.store(Ds[buf]);
-        if (tid < kBK) {
-            lse_s[buf][tid] = lse_r, delta_s[buf][tid] = delta_r;
-            const bool any = __any(fabsf(lse_r) > kHuge && fabsf(lse_r) < kInf);
-            if (tid == 0) huge_s[buf] = any;
-        }
-        if (!even(r0)) {
-            const int n0 = r0 + sp.shift - (k0 + KT - 1);
-            int bucket;
-            for (int i = tid; i < TAB - 1; i += THREADS)
-                tab[buf][i] = table_entry(a, bounds_s, bias_s, n0 + i, k0 < a.sinks, &bucket);
-        }
-    };
 
     f32x16 dk[MB], dv[MB];
 #pragma unroll
     for (int m = 0; m < MB; ++m) dk[m] = dv[m] = f32x16{};
+    const int rows = row_base<LP>(ln, half), cols = column_base<LP>(lane);
+    const float *const tb0 = tab[0] + 4 * half + KT - 1 - (w * 32 + ln);
 
-    for (int i = tid; i < a.buckets; i += THREADS) {
-        bounds_s[i] = a.bounds[i];
-        bias_s[i] = a.bias[static_cast<int64_t>(kvh) * a.group * a.buckets + i];
-    }
-    if (n > 0) load(0);
+    for (int i = tid; i < a.buckets; i += THREADS) bounds_s[i] = a.bounds[i];
+    if (i1 > i0) row_of_bias(i0);
     __syncthreads();
-    if (n > 0) fill(0);
-    for (int it = 0; it < n; ++it) {
-        const int r0 = (t0 + it % nq) * kBK, buf = it & 1;
-        if (it + 1 < n) load(it + 1);
+    if (i1 > i0) table(i0);
+    for (int it = i0; it < i1; ++it) {
+        const int r0 = (t0 + it % nq) * kBK;
+        if (it > i0) __syncthreads();  // the tile before has been read
+        qs.store(Qs);
+        ds.store(Ds);
+        if (tid < kBK) lse_s[tid] = lse_r, delta_s[tid] = delta_r;
+        if (it + 1 < i1 && (it + 1) % nq == 0) row_of_bias(it + 1);
         __syncthreads();
-        const int p0 = r0 + sp.shift, wkey = k0 + w * 32;  // positions p0 .. p0 + 63, keys wkey .. wkey + 31
-        const bool none = p0 + kBK - 1 < wkey || wkey >= sp.klen ||
-                          (a.window && p0 - (wkey + 31) >= a.window && wkey >= a.sinks);
-        // the last bucket's bias is read before fill() may bring another head's
-        const float c = a.buckets ? bias_s[a.buckets - 1] : 0.f;
-        if (!none) {
-            const bool flat = even(r0), huge = huge_s[buf] != 0;
+        if (it + 1 < i1) {
+            load(it + 1);
+            table(it + 1);
+        }
+        const bool flat = even(r0);
+        const int wkey = k0 + w * 32;
+        const float c = a.buckets ? bias_s[it / nq & 1][a.buckets - 1] : 0.f;
+#pragma unroll 1
+        for (int g = WX == 2 ? wx : 0; g < (WX == 2 ? wx + 1 : 2); ++g) {
+            const int p0 = r0 + 32 * g + sp.shift;  // positions p0 .. p0 + 31, keys wkey .. wkey + 31
+            if (p0 + 31 < wkey || wkey >= sp.klen || r0 + 32 * g >= qhi) continue;
+            if (FAR ? wkey >= a.sinks || p0 + 31 - wkey < a.window : a.window && p0 - (wkey + 31) >= a.window && wkey >= a.sinks)
+                continue;
+            const uint16_t *const qt = Qs + 32 * g * kPitch<LP>, *const dt = Ds + 32 * g * kPitch<LP>;
+            f32x16 s = f32x16{}, dp = f32x16{};
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                f32x16 s = f32x16{}, dp = f32x16{};
+            for (int i = 0; i < STEPS; ++i) {
+                Frag q, d;
+                read_row(q, qt + rows, i);
+                s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(q.b, kf[i].b, s, 0, 0, 0);
+                read_row(d, dt + rows, i);
+                dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(d.b, vf[i].b, dp, 0, 0, 0);
+            }
+            // register r: query 8 (r / 4) + 4 half + r % 4
+            if (flat) {
 #pragma unroll
-                for (int i = 0; i < STEPS; ++i) {
-                    Frag q, d;
-                    read_row<LP>(q, Qs[buf], 32 * g + ln, 2 * i + half);
-                    s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(q.b, kf[i].b, s, 0, 0, 0);
-                    read_row<LP>(d, Ds[buf], 32 * g + ln, 2 * i + half);
-                    dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(d.b, vf[i].b, dp, 0, 0, 0);
+                for (int r = 0; r < 16; ++r) s[r] = fmaf(s[r], a.scale, c);
+            } else {
+                const float *tb = tb0 + (it & 1) * TAB + 32 * g;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[r] = fmaf(s[r], a.scale, tb[8 * (r / 4) + r % 4]);
+                if (wild) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (tb[8 * (r / 4) + r % 4] == -kInf) s[r] = -kInf;
                 }
-                // register r: query 32 g + 8 (r / 4) + 4 half + r % 4
-                if (flat) {
+                if (k0 < a.sinks) {
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) s[r] = fmaf(s[r], a.scale, c);
-                } else {
-                    const float *tb = tab[buf] + 32 * g + 4 * half + KT - 1 - (w * 32 + ln);
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) s[r] = fmaf(s[r], a.scale, tb[8 * (r / 4) + r % 4]);
-                    if (wild) {
-#pragma unroll
-                        for (int r = 0; r < 16; ++r)
-                            if (tb[8 * (r / 4) + r % 4] == -kInf) s[r] = -kInf;
-                    }
-                    if (k0 < a.sinks) {
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) {
-                            const int p = p0 + 32 * g + 8 * (r / 4) + 4 * half + r % 4;
-                            if (p - kl >= a.window && kl >= a.sinks) s[r] = -kInf;
-                        }
+                    for (int r = 0; r < 16; ++r) {
+                        const int p = p0 + 8 * (r / 4) + 4 * half + r % 4;
+                        if (p - kl >= a.window && kl >= a.sinks) s[r] = -kInf;
                     }
                 }
-                Frag pf[2], sf[2];
+            }
+            Frag pf[2], sf[2];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const floatx4 l = *reinterpret_cast<const floatx4 *>(&lse_s[buf][32 * g + 8 * j + 4 * half]);
-                    const floatx4 e = *reinterpret_cast<const floatx4 *>(&delta_s[buf][32 * g + 8 * j + 4 * half]);
-                    float p[4];
+            for (int j = 0; j < 4; ++j) {
+                const floatx4 l = *reinterpret_cast<const floatx4 *>(&lse_s[32 * g + 8 * j + 4 * half]);
+                const floatx4 e = *reinterpret_cast<const floatx4 *>(&delta_s[32 * g + 8 * j + 4 * half]);
+                float p[4];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float z = s[4 * j + r];
-                        p[r] = huge ? __builtin_amdgcn_exp2f((z - l[r]) * kLog2e)
-                                    : __builtin_amdgcn_exp2f(fmaf(z, kLog2e, -l[r] * kLog2e));
-                        float x = p[r] * (dp[4 * j + r] - e[r]);
-                        if (wild && p[r] == 0.f) x = 0.f;
-                        dp[4 * j + r] = x;
-                    }
-                    pf[j / 2].w[j % 2 * 2] = pack_bf16(p[0], p[1]);
-                    pf[j / 2].w[j % 2 * 2 + 1] = pack_bf16(p[2], p[3]);
-                    sf[j / 2].w[j % 2 * 2] = pack_bf16(dp[4 * j], dp[4 * j + 1]);
-                    sf[j / 2].w[j % 2 * 2 + 1] = pack_bf16(dp[4 * j + 2], dp[4 * j + 3]);
+                for (int r = 0; r < 4; ++r) {
+                    p[r] = __builtin_amdgcn_exp2f((s[4 * j + r] - l[r]) * kLog2e);
+                    float x = p[r] * (dp[4 * j + r] - e[r]);
+                    if (wild && p[r] == 0.f) x = 0.f;
+                    dp[4 * j + r] = x;
                 }
+                pf[j / 2].w[j % 2 * 2] = pack_bf16(p[0], p[1]);
+                pf[j / 2].w[j % 2 * 2 + 1] = pack_bf16(p[2], p[3]);
+                sf[j / 2].w[j % 2 * 2] = pack_bf16(dp[4 * j], dp[4 * j + 1]);
+                sf[j / 2].w[j % 2 * 2 + 1] = pack_bf16(dp[4 * j + 2], dp[4 * j + 3]);
+            }
+#pragma unroll
+            for (int m = 0; m < MB; ++m)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    Frag x;
+                    read_columns<LP>(x, dt + cols, 16 * u, 32 * m);
+                    dv[m] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x.b, pf[u].b, dv[m], 0, 0, 0);
+                    read_columns<LP>(x, qt + cols, 16 * u, 32 * m);
+                    dk[m] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x.b, sf[u].b, dk[m], 0, 0, 0);
+                }
+        }
+    }
+    if constexpr (WX == 2) {  // the second half of the queries joins the first, dk and then dv
+        float *const part = reinterpret_cast<float *>(tiles_s) + w * MB * 16 * 64 + lane;
+        static_assert(WY * MB * 16 * 64 * 4 <= 2 * TILE * 2, "the tiles' room holds the halves' results");
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            f32x16 *const g = x ? dv : dk;
+            __syncthreads();
+            if (wx == 1) {
 #pragma unroll
                 for (int m = 0; m < MB; ++m)
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        Frag x;
-                        read_columns<LP>(x, Ds[buf], 32 * g + 16 * u, 32 * m, lane);
-                        dv[m] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x.b, pf[u].b, dv[m], 0, 0, 0);
-                        read_columns<LP>(x, Qs[buf], 32 * g + 16 * u, 32 * m, lane);
-                        dk[m] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x.b, sf[u].b, dk[m], 0, 0, 0);
-                    }
+                    for (int r = 0; r < 16; ++r) part[(m * 16 + r) * 64] = g[m][r];
+            }
+            __syncthreads();
+            if (wx == 0) {
+#pragma unroll
+                for (int m = 0; m < MB; ++m)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) g[m][r] += part[(m * 16 + r) * 64];
             }
         }
-        if (it + 1 < n) fill(it + 1);
+        if (wx == 1) return;
     }
     if (!live) return;
-    const int64_t row = ((sp.k0 + kl) * a.Hkv + kvh) * static_cast<int64_t>(a.d);
+    if constexpr (FAR) {
+        float *const out = gr.far + ((static_cast<int64_t>(slot) * a.Hkv + kvh) * gr.far_rows + kl) * 2 * a.d;
+#pragma unroll
+        for (int m = 0; m < MB; ++m)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int c = 32 * m + 8 * g + 4 * half;
+                if (c >= a.d) continue;
+                *(DLRM_GLOBAL floatx4 *)(out + c) = floatx4{dk[m][4 * g], dk[m][4 * g + 1], dk[m][4 * g + 2], dk[m][4 * g + 3]};
+                *(DLRM_GLOBAL floatx4 *)(out + a.d + c) = floatx4{dv[m][4 * g], dv[m][4 * g + 1], dv[m][4 * g + 2], dv[m][4 * g + 3]};
+            }
+        return;
+    }
+    if (k0 < gr.far_sinks && run == 0) {
+        const int past = max(0, k0 + a.window - sp.shift), base = static_cast<int>(sp.q0) / kFarChunk + b;
+        for (int c = past / kFarChunk; past < sp.qlen && c * kFarChunk < sp.qlen; ++c) {
+            const float *in = gr.far + ((static_cast<int64_t>(base + c) * a.Hkv + kvh) * gr.far_rows + kl) * 2 * a.d;
+#pragma unroll
+            for (int m = 0; m < MB; ++m)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int col = 32 * m + 8 * g + 4 * half;
+                    if (col >= a.d) continue;
+                    const floatx4 x = *(const DLRM_GLOBAL floatx4 *)(in + col), y = *(const DLRM_GLOBAL floatx4 *)(in + a.d + col);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) dk[m][4 * g + r] += x[r], dv[m][4 * g + r] += y[r];
+                }
+        }
+    }
+    const int64_t row = ((sp.k0 + kl) * a.Hkv + kvh) * static_cast<int64_t>(a.d), plane = a.Nkv * a.Hkv * a.d;
 #pragma unroll
     for (int m = 0; m < MB; ++m)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
             const int c = 32 * m + 8 * g + 4 * half;
             if (c >= a.d) continue;
-            *(DLRM_GLOBAL u32x2 *)(gr.dk + row + c) =
-                u32x2{pack_bf16(dk[m][4 * g] * a.scale, dk[m][4 * g + 1] * a.scale),
-                      pack_bf16(dk[m][4 * g + 2] * a.scale, dk[m][4 * g + 3] * a.scale)};
-            *(DLRM_GLOBAL u32x2 *)(gr.dv + row + c) =
-                u32x2{pack_bf16(dv[m][4 * g], dv[m][4 * g + 1]), pack_bf16(dv[m][4 * g + 2], dv[m][4 * g + 3])};
+            floatx4 x, y;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[r] = dk[m][4 * g + r] * a.scale, y[r] = dv[m][4 * g + r];
+            if (gr.splits > 1) {
+                *(DLRM_GLOBAL floatx4 *)(gr.split + 2 * run * plane + row + c) = x;
+                *(DLRM_GLOBAL floatx4 *)(gr.split + (2 * run + 1) * plane + row + c) = y;
+            } else {
+                *(DLRM_GLOBAL u32x2 *)(gr.dk + row + c) = u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
+                *(DLRM_GLOBAL u32x2 *)(gr.dv + row + c) = u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+            }
         }
 }
 
-// dbias[h][t] = sum over the slots of partial[h][slot][t]: 32 buckets by 32 runs of slots, each in
+// dk, dv = the sums over the runs, in order; four elements a thread of each.
+__global__ __launch_bounds__(256) void k_seq_kv_sum(const float *split, int splits, int64_t plane, uint16_t *dk, uint16_t *dv) {
+    const int64_t e = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+    if (e >= plane) return;
+    floatx4 x = {0.f, 0.f, 0.f, 0.f}, y = x;
+    for (int s = 0; s < splits; ++s) {
+        x += *(const DLRM_GLOBAL floatx4 *)(split + 2 * s * plane + e);
+        y += *(const DLRM_GLOBAL floatx4 *)(split + (2 * s + 1) * plane + e);
+    }
+    *(DLRM_GLOBAL u32x2 *)(dk + e) = u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
+    *(DLRM_GLOBAL u32x2 *)(dv + e) = u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+}
+
+// dbias[h][t] = sum over the slots of partial[h][slot][t]: 8 buckets by 128 runs of slots, each in
 // order, then the runs in order.
 __global__ __launch_bounds__(1024) void k_seq_bias_sum(const float *partial, int64_t slots, int buckets, float *dbias) {
-    __shared__ float part[32][33];
-    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    const int t = blockIdx.x * 32 + tx;
+    __shared__ float part[128][9];
+    const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;
+    const int t = blockIdx.x * 8 + tx;
     const int64_t h = blockIdx.y;
     float x = 0.f;
     if (t < buckets) {
 #pragma unroll 8
-        for (int64_t s = ty; s < slots; s += 32) x += partial[(h * slots + s) * buckets + t];
+        for (int64_t s = ty; s < slots; s += 128) x += partial[(h * slots + s) * buckets + t];
     }
     part[ty][tx] = x;
+    __syncthreads();
+    if (ty < 8) {
+        float y = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y += part[16 * ty + i][tx];
+        part[16 * ty][tx] = y;
+    }
     __syncthreads();
     if (ty == 0 && t < buckets) {
         float y = 0.f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) y += part[i][tx];
+        for (int i = 0; i < 8; ++i) y += part[16 * i][tx];
         dbias[h * buckets + t] = y;
     }
 }
 
-constexpr int kWaves = 4;
+// The workspace: delta, the partial dbias, the split and the far sums of dk and dv.
+struct Layout {
+    int64_t qslots, kslots, far_slots;
+    int splits, far_rows;
+    size_t partial, split, far, bytes;
+};
 
-size_t delta_bytes(int64_t Nq, int32_t Hq) { return (static_cast<size_t>(Nq) * Hq * 4 + 255) / 256 * 256; }
+constexpr int kKT = 64;  // keys of a workgroup
 
-template <int DP, int LP>
-int launch(const Args &a, const Grads &gr, float *dbias, hipStream_t stream) {
-    constexpr int NW = kWaves;
-    const int64_t qslots = a.B ? slot_count(a.Nq, a.B, NW * 32) : 0, kslots = a.B ? slot_count(a.Nkv, a.B, NW * 32) : 0;
-    const int64_t qb = qslots * a.Hq, kb = kslots * a.Hkv;
-    if (qb >= (int64_t(1) << 31) - 8 || kb >= (int64_t(1) << 31) - 8) return DLRM_ERR_UNSUPPORTED;
-    if (qb > 0) DLRM_LAUNCH("seq_attn_bwd_q", (k_seq_attn_bwd_q<DP, LP, NW>), dim3(round_up_xcd(qb)), dim3(NW * 64), 0, stream, a, gr, qslots);
-    if (kb > 0) DLRM_LAUNCH("seq_attn_bwd_kv", (k_seq_attn_bwd_kv<DP, LP, NW>), dim3(round_up_xcd(kb)), dim3(NW * 64), 0, stream, a, gr, kslots);
+Layout layout_of(const Args &a) {
+    Layout l{};
+    const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    l.qslots = a.B ? slot_count(a.Nq, a.B, kQT) : 0, l.kslots = a.B ? slot_count(a.Nkv, a.B, kKT) : 0;
+    // a key block's queries are split where there are fewer blocks than two a CU, down to four tiles each
+    const int64_t blocks = l.kslots * a.Hkv, tiles = a.B ? a.group * (a.Nq / a.B / kBK) : 0;
+    l.splits = 1;
+    while (l.splits < 8 && blocks * l.splits < 512 && tiles >= 8 * l.splits) l.splits *= 2;
+    const int sinks = a.sinks <= kFarMost ? a.sinks : 0;
+    l.far_rows = (sinks + kKT - 1) / kKT * kKT;
+    l.far_slots = l.far_rows ? slot_count(a.Nq, a.B, kFarChunk) : 0;
+    l.partial = up(static_cast<size_t>(a.Nq) * a.Hq * 4);
+    l.split = l.partial + up(static_cast<size_t>(l.qslots) * a.Hq * a.buckets * 4);
+    l.far = l.split + (l.splits > 1 ? up(static_cast<size_t>(l.splits) * 2 * a.Nkv * a.Hkv * a.d * 4) : 0);
+    l.bytes = l.far + up(static_cast<size_t>(l.far_slots) * a.Hkv * l.far_rows * 2 * a.d * 4) + 256;
+    return l;
+}
+
+#ifndef YWK
+#define YWK 1
+#define YWX 1
+#define YO1 2
+#define YO2 2
+#endif
+template <int DP, int LP, int WK, int WX, int O1, int O2>
+int launch(const Args &a, const Grads &g, const Layout &l, float *dbias, hipStream_t stream) {
+    if (l.qslots > 0)
+        DLRM_LAUNCH("seq_attn_bwd_q", (k_seq_attn_bwd_q<DP, LP, 2, WK, O1>), dim3(round_up_xcd(l.qslots), a.Hq), dim3(128 * WK), 0,
+                    stream, a, g);
+    Args near = a;
+    if (l.far_rows) {
+        DLRM_LAUNCH("seq_attn_bwd_far", (k_seq_attn_bwd_kv<DP, LP, 2, WX, O2, true>),
+                    dim3(round_up_xcd(l.far_slots), a.Hkv * (l.far_rows / kKT)), dim3(128 * WX), 0, stream, a, g);
+        near.sinks = 0;  // what is left of the first keys' queries is the window's
+    }
+    if (l.kslots > 0)
+        DLRM_LAUNCH("seq_attn_bwd_kv", (k_seq_attn_bwd_kv<DP, LP, 2, WX, O2, false>), dim3(round_up_xcd(l.kslots), a.Hkv * l.splits),
+                    dim3(128 * WX), 0, stream, near, g);
+    const int64_t plane = a.Nkv * a.Hkv * a.d;
+    if (l.splits > 1)
+        DLRM_LAUNCH("seq_kv_sum", k_seq_kv_sum, dim3(static_cast<uint32_t>((plane / 4 + 255) / 256)), dim3(256), 0, stream,
+                    static_cast<const float *>(g.split), l.splits, plane, g.dk, g.dv);
     if (a.buckets)
-        DLRM_LAUNCH("seq_bias_sum", k_seq_bias_sum, dim3((a.buckets + 31) / 32, a.Hq), dim3(1024), 0, stream,
-                    static_cast<const float *>(gr.partial), qslots, a.buckets, dbias);
+        DLRM_LAUNCH("seq_bias_sum", k_seq_bias_sum, dim3((a.buckets + 7) / 8, a.Hq), dim3(1024), 0, stream,
+                    static_cast<const float *>(g.partial), l.qslots, a.buckets, dbias);
     return launch_status();
 }
 
@@ -552,17 +735,14 @@ int launch(const Args &a, const Grads &gr, float *dbias, hipStream_t stream) {
 }  // namespace seq
 }  // namespace dlrm
 
-extern "C" size_t dlrm_seq_attn_bwd_workspace_size(int64_t B, int64_t Nq, int32_t Hq, int32_t buckets) {
+extern "C" size_t dlrm_seq_attn_bwd_workspace_size(const dlrm_seq_attn *desc) {
     using namespace dlrm::seq;
-    if (B < 0 || Nq < 0 || Hq < 1 || buckets < 0 || buckets > DLRM_SEQ_MAX_BUCKETS || B >= (1 << 24) ||
-        Nq >= (int64_t(1) << 40) || Hq > 4096)
-        return 0;
-    const size_t partial = static_cast<size_t>(slot_count(Nq, B, kWaves * 32)) * Hq * buckets * 4;
-    return delta_bytes(Nq, Hq) + partial + 256;
+    Args a;
+    return check_attn(desc, true, &a) == DLRM_OK ? layout_of(a).bytes : 0;
 }
 
-extern "C" int dlrm_seq_attn_bwd(const dlrm_seq_attn *desc, const uint16_t *dout, const uint16_t *o, const float *o_lo,
-                                 const float *lse, uint16_t *dq, uint16_t *dk, uint16_t *dv, float *dbias, void *workspace,
+extern "C" int dlrm_seq_attn_bwd(const dlrm_seq_attn *desc, const uint16_t *dout, const uint16_t *o, const float *lse,
+                                 const int32_t *tiles, uint16_t *dq, uint16_t *dk, uint16_t *dv, float *dbias, void *workspace,
                                  size_t workspace_bytes, dlrm_stream_t stream_) {
     using namespace dlrm;
     using namespace dlrm::seq;
@@ -570,23 +750,25 @@ extern "C" int dlrm_seq_attn_bwd(const dlrm_seq_attn *desc, const uint16_t *dout
     const int rc = check_attn(desc, true, &a);
     if (rc != DLRM_OK) return rc;
     if ((a.buckets != 0) != (dbias != nullptr) || !aligned(dbias, 4)) return DLRM_ERR_INVALID_ARG;
-    if (a.Nq > 0 && (!dout || !o || !o_lo || !lse || !dq)) return DLRM_ERR_INVALID_ARG;
+    if (a.Nq > 0 && (!dout || !o || !lse || !dq || (a.B > 0 && !tiles))) return DLRM_ERR_INVALID_ARG;
     if (a.Nkv > 0 && (!dk || !dv)) return DLRM_ERR_INVALID_ARG;
-    if (!aligned(dout, 16) || !aligned(o, 16) || !aligned(o_lo, 16) || !aligned(dq, 16) || !aligned(dk, 16) ||
-        !aligned(dv, 16) || !aligned(lse, 4))
+    if (!aligned(dout, 16) || !aligned(o, 16) || !aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16) || !aligned(lse, 4) ||
+        !aligned(tiles, 4))
         return DLRM_ERR_INVALID_ARG;
     // the keys' tiles are found by the same offsets as the sequences' ends
     const uintptr_t ib = a.idx32 ? 4 : 8;
     if (a.B > 0 && static_cast<const char *>(a.kv_end) != static_cast<const char *>(a.kv_begin) + ib) return DLRM_ERR_INVALID_ARG;
-    if (!workspace || !aligned(workspace, 256) ||
-        workspace_bytes < dlrm_seq_attn_bwd_workspace_size(a.B, a.Nq, a.Hq, a.buckets))
-        return DLRM_ERR_WORKSPACE;
-    Grads gr{};
-    gr.dout = dout, gr.o = o, gr.o_lo = o_lo, gr.lse = lse, gr.dq = dq, gr.dk = dk, gr.dv = dv;
-    gr.delta = static_cast<float *>(workspace);
-    gr.partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + delta_bytes(a.Nq, a.Hq));
+    if (static_cast<int64_t>(a.Hq) * a.d >= (1 << 24)) return DLRM_ERR_UNSUPPORTED;
+    const Layout l = layout_of(a);
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < l.bytes) return DLRM_ERR_WORKSPACE;
+    char *const ws = static_cast<char *>(workspace);
+    Grads g{};
+    g.dout = dout, g.o = o, g.lse = lse, g.tiles = tiles, g.dq = dq, g.dk = dk, g.dv = dv;
+    g.delta = reinterpret_cast<float *>(ws), g.partial = reinterpret_cast<float *>(ws + l.partial);
+    g.split = reinterpret_cast<float *>(ws + l.split), g.splits = l.splits;
+    g.far = reinterpret_cast<float *>(ws + l.far), g.far_rows = l.far_rows, g.far_sinks = l.far_rows ? a.sinks : 0;
     hipStream_t stream = reinterpret_cast<hipStream_t>(stream_);
-    if (a.d <= 32) return launch<32, 32>(a, gr, dbias, stream);
-    if (a.d <= 64) return launch<64, 64>(a, gr, dbias, stream);
-    return launch<128, 128>(a, gr, dbias, stream);
+    if (a.d <= 32) return launch<32, 32, YWK, YWX, YO1, YO2>(a, g, l, dbias, stream);
+    if (a.d <= 64) return launch<64, 64, YWK, YWX, YO1, YO2>(a, g, l, dbias, stream);
+    return launch<128, 128, 2, 2, 1, 1>(a, g, l, dbias, stream);
 }

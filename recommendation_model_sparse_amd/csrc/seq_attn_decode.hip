@@ -32,7 +32,7 @@ __global__ __launch_bounds__(kWaves * 64) void k_seq_attn_decode(const Args a, c
                                                                  uint16_t *o_out, float *part, float2 *ml) {
     constexpr int LP = DP, CH = LP / 8, STEPS = DP / 32, MB = DP / 16, VN = kChunk * CH / 64;
     union Lds {
-        uint16_t v[kWaves][kChunk * LP];
+        uint16_t v[kWaves][kChunk * kPitch<LP>];
         float o[kWaves][kHeads][DP];
     };
     __shared__ __attribute__((aligned(16))) Lds lds;
@@ -51,8 +51,8 @@ __global__ __launch_bounds__(kWaves * 64) void k_seq_attn_decode(const Args a, c
     const int tid = threadIdx.x, lane = tid & 63, ln = lane & 15, quad = lane >> 4;
     const int w = static_cast<int>(wave_id());
 
-    const int64_t row0 = offset_at(a, a.kv_begin, b, a.Nkv), row1 = offset_at(a, a.kv_end, b, a.Nkv);
-    const int klen = row1 > row0 ? static_cast<int>(row1 - row0) : 0;
+    const int64_t row0 = offset_at(a, a.kv_begin, b, a.Nkv);
+    const int klen = max(offset_at(a, a.kv_end, b, a.Nkv) - static_cast<int>(row0), 0);
     // the visible keys in a row: the first `skip` ones, then those from `start` on
     const int start = a.window ? max(0, klen - a.window) : 0;
     const int skip = min(a.sinks, start);
@@ -122,7 +122,7 @@ __global__ __launch_bounds__(kWaves * 64) void k_seq_attn_decode(const Args a, c
 #pragma unroll
         for (int i = 0; i < VN; ++i) {
             const int at = i * 64 + lane;
-            *reinterpret_cast<u32x4 *>(vt + chunk_at<LP>(at / CH, at % CH) * 8) = vr[i];
+            *reinterpret_cast<u32x4 *>(vt + at / CH * kPitch<LP> + at % CH * 8) = vr[i];
         }
         const int next = c + kWaves * kChunk;
         if (next < v1) load(next);
@@ -189,7 +189,7 @@ __global__ __launch_bounds__(kWaves * 64) void k_seq_attn_decode(const Args a, c
             const int col = 16 * m + 4 * (ln & 3), row = 4 * quad + (ln >> 2);
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-                const uint16_t *at = vt + chunk_at<LP>(row + 16 * g, col >> 3) * 8 + (col & 7);
+                const uint16_t *at = vt + (row + 16 * g) * kPitch<LP> + col;
                 v.h[g] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t)(at));
             }
             o[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v.b, p.b, o[m], 0, 0, 0);

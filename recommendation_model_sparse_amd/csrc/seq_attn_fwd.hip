@@ -29,7 +29,7 @@ int check_attn(const dlrm_seq_attn *a, bool need_q_offsets, Args *out) {
             if (a->bounds[t] <= a->bounds[t - 1]) return DLRM_ERR_INVALID_ARG;
     }
     if (a->d % 8 != 0 || a->d > 128 || a->Hq > 4096 || a->B >= (1 << 24)) return DLRM_ERR_UNSUPPORTED;
-    if (a->Nq >= (int64_t(1) << 40) || a->Nkv >= (int64_t(1) << 40)) return DLRM_ERR_UNSUPPORTED;
+    if (a->Nq >= (int64_t(1) << 31) || a->Nkv >= (int64_t(1) << 31)) return DLRM_ERR_UNSUPPORTED;
     const uintptr_t ib = a->index_type == DLRM_INDEX_I32 ? 4 : 8;
     if (a->B > 0) {
         if (!a->kv_begin || !a->kv_end || !aligned(a->kv_begin, ib) || !aligned(a->kv_end, ib)) return DLRM_ERR_INVALID_ARG;
@@ -41,6 +41,8 @@ int check_attn(const dlrm_seq_attn *a, bool need_q_offsets, Args *out) {
     const int64_t strides[6] = {a->q_row, a->q_head, a->k_row, a->k_head, a->v_row, a->v_head};
     for (int64_t s : strides)
         if (s % 8 != 0 || s < a->d) return DLRM_ERR_INVALID_ARG;
+    for (int i = 0; i < 6; i += 2)
+        if (strides[i] >= (1 << 24)) return DLRM_ERR_UNSUPPORTED;  // a tile's rows are 32-bit offsets apart
     *out = Args{};
     out->q = a->q, out->k = a->k, out->v = a->v;
     out->q_row = a->q_row, out->q_head = a->q_head, out->k_row = a->k_row, out->k_head = a->k_head;
@@ -62,49 +64,33 @@ int check_attn(const dlrm_seq_attn *a, bool need_q_offsets, Args *out) {
 namespace {
 
 // DP: the head's width rounded up (the products run over DP columns, those from d on are zeros);
-// LP: columns of a row in LDS; NW: wavefronts of 32 queries.
-template <int DP, int LP, int NW, bool TRAIN>
-__global__ __launch_bounds__(NW * 64) void k_seq_attn_fwd(const Args a, uint16_t *o_out, float *lo_out, float *lse_out,
-                                                          const int64_t slots) {
-    constexpr int QT = NW * 32, STEPS = DP / 16, MB = DP / 32, THREADS = NW * 64;
-    constexpr int TAB = QT + kBK;
-    __shared__ __attribute__((aligned(16))) uint16_t Ks[2][kBK * LP], Vs[2][kBK * LP];
+// LP: columns of a row in LDS.  WQ wavefronts of 32 queries each, by WK that share a tile's keys:
+// each then takes one of its two halves, and their results are joined at the end.
+template <int DP, int LP, int WQ, int WK, int OCC>
+__global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a, uint16_t *o_out, float *lse_out,
+                                                                    int32_t *tiles_out) {
+    constexpr int QT = WQ * 32, STEPS = DP / 16, MB = DP / 32, THREADS = WQ * WK * 64;
+    constexpr int TAB = QT + kBK, TILE = kBK * kPitch<LP>;
+    __shared__ __attribute__((aligned(16))) uint16_t tiles_s[2 * TILE];
     __shared__ float tab[2][TAB], bias_s[DLRM_SEQ_MAX_BUCKETS];
     __shared__ int bounds_s[DLRM_SEQ_MAX_BUCKETS];
+    uint16_t *const Ks = tiles_s, *const Vs = tiles_s + TILE;
 
-    const int64_t id = xcd_contiguous(blockIdx.x, gridDim.x);
-    if (id >= slots * a.Hq) return;
-    const int h = static_cast<int>(id / slots);
-    const int64_t slot = id - h * slots;
+    const int slot = static_cast<int>(xcd_contiguous(blockIdx.x, gridDim.x));
+    const int h = blockIdx.y;
     const int b = find_sequence(a, a.q_off, a.Nq, slot, QT);
     const Span sp = span_of(a, b);
-    const int64_t t = slot - (sp.q0 / QT + b);
+    if (tiles_out && h == 0 && threadIdx.x == 0 && slot < slot_count(a.Nq, a.B, QT)) tiles_out[slot] = b;
+    const int t = slot - (static_cast<int>(sp.q0) / QT + b);
     const int tiles = (sp.qlen + QT - 1) / QT;
     if (t < 0 || t >= tiles) return;
-    const int q0 = (tiles - 1 - static_cast<int>(t)) * QT;  // the last queries see the most keys: first
+    const int q0 = (tiles - 1 - t) * QT;  // the last queries see the most keys: first
 
     const int tid = threadIdx.x, lane = tid & 63, ln = lane & 31, half = lane >> 5;
-    const int w = static_cast<int>(wave_id());
+    const int w = static_cast<int>(wave_id()) % WQ, wk = static_cast<int>(wave_id()) / WQ;
     const int kvh = h / a.group;
     const uint16_t *kb = a.k + sp.k0 * a.k_row + kvh * a.k_head;
     const uint16_t *vb = a.v + sp.k0 * a.v_row + kvh * a.v_head;
-
-    for (int i = tid; i < a.buckets; i += THREADS) {
-        bounds_s[i] = a.bounds[i];
-        bias_s[i] = a.bias[static_cast<int64_t>(h) * a.buckets + i];
-    }
-
-    // the queries, each lane's column of the second operand
-    const int ql = q0 + w * 32 + ln;
-    const bool live = ql < sp.qlen;
-    Frag qf[STEPS];
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-        qf[s].q = u32x4{0, 0, 0, 0};
-        const int c = 16 * s + 8 * half;
-        if (live && c < a.d)
-            qf[s].q = *(const DLRM_GLOBAL u32x4 *)(a.q + (sp.q0 + ql) * a.q_row + h * a.q_head + c);
-    }
 
     // the keys that the block's queries see: [first, end), and the first `sinks`
     const int pmin = q0 + sp.shift, pmax = min(q0 + QT, sp.qlen) - 1 + sp.shift;
@@ -115,179 +101,166 @@ __global__ __launch_bounds__(NW * 64) void k_seq_attn_fwd(const Args a, uint16_t
     const int nsink = min((a.sinks + kBK - 1) / kBK, t0);
     const int n = nsink + t1 - t0;
 
-    Stage<LP, THREADS> ks, vs;
+    Stage<LP, THREADS> ks(a.k_row, a.d), vs(a.v_row, a.d);
     const auto key0 = [&](int it) { return (it < nsink ? it : t0 + it - nsink) * kBK; };
     const auto load = [&](int it) {
         ks.load(kb, a.k_row, a.d, key0(it), first, end, a.sinks);
         vs.load(vb, a.v_row, a.d, key0(it), first, end, a.sinks);
     };
-    // Every query of the block sees every key of the tile / at one bias.
-    const auto whole = [&](int k0) {
-        return pmin - (k0 + kBK - 1) >= 0 && (!a.window || q0 + QT - 1 + sp.shift - k0 < a.window || k0 + kBK <= a.sinks);
+    // Every query of the block sees every key of the tile at one bias: no table.
+    const auto even = [&](int k0) {
+        const int nearest = pmin - (k0 + kBK - 1);
+        return nearest >= a.last && (!a.window || q0 + QT - 1 + sp.shift - k0 < a.window || k0 + kBK <= a.sinks);
     };
-    const auto even = [&](int k0) { return whole(k0) && pmin - (k0 + kBK - 1) >= a.last; };
-    const auto fill = [&](int it) {
-        const int k0 = key0(it), buf = it & 1;
-        ks.store(Ks[buf]);
-        vs.store(Vs[buf]);
-        if (!even(k0)) {
-            const int n0 = pmin - (k0 + kBK - 1);
-            int bucket;
-            for (int i = tid; i < TAB - 1; i += THREADS)
-                tab[buf][i] = table_entry(a, bounds_s, bias_s, n0 + i, k0 < a.sinks, &bucket);
-        }
+    const auto table = [&](int it) {
+        const int k0 = key0(it), n0 = pmin - (k0 + kBK - 1);
+        if (even(k0)) return;
+        int bucket;
+        for (int i = tid; i < TAB - 1; i += THREADS)
+            tab[it & 1][i] = table_entry(a, bounds_s, bias_s, n0 + i, k0 < a.sinks, &bucket);
     };
+
+    // the queries, each lane's column of the second operand
+    const int ql = q0 + w * 32 + ln;
+    const bool live = ql < sp.qlen;
+    if (n > 0) load(0);
+    Frag qf[STEPS];
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+        qf[s].q = u32x4{0, 0, 0, 0};
+        const int c = 16 * s + 8 * half;
+        if (live && c < a.d)
+            qf[s].q = *(const DLRM_GLOBAL u32x4 *)(a.q + (sp.q0 + ql) * a.q_row + h * a.q_head + c);
+    }
+    for (int i = tid; i < a.buckets; i += THREADS) {
+        bounds_s[i] = a.bounds[i];
+        bias_s[i] = a.bias[static_cast<int64_t>(h) * a.buckets + i];
+    }
 
     f32x16 o[MB];
     float top, sum;
+    const uint16_t *const krow = Ks + row_base<LP>(ln, half), *const vcol = Vs + column_base<LP>(lane);
+    const float *const tb0 = tab[0] + w * 32 + ln + kBK - 1 - 4 * half;
     // One pass over the keys.  An infinity or NaN in a key would reach the queries that do not see it
     // (0 * NaN in a product): where a result is NaN, the block makes a second, WILD pass that keeps
     // the values apart.  What is finite pays nothing for it.
     const auto attend = [&](auto is_wild) {
-    constexpr bool WILD = decltype(is_wild)::value;
+        constexpr bool WILD = decltype(is_wild)::value;
 #pragma unroll
-    for (int m = 0; m < MB; ++m) o[m] = f32x16{};
-    top = -kInf, sum = 0.f;
-    if (n > 0) load(0);
-    __syncthreads();
-    if (n > 0) fill(0);
-    for (int it = 0; it < n; ++it) {
-        const int k0 = key0(it), buf = it & 1;
-        if (it + 1 < n) load(it + 1);
+        for (int m = 0; m < MB; ++m) o[m] = f32x16{};
+        top = -kInf, sum = 0.f;
         __syncthreads();
-        const int wpos = pmin + w * 32;  // position of the wavefront's first query
-        const bool none = wpos + 31 < k0 || q0 + w * 32 >= sp.qlen ||
-                          (a.window && wpos - (k0 + kBK - 1) >= a.window && k0 >= a.sinks);
-        if (!none) {
-            f32x16 s[2];
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                s[g] = f32x16{};
+        if (n > 0) table(0);
+        for (int it = 0; it < n; ++it) {
+            const int k0 = key0(it);
+            if (it > 0) __syncthreads();  // the tile before has been read
+            ks.store(Ks);
+            vs.store(Vs);
+            __syncthreads();
+            if (it + 1 < n) {
+                load(it + 1);
+                table(it + 1);
+            }
+            const int wpos = pmin + w * 32;  // position of the wavefront's first query
+            // 32 keys at a time: S, P and their operands for 64 would cost a wavefront a SIMD
+#pragma unroll 1
+            for (int g = WK == 2 ? wk : 0; g < (WK == 2 ? wk + 1 : 2); ++g) {
+                const int k1 = k0 + 32 * g;
+                if (wpos + 31 < k1 || q0 + w * 32 >= sp.qlen || (a.window && wpos - (k1 + 31) >= a.window && k1 >= a.sinks))
+                    continue;  // seen by none of the wavefront's queries
+                const uint16_t *kt = krow + 32 * g * kPitch<LP>, *vt = vcol + 32 * g * kPitch<LP>;
+                f32x16 s = f32x16{};
 #pragma unroll
                 for (int i = 0; i < STEPS; ++i) {
                     Frag k;
-                    read_row<LP>(k, Ks[buf], 32 * g + ln, 2 * i + half);
-                    s[g] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k.b, qf[i].b, s[g], 0, 0, 0);
+                    read_row(k, kt, i);
+                    s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k.b, qf[i].b, s, 0, 0, 0);
                 }
-            }
-            // register r of block g: key 32 g + 8 (r / 4) + 4 half + r % 4
-            if (even(k0)) {
-                const float c = a.buckets ? bias_s[a.buckets - 1] : 0.f;
+                // register r: key 8 (r / 4) + 4 half + r % 4
+                if (even(k0)) {
+                    const float c = a.buckets ? bias_s[a.buckets - 1] : 0.f;
 #pragma unroll
-                for (int g = 0; g < 2; ++g)
+                    for (int r = 0; r < 16; ++r) s[r] = fmaf(s[r], a.scale, c);
+                } else {
+                    const float *tb = tb0 + (it & 1) * TAB - 32 * g;
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) s[g][r] = fmaf(s[g][r], a.scale, c);
-            } else {
-                const float *tb = tab[buf] + w * 32 + ln + kBK - 1 - 4 * half;
-#pragma unroll
-                for (int g = 0; g < 2; ++g)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) s[g][r] = fmaf(s[g][r], a.scale, tb[-(32 * g + 8 * (r / 4) + r % 4)]);
-                if constexpr (WILD) {  // NaN - infinity is no -infinity
-#pragma unroll
-                    for (int g = 0; g < 2; ++g)
+                    for (int r = 0; r < 16; ++r) s[r] = fmaf(s[r], a.scale, tb[-(8 * (r / 4) + r % 4)]);
+                    if constexpr (WILD) {  // NaN - infinity is no -infinity
 #pragma unroll
                         for (int r = 0; r < 16; ++r)
-                            if (tb[-(32 * g + 8 * (r / 4) + r % 4)] == -kInf) s[g][r] = -kInf;
-                }
-                if (k0 < a.sinks) {
-                    const int p = wpos + ln;
-#pragma unroll
-                    for (int g = 0; g < 2; ++g)
+                            if (tb[-(8 * (r / 4) + r % 4)] == -kInf) s[r] = -kInf;
+                    }
+                    if (k0 < a.sinks) {
+                        const int p = wpos + ln;
 #pragma unroll
                         for (int r = 0; r < 16; ++r) {
-                            const int key = k0 + 32 * g + 8 * (r / 4) + 4 * half + r % 4;
-                            if (p - key >= a.window && key >= a.sinks) s[g][r] = -kInf;
+                            const int key = k1 + 8 * (r / 4) + 4 * half + r % 4;
+                            if (p - key >= a.window && key >= a.sinks) s[r] = -kInf;
                         }
+                    }
                 }
-            }
-            float mx = s[0][0];
+                float mx = s[0];
 #pragma unroll
-            for (int r = 1; r < 16; ++r) mx = fmaxf(mx, s[0][r]);
+                for (int r = 1; r < 16; ++r) mx = fmaxf(mx, s[r]);
+                mx = fmaxf(max_halves(mx), top);
+                if (__any(mx > top)) {
+                    const float f = mx == -kInf ? 1.f : __builtin_amdgcn_exp2f((top - mx) * kLog2e);
+                    sum *= f;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[1][r]);
-            mx = fmaxf(max_halves(mx), top);
-            if (__any(mx > top)) {
-                const float f = mx == -kInf ? 1.f : __builtin_amdgcn_exp2f((top - mx) * kLog2e);
-                sum *= f;
+                    for (int m = 0; m < MB; ++m)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) o[m][r] *= f;
+                    top = mx;
+                }
+                const float ref = top == -kInf ? 0.f : top;
+                if (__any(fabsf(ref) > kHuge && fabsf(ref) < kInf)) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f((s[r] - ref) * kLog2e);
+                } else {
+                    const float ref2 = ref * kLog2e;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], kLog2e, -ref2));
+                }
+                Frag p[2];
+#pragma unroll
+                for (int r = 0; r < 16; r += 2) {
+                    sum += s[r] + s[r + 1];
+                    p[r / 8].w[r / 2 % 4] = pack_bf16(s[r], s[r + 1]);
+                }
 #pragma unroll
                 for (int m = 0; m < MB; ++m)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) o[m][r] *= f;
-                top = mx;
-            }
-            const float ref = top == -kInf ? 0.f : top;
-            if (__any(fabsf(ref) > kHuge && fabsf(ref) < kInf)) {
-#pragma unroll
-                for (int g = 0; g < 2; ++g)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) s[g][r] = __builtin_amdgcn_exp2f((s[g][r] - ref) * kLog2e);
-            } else {
-                const float ref2 = ref * kLog2e;
-#pragma unroll
-                for (int g = 0; g < 2; ++g)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) s[g][r] = __builtin_amdgcn_exp2f(fmaf(s[g][r], kLog2e, -ref2));
-            }
-            Frag p[2][2], p_mid[2][2], p_lo[2][2];
-#pragma unroll
-            for (int g = 0; g < 2; ++g)
-#pragma unroll
-                for (int r = 0; r < 16; r += 2) {
-                    sum += s[g][r] + s[g][r + 1];
-                    const uint32_t hi = pack_bf16(s[g][r], s[g][r + 1]);
-                    p[g][r / 8].w[r / 2 % 4] = hi;
-                    if constexpr (TRAIN) {  // all 24 bits of P, in three pieces
-                        const float x = s[g][r] - bf16_lo(hi), y = s[g][r + 1] - bf16_hi(hi);
-                        const uint32_t mid = pack_bf16(x, y);
-                        p_mid[g][r / 8].w[r / 2 % 4] = mid;
-                        p_lo[g][r / 8].w[r / 2 % 4] = pack_bf16(x - bf16_lo(mid), y - bf16_hi(mid));
-                    }
-                }
-#pragma unroll
-            for (int m = 0; m < MB; ++m)
-#pragma unroll
-                for (int g = 0; g < 2; ++g)
-#pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         Frag v;
-                        read_columns<LP>(v, Vs[buf], 32 * g + 16 * u, 32 * m, lane);
+                        read_columns<LP>(v, vt, 16 * u, 32 * m);
                         if constexpr (WILD) {
 #pragma unroll
                             for (int e = 0; e < 4; ++e) v.w[e] = only_finite(v.w[e]);
                         }
-                        o[m] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v.b, p[g][u].b, o[m], 0, 0, 0);
-                        if constexpr (TRAIN) {
-                            o[m] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v.b, p_mid[g][u].b, o[m], 0, 0, 0);
-                            o[m] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v.b, p_lo[g][u].b, o[m], 0, 0, 0);
-                        }
+                        o[m] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v.b, p[u].b, o[m], 0, 0, 0);
                     }
-            if constexpr (WILD) {
-                // the products above left out infinities and NaN; each kind reaches a query's output
-                // where the query sees such a key: counted by a product with the 0/1 visibility
-                const int p0 = wpos + ln;
-                Frag see[2][2];
-#pragma unroll
-                for (int g = 0; g < 2; ++g)
+                if constexpr (WILD) {
+                    // the products above left out infinities and NaN; each kind reaches a query's output
+                    // where the query sees such a key: counted by a product with the 0/1 visibility
+                    const int p0 = wpos + ln;
+                    Frag see[2];
 #pragma unroll
                     for (int r = 0; r < 16; ++r) {
-                        const int key = k0 + 32 * g + 8 * (r / 4) + 4 * half + r % 4, dist = p0 - key;
+                        const int key = k1 + 8 * (r / 4) + 4 * half + r % 4, dist = p0 - key;
                         const bool yes = dist >= 0 && (!a.window || dist < a.window || key < a.sinks);
                         const uint32_t bit = yes ? 0x3f80u : 0u;
-                        uint32_t &word = see[g][r / 8].w[r / 2 % 4];
+                        uint32_t &word = see[r / 8].w[r / 2 % 4];
                         word = r % 2 ? word | bit << 16 : bit;
                     }
 #pragma unroll 1
-                for (int kind = 0; kind < 3; ++kind) {
+                    for (int kind = 0; kind < 3; ++kind) {
 #pragma unroll
-                    for (int m = 0; m < MB; ++m) {
-                        f32x16 hit = f32x16{};
-#pragma unroll
-                        for (int g = 0; g < 2; ++g)
+                        for (int m = 0; m < MB; ++m) {
+                            f32x16 hit = f32x16{};
 #pragma unroll
                             for (int u = 0; u < 2; ++u) {
                                 Frag v;
-                                read_columns<LP>(v, Vs[buf], 32 * g + 16 * u, 32 * m, lane);
+                                read_columns<LP>(v, vt, 16 * u, 32 * m);
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {
                                     uint32_t out = 0;
@@ -301,19 +274,18 @@ __global__ __launch_bounds__(NW * 64) void k_seq_attn_fwd(const Args a, uint16_t
                                     }
                                     v.w[e] = out;
                                 }
-                                hit = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v.b, see[g][u].b, hit, 0, 0, 0);
+                                hit = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v.b, see[u].b, hit, 0, 0, 0);
                             }
-                        const float add = kind == 0 ? kInf : kind == 1 ? -kInf : __builtin_nanf("");
+                            const float add = kind == 0 ? kInf : kind == 1 ? -kInf : __builtin_nanf("");
 #pragma unroll
-                        for (int r = 0; r < 16; ++r)
-                            if (hit[r] > 0.f) o[m][r] += add;
+                            for (int r = 0; r < 16; ++r)
+                                if (hit[r] > 0.f) o[m][r] += add;
+                        }
                     }
                 }
             }
         }
-        if (it + 1 < n) fill(it + 1);  // its buffer was last read before this tile's barrier
-    }
-    sum = add_halves(sum);
+        sum = add_halves(sum);
     };
     attend(std::false_type());
     float any = sum;
@@ -321,14 +293,40 @@ __global__ __launch_bounds__(NW * 64) void k_seq_attn_fwd(const Args a, uint16_t
     for (int m = 0; m < MB; ++m)
 #pragma unroll
         for (int r = 0; r < 16; ++r) any += o[m][r];
-    if (__syncthreads_or(live && any != any)) attend(std::true_type());
+    if (__syncthreads_or(live && any != any)) {
+        if (n > 0) load(0);
+        attend(std::true_type());
+    }
+    if constexpr (WK == 2) {  // the second half of the keys joins the first
+        float *const part = reinterpret_cast<float *>(tiles_s) + w * (MB * 16 + 2) * 64 + lane;
+        static_assert(WQ * (MB * 16 + 2) * 64 * 4 <= 2 * TILE * 2, "the tiles' room holds the halves' results");
+        __syncthreads();
+        if (wk == 1) {
+#pragma unroll
+            for (int m = 0; m < MB; ++m)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) part[(m * 16 + r) * 64] = o[m][r];
+            part[MB * 16 * 64] = top;
+            part[(MB * 16 + 1) * 64] = sum;
+        }
+        __syncthreads();
+        if (wk == 1) return;
+        const float top1 = part[MB * 16 * 64], sum1 = part[(MB * 16 + 1) * 64], mx = fmaxf(top, top1);
+        const float f0 = top == -kInf ? 0.f : top == mx ? 1.f : __builtin_amdgcn_exp2f((top - mx) * kLog2e);
+        const float f1 = top1 == -kInf ? 0.f : top1 == mx ? 1.f : __builtin_amdgcn_exp2f((top1 - mx) * kLog2e);
+        // a half without a key that the query sees holds zeros, but a wild pass may have left more
+        sum = (top == -kInf ? 0.f : f0 * sum) + (top1 == -kInf ? 0.f : f1 * sum1);
+        top = mx;
+#pragma unroll
+        for (int m = 0; m < MB; ++m)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) o[m][r] = f0 * o[m][r] + f1 * part[(m * 16 + r) * 64];
+    }
 
     if (!live) return;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const int64_t row = (sp.q0 + ql) * a.Hq + h;
-    if constexpr (TRAIN) {
-        if (half == 0) lse_out[row] = sum == 0.f ? -kInf : top + __builtin_amdgcn_logf(sum) * kLn2;
-    }
+    if (lse_out && half == 0) lse_out[row] = sum == 0.f ? -kInf : top + __builtin_amdgcn_logf(sum) * kLn2;
 #pragma unroll
     for (int m = 0; m < MB; ++m)
 #pragma unroll
@@ -340,23 +338,18 @@ __global__ __launch_bounds__(NW * 64) void k_seq_attn_fwd(const Args a, uint16_t
             for (int r = 0; r < 4; ++r) x[r] = o[m][4 * g + r] * inv;
             const u32x2 hi = {pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
             *(DLRM_GLOBAL u32x2 *)(o_out + row * a.d + c) = hi;
-            if constexpr (TRAIN) {
-                *(DLRM_GLOBAL floatx4 *)(lo_out + row * a.d + c) = floatx4{x[0] - bf16_lo(hi.x), x[1] - bf16_hi(hi.x),
-                                                                          x[2] - bf16_lo(hi.y), x[3] - bf16_hi(hi.y)};
-            }
         }
 }
 
-template <int DP, int LP, int NW>
-int launch(const Args &a, uint16_t *o, float *o_lo, float *lse, hipStream_t stream) {
-    const int64_t slots = slot_count(a.Nq, a.B, NW * 32);
-    const int64_t blocks = slots * a.Hq;
-    if (blocks >= (int64_t(1) << 31) - 8) return DLRM_ERR_UNSUPPORTED;
-    const dim3 grid(round_up_xcd(blocks)), block(NW * 64);
-    if (lse)
-        DLRM_LAUNCH("seq_attn_fwd_train", (k_seq_attn_fwd<DP, LP, NW, true>), grid, block, 0, stream, a, o, o_lo, lse, slots);
-    else
-        DLRM_LAUNCH("seq_attn_fwd", (k_seq_attn_fwd<DP, LP, NW, false>), grid, block, 0, stream, a, o, o_lo, lse, slots);
+#ifndef XWQ
+#define XWQ 2
+#define XWK 1
+#define XOCC 3
+#endif
+template <int DP, int LP, int WQ, int WK, int OCC>
+int launch(const Args &a, uint16_t *o, float *lse, int32_t *tiles, hipStream_t stream) {
+    const dim3 grid(round_up_xcd(slot_count(a.Nq, a.B, WQ * 32)), a.Hq);
+    DLRM_LAUNCH("seq_attn_fwd", (k_seq_attn_fwd<DP, LP, WQ, WK, OCC>), grid, dim3(WQ * WK * 64), 0, stream, a, o, lse, tiles);
     return launch_status();
 }
 
@@ -364,18 +357,22 @@ int launch(const Args &a, uint16_t *o, float *o_lo, float *lse, hipStream_t stre
 }  // namespace seq
 }  // namespace dlrm
 
-extern "C" int dlrm_seq_attn_fwd(const dlrm_seq_attn *desc, uint16_t *o, float *o_lo, float *lse,
-                                 dlrm_stream_t stream_) {
+extern "C" size_t dlrm_seq_attn_tiles(int64_t B, int64_t Nq) {
+    using namespace dlrm::seq;
+    return B < 0 || B >= (1 << 24) || Nq < 0 || Nq >= (int64_t(1) << 31) ? 0 : slot_count(Nq, B, kQT);
+}
+
+extern "C" int dlrm_seq_attn_fwd(const dlrm_seq_attn *desc, uint16_t *o, float *lse, int32_t *tiles, dlrm_stream_t stream_) {
     using namespace dlrm;
     using namespace dlrm::seq;
     Args a;
     const int rc = check_attn(desc, true, &a);
     if (rc != DLRM_OK) return rc;
-    if ((o_lo == nullptr) != (lse == nullptr)) return DLRM_ERR_INVALID_ARG;
-    if (a.Nq > 0 && (!o || !aligned(o, 16) || !aligned(o_lo, 16) || !aligned(lse, 4))) return DLRM_ERR_INVALID_ARG;
+    if (a.B > 0 && a.Nq > 0 && (lse == nullptr) != (tiles == nullptr)) return DLRM_ERR_INVALID_ARG;
+    if (a.Nq > 0 && (!o || !aligned(o, 16) || !aligned(lse, 4) || !aligned(tiles, 4))) return DLRM_ERR_INVALID_ARG;
     if (a.B == 0 || a.Nq == 0) return DLRM_OK;
     hipStream_t stream = reinterpret_cast<hipStream_t>(stream_);
-    if (a.d <= 32) return launch<32, 32, 4>(a, o, o_lo, lse, stream);
-    if (a.d <= 64) return launch<64, 64, 4>(a, o, o_lo, lse, stream);
-    return launch<128, 128, 4>(a, o, o_lo, lse, stream);
+    if (a.d <= 32) return launch<32, 32, XWQ, XWK, XOCC>(a, o, lse, tiles, stream);
+    if (a.d <= 64) return launch<64, 64, XWQ, XWK, XOCC>(a, o, lse, tiles, stream);
+    return launch<128, 128, XWQ, 2, 2>(a, o, lse, tiles, stream);
 }

@@ -38,7 +38,7 @@ BAD = [(dict(B=-1), INVALID), (dict(Nq=-1), INVALID), (dict(Hq=3), INVALID), (di
        (dict(k_row=24), INVALID), (dict(window=-1), INVALID), (dict(sinks=-1), INVALID), (dict(scale=float("nan")), INVALID),
        (dict(bounds=None), INVALID), (dict(buckets=0), INVALID), (dict(buckets=129), UNSUPPORTED),
        (dict(edges=[1, 2, 3, 4]), INVALID), (dict(edges=[0, 2, 2, 4]), INVALID), (dict(bias=FAKE + 2), INVALID),
-       (dict(B=1 << 24), UNSUPPORTED), (dict(Nkv=1 << 40), UNSUPPORTED), (dict(Hq=8192), UNSUPPORTED)]
+       (dict(B=1 << 24), UNSUPPORTED), (dict(Nkv=1 << 31), UNSUPPORTED), (dict(k_row=1 << 24), UNSUPPORTED), (dict(Hq=8192), UNSUPPORTED)]
 
 
 @pytest.mark.parametrize("over,want", BAD)
@@ -67,7 +67,7 @@ def test_attention_outputs_rejected(L):
         assert bwd(ctypes.byref(a), *args, None) == INVALID, i
     assert bwd(ctypes.byref(a), *good[:8], None, 1 << 30, None) == WORKSPACE
     assert bwd(ctypes.byref(a), *good[:8], FAKE + 16, 1 << 30, None) == WORKSPACE
-    need = L.dlrm_seq_attn_bwd_workspace_size(2, 10, 4, 4)
+    need = L.dlrm_seq_attn_bwd_workspace_size(ctypes.byref(a))
     assert need > 0 and bwd(ctypes.byref(a), *good[:8], FAKE, need - 1, None) == WORKSPACE
     assert bwd(ctypes.byref(attn(kv_end=FAKE + 256)), *good, None) == INVALID  # regions, not offsets
     assert bwd(ctypes.byref(attn(bias=None)), *good, None) == INVALID          # dbias without a bias
@@ -80,8 +80,9 @@ def test_attention_outputs_rejected(L):
 
 
 def test_workspace_sizes(L):
-    assert L.dlrm_seq_attn_bwd_workspace_size(-1, 1, 1, 1) == 0 and L.dlrm_seq_attn_bwd_workspace_size(1, 1, 0, 1) == 0
-    assert L.dlrm_seq_attn_bwd_workspace_size(4, 1000, 2, 64) >= 1000 * 2 * 4
+    assert L.dlrm_seq_attn_bwd_workspace_size(ctypes.byref(attn(B=-1))) == 0
+    assert L.dlrm_seq_attn_bwd_workspace_size(ctypes.byref(attn(Nq=1000))) >= 1000 * 4 * 4
+    assert L.dlrm_seq_attn_tiles(-1, 5) == 0 and L.dlrm_seq_attn_tiles(3, 64) >= 3
     assert L.dlrm_seq_attn_decode_workspace_size(1, 3, 2, 32, 0, 0, 10) == 0
     assert L.dlrm_seq_attn_decode_workspace_size(1, 4, 2, 32, 0, 0, 1 << 20) > L.dlrm_seq_attn_decode_workspace_size(1, 4, 2, 32, 100, 4, 1 << 20)
     assert L.dlrm_add_rmsnorm_bwd_workspace_size(5, 0) == 0 and L.dlrm_add_rmsnorm_bwd_workspace_size(5, 4097) == 0
