@@ -106,12 +106,13 @@ __device__ __forceinline__ Span span_of(const Args &a, int b) {
 
 // ---------------------------------------------------------------- LDS tiles
 //
-// A tile holds 64 rows of LP elements (LP = 32, 64 or 128: the head's width rounded up), 16 elements
-// apart: the rows that one read instruction touches (8 of 16 bytes, or 4 of 32 in the transposing
-// read) lie in different banks, and every address is a lane's base plus a constant.
+// A tile holds 64 rows of LP elements (LP = 32, 64 or 128: the head's width rounded up), 8 or 16
+// elements apart: the rows that one read instruction touches (8 of 16 bytes, or 4 of 32 in the
+// transposing read) lie in different banks, and every address is a lane's base plus a constant
+// (swapping 16-byte chunks instead cost about 25 registers of addresses).
 
 template <int LP>
-constexpr int kPitch = LP + 16;
+constexpr int kPitch = LP == 64 ? 72 : LP + 16;
 
 // A lane's place in a tile for read_row: row `row`, columns from 8 * half on.
 template <int LP>
@@ -145,7 +146,9 @@ __device__ __forceinline__ void read_columns(Frag &f, const uint16_t *at, int ro
 
 // 64 rows of a [rows][d] bf16 matrix on their way to LDS, through registers: `load` issues the
 // reads for a tile (rows outside [first, end), but for those below `sinks`, are zeros, as are
-// columns from d on), `store` writes it.
+// columns from d on), `store` writes it.  The next tile is not read ahead: its 16 to 32 registers a
+// matrix cost a wavefront a SIMD, which hides more (heads of 128: 361 -> 318 us for the backward's
+// first kernel; of 64: no difference).
 template <int LP, int THREADS>
 struct Stage {
     static constexpr int CH = LP / 8;

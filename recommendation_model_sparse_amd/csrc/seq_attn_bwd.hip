@@ -14,10 +14,9 @@
 // delta.  Without a bias it is <dO, o> from the forward's output.  That o is rounded to bf16, which
 // the gradients, rounded to bf16 too, bear; dbias does not: it sums ds over up to every pair, where
 // most cancels, and would be 1e-3 off.  With a bias the first kernel therefore goes over its keys
-// twice, first for delta = sum P dP in fp32.  The other way, an output kept in 24 bits by a forward
-// that multiplies P in three bf16 pieces, was measured: 6 more bytes an element to write and read
-// and as much arithmetic (1024 sequences of up to 512, two heads of 64: 0.62 against 0.46 ms for
-// forward and backward).
+// twice, first for delta = sum P dP in fp32.  (An output kept in 24 bits by a forward
+// that multiplies P in three bf16 pieces was the other way: as much arithmetic, and 6 more bytes an
+// element to write and read.)
 #include <type_traits>
 
 #include "seq.h"
@@ -71,7 +70,7 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_bwd_q(const Args
     constexpr int TAB = QT + kBK, TILE = kBK * kPitch<LP>, PITCH = 36;
     static_assert(QT == kQT, "the forward's tiles");
     __shared__ __attribute__((aligned(16))) uint16_t tiles_s[2 * TILE];
-    __shared__ __attribute__((aligned(16))) float skew[NW][32 * PITCH];
+    __shared__ __attribute__((aligned(16))) float skew[NW][16 * PITCH];
     __shared__ float tab[2][TAB], bias_s[DLRM_SEQ_MAX_BUCKETS], sums[NW][DLRM_SEQ_MAX_BUCKETS], half_s[WQ][32];
     __shared__ int bounds_s[DLRM_SEQ_MAX_BUCKETS];
     __shared__ uint8_t btab[2][TAB];
@@ -128,7 +127,6 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_bwd_q(const Args
     const int ql = q0 + w * 32 + ln;
     const bool live = ql < sp.qlen;
     const int64_t orow = ((sp.q0 + ql) * a.Hq + h) * static_cast<int64_t>(a.d);
-    if (n > 0) load(0);
     Frag qf[STEPS], df[STEPS];
     float delta = 0.f, lse = kInf;  // a query that sees nothing: P = exp(z - infinity) = 0
 #pragma unroll
@@ -175,12 +173,12 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_bwd_q(const Args
             const int k0 = key0(it);
             if (!staged) {
                 if (it > 0) __syncthreads();
+                load(it);
                 ks.store(Ks);
                 vs.store(Vs);
                 __syncthreads();
             }
             if (it + 1 < n) {
-                load(it + 1);
                 table(it + 1);
             }
             const int wpos = pmin + w * 32;
@@ -264,21 +262,25 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_bwd_q(const Args
                     // lane ln then takes key q - ln (mod 32) of query q.  Those with q >= ln are at
                     // distance D + ln, the others at D + ln - 32, D = wpos - k1.
                     float *sk = skew[wave];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        *reinterpret_cast<floatx4 *>(sk + ln * PITCH + 8 * j + 4 * half) =
-                            floatx4{dp[4 * j], dp[4 * j + 1], dp[4 * j + 2], dp[4 * j + 3]};
-                    wave_lds_sync();
                     float upper = 0.f, lower = 0.f;
-                    const int edge = ln - 16 * half;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int q = 16 * half + i;
-                        const float x = sk[q * PITCH + ((q - ln) & 31)];
-                        upper += i >= edge ? x : 0.f;
-                        lower += i >= edge ? 0.f : x;
+                    for (int q16 = 0; q16 < 32; q16 += 16) {  // 16 queries at a time, for LDS's sake
+                        wave_lds_sync();
+                        if ((ln & 16) == q16) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                *reinterpret_cast<floatx4 *>(sk + (ln & 15) * PITCH + 8 * j + 4 * half) =
+                                    floatx4{dp[4 * j], dp[4 * j + 1], dp[4 * j + 2], dp[4 * j + 3]};
+                        }
+                        wave_lds_sync();
+                        const int edge = ln - q16 - 8 * half;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float x = sk[(8 * half + i) * PITCH + ((q16 + 8 * half + i - ln) & 31)];
+                            upper += i >= edge ? x : 0.f;
+                            lower += i >= edge ? 0.f : x;
+                        }
                     }
-                    wave_lds_sync();
                     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(lower), __float_as_uint(upper), false, false);
                     const float x = __uint_as_float(r[0]) + __uint_as_float(r[1]);  // distance D - 32 + lane
                     add_by_bucket(sums[wave], x, btab[it & 1][w * 32 + 31 - 32 * g + lane], lane);
@@ -291,7 +293,6 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_bwd_q(const Args
             far = delta = 0.f;
             sweep(is_wild, std::true_type(), staged);
             staged = n == 1;  // its only tile is still there
-            if (n > 1) load(0);
             delta = add_halves(far);
             if constexpr (WK == 2) {
                 __syncthreads();
@@ -319,8 +320,7 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_bwd_q(const Args
 #pragma unroll
         for (int r = 0; r < 16; ++r) any += dq[m][r];
     if (__syncthreads_or(any != any)) {
-        if (n > 0) load(0);
-        both(std::true_type(), false);
+            both(std::true_type(), false);
     }
     if (a.buckets) {
 #pragma unroll
@@ -448,7 +448,6 @@ __global__ __launch_bounds__(WY * WX * 64, OCC) void k_seq_attn_bwd_kv(const Arg
         }
     };
 
-    if (i1 > i0) load(i0);
     Frag kf[STEPS], vf[STEPS];
     bool odd = false;
 #pragma unroll
@@ -480,13 +479,13 @@ __global__ __launch_bounds__(WY * WX * 64, OCC) void k_seq_attn_bwd_kv(const Arg
     for (int it = i0; it < i1; ++it) {
         const int r0 = (t0 + it % nq) * kBK;
         if (it > i0) __syncthreads();  // the tile before has been read
+        load(it);
         qs.store(Qs);
         ds.store(Ds);
         if (tid < kBK) lse_s[tid] = lse_r, delta_s[tid] = delta_r;
         if (it + 1 < i1 && (it + 1) % nq == 0) row_of_bias(it + 1);
         __syncthreads();
         if (it + 1 < i1) {
-            load(it + 1);
             table(it + 1);
         }
         const bool flat = even(r0);
@@ -701,12 +700,6 @@ Layout layout_of(const Args &a) {
     return l;
 }
 
-#ifndef YWK
-#define YWK 1
-#define YWX 1
-#define YO1 2
-#define YO2 2
-#endif
 template <int DP, int LP, int WK, int WX, int O1, int O2>
 int launch(const Args &a, const Grads &g, const Layout &l, float *dbias, hipStream_t stream) {
     if (l.qslots > 0)
@@ -768,7 +761,7 @@ extern "C" int dlrm_seq_attn_bwd(const dlrm_seq_attn *desc, const uint16_t *dout
     g.split = reinterpret_cast<float *>(ws + l.split), g.splits = l.splits;
     g.far = reinterpret_cast<float *>(ws + l.far), g.far_rows = l.far_rows, g.far_sinks = l.far_rows ? a.sinks : 0;
     hipStream_t stream = reinterpret_cast<hipStream_t>(stream_);
-    if (a.d <= 32) return launch<32, 32, YWK, YWX, YO1, YO2>(a, g, l, dbias, stream);
-    if (a.d <= 64) return launch<64, 64, YWK, YWX, YO1, YO2>(a, g, l, dbias, stream);
-    return launch<128, 128, 2, 2, 1, 1>(a, g, l, dbias, stream);
+    if (a.d <= 32) return launch<32, 32, 1, 1, 3, 2>(a, g, l, dbias, stream);
+    if (a.d <= 64) return launch<64, 64, 1, 1, 3, 2>(a, g, l, dbias, stream);
+    return launch<128, 128, 2, 2, 2, 2>(a, g, l, dbias, stream);
 }

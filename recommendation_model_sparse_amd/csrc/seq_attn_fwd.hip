@@ -123,7 +123,6 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a
     // the queries, each lane's column of the second operand
     const int ql = q0 + w * 32 + ln;
     const bool live = ql < sp.qlen;
-    if (n > 0) load(0);
     Frag qf[STEPS];
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
@@ -154,11 +153,11 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a
         for (int it = 0; it < n; ++it) {
             const int k0 = key0(it);
             if (it > 0) __syncthreads();  // the tile before has been read
+            load(it);
             ks.store(Ks);
             vs.store(Vs);
             __syncthreads();
             if (it + 1 < n) {
-                load(it + 1);
                 table(it + 1);
             }
             const int wpos = pmin + w * 32;  // position of the wavefront's first query
@@ -294,8 +293,7 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a
 #pragma unroll
         for (int r = 0; r < 16; ++r) any += o[m][r];
     if (__syncthreads_or(live && any != any)) {
-        if (n > 0) load(0);
-        attend(std::true_type());
+            attend(std::true_type());
     }
     if constexpr (WK == 2) {  // the second half of the keys joins the first
         float *const part = reinterpret_cast<float *>(tiles_s) + w * (MB * 16 + 2) * 64 + lane;
@@ -341,11 +339,6 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a
         }
 }
 
-#ifndef XWQ
-#define XWQ 2
-#define XWK 1
-#define XOCC 3
-#endif
 template <int DP, int LP, int WQ, int WK, int OCC>
 int launch(const Args &a, uint16_t *o, float *lse, int32_t *tiles, hipStream_t stream) {
     const dim3 grid(round_up_xcd(slot_count(a.Nq, a.B, WQ * 32)), a.Hq);
@@ -372,7 +365,7 @@ extern "C" int dlrm_seq_attn_fwd(const dlrm_seq_attn *desc, uint16_t *o, float *
     if (a.Nq > 0 && (!o || !aligned(o, 16) || !aligned(lse, 4) || !aligned(tiles, 4))) return DLRM_ERR_INVALID_ARG;
     if (a.B == 0 || a.Nq == 0) return DLRM_OK;
     hipStream_t stream = reinterpret_cast<hipStream_t>(stream_);
-    if (a.d <= 32) return launch<32, 32, XWQ, XWK, XOCC>(a, o, lse, tiles, stream);
-    if (a.d <= 64) return launch<64, 64, XWQ, XWK, XOCC>(a, o, lse, tiles, stream);
-    return launch<128, 128, XWQ, 2, 2>(a, o, lse, tiles, stream);
+    if (a.d <= 32) return launch<32, 32, 2, 1, 4>(a, o, lse, tiles, stream);
+    if (a.d <= 64) return launch<64, 64, 2, 1, 4>(a, o, lse, tiles, stream);
+    return launch<128, 128, 2, 2, 2>(a, o, lse, tiles, stream);
 }
