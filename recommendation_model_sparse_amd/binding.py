@@ -7,8 +7,11 @@ library is not built, loading it raises.
 """
 from __future__ import annotations
 
+import array
 import ctypes
+import operator
 import os
+import struct
 from typing import List, Optional, Sequence, Tuple
 
 import torch
@@ -34,16 +37,8 @@ class DlrmError(RuntimeError):
         super().__init__(f"{what}: {status_string(status)} (status {status})")
 
 
-class _SeqAttn(ctypes.Structure):
-    """dlrm_seq_attn (dlrm_seq.h)."""
-    _fields_ = [("B", ctypes.c_int64), ("Nq", ctypes.c_int64), ("Nkv", ctypes.c_int64), ("Hq", ctypes.c_int32),
-                ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32), ("index_type", ctypes.c_int32),
-                ("q_offsets", ctypes.c_void_p), ("kv_begin", ctypes.c_void_p), ("kv_end", ctypes.c_void_p),
-                ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q_row", ctypes.c_int64),
-                ("q_head", ctypes.c_int64), ("k_row", ctypes.c_int64), ("k_head", ctypes.c_int64),
-                ("v_row", ctypes.c_int64), ("v_head", ctypes.c_int64), ("window", ctypes.c_int32),
-                ("sinks", ctypes.c_int32), ("scale", ctypes.c_float), ("buckets", ctypes.c_int32),
-                ("bias", ctypes.c_void_p), ("bounds", ctypes.c_void_p)]
+# dlrm_seq_attn (dlrm_seq.h), field by field
+_SEQ_ATTN = struct.Struct("@3q4i6Q6q2ifi2Q")
 
 
 class _Dropout(ctypes.Structure):
@@ -138,7 +133,8 @@ def _check(rc: int, what: str):
 
 
 def _stream(dev: torch.device) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+    # the raw handle: torch.cuda.current_stream(dev) builds a Stream object around it, 2 us a call
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(dev.index))
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -779,27 +775,27 @@ def dlrm_seq_bucket_bounds(buckets: int, reach: int) -> List[int]:
     return out
 
 
-def _head_rows(t, name: str, heads: Optional[int] = None, d: Optional[int] = None) -> torch.Tensor:
-    """[rows, heads, d] bf16 whose heads are packed and whose row and head strides are free (a part
-    of a joint projection, for instance)."""
+def _head_rows(t, name: str, heads: Optional[int] = None, d: Optional[int] = None):
+    """Checks [rows, heads, d] bf16 whose heads are packed and whose row and head strides are free (a
+    part of a joint projection, for instance); returns (rows, heads, d, row stride, head stride)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or (d is not None and t.shape[2] != d):
-        raise ValueError(f"{name} must be [rows, heads={heads}, d={d}], got {tuple(t.shape)}")
-    if t.shape[1] < 1 or t.shape[2] < 1:
-        raise ValueError(f"{name} must have heads and columns, got {tuple(t.shape)}")
-    if t.numel() and t.shape[2] > 1 and t.stride(2) != 1:
+    shape = t.shape
+    if len(shape) != 3 or (heads is not None and shape[1] != heads) or (d is not None and shape[2] != d):
+        raise ValueError(f"{name} must be [rows, heads={heads}, d={d}], got {tuple(shape)}")
+    rows, H, w = shape
+    if H < 1 or w < 1:
+        raise ValueError(f"{name} must have heads and columns, got {tuple(shape)}")
+    row, head, one = t.stride()
+    if one != 1 and rows and w > 1:
         raise ValueError(f"{name} must have packed heads (stride 1 in the last dimension)")
-    return t
-
-
-def _head_strides(t: torch.Tensor) -> Tuple[int, int]:
-    """Row and head strides; those of a dimension of one entry are of no account."""
-    rows, heads, d = t.shape
-    head = t.stride(1) if heads > 1 and rows else d
-    return (t.stride(0) if rows > 1 else max(heads * head, d)), head
+    if H == 1 or not rows:  # the stride of a dimension of one entry is of no account
+        head = w
+    if rows < 2:
+        row = max(H * head, w)
+    return rows, H, w, row, head
 
 
 def _offsets(t, name: str, n: Optional[int] = None) -> torch.Tensor:
@@ -817,38 +813,38 @@ def _count(v, name: str) -> int:
 
 
 def _seq_attn(q, k, v, q_offsets, begin, end, B, window, sinks, scale, bias, bounds):
-    """The checked description of an attention call; returns (struct, what it points to, device)."""
-    _head_rows(q, "q")
-    Hq, d = q.shape[1], q.shape[2]
-    _head_rows(k, "k", None, d)
-    Hkv = k.shape[1]
-    _head_rows(v, "v", Hkv, d)
-    if v.shape[0] != k.shape[0]:
-        raise ValueError(f"k and v must have the same rows, got {k.shape[0]} and {v.shape[0]}")
+    """The checked description of an attention call: (its bytes, what they point to, device, (Nq, Hq, d),
+    buckets)."""
+    Nq, Hq, d, q_row, q_head = _head_rows(q, "q")
+    Nkv, Hkv, _, k_row, k_head = _head_rows(k, "k", None, d)
+    Nv, _, _, v_row, v_head = _head_rows(v, "v", Hkv, d)
+    if Nv != Nkv:
+        raise ValueError(f"k and v must have the same rows, got {Nkv} and {Nv}")
     if Hq % Hkv:
         raise ValueError(f"q's heads must be a multiple of k's, got {Hq} and {Hkv}")
     if d % 8 or d > 128:
         raise ValueError(f"a head must have a multiple of 8 columns, at most 128, got {d}")
-    if q_offsets is not None and begin.dtype != q_offsets.dtype or end.dtype != begin.dtype:
+    if (q_offsets is not None and begin.dtype != q_offsets.dtype) or end.dtype != begin.dtype:
         raise ValueError("all offsets must have one type")
     if (bias is None) != (bounds is None):
         raise ValueError("bias and bounds go together")
-    n, edges = 0, None
+    n, edges, at = 0, None, 0
     if bias is not None:
         n = len(bounds)
-        if not 1 <= n <= DLRM_SEQ_MAX_BUCKETS or bounds[0] != 0 or any(b <= a for a, b in zip(bounds, bounds[1:])):
+        if not 1 <= n <= DLRM_SEQ_MAX_BUCKETS or bounds[0] != 0 or not all(map(operator.lt, bounds, bounds[1:])):
             raise ValueError(f"bounds must be 1 to {DLRM_SEQ_MAX_BUCKETS} strictly increasing distances from 0 on")
         if bounds[-1] >= 1 << 31:
             raise ValueError("bounds must be below 2^31")
         _need(bias, "bias", torch.float32, (Hq, n))
-        edges = (ctypes.c_int32 * n)(*bounds)
+        edges = array.array("i", bounds)
+        at = edges.buffer_info()[0]
     dev = _device(q, k, v, q_offsets, begin, end, bias)
-    a = _SeqAttn(B, q.shape[0], k.shape[0], Hq, Hkv, d, DLRM_INDEX_I32 if begin.dtype == torch.int32 else DLRM_INDEX_I64,
-                 None if q_offsets is None else q_offsets.data_ptr(), begin.data_ptr(), end.data_ptr(),
-                 q.data_ptr(), k.data_ptr(), v.data_ptr(), *_head_strides(q), *_head_strides(k), *_head_strides(v),
-                 _count(window, "window"), _count(sinks, "sinks"), 1.0 / d ** 0.5 if scale is None else float(scale), n,
-                 None if bias is None else bias.data_ptr(), None if edges is None else ctypes.addressof(edges))
-    return a, edges, dev
+    code = DLRM_INDEX_I32 if begin.dtype is torch.int32 else DLRM_INDEX_I64
+    desc = _SEQ_ATTN.pack(B, Nq, Nkv, Hq, Hkv, d, code, 0 if q_offsets is None else q_offsets.data_ptr(), begin.data_ptr(),
+                          end.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), q_row, q_head, k_row, k_head, v_row, v_head,
+                          _count(window, "window"), _count(sinks, "sinks"), d ** -0.5 if scale is None else float(scale), n,
+                          0 if bias is None else bias.data_ptr(), at)
+    return desc, edges, dev, (Nq, Hq, d), n
 
 
 def _kv_ranges(kv_offsets, B: int):
@@ -877,8 +873,7 @@ def dlrm_seq_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offse
     _offsets(q_offsets, "q_offsets")
     B = q_offsets.numel() - 1
     begin, end = _kv_ranges(q_offsets if kv_offsets is None else kv_offsets, B)
-    a, edges, dev = _seq_attn(q, k, v, q_offsets, begin, end, B, window, sinks, scale, bias, bounds)
-    shape = tuple(q.shape)
+    a, edges, dev, shape, _ = _seq_attn(q, k, v, q_offsets, begin, end, B, window, sinks, scale, bias, bounds)
     for_backward = for_backward or tiles is not None or lse is not None
     out = _opt(out, "out", torch.bfloat16, shape)
     if for_backward:
@@ -891,7 +886,7 @@ def dlrm_seq_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offse
         _device(q, out)
     if out is None:
         out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    _check(lib().dlrm_seq_attn_fwd(ctypes.byref(a), _ptr(out), _ptr(lse), _ptr(tiles), _stream(dev)), "dlrm_seq_attn_fwd")
+    _check(lib().dlrm_seq_attn_fwd(a, _ptr(out), _ptr(lse), _ptr(tiles), _stream(dev)), "dlrm_seq_attn_fwd")
     return (out, tiles, lse) if for_backward else out
 
 
@@ -909,8 +904,8 @@ def dlrm_seq_attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: t
     if isinstance(kv_offsets, (tuple, list)):
         raise ValueError("the backward takes kv_offsets [B+1]: every key row in one sequence")
     begin, end = _kv_ranges(q_offsets if kv_offsets is None else kv_offsets, B)
-    a, edges, dev = _seq_attn(q, k, v, q_offsets, begin, end, B, window, sinks, scale, bias, bounds)
-    qs, ks = tuple(q.shape), tuple(k.shape)
+    a, edges, dev, qs, _ = _seq_attn(q, k, v, q_offsets, begin, end, B, window, sinks, scale, bias, bounds)
+    ks = tuple(k.shape)
     _need(dout, "dout", torch.bfloat16, qs)
     _need(o, "o", torch.bfloat16, qs)
     _need(tiles, "tiles", torch.int32, (int(lib().dlrm_seq_attn_tiles(B, qs[0])),))
@@ -926,8 +921,8 @@ def dlrm_seq_attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: t
     dv = torch.empty(ks, **bf) if dv is None else dv
     if bias is not None and dbias is None:
         dbias = torch.empty_like(bias)
-    ws = _ws(int(lib().dlrm_seq_attn_bwd_workspace_size(ctypes.byref(a))), dev, workspace)
-    _check(lib().dlrm_seq_attn_bwd(ctypes.byref(a), _ptr(dout), _ptr(o), _ptr(lse), _ptr(tiles), _ptr(dq), _ptr(dk), _ptr(dv),
+    ws = _ws(int(lib().dlrm_seq_attn_bwd_workspace_size(a)), dev, workspace)
+    _check(lib().dlrm_seq_attn_bwd(a, _ptr(dout), _ptr(o), _ptr(lse), _ptr(tiles), _ptr(dq), _ptr(dk), _ptr(dv),
                                    _ptr(dbias), _ptr(ws), ws.numel(), _stream(dev)), "dlrm_seq_attn_bwd")
     return dq, dk, dv, dbias
 
@@ -945,19 +940,21 @@ def dlrm_seq_attn_decode(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_b
     bf16.  q is [B, Hq, d]; sequence b's keys are the rows kv_begin[b] .. kv_end[b] - 1 of k and v
     [rows, Hkv, d], the event's own the last.  max_kv_len (the sequences' longest, None: k's rows)
     only chooses how far a sequence is split."""
-    _head_rows(q, "q")
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be [B, heads, d]")
     B = q.shape[0]
     begin, end = _offsets_b(kv_begin, "kv_begin", B), _offsets_b(kv_end, "kv_end", B)
-    a, edges, dev = _seq_attn(q, k, v, None, begin, end, B, window, sinks, scale, bias, bounds)
+    a, edges, dev, shape, _ = _seq_attn(q, k, v, None, begin, end, B, window, sinks, scale, bias, bounds)
     longest = k.shape[0] if max_kv_len is None else int(max_kv_len)
     if longest < 0:
         raise ValueError(f"max_kv_len must not be negative, got {longest}")
-    out = _opt(out, "out", torch.bfloat16, tuple(q.shape))
-    _device(q, out)
     if out is None:
-        out = torch.empty(tuple(q.shape), dtype=torch.bfloat16, device=dev)
-    ws = _ws(dlrm_seq_attn_decode_workspace_size(B, a.Hq, a.Hkv, a.d, a.window, a.sinks, longest), dev, workspace)
-    _check(lib().dlrm_seq_attn_decode(ctypes.byref(a), longest, _ptr(out), _ptr(ws), ws.numel(), _stream(dev)),
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _need(out, "out", torch.bfloat16, shape)
+        _device(q, out)
+    ws = _ws(lib().dlrm_seq_attn_decode_workspace_size(B, shape[1], k.shape[1], shape[2], window, sinks, longest), dev, workspace)
+    _check(lib().dlrm_seq_attn_decode(a, longest, _ptr(out), _ptr(ws), ws.numel(), _stream(dev)),
            "dlrm_seq_attn_decode")
     return out
 

@@ -28,7 +28,8 @@ __device__ __forceinline__ float add_quarters(float x) {
 
 // part: [B][Hq][splits] rows of d floats; ml: their (maximum, sum)
 template <int DP>
-__global__ __launch_bounds__(kWaves * 64) void k_seq_attn_decode(const Args a, const int splits, const int head_groups,
+__global__ __launch_bounds__(kWaves * 64) void k_seq_attn_decode(const Args a, const int splits, const int quantum, const bool splits_first,
+                                                                 const int head_groups,
                                                                  uint16_t *o_out, float *part, float2 *ml) {
     constexpr int LP = DP, CH = LP / 8, STEPS = DP / 32, MB = DP / 16, VN = kChunk * CH / 64;
     union Lds {
@@ -41,9 +42,8 @@ __global__ __launch_bounds__(kWaves * 64) void k_seq_attn_decode(const Args a, c
     __shared__ float bias_s[kHeads * DLRM_SEQ_MAX_BUCKETS];
     __shared__ int bounds_s[DLRM_SEQ_MAX_BUCKETS];
 
-    int64_t id = blockIdx.x;
-    const int split = static_cast<int>(id % splits);
-    id /= splits;
+    const int split = splits_first ? blockIdx.x : blockIdx.y;
+    uint32_t id = splits_first ? blockIdx.y : blockIdx.x;
     const int hg = static_cast<int>(id % head_groups);
     id /= head_groups;
     const int kvh = static_cast<int>(id % a.Hkv), b = static_cast<int>(id / a.Hkv);
@@ -57,22 +57,13 @@ __global__ __launch_bounds__(kWaves * 64) void k_seq_attn_decode(const Args a, c
     const int start = a.window ? max(0, klen - a.window) : 0;
     const int skip = min(a.sinks, start);
     const int seen = skip + klen - start;
-    const int per = ((seen + kChunk - 1) / kChunk + splits - 1) / splits * kChunk;
+    const int per = max(((seen + kChunk - 1) / kChunk + splits - 1) / splits * kChunk, quantum);
     const int v0 = min(static_cast<int64_t>(split) * per, static_cast<int64_t>(seen)), v1 = min(v0 + per, seen);
-
-    for (int i = tid; i < a.buckets; i += kWaves * 64) bounds_s[i] = a.bounds[i];
-    for (int i = tid; i < a.buckets * heads; i += kWaves * 64) bias_s[i] = a.bias[static_cast<int64_t>(h0) * a.buckets + i];
-    __syncthreads();
-    const float *my_bias = bias_s + (ln < heads ? ln * a.buckets : 0);
-    const float far = a.buckets ? my_bias[a.buckets - 1] : 0.f;
-
-    Frag qf[STEPS];
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-        qf[s].q = u32x4{0, 0, 0, 0};
-        const int c = 32 * s + 8 * quad;
-        if (ln < heads && c < a.d) qf[s].q = *(const DLRM_GLOBAL u32x4 *)(a.q + b * a.q_row + (h0 + ln) * a.q_head + c);
+    if (splits > 1 && v0 >= v1) {  // a run without keys: the join passes it over
+        if (tid < heads) ml[(static_cast<int64_t>(b) * a.Hq + h0 + tid) * splits + split] = make_float2(-kInf, 0.f);
+        return;
     }
+
     const uint16_t *kb = a.k + row0 * a.k_row + kvh * a.k_head;
     const uint16_t *vb = a.v + row0 * a.v_row + kvh * a.v_head;
 
@@ -103,8 +94,22 @@ __global__ __launch_bounds__(kWaves * 64) void k_seq_attn_decode(const Args a, c
         }
     };
 
+    // the first chunk and the queries are on their way while the bias is fetched
     int c = v0 + w * kChunk;
     if (c < v1) load(c);
+    for (int i = tid; i < a.buckets; i += kWaves * 64) bounds_s[i] = a.bounds[i];
+    for (int i = tid; i < a.buckets * heads; i += kWaves * 64) bias_s[i] = a.bias[static_cast<int64_t>(h0) * a.buckets + i];
+    __syncthreads();
+    const float *my_bias = bias_s + (ln < heads ? ln * a.buckets : 0);
+    const float far = a.buckets ? my_bias[a.buckets - 1] : 0.f;
+
+    Frag qf[STEPS];
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+        qf[s].q = u32x4{0, 0, 0, 0};
+        const int c = 32 * s + 8 * quad;
+        if (ln < heads && c < a.d) qf[s].q = *(const DLRM_GLOBAL u32x4 *)(a.q + b * a.q_row + (h0 + ln) * a.q_head + c);
+    }
     for (; c < v1; c += kWaves * kChunk) {
         uint16_t *vt = lds.v[w];
         floatx4 s[2];
@@ -232,51 +237,78 @@ __global__ __launch_bounds__(kWaves * 64) void k_seq_attn_decode(const Args a, c
     }
 }
 
-// Joins the runs of a row: one wavefront a row, two columns a lane.
-__global__ __launch_bounds__(256) void k_seq_decode_join(const float *part, const float2 *ml, int64_t rows, int splits, int d,
-                                                         uint16_t *o) {
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-    const int lane = threadIdx.x & 63;
-    if (row >= rows) return;
-    float mx = -kInf;
-    for (int s = 0; s < splits; ++s) mx = fmaxf(mx, ml[row * splits + s].x);
-    float total = 0.f, x = 0.f, y = 0.f;
-    for (int s = 0; s < splits; ++s) {
-        const float2 t = ml[row * splits + s];
-        const float f = t.x == -kInf ? 0.f : __builtin_amdgcn_exp2f((t.x - mx) * kLog2e);
-        total += f * t.y;
-        if (2 * lane < d) {
-            const float2 v = *reinterpret_cast<const float2 *>(part + (row * splits + s) * d + 2 * lane);
-            x += f * v.x, y += f * v.y;
+// Joins the runs of a row: a workgroup a row, its wavefronts one run each in turn, so that all reads are
+// under way at once; then the wavefronts' sums in order.
+__global__ __launch_bounds__(256) void k_seq_decode_join(const float *part, const float2 *ml, int splits, int d, uint16_t *o) {
+    __shared__ float2 sums[kWaves][64];
+    __shared__ float factor[kWaves][64];
+    const int64_t row = blockIdx.x;
+    const int lane = threadIdx.x & 63, w = static_cast<int>(wave_id());
+    const float2 t = lane < splits ? ml[row * splits + lane] : make_float2(-kInf, 0.f);
+    float mx = t.x;
+#pragma unroll
+    for (int i = 1; i < 64; i <<= 1) mx = fmaxf(mx, __shfl_xor(mx, i));
+    const float f = t.x == -kInf ? 0.f : __builtin_amdgcn_exp2f((t.x - mx) * kLog2e);
+    float total = f * t.y;
+#pragma unroll
+    for (int i = 1; i < 64; i <<= 1) total += __shfl_xor(total, i);
+    float x = 0.f, y = 0.f;
+    const float *p = part + row * splits * d + 2 * lane;
+    factor[w][lane] = f;
+    wave_lds_sync();
+#pragma unroll 16
+    for (int s = w; s < splits; s += kWaves) {
+        const float g = factor[w][s];
+        if (g != 0.f && 2 * lane < d) {  // nothing was written for a run without keys
+            const float2 v = *reinterpret_cast<const float2 *>(p + static_cast<int64_t>(s) * d);
+            x = fmaf(g, v.x, x), y = fmaf(g, v.y, y);
         }
     }
+    sums[w][lane] = make_float2(x, y);
+    __syncthreads();
+    if (w != 0 || 2 * lane >= d) return;
+    x = y = 0.f;
+#pragma unroll
+    for (int v = 0; v < kWaves; ++v) x += sums[v][lane].x, y += sums[v][lane].y;
     const float inv = total == 0.f ? 0.f : 1.f / total;
-    if (2 * lane < d) *reinterpret_cast<uint32_t *>(o + row * d + 2 * lane) = pack_bf16(x * inv, y * inv);
+    *reinterpret_cast<uint32_t *>(o + row * d + 2 * lane) = pack_bf16(x * inv, y * inv);
 }
 
-// Runs a sequence's keys are split into: enough workgroups for four a CU, at least 256 keys each.
-int split_count(int64_t B, int32_t Hq, int32_t Hkv, int32_t window, int32_t sinks, int64_t max_kv_len) {
+// How the keys of a sequence are split: into at most 64 runs of at least `quantum` keys.  A workgroup a
+// sequence and key head is enough where there are many of one length; lengths differ, and the longest
+// would end long after the others, so that some 4096 runs are aimed at, of 256 keys at least.
+struct Split {
+    int runs, quantum;
+};
+
+Split split_of(int64_t B, int32_t Hq, int32_t Hkv, int32_t window, int32_t sinks, int64_t max_kv_len) {
     const int64_t blocks = B * Hkv * ((Hq / Hkv + kHeads - 1) / kHeads);
-    int64_t seen = max_kv_len;
+    int64_t seen = max_kv_len < (int64_t(1) << 30) ? max_kv_len : int64_t(1) << 30;
     if (window > 0 && static_cast<int64_t>(window) + sinks < seen) seen = static_cast<int64_t>(window) + sinks;
-    int64_t s = blocks > 0 ? (1024 + blocks - 1) / blocks : 1;
-    const int64_t most = (seen + 255) / 256;
-    s = s < most ? s : most;
-    return static_cast<int>(s < 1 ? 1 : s > 256 ? 256 : s);
+    int64_t quantum = (blocks * seen / 4096 + kChunk * kWaves - 1) / (kChunk * kWaves) * (kChunk * kWaves);
+    quantum = quantum < 256 ? 256 : quantum > (1 << 20) ? 1 << 20 : quantum;
+    const int64_t runs = (seen + quantum - 1) / quantum;
+    return Split{static_cast<int>(runs < 1 ? 1 : runs > 64 ? 64 : runs), static_cast<int>(quantum)};
 }
 
 template <int DP>
-int launch(const Args &a, int splits, uint16_t *o, void *ws, hipStream_t stream) {
+int launch(const Args &a, const Split &sp, uint16_t *o, void *ws, hipStream_t stream) {
+    const int splits = sp.runs;
     const int head_groups = (a.group + kHeads - 1) / kHeads;
-    const int64_t rows = static_cast<int64_t>(a.B) * a.Hq, blocks = static_cast<int64_t>(a.B) * a.Hkv * head_groups * splits;
+    const int64_t rows = static_cast<int64_t>(a.B) * a.Hq, blocks = static_cast<int64_t>(a.B) * a.Hkv * head_groups;
     if (blocks >= (int64_t(1) << 31)) return DLRM_ERR_UNSUPPORTED;
     float *part = static_cast<float *>(ws);
     float2 *ml = reinterpret_cast<float2 *>(part ? part + rows * splits * a.d : nullptr);
-    DLRM_LAUNCH("seq_attn_decode", (k_seq_attn_decode<DP>), dim3(static_cast<uint32_t>(blocks)), dim3(kWaves * 64), 0, stream, a,
-                splits, head_groups, o, part, ml);
+    // Many sequences: the first runs of all start first, as every one of them has keys; the runs that only
+    // long sequences have fill in (256 sequences of 64 to 8192: 82 -> 48 us).  Few: a sequence's runs side
+    // by side, as neighbours in memory (32 of up to 65536: 166 -> 152 us).
+    const bool splits_first = blocks < 256;
+    const dim3 grid = splits_first ? dim3(splits, static_cast<uint32_t>(blocks)) : dim3(static_cast<uint32_t>(blocks), splits);
+    DLRM_LAUNCH("seq_attn_decode", (k_seq_attn_decode<DP>), grid, dim3(kWaves * 64), 0, stream, a,
+                splits, sp.quantum, splits_first, head_groups, o, part, ml);
     if (splits > 1)
-        DLRM_LAUNCH("seq_decode_join", k_seq_decode_join, dim3(static_cast<uint32_t>((rows + 3) / 4)), dim3(256), 0, stream,
-                    static_cast<const float *>(part), static_cast<const float2 *>(ml), rows, splits, a.d, o);
+        DLRM_LAUNCH("seq_decode_join", k_seq_decode_join, dim3(static_cast<uint32_t>(rows)), dim3(256), 0, stream,
+                    static_cast<const float *>(part), static_cast<const float2 *>(ml), splits, a.d, o);
     return launch_status();
 }
 
@@ -290,7 +322,7 @@ extern "C" size_t dlrm_seq_attn_decode_workspace_size(int64_t B, int32_t Hq, int
     if (B < 0 || B >= (1 << 24) || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Hq > 4096 || d < 1 || d > 128 || window < 0 || sinks < 0 ||
         max_kv_len < 0)
         return 0;
-    const int splits = split_count(B, Hq, Hkv, window, sinks, max_kv_len);
+    const int splits = split_of(B, Hq, Hkv, window, sinks, max_kv_len).runs;
     return 256 + (splits > 1 ? static_cast<size_t>(B) * Hq * splits * (d + 2) * 4 : 0);
 }
 
@@ -304,12 +336,12 @@ extern "C" int dlrm_seq_attn_decode(const dlrm_seq_attn *desc, int64_t max_kv_le
     if (a.Nq != a.B || max_kv_len < 0) return DLRM_ERR_INVALID_ARG;
     if (a.B == 0) return DLRM_OK;
     if (!o || !aligned(o, 16)) return DLRM_ERR_INVALID_ARG;
-    const int splits = split_count(a.B, a.Hq, a.Hkv, a.window, a.sinks, max_kv_len);
-    if (splits > 1 && (!workspace || !aligned(workspace, 256) ||
+    const Split sp = split_of(a.B, a.Hq, a.Hkv, a.window, a.sinks, max_kv_len);
+    if (sp.runs > 1 && (!workspace || !aligned(workspace, 256) ||
                        workspace_bytes < dlrm_seq_attn_decode_workspace_size(a.B, a.Hq, a.Hkv, a.d, a.window, a.sinks, max_kv_len)))
         return DLRM_ERR_WORKSPACE;
     hipStream_t stream = reinterpret_cast<hipStream_t>(stream_);
-    if (a.d <= 32) return launch<32>(a, splits, o, workspace, stream);
-    if (a.d <= 64) return launch<64>(a, splits, o, workspace, stream);
-    return launch<128>(a, splits, o, workspace, stream);
+    if (a.d <= 32) return launch<32>(a, sp, o, workspace, stream);
+    if (a.d <= 64) return launch<64>(a, sp, o, workspace, stream);
+    return launch<128>(a, sp, o, workspace, stream);
 }

@@ -19,13 +19,29 @@ def L():
     return binding.lib()
 
 
+class SeqAttn(ctypes.Structure):
+    """dlrm_seq_attn as the header declares it."""
+    _fields_ = [("B", ctypes.c_int64), ("Nq", ctypes.c_int64), ("Nkv", ctypes.c_int64), ("Hq", ctypes.c_int32),
+                ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32), ("index_type", ctypes.c_int32),
+                ("q_offsets", ctypes.c_void_p), ("kv_begin", ctypes.c_void_p), ("kv_end", ctypes.c_void_p),
+                ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q_row", ctypes.c_int64),
+                ("q_head", ctypes.c_int64), ("k_row", ctypes.c_int64), ("k_head", ctypes.c_int64),
+                ("v_row", ctypes.c_int64), ("v_head", ctypes.c_int64), ("window", ctypes.c_int32),
+                ("sinks", ctypes.c_int32), ("scale", ctypes.c_float), ("buckets", ctypes.c_int32),
+                ("bias", ctypes.c_void_p), ("bounds", ctypes.c_void_p)]
+
+
+def test_description_layout():
+    assert ctypes.sizeof(SeqAttn) == binding._SEQ_ATTN.size
+
+
 def attn(**over):
     keep = (ctypes.c_int32 * 4)(*over.pop("edges", [0, 1, 2, 3]))
     f = dict(B=2, Nq=10, Nkv=10, Hq=4, Hkv=2, d=32, index_type=0, q_offsets=FAKE, kv_begin=FAKE, kv_end=FAKE + 8, q=FAKE,
              k=FAKE, v=FAKE, q_row=128, q_head=32, k_row=64, k_head=32, v_row=64, v_head=32, window=0, sinks=0, scale=1.0,
              buckets=4, bias=FAKE, bounds=ctypes.addressof(keep))
     f.update(over)
-    a = binding._SeqAttn(**f)
+    a = SeqAttn(**f)
     a.keep = keep
     return a
 
