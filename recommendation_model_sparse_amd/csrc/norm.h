@@ -132,6 +132,13 @@ __device__ __forceinline__ float rounded(float x) {
     return x;
 }
 
+// Orders one wavefront's LDS writes before its lanes' reads of each other's.
+__device__ __forceinline__ void wave_lds_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // ---------------------------------------------------------------- sums over a row's lanes
 
 struct Add { __device__ float operator()(float a, float b) const { return a + b; } };
@@ -151,12 +158,47 @@ __device__ __forceinline__ float over_row(float x, float *part, Op op) {
     return x;
 }
 
-// The dropout factors of elements e .. e + V - 1.
-template <int V>
-__device__ __forceinline__ void factors(const Drop &d, uint64_t offset, int64_t e, float *m) {
-    const uint32_t bits = keep_bits(d, offset, static_cast<uint64_t>(e) >> 3);
+// The dropout factors of a row's elements.  Rows of whole groups of 8 (V = 8): one number a piece.
+// Others (V = 1, piece i of a wavefront's lane at column base + LW i + lane): the groups that the
+// lanes of a row segment cover are numbered through, each lane makes N / 8 of them, and their bits go
+// through LDS, a byte a group; a number an element would be eight times the work.
+template <int LW, int N, int V>
+struct Keep {
+    static constexpr int GROUPS = LW * N / 8 + 1;
+    typedef uint8_t Bytes[256 / LW][GROUPS + 7];
+    const uint8_t *mine;
+    int64_t first;  // element of the segment's first column
+
+    // Before the row's factors are asked for (V = 1): columns [0, cols) of the segment are in use.
+    __device__ __forceinline__ void row(const Drop &d, uint64_t offset, Bytes &bytes, int64_t e0, int cols) {
+        const int sub = threadIdx.x % LW, seg = threadIdx.x / LW;
+        const int last = static_cast<int>(((e0 & 7) + cols - 1) >> 3);
+        wave_lds_sync();
 #pragma unroll
-    for (int j = 0; j < V; ++j) m[j] = bits >> ((V == 8 ? 0 : e & 7) + j) & 1 ? d.scale : 0.f;
+        for (int k = 0; k < N / 8; ++k)
+            if (LW * k + sub <= last) bytes[seg][LW * k + sub] = static_cast<uint8_t>(keep_bits(d, offset, (e0 >> 3) + LW * k + sub));
+        if (last >= LW * N / 8 && sub == 0) bytes[seg][LW * N / 8] = static_cast<uint8_t>(keep_bits(d, offset, (e0 >> 3) + LW * N / 8));
+        wave_lds_sync();
+        mine = bytes[seg], first = e0;
+    }
+    __device__ __forceinline__ void get(const Drop &d, uint64_t offset, int64_t e, float *m) const {
+        if constexpr (V == 8) {
+            const uint32_t bits = keep_bits(d, offset, static_cast<uint64_t>(e) >> 3);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) m[j] = bits >> j & 1 ? d.scale : 0.f;
+        } else {
+            m[0] = mine[(e >> 3) - (first >> 3)] >> (e & 7) & 1 ? d.scale : 0.f;
+        }
+    }
+};
+
+// Column of piece i: rows of 8-element groups go round the row's lanes; others give each wavefront a
+// run of its own, for Keep.
+template <int L, int N, int V>
+__device__ __forceinline__ int column(int i) {
+    const int lane = threadIdx.x % L;
+    if constexpr (V == 8 || L < 256) return (lane + L * i) * V;
+    return (lane >> 6) * 64 * N + 64 * i + (lane & 63);
 }
 
 // A kept element times the scale, a dropped one 0 (not its value times 0: that may be NaN).

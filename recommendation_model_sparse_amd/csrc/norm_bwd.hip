@@ -14,25 +14,31 @@ template <typename G, typename R, typename X, int L, int N, int V, bool DROP>
 __global__ __launch_bounds__(256) void k_add_rmsnorm_bwd(const void *dy, const void *ds, const void *s, const float *w,
                                                          const float *rstd, Drop drop, int64_t M, int D, void *dx, void *dres,
                                                          float *partial) {
-    constexpr int ROWS = 256 / L;
+    constexpr int ROWS = 256 / L, LW = L < 64 ? L : 64;
     __shared__ float part[4];
+    __shared__ typename Keep<LW, V == 1 ? N : 8, V>::Bytes bytes;
     __shared__ float join[ROWS > 1 ? 256 * N * V : 1];
     const int lane = threadIdx.x % L, sub = threadIdx.x / L;
     const uint64_t offset = DROP ? base_offset(drop) : 0;
     float wv[N * V], dw[N * V];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const int c = (lane + L * i) * V;
+        const int c = column<L, N, V>(i);
 #pragma unroll
         for (int j = 0; j < V; ++j) wv[i * V + j] = dw[i * V + j] = 0.f;
         if (c < D) load<F32, V>(w, c, wv + i * V);
     }
     for (int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + sub; row < M; row += static_cast<int64_t>(gridDim.x) * ROWS) {
         const float inv = rstd[row];
+        Keep<LW, V == 1 ? N : 8, V> keep;
+        if constexpr (DROP && V == 1) {
+            const int c0 = L == 256 ? lane / 64 * 64 * N : 0;
+            if (c0 < D) keep.row(drop, offset, bytes, row * D + c0, min(D - c0, LW * N));
+        }
         float g[N * V], hat[N * V], dot = 0.f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int c = (lane + L * i) * V;
+            const int c = column<L, N, V>(i);
 #pragma unroll
             for (int j = 0; j < V; ++j) g[i * V + j] = hat[i * V + j] = 0.f;
             if (c >= D) continue;
@@ -50,7 +56,7 @@ __global__ __launch_bounds__(256) void k_add_rmsnorm_bwd(const void *dy, const v
         const float mean = over_row<L>(dot, part, Add()) / static_cast<float>(D);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int c = (lane + L * i) * V;
+            const int c = column<L, N, V>(i);
             if (c >= D) continue;
             const int64_t e = row * D + c;
             float d[V];
@@ -64,7 +70,7 @@ __global__ __launch_bounds__(256) void k_add_rmsnorm_bwd(const void *dy, const v
             if (dres) store<R, V>(dres, e, d);
             if constexpr (DROP) {
                 float m[V];
-                factors<V>(drop, offset, e, m);
+                keep.get(drop, offset, e, m);
 #pragma unroll
                 for (int j = 0; j < V; ++j) d[j] = drop_one(d[j], m[j]);
             }
@@ -86,26 +92,33 @@ __global__ __launch_bounds__(256) void k_add_rmsnorm_bwd(const void *dy, const v
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const int c = (lane + L * i) * V;
+        const int c = column<L, N, V>(i);
         if (c < D) store<F32, V>(partial, static_cast<int64_t>(blockIdx.x) * D + c, dw + i * V);
     }
 }
 
-// dw[c] = sum over the workgroups' partial sums: 32 columns by 32 runs of rows, then the runs.
+// dw[c] = sum over the workgroups' partial sums: 16 columns by 64 runs of rows, then the runs in order.
 __global__ __launch_bounds__(1024) void k_rmsnorm_dw(const float *partial, int rows, int D, float *dw) {
-    __shared__ float part[32][33];
-    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, c = blockIdx.x * 32 + tx;
+    __shared__ float part[64][17];
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, c = blockIdx.x * 16 + tx;
     float x = 0.f;
     if (c < D) {
-#pragma unroll 8
-        for (int r = ty; r < rows; r += 32) x += partial[static_cast<int64_t>(r) * D + c];
+#pragma unroll 16
+        for (int r = ty; r < rows; r += 64) x += partial[static_cast<int64_t>(r) * D + c];
     }
     part[ty][tx] = x;
+    __syncthreads();
+    if (ty < 8) {
+        float y = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y += part[8 * ty + i][tx];
+        part[8 * ty][tx] = y;
+    }
     __syncthreads();
     if (ty == 0 && c < D) {
         float y = 0.f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) y += part[i][tx];
+        for (int i = 0; i < 8; ++i) y += part[8 * i][tx];
         dw[c] = y;
     }
 }
@@ -138,12 +151,12 @@ void Bwd::run(const Bwd &b) {
 
 int rows_at_once(int D) { return D <= 128 ? 16 : D <= 256 && D % 8 == 0 ? 8 : D <= (D % 8 == 0 ? 2048 : 1024) ? 4 : 1; }
 
-// Workgroups of the backward: eight a CU, fewer where the rows or the table of their dw sums (8 MB)
+// Workgroups of the backward: four a CU, fewer where the rows or the table of their dw sums (8 MB)
 // do not ask for them.
 int bwd_blocks(int64_t M, int D) {
     const int64_t r = rows_at_once(D), want = (M + r - 1) / r;
     int64_t most = (int64_t(1) << 21) / D;
-    most = most < 256 ? 256 : most > 2048 ? 2048 : most;
+    most = most < 256 ? 256 : most > 1024 ? 1024 : most;
     return static_cast<int>(want < 1 ? 1 : want < most ? want : most);
 }
 
@@ -184,7 +197,7 @@ extern "C" int dlrm_add_rmsnorm_bwd(const void *dy, int32_t dy_dtype, const void
     else if (dy_dtype == DLRM_F32) by_x(F32(), BF16());
     else if (res_dtype == DLRM_F32) by_x(BF16(), F32());
     else by_x(BF16(), BF16());
-    DLRM_LAUNCH("rmsnorm_dw", k_rmsnorm_dw, dim3((D + 31) / 32), dim3(1024), 0, b.stream, static_cast<const float *>(b.partial),
+    DLRM_LAUNCH("rmsnorm_dw", k_rmsnorm_dw, dim3((D + 15) / 16), dim3(1024), 0, b.stream, static_cast<const float *>(b.partial),
                 b.blocks, D, dw);
     return launch_status();
 }

@@ -9,19 +9,26 @@
 namespace dlrm {
 namespace {
 
-// One row by L lanes, each with N pieces of V elements; piece i of lane l starts at column (l + L i) V.
+// One row by L lanes, each with N pieces of V elements (columns: column<L, N, V>).
 template <typename X, typename R, typename Y, int L, int N, int V, bool DROP>
 __global__ __launch_bounds__(256) void k_add_rmsnorm_fwd(const void *x, const void *res, const float *w, float eps, Drop drop,
                                                          int64_t M, int D, void *s, void *y, float *y_scale, float *rstd) {
+    constexpr int LW = L < 64 ? L : 64;
     __shared__ float part[4];
+    __shared__ typename Keep<LW, V == 1 ? N : 8, V>::Bytes bytes;
     const int lane = threadIdx.x % L;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * (256 / L) + threadIdx.x / L;
     if (row >= M) return;  // L == 256: the whole workgroup
     const uint64_t offset = DROP ? base_offset(drop) : 0;
+    Keep<LW, V == 1 ? N : 8, V> keep;
+    if constexpr (DROP && V == 1) {
+        const int c0 = L == 256 ? lane / 64 * 64 * N : 0;
+        if (c0 < D) keep.row(drop, offset, bytes, row * D + c0, min(D - c0, LW * N));
+    }
     float h[N * V], sq = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const int c = (lane + L * i) * V;
+        const int c = column<L, N, V>(i);
 #pragma unroll
         for (int j = 0; j < V; ++j) h[i * V + j] = 0.f;
         if (c >= D) continue;
@@ -35,7 +42,7 @@ __global__ __launch_bounds__(256) void k_add_rmsnorm_fwd(const void *x, const vo
         }
         if constexpr (DROP) {
             float m[V];
-            factors<V>(drop, offset, e, m);
+            keep.get(drop, offset, e, m);
 #pragma unroll
             for (int j = 0; j < V; ++j) a[j] = drop_one(a[j], m[j]);
         }
@@ -53,7 +60,7 @@ __global__ __launch_bounds__(256) void k_add_rmsnorm_fwd(const void *x, const vo
     float most = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const int c = (lane + L * i) * V;
+        const int c = column<L, N, V>(i);
         if (c >= D) continue;
         float g[V];
         load<F32, V>(w, c, g);
@@ -70,7 +77,7 @@ __global__ __launch_bounds__(256) void k_add_rmsnorm_fwd(const void *x, const vo
         if (lane == 0) y_scale[row] = most == 0.f ? 1.f : most / 448.f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int c = (lane + L * i) * V;
+            const int c = column<L, N, V>(i);
             if (c >= D) continue;
 #pragma unroll
             for (int j = 0; j < V; ++j) h[i * V + j] *= f;
