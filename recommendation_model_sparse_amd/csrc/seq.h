@@ -214,7 +214,8 @@ __device__ __forceinline__ float add_halves(float x) {
 // ---------------------------------------------------------------- bias by distance
 
 // The bucket of distance n >= 0: the last t with bounds[t] <= n.
-__device__ __forceinline__ int bucket_of(const int *bounds, int buckets, int n) {
+template <typename Bounds>
+__device__ __forceinline__ int bucket_of(const Bounds *bounds, int buckets, int n) {
     int lo = 0, hi = buckets;  // bounds[lo] <= n < bounds[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -224,16 +225,21 @@ __device__ __forceinline__ int bucket_of(const int *bounds, int buckets, int n) 
     return lo;
 }
 
-// What a tile's table adds to the logits at distance n: the bias, or -infinity where it is not visible
-// (`sink_tile`: the window is left to the caller, who knows which keys are first ones).
-// bounds_s and bias_s are in LDS.
-__device__ __forceinline__ float table_entry(const Args &a, const int *bounds_s, const float *bias_s, int n, bool sink_tile,
-                                             int *bucket) {
-    const int t = n > 0 && a.buckets ? bucket_of(bounds_s, a.buckets, n) : 0;
+// What is added to the logits at distance n: the bias, or -infinity where the distance is not visible.
+// `past_window`: the window is left to the caller, who knows which keys are first ones.
+template <typename Bounds, typename Bias>
+__device__ __forceinline__ float bias_at(const Args &a, const Bounds *bounds, const Bias *bias, int n, bool past_window, int *bucket) {
+    const int t = n > 0 && a.buckets ? bucket_of(bounds, a.buckets, n) : 0;
     *bucket = t;
-    if (n < 0 || (a.window && n >= a.window && !sink_tile)) return -kInf;
-    return a.buckets ? bias_s[t] : 0.f;
+    if (n < 0 || (a.window && n >= a.window && !past_window)) return -kInf;
+    return a.buckets ? bias[t] : 0.f;
 }
+
+// A workgroup looks the biases of the distances [-kPad, NEAR) up once, as far as its tiles need them;
+// a tile's distances are a run of them.  (A table for each tile took 900 of its 6200 cycles: every
+// search is a chain of LDS reads.)  Tiles further out have a table of their own, unless the bias is
+// one value there.
+constexpr int kPad = 128;
 
 }  // namespace seq
 }  // namespace dlrm

@@ -25,8 +25,9 @@ namespace dlrm {
 namespace seq {
 namespace {
 
-constexpr int kFarChunk = 256;  // queries of a workgroup of the far part, below
-constexpr int kFarMost = 128;   // most first keys that have a far part of their own
+// Most first keys, and bytes of their sums, that have a far part of their own (below).
+constexpr int kFarMost = 128;
+constexpr size_t kFarBytes = size_t(256) << 20;
 
 struct Grads {
     const uint16_t *dout, *o;
@@ -37,9 +38,9 @@ struct Grads {
     uint16_t *dq, *dk, *dv;
     float *split;          // [splits][2][Nkv][Hkv][d]: dk and dv, where a key block's queries are split
     int splits;
-    // first keys under a window: their gradients from the queries past it, [slot][Hkv][far_rows][2][d]
+    // first keys under a window: their gradients from the queries past it, [slot][Hkv][far_sinks][2][d]
     float *far;
-    int far_sinks, far_rows;
+    int far_sinks;
 };
 
 template <int CTRL, int ROWS>
@@ -64,17 +65,18 @@ __device__ __forceinline__ void add_by_bucket(float *sums, float x, int t, int l
 }
 
 // WQ wavefronts of 32 queries, by WK that take one half each of a tile's 64 keys.
-template <int DP, int LP, int WQ, int WK, int OCC>
+template <int DP, int LP, int WQ, int WK, int OCC, int NEAR>
 __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_bwd_q(const Args a, const Grads gr) {
     constexpr int QT = WQ * 32, STEPS = DP / 16, MB = DP / 32, THREADS = WQ * WK * 64, NW = WQ * WK;
     constexpr int TAB = QT + kBK, TILE = kBK * kPitch<LP>, PITCH = 36;
     static_assert(QT == kQT, "the forward's tiles");
     __shared__ __attribute__((aligned(16))) uint16_t tiles_s[2 * TILE];
     __shared__ __attribute__((aligned(16))) float skew[NW][16 * PITCH];
-    __shared__ float tab[2][TAB], bias_s[DLRM_SEQ_MAX_BUCKETS], sums[NW][DLRM_SEQ_MAX_BUCKETS], half_s[WQ][32];
-    __shared__ int bounds_s[DLRM_SEQ_MAX_BUCKETS];
-    __shared__ uint8_t btab[2][TAB];
+    __shared__ float near_s[kPad + NEAR], tab[TAB], sums[NW][DLRM_SEQ_MAX_BUCKETS], half_s[WK == 2 ? WQ : 1][32];
+    __shared__ uint8_t bnear_s[kPad + NEAR], btab[TAB];
     uint16_t *const Ks = tiles_s, *const Vs = tiles_s + TILE;
+    int *const bounds_s = reinterpret_cast<int *>(tiles_s);  // before the first tile
+    float *const bias_s = reinterpret_cast<float *>(tiles_s) + DLRM_SEQ_MAX_BUCKETS;
 
     const int slots = static_cast<int>(slot_count(a.Nq, a.B, QT));
     const int slot = static_cast<int>(xcd_contiguous(blockIdx.x, gridDim.x));
@@ -114,13 +116,16 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_bwd_q(const Args
         const int nearest = pmin - (k0 + kBK - 1);
         return nearest >= a.last && (!a.window || q0 + QT - 1 + sp.shift - k0 < a.window || k0 + kBK <= a.sinks);
     };
-    const auto table = [&](int it) {
-        const int k0 = key0(it), n0 = pmin - (k0 + kBK - 1);
-        if (even(k0)) return;
+    const auto close = [&](int k0) { return pmin - k0 + QT - 1 < NEAR && k0 >= a.sinks; };
+    const float *const bias_row = a.buckets ? a.bias + static_cast<int64_t>(h) * a.buckets : nullptr;
+    const float last_bias = a.buckets ? bias_row[a.buckets - 1] : 0.f;
+    const auto table = [&](int k0) {
+        if (even(k0) || close(k0)) return;
+        const int n0 = pmin - (k0 + kBK - 1);
         for (int i = tid; i < TAB - 1; i += THREADS) {
             int bucket;
-            tab[it & 1][i] = table_entry(a, bounds_s, bias_s, n0 + i, k0 < a.sinks, &bucket);
-            btab[it & 1][i] = static_cast<uint8_t>(bucket);
+            tab[i] = bias_at(a, a.bounds, bias_row, n0 + i, k0 < a.sinks, &bucket);
+            btab[i] = static_cast<uint8_t>(bucket);
         }
     };
 
@@ -155,32 +160,38 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_bwd_q(const Args
     const float lse2 = lse * kLog2e;
     for (int i = tid; i < a.buckets; i += THREADS) {
         bounds_s[i] = a.bounds[i];
-        bias_s[i] = a.bias[static_cast<int64_t>(h) * a.buckets + i];
+        bias_s[i] = bias_row[i];
+    }
+    __syncthreads();
+    {
+        const int reach = n > 0 ? min(NEAR, pmin + QT - t0 * kBK) : 0;
+        for (int i = tid; i < reach; i += THREADS) {
+            int bucket;
+            near_s[kPad + i] = bias_at(a, bounds_s, bias_s, i, false, &bucket);
+            bnear_s[kPad + i] = static_cast<uint8_t>(bucket);
+        }
+        for (int i = tid; i < kPad; i += THREADS) near_s[i] = -kInf, bnear_s[i] = 0;
     }
 
     f32x16 dq[MB];
     float far = 0.f;  // ds summed over the pairs of the last bucket, where a tile has only those
     const uint16_t *const krow = Ks + row_base<LP>(ln, half), *const vrow = Vs + row_base<LP>(ln, half);
     const uint16_t *const kcol = Ks + column_base<LP>(lane);
-    const float *const tb0 = tab[0] + w * 32 + ln + kBK - 1 - 4 * half;
 
     // One pass over the keys: for delta alone, or for the gradients.  WILD as in the forward.
     const auto sweep = [&](auto is_wild, auto is_delta, bool staged) {
         constexpr bool WILD = decltype(is_wild)::value, DELTA = decltype(is_delta)::value;
-        if (!staged) __syncthreads();
-        if (n > 0 && !staged) table(0);
         for (int it = 0; it < n; ++it) {
             const int k0 = key0(it);
             if (!staged) {
-                if (it > 0) __syncthreads();
                 load(it);
+                __syncthreads();
+                table(k0);
                 ks.store(Ks);
                 vs.store(Vs);
                 __syncthreads();
             }
-            if (it + 1 < n) {
-                table(it + 1);
-            }
+            const bool by_near = close(k0);
             const int wpos = pmin + w * 32;
             const bool flat = even(k0);
 #pragma unroll 1
@@ -199,11 +210,11 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_bwd_q(const Args
                     dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v.b, df[i].b, dp, 0, 0, 0);
                 }
                 if (flat) {
-                    const float c = a.buckets ? bias_s[a.buckets - 1] : 0.f;
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) s[r] = fmaf(s[r], a.scale, c);
+                    #pragma unroll
+                    for (int r = 0; r < 16; ++r) s[r] = fmaf(s[r], a.scale, last_bias);
                 } else {
-                    const float *tb = tb0 + (it & 1) * TAB - 32 * g;
+                    const float *tb = by_near ? near_s + kPad + wpos - k1 + ln - 4 * half
+                                              : tab + w * 32 + ln + kBK - 1 - 32 * g - 4 * half;
 #pragma unroll
                     for (int r = 0; r < 16; ++r) s[r] = fmaf(s[r], a.scale, tb[-(8 * (r / 4) + r % 4)]);
                     if constexpr (WILD) {
@@ -283,7 +294,7 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_bwd_q(const Args
                     }
                     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(lower), __float_as_uint(upper), false, false);
                     const float x = __uint_as_float(r[0]) + __uint_as_float(r[1]);  // distance D - 32 + lane
-                    add_by_bucket(sums[wave], x, btab[it & 1][w * 32 + 31 - 32 * g + lane], lane);
+                    add_by_bucket(sums[wave], x, by_near ? bnear_s[kPad + wpos - k1 - 32 + lane] : btab[w * 32 + 31 - 32 * g + lane], lane);
                 }
             }
         }
@@ -368,8 +379,9 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_bwd_q(const Args
 // key head, and which run of the queries (of all heads that share it) where they are split.
 //
 // FAR: the few first keys that every later query sees, and only the queries past the window: a key
-// block of its own would walk all queries of a long sequence after the others are done.  A workgroup
-// takes kFarChunk queries; the block that owns the keys adds their sums in order.
+// block of its own would walk all queries of a long sequence after the others are done (4 sequences of
+// up to 4096 under a window of 1024: 1367 us with that, 35 + 252 us as it is).  A workgroup takes one of
+// the forward's tiles of queries; the block that owns the keys adds their sums in order.
 template <int DP, int LP, int WY, int WX, int OCC, bool FAR>
 __global__ __launch_bounds__(WY * WX * 64, OCC) void k_seq_attn_bwd_kv(const Args a, const Grads gr) {
     constexpr int KT = WY * 32, STEPS = DP / 16, MB = DP / 32, THREADS = WY * WX * 64;
@@ -381,14 +393,15 @@ __global__ __launch_bounds__(WY * WX * 64, OCC) void k_seq_attn_bwd_kv(const Arg
     uint16_t *const Qs = tiles_s, *const Ds = tiles_s + TILE;
 
     const int slot = static_cast<int>(xcd_contiguous(blockIdx.x, gridDim.x));
-    const int b = FAR ? find_sequence(a, a.q_off, a.Nq, slot, kFarChunk) : find_sequence(a, a.kv_begin, a.Nkv, slot, KT);
+    if (FAR && slot >= slot_count(a.Nq, a.B, kQT)) return;
+    const int b = FAR ? min(max(gr.tiles[slot], 0), a.B - 1) : find_sequence(a, a.kv_begin, a.Nkv, slot, KT);
     const Span sp = span_of(a, b);
     int kvh, run = 0, k0, qlo, qhi;
     if constexpr (FAR) {
-        const int blocks = gr.far_rows / KT, c = slot - (static_cast<int>(sp.q0) / kFarChunk + b);
+        const int blocks = (gr.far_sinks + KT - 1) / KT, c = slot - (static_cast<int>(sp.q0) / kQT + b);
         kvh = blockIdx.y / blocks, k0 = blockIdx.y % blocks * KT;
-        qlo = max(c * kFarChunk, k0 + a.window - sp.shift);
-        qhi = min((c + 1) * kFarChunk, sp.qlen);
+        qlo = max(c * kQT, k0 + a.window - sp.shift);
+        qhi = min((c + 1) * kQT, sp.qlen);
         if (c < 0 || k0 >= sp.klen || qlo >= qhi) return;
     } else {
         kvh = blockIdx.y / gr.splits, run = blockIdx.y % gr.splits;
@@ -442,7 +455,7 @@ __global__ __launch_bounds__(WY * WX * 64, OCC) void k_seq_attn_bwd_kv(const Arg
         if (even(r0)) return;
         for (int i = tid; i < TAB - 1; i += THREADS) {
             int bucket;
-            float x = table_entry(a, bounds_s, bias_s[it / nq & 1], n0 + i, k0 < a.sinks, &bucket);
+            float x = bias_at(a, bounds_s, bias_s[it / nq & 1], n0 + i, k0 < a.sinks, &bucket);
             if (FAR && n0 + i < a.window) x = -kInf;
             tab[it & 1][i] = x;
         }
@@ -464,7 +477,13 @@ __global__ __launch_bounds__(WY * WX * 64, OCC) void k_seq_attn_bwd_kv(const Arg
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             odd |= only_finite(kf[s].w[e]) != kf[s].w[e] || only_finite(vf[s].w[e]) != vf[s].w[e];
-    const bool wild = __any(odd);  // a hidden key that is not finite keeps its gradients of zero
+    // An infinity or NaN in a key makes its gradients NaN, from hidden queries too (0 * NaN): right where
+    // a query sees it; where none does, the zeros are put in at the end.
+    const auto unseen = [&] {
+        const bool any = (__ballot(odd) >> ln & 0x100000001ull) != 0;
+        const int least = max(0, sp.shift - kl);  // distance to the first query that is not before the key
+        return any && (sp.qlen == 0 || (a.window && least >= a.window && kl >= max(a.sinks, gr.far_sinks)));
+    };
 
     f32x16 dk[MB], dv[MB];
 #pragma unroll
@@ -515,11 +534,6 @@ __global__ __launch_bounds__(WY * WX * 64, OCC) void k_seq_attn_bwd_kv(const Arg
                 const float *tb = tb0 + (it & 1) * TAB + 32 * g;
 #pragma unroll
                 for (int r = 0; r < 16; ++r) s[r] = fmaf(s[r], a.scale, tb[8 * (r / 4) + r % 4]);
-                if (wild) {
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        if (tb[8 * (r / 4) + r % 4] == -kInf) s[r] = -kInf;
-                }
                 if (k0 < a.sinks) {
 #pragma unroll
                     for (int r = 0; r < 16; ++r) {
@@ -537,9 +551,7 @@ __global__ __launch_bounds__(WY * WX * 64, OCC) void k_seq_attn_bwd_kv(const Arg
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     p[r] = __builtin_amdgcn_exp2f((s[4 * j + r] - l[r]) * kLog2e);
-                    float x = p[r] * (dp[4 * j + r] - e[r]);
-                    if (wild && p[r] == 0.f) x = 0.f;
-                    dp[4 * j + r] = x;
+                    dp[4 * j + r] = p[r] * (dp[4 * j + r] - e[r]);
                 }
                 pf[j / 2].w[j % 2 * 2] = pack_bf16(p[0], p[1]);
                 pf[j / 2].w[j % 2 * 2 + 1] = pack_bf16(p[2], p[3]);
@@ -583,7 +595,8 @@ __global__ __launch_bounds__(WY * WX * 64, OCC) void k_seq_attn_bwd_kv(const Arg
     }
     if (!live) return;
     if constexpr (FAR) {
-        float *const out = gr.far + ((static_cast<int64_t>(slot) * a.Hkv + kvh) * gr.far_rows + kl) * 2 * a.d;
+        if (kl >= a.sinks) return;
+        float *const out = gr.far + ((static_cast<int64_t>(slot) * a.Hkv + kvh) * gr.far_sinks + kl) * 2 * a.d;
 #pragma unroll
         for (int m = 0; m < MB; ++m)
 #pragma unroll
@@ -595,10 +608,10 @@ __global__ __launch_bounds__(WY * WX * 64, OCC) void k_seq_attn_bwd_kv(const Arg
             }
         return;
     }
-    if (k0 < gr.far_sinks && run == 0) {
-        const int past = max(0, k0 + a.window - sp.shift), base = static_cast<int>(sp.q0) / kFarChunk + b;
-        for (int c = past / kFarChunk; past < sp.qlen && c * kFarChunk < sp.qlen; ++c) {
-            const float *in = gr.far + ((static_cast<int64_t>(base + c) * a.Hkv + kvh) * gr.far_rows + kl) * 2 * a.d;
+    if (kl < gr.far_sinks && run == 0) {
+        const int past = max(0, k0 + a.window - sp.shift), base = static_cast<int>(sp.q0) / kQT + b;
+        for (int c = past / kQT; past < sp.qlen && c * kQT < sp.qlen; ++c) {
+            const float *in = gr.far + ((static_cast<int64_t>(base + c) * a.Hkv + kvh) * gr.far_sinks + kl) * 2 * a.d;
 #pragma unroll
             for (int m = 0; m < MB; ++m)
 #pragma unroll
@@ -612,6 +625,7 @@ __global__ __launch_bounds__(WY * WX * 64, OCC) void k_seq_attn_bwd_kv(const Arg
         }
     }
     const int64_t row = ((sp.k0 + kl) * a.Hkv + kvh) * static_cast<int64_t>(a.d), plane = a.Nkv * a.Hkv * a.d;
+    const bool clear = unseen();
 #pragma unroll
     for (int m = 0; m < MB; ++m)
 #pragma unroll
@@ -620,7 +634,7 @@ __global__ __launch_bounds__(WY * WX * 64, OCC) void k_seq_attn_bwd_kv(const Arg
             if (c >= a.d) continue;
             floatx4 x, y;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) x[r] = dk[m][4 * g + r] * a.scale, y[r] = dv[m][4 * g + r];
+            for (int r = 0; r < 4; ++r) x[r] = clear ? 0.f : dk[m][4 * g + r] * a.scale, y[r] = clear ? 0.f : dv[m][4 * g + r];
             if (gr.splits > 1) {
                 *(DLRM_GLOBAL floatx4 *)(gr.split + 2 * run * plane + row + c) = x;
                 *(DLRM_GLOBAL floatx4 *)(gr.split + (2 * run + 1) * plane + row + c) = y;
@@ -675,8 +689,8 @@ __global__ __launch_bounds__(1024) void k_seq_bias_sum(const float *partial, int
 
 // The workspace: delta, the partial dbias, the split and the far sums of dk and dv.
 struct Layout {
-    int64_t qslots, kslots, far_slots;
-    int splits, far_rows;
+    int64_t qslots, kslots;
+    int splits, far_sinks;
     size_t partial, split, far, bytes;
 };
 
@@ -690,25 +704,25 @@ Layout layout_of(const Args &a) {
     const int64_t blocks = l.kslots * a.Hkv, tiles = a.B ? a.group * (a.Nq / a.B / kBK) : 0;
     l.splits = 1;
     while (l.splits < 8 && blocks * l.splits < 512 && tiles >= 8 * l.splits) l.splits *= 2;
-    const int sinks = a.sinks <= kFarMost ? a.sinks : 0;
-    l.far_rows = (sinks + kKT - 1) / kKT * kKT;
-    l.far_slots = l.far_rows ? slot_count(a.Nq, a.B, kFarChunk) : 0;
+    size_t far = a.sinks <= kFarMost ? static_cast<size_t>(l.qslots) * a.Hkv * a.sinks * 2 * a.d * 4 : 0;
+    if (far > kFarBytes) far = 0;
+    l.far_sinks = far ? a.sinks : 0;
     l.partial = up(static_cast<size_t>(a.Nq) * a.Hq * 4);
     l.split = l.partial + up(static_cast<size_t>(l.qslots) * a.Hq * a.buckets * 4);
     l.far = l.split + (l.splits > 1 ? up(static_cast<size_t>(l.splits) * 2 * a.Nkv * a.Hkv * a.d * 4) : 0);
-    l.bytes = l.far + up(static_cast<size_t>(l.far_slots) * a.Hkv * l.far_rows * 2 * a.d * 4) + 256;
+    l.bytes = l.far + up(far) + 256;
     return l;
 }
 
-template <int DP, int LP, int WK, int WX, int O1, int O2>
+template <int DP, int LP, int WK, int WX, int O1, int O2, int NEAR>
 int launch(const Args &a, const Grads &g, const Layout &l, float *dbias, hipStream_t stream) {
     if (l.qslots > 0)
-        DLRM_LAUNCH("seq_attn_bwd_q", (k_seq_attn_bwd_q<DP, LP, 2, WK, O1>), dim3(round_up_xcd(l.qslots), a.Hq), dim3(128 * WK), 0,
+        DLRM_LAUNCH("seq_attn_bwd_q", (k_seq_attn_bwd_q<DP, LP, 2, WK, O1, NEAR>), dim3(round_up_xcd(l.qslots), a.Hq), dim3(128 * WK), 0,
                     stream, a, g);
     Args near = a;
-    if (l.far_rows) {
+    if (l.far_sinks && l.qslots > 0) {
         DLRM_LAUNCH("seq_attn_bwd_far", (k_seq_attn_bwd_kv<DP, LP, 2, WX, O2, true>),
-                    dim3(round_up_xcd(l.far_slots), a.Hkv * (l.far_rows / kKT)), dim3(128 * WX), 0, stream, a, g);
+                    dim3(round_up_xcd(l.qslots), a.Hkv * ((l.far_sinks + kKT - 1) / kKT)), dim3(128 * WX), 0, stream, a, g);
         near.sinks = 0;  // what is left of the first keys' queries is the window's
     }
     if (l.kslots > 0)
@@ -759,9 +773,9 @@ extern "C" int dlrm_seq_attn_bwd(const dlrm_seq_attn *desc, const uint16_t *dout
     g.dout = dout, g.o = o, g.lse = lse, g.tiles = tiles, g.dq = dq, g.dk = dk, g.dv = dv;
     g.delta = reinterpret_cast<float *>(ws), g.partial = reinterpret_cast<float *>(ws + l.partial);
     g.split = reinterpret_cast<float *>(ws + l.split), g.splits = l.splits;
-    g.far = reinterpret_cast<float *>(ws + l.far), g.far_rows = l.far_rows, g.far_sinks = l.far_rows ? a.sinks : 0;
+    g.far = reinterpret_cast<float *>(ws + l.far), g.far_sinks = l.far_sinks;
     hipStream_t stream = reinterpret_cast<hipStream_t>(stream_);
-    if (a.d <= 32) return launch<32, 32, 1, 1, 3, 2>(a, g, l, dbias, stream);
-    if (a.d <= 64) return launch<64, 64, 1, 1, 3, 2>(a, g, l, dbias, stream);
-    return launch<128, 128, 2, 2, 2, 2>(a, g, l, dbias, stream);
+    if (a.d <= 32) return launch<32, 32, 1, 1, 3, 2, 896>(a, g, l, dbias, stream);
+    if (a.d <= 64) return launch<64, 64, 1, 1, 3, 2, 384>(a, g, l, dbias, stream);
+    return launch<128, 128, 2, 2, 2, 2, 1280>(a, g, l, dbias, stream);
 }

@@ -66,13 +66,13 @@ namespace {
 // DP: the head's width rounded up (the products run over DP columns, those from d on are zeros);
 // LP: columns of a row in LDS.  WQ wavefronts of 32 queries each, by WK that share a tile's keys:
 // each then takes one of its two halves, and their results are joined at the end.
-template <int DP, int LP, int WQ, int WK, int OCC>
+template <int DP, int LP, int WQ, int WK, int OCC, int NEAR>
 __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a, uint16_t *o_out, float *lse_out,
                                                                     int32_t *tiles_out) {
     constexpr int QT = WQ * 32, STEPS = DP / 16, MB = DP / 32, THREADS = WQ * WK * 64;
     constexpr int TAB = QT + kBK, TILE = kBK * kPitch<LP>;
     __shared__ __attribute__((aligned(16))) uint16_t tiles_s[2 * TILE];
-    __shared__ float tab[2][TAB], bias_s[DLRM_SEQ_MAX_BUCKETS];
+    __shared__ float near_s[kPad + NEAR], tab[TAB], bias_s[DLRM_SEQ_MAX_BUCKETS];
     __shared__ int bounds_s[DLRM_SEQ_MAX_BUCKETS];
     uint16_t *const Ks = tiles_s, *const Vs = tiles_s + TILE;
 
@@ -112,12 +112,12 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a
         const int nearest = pmin - (k0 + kBK - 1);
         return nearest >= a.last && (!a.window || q0 + QT - 1 + sp.shift - k0 < a.window || k0 + kBK <= a.sinks);
     };
-    const auto table = [&](int it) {
-        const int k0 = key0(it), n0 = pmin - (k0 + kBK - 1);
-        if (even(k0)) return;
+    const auto close = [&](int k0) { return pmin - k0 + QT - 1 < NEAR && k0 >= a.sinks; };
+    const auto table = [&](int k0) {
+        if (even(k0) || close(k0)) return;
+        const int n0 = pmin - (k0 + kBK - 1);
         int bucket;
-        for (int i = tid; i < TAB - 1; i += THREADS)
-            tab[it & 1][i] = table_entry(a, bounds_s, bias_s, n0 + i, k0 < a.sinks, &bucket);
+        for (int i = tid; i < TAB - 1; i += THREADS) tab[i] = bias_at(a, bounds_s, bias_s, n0 + i, k0 < a.sinks, &bucket);
     };
 
     // the queries, each lane's column of the second operand
@@ -136,10 +136,17 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a
         bias_s[i] = a.bias[static_cast<int64_t>(h) * a.buckets + i];
     }
 
+    __syncthreads();
+    {
+        const int reach = n > 0 ? min(NEAR, pmin + QT - t0 * kBK) : 0;  // past the furthest but for first keys'
+        int bucket;
+        for (int i = tid; i < reach; i += THREADS) near_s[kPad + i] = bias_at(a, bounds_s, bias_s, i, false, &bucket);
+        for (int i = tid; i < kPad; i += THREADS) near_s[i] = -kInf;
+    }
+
     f32x16 o[MB];
     float top, sum;
     const uint16_t *const krow = Ks + row_base<LP>(ln, half), *const vcol = Vs + column_base<LP>(lane);
-    const float *const tb0 = tab[0] + w * 32 + ln + kBK - 1 - 4 * half;
     // One pass over the keys.  An infinity or NaN in a key would reach the queries that do not see it
     // (0 * NaN in a product): where a result is NaN, the block makes a second, WILD pass that keeps
     // the values apart.  What is finite pays nothing for it.
@@ -148,18 +155,14 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a
 #pragma unroll
         for (int m = 0; m < MB; ++m) o[m] = f32x16{};
         top = -kInf, sum = 0.f;
-        __syncthreads();
-        if (n > 0) table(0);
         for (int it = 0; it < n; ++it) {
             const int k0 = key0(it);
-            if (it > 0) __syncthreads();  // the tile before has been read
             load(it);
+            __syncthreads();  // the tile before has been read
+            table(k0);
             ks.store(Ks);
             vs.store(Vs);
             __syncthreads();
-            if (it + 1 < n) {
-                table(it + 1);
-            }
             const int wpos = pmin + w * 32;  // position of the wavefront's first query
             // 32 keys at a time: S, P and their operands for 64 would cost a wavefront a SIMD
 #pragma unroll 1
@@ -181,7 +184,9 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a
 #pragma unroll
                     for (int r = 0; r < 16; ++r) s[r] = fmaf(s[r], a.scale, c);
                 } else {
-                    const float *tb = tb0 + (it & 1) * TAB - 32 * g;
+                    // distance wpos + ln - k1 - 4 half - (key): entry 63 - that of tab's
+                    const float *tb = close(k0) ? near_s + kPad + wpos - k1 + ln - 4 * half
+                                                : tab + w * 32 + ln + kBK - 1 - 32 * g - 4 * half;
 #pragma unroll
                     for (int r = 0; r < 16; ++r) s[r] = fmaf(s[r], a.scale, tb[-(8 * (r / 4) + r % 4)]);
                     if constexpr (WILD) {  // NaN - infinity is no -infinity
@@ -201,15 +206,18 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a
                 float mx = s[0];
 #pragma unroll
                 for (int r = 1; r < 16; ++r) mx = fmaxf(mx, s[r]);
-                mx = fmaxf(max_halves(mx), top);
-                if (__any(mx > top)) {
-                    const float f = mx == -kInf ? 1.f : __builtin_amdgcn_exp2f((top - mx) * kLog2e);
+                mx = max_halves(mx);
+                // the reference is moved when the maximum is over it by 8 (P up to e^8, which bf16 and the
+                // fp32 sums bear): with 32 rows one of them has a new maximum nearly every time
+                const bool over = mx > top + 8.f;
+                if (__any(over)) {
+                    const float f = over ? __builtin_amdgcn_exp2f((top - mx) * kLog2e) : 1.f;
                     sum *= f;
 #pragma unroll
                     for (int m = 0; m < MB; ++m)
 #pragma unroll
                         for (int r = 0; r < 16; ++r) o[m][r] *= f;
-                    top = mx;
+                    top = over ? mx : top;
                 }
                 const float ref = top == -kInf ? 0.f : top;
                 if (__any(fabsf(ref) > kHuge && fabsf(ref) < kInf)) {
@@ -339,10 +347,10 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a
         }
 }
 
-template <int DP, int LP, int WQ, int WK, int OCC>
+template <int DP, int LP, int WQ, int WK, int OCC, int NEAR>
 int launch(const Args &a, uint16_t *o, float *lse, int32_t *tiles, hipStream_t stream) {
     const dim3 grid(round_up_xcd(slot_count(a.Nq, a.B, WQ * 32)), a.Hq);
-    DLRM_LAUNCH("seq_attn_fwd", (k_seq_attn_fwd<DP, LP, WQ, WK, OCC>), grid, dim3(WQ * WK * 64), 0, stream, a, o, lse, tiles);
+    DLRM_LAUNCH("seq_attn_fwd", (k_seq_attn_fwd<DP, LP, WQ, WK, OCC, NEAR>), grid, dim3(WQ * WK * 64), 0, stream, a, o, lse, tiles);
     return launch_status();
 }
 
@@ -365,7 +373,7 @@ extern "C" int dlrm_seq_attn_fwd(const dlrm_seq_attn *desc, uint16_t *o, float *
     if (a.Nq > 0 && (!o || !aligned(o, 16) || !aligned(lse, 4) || !aligned(tiles, 4))) return DLRM_ERR_INVALID_ARG;
     if (a.B == 0 || a.Nq == 0) return DLRM_OK;
     hipStream_t stream = reinterpret_cast<hipStream_t>(stream_);
-    if (a.d <= 32) return launch<32, 32, 2, 1, 4>(a, o, lse, tiles, stream);
-    if (a.d <= 64) return launch<64, 64, 2, 1, 4>(a, o, lse, tiles, stream);
-    return launch<128, 128, 2, 2, 2>(a, o, lse, tiles, stream);
+    if (a.d <= 32) return launch<32, 32, 2, 1, 4, 896>(a, o, lse, tiles, stream);
+    if (a.d <= 64) return launch<64, 64, 2, 1, 4, 640>(a, o, lse, tiles, stream);
+    return launch<128, 128, 2, 2, 2, 1280>(a, o, lse, tiles, stream);
 }
