@@ -165,6 +165,13 @@ def _need(t, name, dtype=None, shape=None, min_numel: Optional[int] = None) -> t
     return t
 
 
+def _is(t, name: str, dtype: torch.dtype, shape) -> torch.Tensor:
+    """_need for one type and shape, at half its cost where the tensor is right."""
+    if type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return t
+    return _need(t, name, dtype, shape)
+
+
 def _name(name) -> str:
     return name() if callable(name) else name
 
@@ -603,6 +610,7 @@ def dlrm_probe_gather(table: torch.Tensor, idx: torch.Tensor, sink: torch.Tensor
 # ---------------------------------------------------------------- dense layers (dlrm_mlp.h)
 
 _TORCH_CODE = {torch.float32: DLRM_F32, torch.bfloat16: DLRM_BF16}
+_NORM_CODE = {**_TORCH_CODE, torch.float8_e4m3fn: DLRM_F8_E4M3}
 
 
 def dlrm_linear_workspace_size(M: int, N: int, K: int) -> int:
@@ -775,6 +783,16 @@ def dlrm_seq_bucket_bounds(buckets: int, reach: int) -> List[int]:
     return out
 
 
+def _out(t, name: str, dtype: torch.dtype, shape, dev: torch.device) -> torch.Tensor:
+    """The caller's output tensor, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _is(t, name, dtype, shape)
+    if t.device != dev:
+        raise ValueError(f"all tensors must be on {dev}, found one on {t.device}")
+    return t
+
+
 def _head_rows(t, name: str, heads: Optional[int] = None, d: Optional[int] = None):
     """Checks [rows, heads, d] bf16 whose heads are packed and whose row and head strides are free (a
     part of a joint projection, for instance); returns (rows, heads, d, row stride, head stride)."""
@@ -875,17 +893,10 @@ def dlrm_seq_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offse
     begin, end = _kv_ranges(q_offsets if kv_offsets is None else kv_offsets, B)
     a, edges, dev, shape, _ = _seq_attn(q, k, v, q_offsets, begin, end, B, window, sinks, scale, bias, bounds)
     for_backward = for_backward or tiles is not None or lse is not None
-    out = _opt(out, "out", torch.bfloat16, shape)
+    out = _out(out, "out", torch.bfloat16, shape, dev)
     if for_backward:
-        n = int(lib().dlrm_seq_attn_tiles(B, shape[0]))
-        tiles, lse = _opt(tiles, "tiles", torch.int32, (n,)), _opt(lse, "lse", torch.float32, shape[:2])
-        _device(q, out, tiles, lse)
-        tiles = torch.empty(n, dtype=torch.int32, device=dev) if tiles is None else tiles
-        lse = torch.empty(shape[:2], dtype=torch.float32, device=dev) if lse is None else lse
-    elif out is not None:
-        _device(q, out)
-    if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        tiles = _out(tiles, "tiles", torch.int32, (lib().dlrm_seq_attn_tiles(B, shape[0]),), dev)
+        lse = _out(lse, "lse", torch.float32, shape[:2], dev)
     _check(lib().dlrm_seq_attn_fwd(a, _ptr(out), _ptr(lse), _ptr(tiles), _stream(dev)), "dlrm_seq_attn_fwd")
     return (out, tiles, lse) if for_backward else out
 
@@ -906,22 +917,18 @@ def dlrm_seq_attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: t
     begin, end = _kv_ranges(q_offsets if kv_offsets is None else kv_offsets, B)
     a, edges, dev, qs, _ = _seq_attn(q, k, v, q_offsets, begin, end, B, window, sinks, scale, bias, bounds)
     ks = tuple(k.shape)
-    _need(dout, "dout", torch.bfloat16, qs)
-    _need(o, "o", torch.bfloat16, qs)
-    _need(tiles, "tiles", torch.int32, (int(lib().dlrm_seq_attn_tiles(B, qs[0])),))
-    _need(lse, "lse", torch.float32, qs[:2])
-    dq, dk, dv = (_opt(t, name, torch.bfloat16, s) for t, name, s in ((dq, "dq", qs), (dk, "dk", ks), (dv, "dv", ks)))
+    bf = torch.bfloat16
+    _is(dout, "dout", bf, qs)
+    _is(o, "o", bf, qs)
+    _is(tiles, "tiles", torch.int32, (lib().dlrm_seq_attn_tiles(B, qs[0]),))
+    _is(lse, "lse", torch.float32, qs[:2])
+    _device(q, dout, o, tiles, lse)
     if bias is None and dbias is not None:
         raise ValueError("dbias without a bias")
-    dbias = _opt(dbias, "dbias", torch.float32, None if bias is None else tuple(bias.shape))
-    _device(q, dout, o, tiles, lse, dq, dk, dv, dbias)
-    bf = dict(dtype=torch.bfloat16, device=dev)
-    dq = torch.empty(qs, **bf) if dq is None else dq
-    dk = torch.empty(ks, **bf) if dk is None else dk
-    dv = torch.empty(ks, **bf) if dv is None else dv
-    if bias is not None and dbias is None:
-        dbias = torch.empty_like(bias)
-    ws = _ws(int(lib().dlrm_seq_attn_bwd_workspace_size(a)), dev, workspace)
+    dq, dk, dv = _out(dq, "dq", bf, qs, dev), _out(dk, "dk", bf, ks, dev), _out(dv, "dv", bf, ks, dev)
+    if bias is not None:
+        dbias = _out(dbias, "dbias", torch.float32, tuple(bias.shape), dev)
+    ws = _ws(lib().dlrm_seq_attn_bwd_workspace_size(a), dev, workspace)
     _check(lib().dlrm_seq_attn_bwd(a, _ptr(dout), _ptr(o), _ptr(lse), _ptr(tiles), _ptr(dq), _ptr(dk), _ptr(dv),
                                    _ptr(dbias), _ptr(ws), ws.numel(), _stream(dev)), "dlrm_seq_attn_bwd")
     return dq, dk, dv, dbias
@@ -948,11 +955,7 @@ def dlrm_seq_attn_decode(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_b
     longest = k.shape[0] if max_kv_len is None else int(max_kv_len)
     if longest < 0:
         raise ValueError(f"max_kv_len must not be negative, got {longest}")
-    if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    else:
-        _need(out, "out", torch.bfloat16, shape)
-        _device(q, out)
+    out = _out(out, "out", torch.bfloat16, shape, dev)
     ws = _ws(lib().dlrm_seq_attn_decode_workspace_size(B, shape[1], k.shape[1], shape[2], window, sinks, longest), dev, workspace)
     _check(lib().dlrm_seq_attn_decode(a, longest, _ptr(out), _ptr(ws), ws.numel(), _stream(dev)),
            "dlrm_seq_attn_decode")
@@ -995,25 +998,22 @@ def dlrm_add_rmsnorm_fwd(x: torch.Tensor, residual: Optional[torch.Tensor], w: t
     _mat(x, "x", (torch.float32, torch.bfloat16))
     M, D = x.shape
     rt = residual.dtype if isinstance(residual, torch.Tensor) else res_dtype or x.dtype
-    _opt(residual, "residual", (torch.float32, torch.bfloat16), (M, D))
+    if residual is not None:
+        _is(residual, "residual", rt, (M, D))
     if rt not in _TORCH_CODE:
         raise ValueError(f"res_dtype must be float32 or bfloat16, got {rt}")
-    _need(w, "w", torch.float32, (D,))
+    _is(w, "w", torch.float32, (D,))
     yt = y_dtype if y is None else y.dtype
-    codes = {**_TORCH_CODE, torch.float8_e4m3fn: DLRM_F8_E4M3}
-    if yt not in codes:
+    if yt not in _NORM_CODE:
         raise ValueError(f"y_dtype must be float32, bfloat16 or float8_e4m3fn, got {yt}")
-    s, y = _opt(s, "s", rt, (M, D)), _opt(y, "y", yt, (M, D))
-    rstd, y_scale = _opt(rstd, "rstd", torch.float32, (M,)), _opt(y_scale, "y_scale", torch.float32, (M,))
     spec = _drop_spec(p, seed, offset, offset_dev)
-    dev = _device(x, residual, w, s, y, rstd, y_scale, offset_dev)
-    s = torch.empty((M, D), dtype=rt, device=dev) if s is None else s
-    y = torch.empty((M, D), dtype=yt, device=dev) if y is None else y
-    rstd = torch.empty(M, dtype=torch.float32, device=dev) if rstd is None else rstd
-    if yt == torch.float8_e4m3fn and y_scale is None:
-        y_scale = torch.empty(M, dtype=torch.float32, device=dev)
+    dev = _device(x, residual, w, offset_dev)
+    s, y = _out(s, "s", rt, (M, D), dev), _out(y, "y", yt, (M, D), dev)
+    rstd = _out(rstd, "rstd", torch.float32, (M,), dev)
+    if yt == torch.float8_e4m3fn:
+        y_scale = _out(y_scale, "y_scale", torch.float32, (M,), dev)
     _check(lib().dlrm_add_rmsnorm_fwd(_ptr(x), _TORCH_CODE[x.dtype], _ptr(residual), _TORCH_CODE[rt], _ptr(w), float(eps),
-                                      ctypes.byref(spec), M, D, _ptr(s), _ptr(y), codes[yt], _ptr(y_scale), _ptr(rstd),
+                                      ctypes.byref(spec), M, D, _ptr(s), _ptr(y), _NORM_CODE[yt], _ptr(y_scale), _ptr(rstd),
                                       _stream(dev)), "dlrm_add_rmsnorm_fwd")
     return s, y, rstd, (y_scale if yt == torch.float8_e4m3fn else None)
 
@@ -1033,20 +1033,18 @@ def dlrm_add_rmsnorm_bwd(dy: torch.Tensor, ds: Optional[torch.Tensor], s: torch.
     _mat(s, "s", (torch.float32, torch.bfloat16))
     M, D = s.shape
     _need(dy, "dy", (torch.float32, torch.bfloat16), (M, D))
-    _opt(ds, "ds", s.dtype, (M, D))
-    _need(w, "w", torch.float32, (D,))
-    _need(rstd, "rstd", torch.float32, (M,))
+    if ds is not None:
+        _is(ds, "ds", s.dtype, (M, D))
+    _is(w, "w", torch.float32, (D,))
+    _is(rstd, "rstd", torch.float32, (M,))
     xt = x_dtype if dx is None else dx.dtype
     if xt not in _TORCH_CODE:
         raise ValueError(f"x_dtype must be float32 or bfloat16, got {xt}")
-    dx, dresidual = _opt(dx, "dx", xt, (M, D)), _opt(dresidual, "dresidual", s.dtype, (M, D))
-    dw = _opt(dw, "dw", torch.float32, (D,))
     spec = _drop_spec(p, seed, offset, offset_dev)
-    dev = _device(dy, ds, s, w, rstd, dx, dresidual, dw, offset_dev)
-    dx = torch.empty((M, D), dtype=xt, device=dev) if dx is None else dx
-    dresidual = torch.empty_like(s) if dresidual is None else dresidual
-    dw = torch.empty(D, dtype=torch.float32, device=dev) if dw is None else dw
-    ws = _ws(dlrm_add_rmsnorm_bwd_workspace_size(M, D), dev, workspace)
+    dev = _device(dy, ds, s, w, rstd, offset_dev)
+    dx, dresidual = _out(dx, "dx", xt, (M, D), dev), _out(dresidual, "dresidual", s.dtype, (M, D), dev)
+    dw = _out(dw, "dw", torch.float32, (D,), dev)
+    ws = _ws(lib().dlrm_add_rmsnorm_bwd_workspace_size(M, D), dev, workspace)
     _check(lib().dlrm_add_rmsnorm_bwd(_ptr(dy), _TORCH_CODE[dy.dtype], _ptr(ds), _ptr(s), _TORCH_CODE[s.dtype], _ptr(w),
                                       _ptr(rstd), ctypes.byref(spec), M, D, _ptr(dx), _TORCH_CODE[xt], _ptr(dresidual),
                                       _ptr(dw), _ptr(ws), ws.numel(), _stream(dev)), "dlrm_add_rmsnorm_bwd")

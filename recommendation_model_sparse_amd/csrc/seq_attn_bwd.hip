@@ -294,7 +294,9 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_bwd_q(const Args
                     }
                     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(lower), __float_as_uint(upper), false, false);
                     const float x = __uint_as_float(r[0]) + __uint_as_float(r[1]);  // distance D - 32 + lane
-                    add_by_bucket(sums[wave], x, by_near ? bnear_s[kPad + wpos - k1 - 32 + lane] : btab[w * 32 + 31 - 32 * g + lane], lane);
+                    // (no pair is at distance D - 32: lane 0 adds a zero, and may stay inside the tile's table)
+                    add_by_bucket(sums[wave], x,
+                                  by_near ? bnear_s[kPad + wpos - k1 - 32 + lane] : btab[max(w * 32 + 31 - 32 * g + lane, 0)], lane);
                 }
             }
         }
