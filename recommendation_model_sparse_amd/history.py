@@ -16,7 +16,7 @@ layers' weights bf16 with fp32 masters (SGD), the table is updated by row-wise A
 jagged: event rows laid end to end, with offsets [B + 1].
 
 Serving keeps each layer's keys and values in a region of `capacity` rows a user: `prefill` encodes the
-events since the last visit against them, `append` one new event a user, and `users_8bit` gives the
+events since the last visit against them, `append` one new event a user, and `append(eight_bit=True)` gives the
 users' vectors as 8-bit rows with scales for a store of candidates.
 """
 from __future__ import annotations
