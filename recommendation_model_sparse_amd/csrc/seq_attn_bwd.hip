@@ -380,11 +380,16 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_bwd_q(const Args
 // WY wavefronts of 32 keys, by WX that take one half each of a tile's 64 queries.  blockIdx.y: the
 // key head, and which run of the queries (of all heads that share it) where they are split.
 //
+// OWN: the block's values are read from LDS at every step instead of kept in registers: at heads of 128
+// 47 fewer registers spill (252 -> 224 us on 4 sequences of 2000 to 4096, 8 heads over 2; the keys in
+// LDS too: 228), at heads of 64 a third wavefront fits a SIMD (114 -> 110 us on 1024 sequences of 16
+// to 512, 2 heads).  Heads of 32 fit as they are.
+//
 // FAR: the few first keys that every later query sees, and only the queries past the window: a key
 // block of its own would walk all queries of a long sequence after the others are done (4 sequences of
 // up to 4096 under a window of 1024: 1367 us with that, 35 + 252 us as it is).  A workgroup takes one of
 // the forward's tiles of queries; the block that owns the keys adds their sums in order.
-template <int DP, int LP, int WY, int WX, int OCC, bool FAR>
+template <int DP, int LP, int WY, int WX, int OCC, bool OWN, bool FAR>
 __global__ __launch_bounds__(WY * WX * 64, OCC) void k_seq_attn_bwd_kv(const Args a, const Grads gr) {
     constexpr int KT = WY * 32, STEPS = DP / 16, MB = DP / 32, THREADS = WY * WX * 64;
     constexpr int TAB = KT + kBK, TILE = kBK * kPitch<LP>;
@@ -392,6 +397,7 @@ __global__ __launch_bounds__(WY * WX * 64, OCC) void k_seq_attn_bwd_kv(const Arg
     __shared__ __attribute__((aligned(16))) float lse_s[kBK], delta_s[kBK];
     __shared__ float tab[2][TAB], bias_s[2][DLRM_SEQ_MAX_BUCKETS];
     __shared__ int bounds_s[DLRM_SEQ_MAX_BUCKETS];
+    __shared__ __attribute__((aligned(16))) uint16_t own_s[OWN ? KT * kPitch<LP> : 8];
     uint16_t *const Qs = tiles_s, *const Ds = tiles_s + TILE;
 
     const int slot = static_cast<int>(xcd_contiguous(blockIdx.x, gridDim.x));
@@ -487,6 +493,15 @@ __global__ __launch_bounds__(WY * WX * 64, OCC) void k_seq_attn_bwd_kv(const Arg
         return any && (sp.qlen == 0 || (a.window && least >= a.window && kl >= max(a.sinks, gr.far_sinks)));
     };
 
+    const uint16_t *const own_row = own_s + w * 32 * kPitch<LP> + row_base<LP>(ln, half);
+    if constexpr (OWN) {  // the barrier before the first table orders it
+        uint16_t *const to = own_s + w * 32 * kPitch<LP> + row_base<LP>(ln, half);
+        if (wx == 0) {
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) *reinterpret_cast<u32x4 *>(to + 16 * s) = vf[s].q;
+        }
+    }
+
     f32x16 dk[MB], dv[MB];
 #pragma unroll
     for (int m = 0; m < MB; ++m) dk[m] = dv[m] = f32x16{};
@@ -522,11 +537,12 @@ __global__ __launch_bounds__(WY * WX * 64, OCC) void k_seq_attn_bwd_kv(const Arg
             f32x16 s = f32x16{}, dp = f32x16{};
 #pragma unroll
             for (int i = 0; i < STEPS; ++i) {
-                Frag q, d;
+                Frag q, d, v = vf[i];
+                if constexpr (OWN) read_row(v, own_row, i);
                 read_row(q, qt + rows, i);
                 s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(q.b, kf[i].b, s, 0, 0, 0);
                 read_row(d, dt + rows, i);
-                dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(d.b, vf[i].b, dp, 0, 0, 0);
+                dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(d.b, v.b, dp, 0, 0, 0);
             }
             // register r: query 8 (r / 4) + 4 half + r % 4
             if (flat) {
@@ -716,19 +732,19 @@ Layout layout_of(const Args &a) {
     return l;
 }
 
-template <int DP, int LP, int WK, int WX, int O1, int O2, int NEAR>
+template <int DP, int LP, int WK, int WX, int O1, int O2, bool OWN, int NEAR>
 int launch(const Args &a, const Grads &g, const Layout &l, float *dbias, hipStream_t stream) {
     if (l.qslots > 0)
         DLRM_LAUNCH("seq_attn_bwd_q", (k_seq_attn_bwd_q<DP, LP, 2, WK, O1, NEAR>), dim3(round_up_xcd(l.qslots), a.Hq), dim3(128 * WK), 0,
                     stream, a, g);
     Args near = a;
     if (l.far_sinks && l.qslots > 0) {
-        DLRM_LAUNCH("seq_attn_bwd_far", (k_seq_attn_bwd_kv<DP, LP, 2, WX, O2, true>),
+        DLRM_LAUNCH("seq_attn_bwd_far", (k_seq_attn_bwd_kv<DP, LP, 2, WX, O2, OWN, true>),
                     dim3(round_up_xcd(l.qslots), a.Hkv * ((l.far_sinks + kKT - 1) / kKT)), dim3(128 * WX), 0, stream, a, g);
         near.sinks = 0;  // what is left of the first keys' queries is the window's
     }
     if (l.kslots > 0)
-        DLRM_LAUNCH("seq_attn_bwd_kv", (k_seq_attn_bwd_kv<DP, LP, 2, WX, O2, false>), dim3(round_up_xcd(l.kslots), a.Hkv * l.splits),
+        DLRM_LAUNCH("seq_attn_bwd_kv", (k_seq_attn_bwd_kv<DP, LP, 2, WX, O2, OWN, false>), dim3(round_up_xcd(l.kslots), a.Hkv * l.splits),
                     dim3(128 * WX), 0, stream, near, g);
     const int64_t plane = a.Nkv * a.Hkv * a.d;
     if (l.splits > 1)
@@ -777,7 +793,7 @@ extern "C" int dlrm_seq_attn_bwd(const dlrm_seq_attn *desc, const uint16_t *dout
     g.split = reinterpret_cast<float *>(ws + l.split), g.splits = l.splits;
     g.far = reinterpret_cast<float *>(ws + l.far), g.far_sinks = l.far_sinks;
     hipStream_t stream = reinterpret_cast<hipStream_t>(stream_);
-    if (a.d <= 32) return launch<32, 32, 1, 1, 3, 2, 896>(a, g, l, dbias, stream);
-    if (a.d <= 64) return launch<64, 64, 1, 1, 3, 2, 384>(a, g, l, dbias, stream);
-    return launch<128, 128, 2, 2, 2, 2, 1280>(a, g, l, dbias, stream);
+    if (a.d <= 32) return launch<32, 32, 1, 1, 3, 2, false, 896>(a, g, l, dbias, stream);
+    if (a.d <= 64) return launch<64, 64, 1, 1, 3, 3, true, 384>(a, g, l, dbias, stream);
+    return launch<128, 128, 2, 2, 2, 2, true, 1280>(a, g, l, dbias, stream);
 }
