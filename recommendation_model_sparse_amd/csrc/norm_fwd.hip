@@ -73,14 +73,14 @@ __global__ __launch_bounds__(256) void k_add_rmsnorm_fwd(const void *x, const vo
     }
     if constexpr (Size<Y>::bytes == 1) {
         most = over_row<L>(most, part, Max());
-        const float f = most == 0.f ? 1.f : 448.f / most;
+        const float f = most == 0.f ? 1.f : 448.f / most;  // infinite for a row below 1.3e-36
         if (lane == 0) y_scale[row] = most == 0.f ? 1.f : most / 448.f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int c = column<L, N, V>(i);
             if (c >= D) continue;
 #pragma unroll
-            for (int j = 0; j < V; ++j) h[i * V + j] *= f;
+            for (int j = 0; j < V; ++j) h[i * V + j] = f <= 3.4e38f ? h[i * V + j] * f : h[i * V + j] / most * 448.f;
             store<F8, V>(y, row * D + c, h + i * V);
         }
     }

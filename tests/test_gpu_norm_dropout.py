@@ -237,3 +237,21 @@ def test_refusals():
                 dict(dx=x[:1])):
         with pytest.raises(ValueError):
             dlrm_add_rmsnorm_bwd(**{**dict(dy=x, ds=x, s=s, w=w, rstd=rstd), **bad})
+
+
+@pytest.mark.parametrize("D", [8, 100, 128, 4096])
+@pytest.mark.parametrize("size", [1e-36, 1e-37])
+def test_norm_8bit_rows_near_the_smallest_numbers(D, size):
+    """448 / max|y| is past the largest fp32 here; the row's zeros stay zeros.  The scale itself, below the
+    smallest normal number, has 2^-17 of room at 1e-37 / 448."""
+    rng = rng_of("tiny", D, size)
+    x = rng.standard_normal((5, D)).astype(np.float32)
+    x[:, ::3] = 0
+    w = np.full(D, size, np.float32)
+    say(f"[norm8 tiny] D={D} size={size}")
+    _, y, _, scale = dlrm_add_rmsnorm_fwd(to_dev(x), None, to_dev(w), 1e-6, y_dtype=E)
+    x64 = x.astype(np.float64)
+    ref = x64 / np.sqrt((x64 ** 2).mean(1, keepdims=True) + 1e-6) * w.astype(np.float64)
+    got, sc = host(y) * host(scale).reshape(-1, 1), np.abs(ref).max(1, keepdims=True) / 448
+    assert np.isfinite(got).all() and (got[:, ::3] == 0).all()
+    assert (np.abs(got - ref) <= (2.0 ** -4 + 2.0 ** -15) * np.abs(ref) + 2.0 ** -10 * sc).all()
