@@ -59,7 +59,9 @@ enum { DLRM_F8_E4M3 = 2 };
  *   bias       [Hq][buckets] fp32, or NULL: no bias;  bounds (host) [buckets], bounds[0] == 0,
  *              strictly increasing: the first distance of each bucket, the last bucket open
  *   Limits: d % 8 == 0, 8 <= d <= 128; 1 <= Hq <= 4096; B < 2^24; Nq, Nkv < 2^31; row strides
- *   < 2^24 elements; a sequence < 2^30 rows; 1 <= buckets <= DLRM_SEQ_MAX_BUCKETS.
+ *   < 2^24 elements; a sequence < 2^30 rows; 1 <= buckets <= DLRM_SEQ_MAX_BUCKETS; Nq / 64 + B and
+ *   Nkv / 64 + B below 2^25 (2^24 for d > 64) in the forward and backward, B * Hkv times the 16s of
+ *   query heads that share one below 2^24 in the form for one event.
  */
 typedef struct {
     int64_t B, Nq, Nkv;

@@ -59,6 +59,9 @@ __device__ __forceinline__ uint32_t keep_bits(const Drop &d, uint64_t offset, ui
 
 __device__ __forceinline__ uint64_t base_offset(const Drop &d) { return d.offset + (d.offset_dev ? *d.offset_dev : 0); }
 
+// Workgroups of 256 in a launch, which holds fewer than 2^32 work-items; more rows are several launches.
+constexpr int64_t kMostBlocks = (int64_t(1) << 24) - 1;
+
 // ---------------------------------------------------------------- typed loads and stores
 
 struct F32 {};

@@ -4,6 +4,8 @@
 //
 // Bound by reading and writing each row once: a row stays in the registers of 16, 32, 64 or 256
 // lanes between its sum and its use, and the dropout factors m are made where they are applied.
+#include <algorithm>
+
 #include "norm.h"
 
 namespace dlrm {
@@ -12,12 +14,13 @@ namespace {
 // One row by L lanes, each with N pieces of V elements (columns: column<L, N, V>).
 template <typename X, typename R, typename Y, int L, int N, int V, bool DROP>
 __global__ __launch_bounds__(256) void k_add_rmsnorm_fwd(const void *x, const void *res, const float *w, float eps, Drop drop,
-                                                         int64_t M, int D, void *s, void *y, float *y_scale, float *rstd) {
+                                                         int64_t row0, int64_t M, int D, void *s, void *y, float *y_scale,
+                                                         float *rstd) {
     constexpr int LW = L < 64 ? L : 64;
     __shared__ float part[4];
     __shared__ typename Keep<LW, V == 1 ? N : 8, V>::Bytes bytes;
     const int lane = threadIdx.x % L;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * (256 / L) + threadIdx.x / L;
+    const int64_t row = row0 + static_cast<int64_t>(blockIdx.x) * (256 / L) + threadIdx.x / L;
     if (row >= M) return;  // L == 256: the whole workgroup
     const uint64_t offset = DROP ? base_offset(drop) : 0;
     Keep<LW, V == 1 ? N : 8, V> keep;
@@ -87,8 +90,8 @@ __global__ __launch_bounds__(256) void k_add_rmsnorm_fwd(const void *x, const vo
 }
 
 template <typename T>
-__global__ __launch_bounds__(256) void k_dropout(const void *x, int64_t n, Drop drop, void *y) {
-    const int64_t group = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, e = group * 8;
+__global__ __launch_bounds__(256) void k_dropout(const void *x, int64_t group0, int64_t n, Drop drop, void *y) {
+    const int64_t group = group0 + static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, e = group * 8;
     if (e >= n) return;
     const uint32_t bits = keep_bits(drop, base_offset(drop), static_cast<uint64_t>(group));
     if (e + 8 <= n) {
@@ -124,13 +127,16 @@ struct Fwd {
 
 template <typename X, typename R, typename Y, int L, int N, int V>
 void Fwd::run(const Fwd &f) {
-    const dim3 grid(static_cast<uint32_t>((f.M + 256 / L - 1) / (256 / L)));
-    if (f.drop.limit)
-        DLRM_LAUNCH("add_rmsnorm_fwd", (k_add_rmsnorm_fwd<X, R, Y, L, N, V, true>), grid, dim3(256), 0, f.stream, f.x, f.res, f.w,
-                    f.eps, f.drop, f.M, f.D, f.s, f.y, f.y_scale, f.rstd);
-    else
-        DLRM_LAUNCH("add_rmsnorm_fwd", (k_add_rmsnorm_fwd<X, R, Y, L, N, V, false>), grid, dim3(256), 0, f.stream, f.x, f.res, f.w,
-                    f.eps, f.drop, f.M, f.D, f.s, f.y, f.y_scale, f.rstd);
+    constexpr int64_t most = kMostBlocks * (256 / L);
+    for (int64_t row0 = 0; row0 < f.M; row0 += most) {
+        const dim3 grid(static_cast<uint32_t>((std::min(f.M - row0, most) + 256 / L - 1) / (256 / L)));
+        if (f.drop.limit)
+            DLRM_LAUNCH("add_rmsnorm_fwd", (k_add_rmsnorm_fwd<X, R, Y, L, N, V, true>), grid, dim3(256), 0, f.stream, f.x, f.res,
+                        f.w, f.eps, f.drop, row0, f.M, f.D, f.s, f.y, f.y_scale, f.rstd);
+        else
+            DLRM_LAUNCH("add_rmsnorm_fwd", (k_add_rmsnorm_fwd<X, R, Y, L, N, V, false>), grid, dim3(256), 0, f.stream, f.x, f.res,
+                        f.w, f.eps, f.drop, row0, f.M, f.D, f.s, f.y, f.y_scale, f.rstd);
+    }
 }
 
 }  // namespace
@@ -146,11 +152,14 @@ extern "C" int dlrm_dropout(const void *x, int32_t dtype, int64_t n, const dlrm_
     if (!x || !y || !aligned(x, 16) || !aligned(y, 16)) return DLRM_ERR_INVALID_ARG;
     if (!drop.limit) drop.scale = 1.f;
     hipStream_t stream = reinterpret_cast<hipStream_t>(stream_);
-    const dim3 grid(static_cast<uint32_t>(((n + 7) / 8 + 255) / 256));
-    if (dtype == DLRM_F32)
-        DLRM_LAUNCH("dropout", k_dropout<F32>, grid, dim3(256), 0, stream, x, n, drop, y);
-    else
-        DLRM_LAUNCH("dropout", k_dropout<BF16>, grid, dim3(256), 0, stream, x, n, drop, y);
+    const int64_t groups = (n + 7) / 8, most = kMostBlocks * 256;
+    for (int64_t g = 0; g < groups; g += most) {
+        const dim3 grid(static_cast<uint32_t>((std::min(groups - g, most) + 255) / 256));
+        if (dtype == DLRM_F32)
+            DLRM_LAUNCH("dropout", k_dropout<F32>, grid, dim3(256), 0, stream, x, g, n, drop, y);
+        else
+            DLRM_LAUNCH("dropout", k_dropout<BF16>, grid, dim3(256), 0, stream, x, g, n, drop, y);
+    }
     return launch_status();
 }
 

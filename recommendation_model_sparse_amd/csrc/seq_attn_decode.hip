@@ -296,7 +296,7 @@ int launch(const Args &a, const Split &sp, uint16_t *o, void *ws, hipStream_t st
     const int splits = sp.runs;
     const int head_groups = (a.group + kHeads - 1) / kHeads;
     const int64_t rows = static_cast<int64_t>(a.B) * a.Hq, blocks = static_cast<int64_t>(a.B) * a.Hkv * head_groups;
-    if (blocks >= (int64_t(1) << 31)) return DLRM_ERR_UNSUPPORTED;
+    if (blocks >= (int64_t(1) << 24)) return DLRM_ERR_UNSUPPORTED;  // a launch holds fewer than 2^32 work-items
     float *part = static_cast<float *>(ws);
     float2 *ml = reinterpret_cast<float2 *>(part ? part + rows * splits * a.d : nullptr);
     // Many sequences: the first runs of all start first, as every one of them has keys; the runs that only

@@ -30,6 +30,10 @@ int check_attn(const dlrm_seq_attn *a, bool need_q_offsets, Args *out) {
     }
     if (a->d % 8 != 0 || a->d > 128 || a->Hq > 4096 || a->B >= (1 << 24)) return DLRM_ERR_UNSUPPORTED;
     if (a->Nq >= (int64_t(1) << 31) || a->Nkv >= (int64_t(1) << 31)) return DLRM_ERR_UNSUPPORTED;
+    if (need_q_offsets) {  // a launch holds fewer than 2^32 work-items
+        const int64_t most = (int64_t(1) << 32) / (a->d <= 64 ? 128 : 256) - kNumXcd;
+        if (slot_count(a->Nq > a->Nkv ? a->Nq : a->Nkv, a->B, kQT) > most) return DLRM_ERR_UNSUPPORTED;
+    }
     const uintptr_t ib = a->index_type == DLRM_INDEX_I32 ? 4 : 8;
     if (a->B > 0) {
         if (!a->kv_begin || !a->kv_end || !aligned(a->kv_begin, ib) || !aligned(a->kv_end, ib)) return DLRM_ERR_INVALID_ARG;

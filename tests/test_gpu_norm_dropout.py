@@ -255,3 +255,44 @@ def test_norm_8bit_rows_near_the_smallest_numbers(D, size):
     got, sc = host(y) * host(scale).reshape(-1, 1), np.abs(ref).max(1, keepdims=True) / 448
     assert np.isfinite(got).all() and (got[:, ::3] == 0).all()
     assert (np.abs(got - ref) <= (2.0 ** -4 + 2.0 ** -15) * np.abs(ref) + 2.0 ** -10 * sc).all()
+
+
+def need(gib):
+    if torch.cuda.mem_get_info()[0] < gib << 30:
+        pytest.skip(f"{gib} GiB of free memory")
+
+
+def test_dropout_past_one_launch():
+    """2^35 elements are 2^32 work-items: the last ones equal a call on them alone, moved by their offset."""
+    need(140)
+    n, tail = (1 << 35) + 40005, 1 << 13
+    say(f"[drop] n={n}")
+    x = torch.empty(n, dtype=H, device=DEV).fill_(1)
+    y = dlrm_dropout(x, 0.25, 77, 5, out=x)
+    first = n // 8 * 8 - tail
+    want = dlrm_dropout(torch.ones(n - first, dtype=H, device=DEV), 0.25, 77, 5 + first // 8)
+    assert torch.equal(y[first:], want) and torch.equal(y[:tail], dlrm_dropout(torch.ones(tail, dtype=H, device=DEV), 0.25, 77, 5))
+    across = ((1 << 24) - 1) * 256 * 8
+    want = dlrm_dropout(torch.ones(2 * tail, dtype=H, device=DEV), 0.25, 77, 5 + (across - tail) // 8)
+    seam = y[across - tail:across + tail].clone()
+    del x, y
+    torch.cuda.empty_cache()
+    assert seam.shape == want.shape and torch.equal(seam, want)
+
+
+def test_norm_past_one_launch():
+    """2^28 rows by 16 lanes each are 2^32 work-items."""
+    need(40)
+    M, D = (1 << 28) + 1037, 8
+    say(f"[norm] M={M} D={D}")
+    rng = rng_of("norm-launch")
+    w_d, _ = draw(rng, F, D)
+    x = torch.empty(M, D, dtype=H, device=DEV).fill_(0.5)
+    some, _ = draw(rng, H, 400, D)
+    x[-400:] = some
+    at = ((1 << 24) - 1) * 16 - 200  # the first launch's end
+    x[at:at + 400] = some
+    _, y, rstd, _ = dlrm_add_rmsnorm_fwd(x, None, w_d, 1e-5)
+    _, y1, rstd1, _ = dlrm_add_rmsnorm_fwd(some, None, w_d, 1e-5)
+    for a in (at, M - 400):
+        assert torch.equal(y[a:a + 400], y1) and torch.equal(rstd[a:a + 400], rstd1)

@@ -139,3 +139,16 @@ def test_wrappers_refuse_cpu_tensors():
     for bad in ((0, 5), (129, 5)):
         with pytest.raises(ValueError):
             dlrm_seq_bucket_bounds(*bad)
+
+
+@pytest.mark.parametrize("d,ok,over", [(32, (1 << 31) - 64 * 64, (1 << 31) - 1), (128, (1 << 30) - 64 * 64, 1 << 30)])
+def test_attention_past_one_launch_rejected(L, d, ok, over):
+    """Tiles by threads reach 2^32 work-items; the sizes just below pass this check and fail a later one."""
+    heads = dict(d=d, q_row=4 * d, q_head=d, k_row=2 * d, k_head=d, v_row=2 * d, v_head=d)
+    for n, want in ((ok, INVALID), (over, UNSUPPORTED)):
+        a = attn(Nq=n, q=None, **heads)
+        assert L.dlrm_seq_attn_fwd(ctypes.byref(a), FAKE, None, None, None) == want
+        a = attn(Nkv=n, k=None, **heads)
+        assert L.dlrm_seq_attn_bwd(ctypes.byref(a), FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 1 << 30, None) == want
+    a = attn(B=1 << 23, Nq=1 << 23, **heads)
+    assert L.dlrm_seq_attn_decode(ctypes.byref(a), 100, FAKE, FAKE, 1 << 62, None) == UNSUPPORTED
