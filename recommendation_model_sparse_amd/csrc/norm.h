@@ -213,6 +213,12 @@ inline int widest(int D) { return D % 8 == 0 ? 16384 : 4096; }
 
 // The lanes of a row and the pieces of a lane, by the width: rows of whole 8-element groups (16-byte
 // accesses), others element by element.  A wavefront holds a row while it fits 32 values a lane.
+// Forward + backward in us for 2^24 bf16 elements with dropout, and with about twice the lanes:
+//   width 64: 65 / 112, 128: 46 / 63, 256: 46 / 62, 512: 46 / 46, 1024: 46 / 55, 2048: 49 / 45 (but 1032:
+//   58 / 62 and 4096: 48 / 48);  odd: 100: 86 / 153, 479: 89 / 393
+// with half the lanes: 256: 48, 1024: 50, 2048: 77, 4096: 65; odd 479: 90.
+// Odd widths up to 2048 take 8 pieces a lane (1500: 162, 2001: 130), as 16 leave half the lanes without
+// any and cost 423 and 332.
 template <typename A, typename B, typename C, typename P>
 void by_width(const P &p) {
     const int D = p.D;
@@ -228,6 +234,7 @@ void by_width(const P &p) {
         if (D <= 128) P::template run<A, B, C, 16, 8, 1>(p);
         else if (D <= 512) P::template run<A, B, C, 64, 8, 1>(p);
         else if (D <= 1024) P::template run<A, B, C, 64, 16, 1>(p);
+        else if (D <= 2048) P::template run<A, B, C, 256, 8, 1>(p);
         else P::template run<A, B, C, 256, 16, 1>(p);
     }
 }

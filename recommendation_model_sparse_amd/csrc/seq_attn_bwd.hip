@@ -13,10 +13,14 @@
 //
 // delta.  Without a bias it is <dO, o> from the forward's output.  That o is rounded to bf16, which
 // the gradients, rounded to bf16 too, bear; dbias does not: it sums ds over up to every pair, where
-// most cancels, and would be 1e-3 off (2.2e-7 to 3.6e-7 as it is).  With a bias the first kernel therefore goes over its keys
-// twice, first for delta = sum P dP in fp32.  (An output kept in 24 bits by a forward
+// most cancels, and would be 1e-3 off (2.2e-7 to 3.6e-7 as it is).  With a bias the first kernel therefore
+// goes over its keys twice, first for delta = sum P dP in fp32.  (An output kept in 24 bits by a forward
 // that multiplies P in three bf16 pieces was the other way: as much arithmetic, and 6 more bytes an
 // element to write and read.)
+//
+// Bound by latency, as the forward (heads of 64: VALU 25 to 27 %, MFMA 8 %, LDS 13 to 17 %).  Measured,
+// for the forward's two cases: over queries 134 and 277 us, of which the sweep for delta takes 36 and 82
+// and dbias 38 and 55; over keys 110 and 224, with 27 for the far part of the second.
 #include <type_traits>
 
 #include "seq.h"
@@ -719,6 +723,8 @@ Layout layout_of(const Args &a) {
     const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     l.qslots = a.B ? slot_count(a.Nq, a.B, kQT) : 0, l.kslots = a.B ? slot_count(a.Nkv, a.B, kKT) : 0;
     // a key block's queries are split where there are fewer blocks than two a CU, down to four tiles each
+    // (4 sequences of 2000 to 4096, 8 heads of 128 over 2: unsplit 331 us, in 2 runs 254 and 11 for the
+    // sum, in 4 263 and 18, in 8 291 and 31)
     const int64_t blocks = l.kslots * a.Hkv, tiles = a.B ? a.group * (a.Nq / a.B / kBK) : 0;
     l.splits = 1;
     while (l.splits < 8 && blocks * l.splits < 512 && tiles >= 8 * l.splits) l.splits *= 2;
@@ -793,7 +799,14 @@ extern "C" int dlrm_seq_attn_bwd(const dlrm_seq_attn *desc, const uint16_t *dout
     g.split = reinterpret_cast<float *>(ws + l.split), g.splits = l.splits;
     g.far = reinterpret_cast<float *>(ws + l.far), g.far_sinks = l.far_sinks;
     hipStream_t stream = reinterpret_cast<hipStream_t>(stream_);
-    if (a.d <= 32) return launch<32, 32, 1, 1, 3, 2, false, 896>(a, g, l, dbias, stream);
-    if (a.d <= 64) return launch<64, 64, 1, 1, 3, 3, true, 384>(a, g, l, dbias, stream);
-    return launch<128, 128, 2, 2, 2, 2, true, 1280>(a, g, l, dbias, stream);
+    // Wavefronts that share a tile: two more at heads of 128 (over queries 361 us against 437 with 2; over
+    // keys 336 either way), none at 64 (149 against 191, and 119 against 173).  The near biases: 2048
+    // distances for 896 at heads of 32, 197 -> 178 us, for 1280 at 128, 240 -> 229, for 384 at 64, 240 ->
+    // 204 (8 sequences of 2048, 4 heads, a bias that differs up to 2048), but there they cost a workgroup a
+    // CU: 134 -> 146 (1024 sequences of 16 to 512) where 384 reach past all that is not even.
+    if (a.d <= 32) return launch<32, 32, 1, 1, 3, 2, false, 2048>(a, g, l, dbias, stream);
+    const int uneven = a.window && a.window < a.last ? a.window : a.last;  // distances of differing biases, or hidden ones
+    if (a.d <= 64 && uneven + 2 * kBK <= 384) return launch<64, 64, 1, 1, 3, 3, true, 384>(a, g, l, dbias, stream);
+    if (a.d <= 64) return launch<64, 64, 1, 1, 2, 3, true, 2048>(a, g, l, dbias, stream);
+    return launch<128, 128, 2, 2, 2, 2, true, 2048>(a, g, l, dbias, stream);
 }

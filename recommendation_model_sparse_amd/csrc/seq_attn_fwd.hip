@@ -9,6 +9,10 @@
 // exchange between lanes l and l + 32, and P^T is, as it stands in the registers, the second
 // operand of O^T = V^T P^T.  P never goes through LDS; V^T is read from the row-major tile of V by
 // transposing LDS loads.
+//
+// Bound by latency: no unit is busy for a third of the time (heads of 64: VALU 30 %, MFMA 7 %, LDS
+// 13 %; of 128: 22, 12, 22).  Measured: 1024 sequences of 16 to 512, 2 heads of 64, 62 us (150 TFLOP/s of
+// the visible pairs' products); 4 of 2000 to 4096, window 1024, 8 heads of 128 over 2, 120 us (305).
 #include <type_traits>
 
 #include "seq.h"
@@ -377,7 +381,13 @@ extern "C" int dlrm_seq_attn_fwd(const dlrm_seq_attn *desc, uint16_t *o, float *
     if (a.Nq > 0 && (!o || !aligned(o, 16) || !aligned(lse, 4) || !aligned(tiles, 4))) return DLRM_ERR_INVALID_ARG;
     if (a.B == 0 || a.Nq == 0) return DLRM_OK;
     hipStream_t stream = reinterpret_cast<hipStream_t>(stream_);
-    if (a.d <= 32) return launch<32, 32, 2, 1, 4, 896>(a, o, lse, tiles, stream);
+    // Wavefronts (queries x halves of a tile's keys) and their number a SIMD, at each width the best of
+    // those tried.  Heads of 64: 2 x 1 took 78 us where 2 x 2 took 93 (the 1024 sequences above, before later
+    // steps).  Of 128: 2 x 2 took 38 us where 4 x 1 took 50 and 2 x 1 with three a SIMD 53 (16 sequences of up
+    // to 300 queries after up to 2048 keys).  The near biases: 2048 distances against 896 at heads of 32, 74 -> 70
+    // us, and against 1280 at 128, 99 -> 97 (8 sequences of 2048, a bias that differs up to 2048); at 64 the
+    // longer table costs a workgroup a CU: 86 -> 87, and 18.7 -> 20.5 for 64 sequences of 256.
+    if (a.d <= 32) return launch<32, 32, 2, 1, 4, 2048>(a, o, lse, tiles, stream);
     if (a.d <= 64) return launch<64, 64, 2, 1, 4, 640>(a, o, lse, tiles, stream);
-    return launch<128, 128, 2, 2, 2, 1280>(a, o, lse, tiles, stream);
+    return launch<128, 128, 2, 2, 2, 2048>(a, o, lse, tiles, stream);
 }

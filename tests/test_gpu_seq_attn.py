@@ -121,6 +121,17 @@ def test_forward_backward(lens, Hq, Hkv, d, window, sinks, buckets, reach, itype
         assert err <= gate, name
 
 
+# Biases that differ to where the backward takes another table (256 at heads of 64), and past every table (2048).
+LENS["longer"] = ([2500, 3, 320], [2500, 3, 320])
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,window,sinks,buckets,reach", [
+    (2, 1, 64, 0, 0, 64, 250), (2, 1, 64, 0, 0, 64, 300), (2, 2, 64, 0, 0, 64, 4096), (1, 1, 64, 2300, 4, 100, 4096),
+    (2, 1, 64, 256, 4, 64, 4096), (2, 1, 64, 257, 4, 64, 4096), (1, 1, 32, 0, 0, 64, 4096), (2, 1, 128, 2300, 70, 64, 4096)])
+def test_bias_past_the_table(Hq, Hkv, d, window, sinks, buckets, reach):
+    test_forward_backward("longer", Hq, Hkv, d, window, sinks, buckets, reach, np.int64)
+
+
 def test_gradients_against_differences():
     """The loss <do, o> along a direction of each input: the kernels' gradients against central
     differences of the oracle's forward in fp64 (step 2^-12: its own error is 2^-24 of the third
