@@ -3,7 +3,7 @@
 //   dh = ds + rstd (dy w - hat mean(dy w hat)), hat = s rstd;  dx = m dh;  dw = sum dy hat
 //
 // Bound by reading and writing each row once, as the forward.  Measured, for its cases: 150000 x 128 53
-// us, 5.8 TB/s; 16384 x 479 fp32 36 us; dw's sum over the workgroups 6 us.  Odd widths past 2048 are far
+// us, 5.8 TB/s; 16384 x 479 fp32 36 us, 4.4; dw's sum over the workgroups 6 us.  Odd widths past 2048 are far
 // from that (4195 x 3999 bf16: 212 us): a workgroup holds one row, and 256 registers a lane leave one
 // wavefront a SIMD; a bound on the registers made it 294.
 #include "norm.h"

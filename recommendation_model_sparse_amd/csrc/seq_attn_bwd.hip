@@ -18,7 +18,7 @@
 // that multiplies P in three bf16 pieces was the other way: as much arithmetic, and 6 more bytes an
 // element to write and read.)
 //
-// Bound by latency, as the forward (heads of 64: VALU 25 to 27 %, MFMA 8 %, LDS 13 to 17 %).  Measured,
+// Bound by waits, as the forward (heads of 64: VALU 25 to 27 %, MFMA 8 %, LDS 13 to 17 %).  Measured,
 // for the forward's two cases: over queries 134 and 277 us, of which the sweep for delta takes 36 and 82
 // and dbias 38 and 55; over keys 110 and 224, with 27 for the far part of the second.
 #include <type_traits>

@@ -10,7 +10,7 @@
 // operand of O^T = V^T P^T.  P never goes through LDS; V^T is read from the row-major tile of V by
 // transposing LDS loads.
 //
-// Bound by latency: no unit is busy for a third of the time (heads of 64: VALU 30 %, MFMA 7 %, LDS
+// Bound by waits, half of the wavefronts' cycles: no unit is busy for a third of the time (heads of 64: VALU 30 %, MFMA 7 %, LDS
 // 13 %; of 128: 22, 12, 22).  Measured: 1024 sequences of 16 to 512, 2 heads of 64, 62 us (150 TFLOP/s of
 // the visible pairs' products); 4 of 2000 to 4096, window 1024, 8 heads of 128 over 2, 120 us (305).
 #include <type_traits>
