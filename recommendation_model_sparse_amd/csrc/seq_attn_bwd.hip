@@ -721,11 +721,11 @@ constexpr int kKT = 64;  // keys of a workgroup
 Layout layout_of(const Args &a) {
     Layout l{};
     const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-    l.qslots = a.B ? slot_count(a.Nq, a.B, kQT) : 0, l.kslots = a.B ? slot_count(a.Nkv, a.B, kKT) : 0;
+    l.qslots = a.B ? slot_count(a.Nq, a.B, kQT) : 0, l.kslots = a.B && a.Nkv ? slot_count(a.Nkv, a.B, kKT) : 0;
     // a key block's queries are split where there are fewer blocks than two a CU, down to four tiles each
     // (4 sequences of 2000 to 4096, 8 heads of 128 over 2: unsplit 331 us, in 2 runs 254 and 11 for the
     // sum, in 4 263 and 18, in 8 291 and 31)
-    const int64_t blocks = l.kslots * a.Hkv, tiles = a.B ? a.group * (a.Nq / a.B / kBK) : 0;
+    const int64_t blocks = l.kslots * a.Hkv, tiles = l.kslots ? a.group * (a.Nq / a.B / kBK) : 0;
     l.splits = 1;
     while (l.splits < 8 && blocks * l.splits < 512 && tiles >= 8 * l.splits) l.splits *= 2;
     size_t far = a.sinks <= kFarMost ? static_cast<size_t>(l.qslots) * a.Hkv * a.sinks * 2 * a.d * 4 : 0;

@@ -428,3 +428,23 @@ def test_refusals():
     for bad in (dict(q=q[:3]), dict(kv_begin=off), dict(kv_end=off[1:].int()), dict(max_kv_len=-1), dict(out=q)):
         with pytest.raises(ValueError):
             dlrm_seq_attn_decode(**{**one, **bad})
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,window,sinks,buckets", [(1, 1, 32, 0, 0, 0), (4, 1, 64, 0, 0, 8), (2, 2, 128, 100, 4, 8)])
+def test_no_keys_at_all(Hq, Hkv, d, window, sinks, buckets):
+    """Queries over k and v of no rows, as many as have a key block's queries split: o and every gradient are 0."""
+    rng = rng_of("seq-keyless", Hq, d)
+    n = 1200
+    qo, ko = to_dev(offsets([n])), to_dev(offsets([0]))
+    q_d, _ = bf16(rng, n, Hq, d)
+    g_d, _ = bf16(rng, n, Hq, d)
+    k = torch.empty((0, Hkv, d), dtype=torch.bfloat16, device=DEV)
+    how = dict(window=window, sinks=sinks)
+    if buckets:
+        how.update(bias=to_dev(rng.standard_normal((Hq, buckets)).astype(np.float32)), bounds=dlrm_seq_bucket_bounds(buckets, 64))
+    say(f"[seq] no keys, Hq={Hq} d={d}")
+    o, tiles, lse = dlrm_seq_attn_fwd(q_d, k, k, qo, ko, for_backward=True, **how)
+    dq, dk, dv, dbias = dlrm_seq_attn_bwd(g_d, q_d, k, k, o, tiles, lse, qo, ko, **how)
+    torch.cuda.synchronize()
+    assert (o == 0).all() and (lse == -float("inf")).all() and (dq == 0).all()
+    assert dk.shape == k.shape and dv.shape == k.shape and (dbias is None or (dbias == 0).all())
