@@ -100,7 +100,7 @@ size_t dlrm_seq_attn_bwd_workspace_size(const dlrm_seq_attn *a);
  *     dbias[h][t] = sum over the pairs of bucket t of ds
  *
  *   a: the forward's, with kv_begin a CSR array of B+1 offsets (kv_end == kv_begin + 1)
- *   dout [Nq][Hq][d] bf16; o, lse, tiles as the forward wrote them (o is read without a bias only:
+ *   dout [Nq][Hq][d] bf16; o, lse, tiles as the forward wrote them (not read where Nq == 0; o is read without a bias only:
  *   with one, <do, o> is summed again in fp32, as dbias needs it)
  *   dq [Nq][Hq][d], dk, dv [Nkv][Hkv][d] bf16 (rows of every sequence are written in full);
  *   dbias [Hq][buckets] fp32 (with a bias; else NULL)

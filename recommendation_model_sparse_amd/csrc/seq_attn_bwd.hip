@@ -721,7 +721,8 @@ constexpr int kKT = 64;  // keys of a workgroup
 Layout layout_of(const Args &a) {
     Layout l{};
     const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-    l.qslots = a.B ? slot_count(a.Nq, a.B, kQT) : 0, l.kslots = a.B && a.Nkv ? slot_count(a.Nkv, a.B, kKT) : 0;
+    // no queries: the forward wrote no tiles, and nothing may look a slot up in them
+    l.qslots = a.B && a.Nq ? slot_count(a.Nq, a.B, kQT) : 0, l.kslots = a.B && a.Nkv ? slot_count(a.Nkv, a.B, kKT) : 0;
     // a key block's queries are split where there are fewer blocks than two a CU, down to four tiles each
     // (4 sequences of 2000 to 4096, 8 heads of 128 over 2: unsplit 331 us, in 2 runs 254 and 11 for the
     // sum, in 4 263 and 18, in 8 291 and 31)
@@ -792,6 +793,7 @@ extern "C" int dlrm_seq_attn_bwd(const dlrm_seq_attn *desc, const uint16_t *dout
     if (static_cast<int64_t>(a.Hq) * a.d >= (1 << 24)) return DLRM_ERR_UNSUPPORTED;
     const Layout l = layout_of(a);
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < l.bytes) return DLRM_ERR_WORKSPACE;
+    if (l.qslots == 0 && l.kslots == 0 && !a.buckets) return DLRM_OK;
     char *const ws = static_cast<char *>(workspace);
     Grads g{};
     g.dout = dout, g.o = o, g.lse = lse, g.tiles = tiles, g.dq = dq, g.dk = dk, g.dv = dv;

@@ -18,6 +18,7 @@ import pytest
 import torch
 
 from oracle import seq
+from recommendation_model_sparse_amd import binding
 from recommendation_model_sparse_amd import (DlrmError, dlrm_seq_attn_bwd, dlrm_seq_attn_decode, dlrm_seq_attn_fwd,
                                              dlrm_seq_bucket_bounds, synth)
 
@@ -448,3 +449,23 @@ def test_no_keys_at_all(Hq, Hkv, d, window, sinks, buckets):
     torch.cuda.synchronize()
     assert (o == 0).all() and (lse == -float("inf")).all() and (dq == 0).all()
     assert dk.shape == k.shape and dv.shape == k.shape and (dbias is None or (dbias == 0).all())
+
+
+@pytest.mark.parametrize("buckets", [0, 4])
+def test_keys_that_nobody_asks(buckets):
+    """Keys without any query: gradients of 0.  The C call takes no tiles then, as the forward writes none."""
+    n, Hkv, d = 200, 2, 64
+    q = torch.empty((0, 4, d), dtype=torch.bfloat16, device=DEV)
+    k = torch.ones((n, Hkv, d), dtype=torch.bfloat16, device=DEV)
+    none, ko = torch.zeros(3, dtype=torch.int64, device=DEV), to_dev(offsets([70, 130]))
+    bias = torch.ones((4, 4), device=DEV) if buckets else None
+    a, edges, dev, _, _ = binding._seq_attn(q, k, k, none, ko[:-1], ko[1:], 2, 50, 3, None, bias, [0, 1, 2, 3] if buckets else None)
+    L = binding.lib()
+    dk, dv = torch.full_like(k, 7), torch.full_like(k, 7)
+    dbias = torch.full((4, 4), 7.0, device=DEV) if buckets else None
+    ws = torch.empty(L.dlrm_seq_attn_bwd_workspace_size(a), dtype=torch.uint8, device=DEV)
+    at = binding._ptr
+    say(f"[seq] no queries, buckets={buckets}")
+    assert L.dlrm_seq_attn_bwd(a, None, None, None, None, None, at(dk), at(dv), at(dbias), at(ws), ws.numel(), binding._stream(dev)) == 0
+    torch.cuda.synchronize()
+    assert (dk == 0).all() and (dv == 0).all() and (dbias is None or (dbias == 0).all())

@@ -152,3 +152,15 @@ def test_attention_past_one_launch_rejected(L, d, ok, over):
         assert L.dlrm_seq_attn_bwd(ctypes.byref(a), FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 1 << 30, None) == want
     a = attn(B=1 << 23, Nq=1 << 23, **heads)
     assert L.dlrm_seq_attn_decode(ctypes.byref(a), 100, FAKE, FAKE, 1 << 62, None) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("bias", [None, FAKE])
+def test_backward_without_queries_takes_no_tiles(L, bias):
+    """The forward of no queries writes no tiles and takes NULL; the backward then has nothing to look up:
+    without keys and a bias it launches nothing, and with them only what does not read tiles."""
+    a = attn(Nq=0, Nkv=0, q=None, k=None, v=None, bias=bias, sinks=3, window=5)
+    assert L.dlrm_seq_attn_fwd(ctypes.byref(a), None, None, None, None) == OK
+    need = L.dlrm_seq_attn_bwd_workspace_size(ctypes.byref(a))
+    assert need == L.dlrm_seq_attn_bwd_workspace_size(ctypes.byref(attn(B=0, Nq=0, Nkv=0, bias=bias)))  # no slots of queries
+    if bias is None:
+        assert L.dlrm_seq_attn_bwd(ctypes.byref(a), *[None] * 8, FAKE, need, None) == OK
