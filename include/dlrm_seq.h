@@ -100,9 +100,10 @@ size_t dlrm_seq_attn_bwd_workspace_size(const dlrm_seq_attn *a);
  *     dbias[h][t] = sum over the pairs of bucket t of ds
  *
  *   a: the forward's, with kv_begin a CSR array of B+1 offsets (kv_end == kv_begin + 1)
- *   dout [Nq][Hq][d] bf16; o, lse, tiles as the forward wrote them (not read where Nq == 0; o is read without a bias only:
- *   with one, <do, o> is summed again in fp32, as dbias needs it)
- *   dq [Nq][Hq][d], dk, dv [Nkv][Hkv][d] bf16 (rows of every sequence are written in full);
+ *   dout [Nq][Hq][d] bf16; o, lse, tiles as the forward wrote them (not read where Nq == 0; o
+ *   is read without a bias only: with one, <do, o> is summed again in fp32, as dbias needs it)
+ *   dq [Nq][Hq][d], dk, dv [Nkv][Hkv][d] bf16 (rows of every sequence are written in full,
+ *   rows outside every sequence not at all);
  *   dbias [Hq][buckets] fp32 (with a bias; else NULL)
  *   Infinities and NaN in a key that a query does not see have no effect on its dq, and a key that
  *   no query sees has gradients of zero; those of q and dout reach every key near by.

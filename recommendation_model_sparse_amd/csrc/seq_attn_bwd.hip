@@ -667,10 +667,11 @@ __global__ __launch_bounds__(WY * WX * 64, OCC) void k_seq_attn_bwd_kv(const Arg
         }
 }
 
-// dk, dv = the sums over the runs, in order; four elements a thread of each.
-__global__ __launch_bounds__(256) void k_seq_kv_sum(const float *split, int splits, int64_t plane, uint16_t *dk, uint16_t *dv) {
-    const int64_t e = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
-    if (e >= plane) return;
+// dk, dv = the sums over the runs, in order; four elements a thread of each.  Only the sequences' rows:
+// the runs wrote no others, and the caller's are not to be touched.
+__global__ __launch_bounds__(256) void k_seq_kv_sum(const Args a, const float *split, int splits, int64_t plane, uint16_t *dk, uint16_t *dv) {
+    const int64_t e = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4, width = static_cast<int64_t>(a.Hkv) * a.d;
+    if (e < offset_at(a, a.kv_begin, 0, a.Nkv) * width || e >= offset_at(a, a.kv_begin, a.B, a.Nkv) * width) return;
     floatx4 x = {0.f, 0.f, 0.f, 0.f}, y = x;
     for (int s = 0; s < splits; ++s) {
         x += *(const DLRM_GLOBAL floatx4 *)(split + 2 * s * plane + e);
@@ -756,7 +757,7 @@ int launch(const Args &a, const Grads &g, const Layout &l, float *dbias, hipStre
     const int64_t plane = a.Nkv * a.Hkv * a.d;
     if (l.splits > 1)
         DLRM_LAUNCH("seq_kv_sum", k_seq_kv_sum, dim3(static_cast<uint32_t>((plane / 4 + 255) / 256)), dim3(256), 0, stream,
-                    static_cast<const float *>(g.split), l.splits, plane, g.dk, g.dv);
+                    a, static_cast<const float *>(g.split), l.splits, plane, g.dk, g.dv);
     if (a.buckets)
         DLRM_LAUNCH("seq_bias_sum", k_seq_bias_sum, dim3((a.buckets + 7) / 8, a.Hq), dim3(1024), 0, stream,
                     static_cast<const float *>(g.partial), l.qslots, a.buckets, dbias);

@@ -469,3 +469,29 @@ def test_keys_that_nobody_asks(buckets):
     assert L.dlrm_seq_attn_bwd(a, None, None, None, None, None, at(dk), at(dv), at(dbias), at(ws), ws.numel(), binding._stream(dev)) == 0
     torch.cuda.synchronize()
     assert (dk == 0).all() and (dv == 0).all() and (dbias is None or (dbias == 0).all())
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,d", [([1500], 4, 1, 32), ([900], 8, 2, 128), ([40, 90], 2, 2, 64)])
+def test_rows_outside_every_sequence(lens, Hq, Hkv, d):
+    """Rows before the first offset and from the last on keep what the outputs held, whether a key block's
+    queries are split (the first two) or not; the others are those of tensors without such rows."""
+    rng = rng_of("seq-padding", lens, Hq, d)
+    n, lead, trail = sum(lens), 37, 50
+    inner = slice(lead, lead + n)
+    qo = to_dev(offsets(lens))
+    q_d, _ = bf16(rng, lead + n + trail, Hq, d)
+    k_d, _ = bf16(rng, lead + n + trail, Hkv, d)
+    v_d, _ = bf16(rng, lead + n + trail, Hkv, d)
+    g_d, _ = bf16(rng, lead + n + trail, Hq, d)
+    say(f"[seq] padding {lens} Hq={Hq} d={d}")
+    ws = torch.full((64 << 20,), 0x7f, dtype=torch.uint8, device=DEV)  # what an earlier call may have left there
+    out = [torch.full_like(t, 7.0) for t in (q_d, q_d, k_d, v_d)]
+    o, tiles, lse = dlrm_seq_attn_fwd(q_d, k_d, v_d, qo + lead, for_backward=True, out=out[0])
+    dlrm_seq_attn_bwd(g_d, q_d, k_d, v_d, o, tiles, lse, qo + lead, dq=out[1], dk=out[2], dv=out[3], workspace=ws)
+    packed = [t[inner].contiguous() for t in (q_d, k_d, v_d)]
+    kept = dlrm_seq_attn_fwd(*packed, qo, for_backward=True)
+    want = (kept[0],) + dlrm_seq_attn_bwd(g_d[inner].contiguous(), *packed, *kept, qo)[:3]
+    torch.cuda.synchronize()
+    for name, x, y in zip(("o", "dq", "dk", "dv"), out, want):
+        assert torch.equal(x[inner], y), name
+        assert (x[:lead] == 7).all() and (x[lead + n:] == 7).all(), name
