@@ -328,8 +328,9 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a
         const float top1 = part[MB * 16 * 64], sum1 = part[(MB * 16 + 1) * 64], mx = fmaxf(top, top1);
         const float f0 = top == -kInf ? 0.f : top == mx ? 1.f : __builtin_amdgcn_exp2f((top - mx) * kLog2e);
         const float f1 = top1 == -kInf ? 0.f : top1 == mx ? 1.f : __builtin_amdgcn_exp2f((top1 - mx) * kLog2e);
-        // a half without a key that the query sees holds zeros, but a wild pass may have left more
-        sum = (top == -kInf ? 0.f : f0 * sum) + (top1 == -kInf ? 0.f : f1 * sum1);
+        // a half without a key that the query sees holds a sum of 0; one whose every logit is NaN has the same
+        // maximum, as that passes NaN over, and its sum is NaN
+        sum = f0 * sum + f1 * sum1;
         top = mx;
 #pragma unroll
         for (int m = 0; m < MB; ++m)

@@ -495,3 +495,22 @@ def test_rows_outside_every_sequence(lens, Hq, Hkv, d):
     for name, x, y in zip(("o", "dq", "dk", "dv"), out, want):
         assert torch.equal(x[inner], y), name
         assert (x[:lead] == 7).all() and (x[lead + n:] == 7).all(), name
+
+
+@pytest.mark.parametrize("d", [32, 64, 96, 128])
+@pytest.mark.parametrize("j", [0, 20, 32, 70, 149])
+def test_lse_of_what_sees_nan(d, j):
+    """A NaN in a key is in the lse of the queries that see it, at either half of a tile, and in no other's."""
+    rng = rng_of("seq-lse", d, j)
+    n = 150
+    qo = to_dev(offsets([n]))
+    q_d, _ = bf16(rng, n, 2, d)
+    k_d, _ = bf16(rng, n, 1, d)
+    v_d, _ = bf16(rng, n, 1, d)
+    clean = dlrm_seq_attn_fwd(q_d, k_d, v_d, qo, for_backward=True)
+    k_d[j, 0, 3] = float("nan")
+    say(f"[seq] lse d={d} j={j}")
+    o, _, lse = dlrm_seq_attn_fwd(q_d, k_d, v_d, qo, for_backward=True)
+    torch.cuda.synchronize()
+    assert torch.isnan(lse[j:]).all() and torch.isnan(o[j:].float()).all()
+    assert torch.equal(lse[:j], clean[2][:j]) and torch.equal(o[:j], clean[0][:j])
