@@ -46,7 +46,7 @@ enum { DLRM_F8_E4M3 = 2 };
  *
  * A query that sees no key (kv_len == 0, or p < 0) has o = 0 and lse = -infinity.  What k and v
  * hold for a key that a query does not see has no effect on its o and lse, NaN and infinities
- * included.
+ * included.  o is finite where the values that it is a mean of are, however large.
  *
  *   B          sequences, >= 0;  Nq, Nkv: rows of q, and of k and v
  *   Hq, Hkv    query and key/value heads, Hq a multiple of Hkv;  d: elements of a head

@@ -30,9 +30,9 @@ __device__ __forceinline__ float add_quarters(float x) {
     return add_halves(__uint_as_float(r[0]) + __uint_as_float(r[1]));
 }
 
-// part: [B][Hq][splits] rows of d floats; ml: their (maximum, sum)
+// part: [B][Hq][splits] rows of d floats, the runs' outputs; ml: their (maximum, sum)
 template <int DP>
-__global__ __launch_bounds__(kWaves * 64) void k_seq_attn_decode(const Args a, const int splits, const int quantum, const bool splits_first,
+__global__ __launch_bounds__(kWaves * 64, DP == 32 ? 5 : DP == 64 ? 4 : 2) void k_seq_attn_decode(const Args a, const int splits, const int quantum, const bool splits_first,
                                                                  const int head_groups,
                                                                  uint16_t *o_out, float *part, float2 *ml) {
     constexpr int LP = DP, CH = LP / 8, STEPS = DP / 32, MB = DP / 16, VN = kChunk * CH / 64;
@@ -42,7 +42,7 @@ __global__ __launch_bounds__(kWaves * 64) void k_seq_attn_decode(const Args a, c
     };
     __shared__ __attribute__((aligned(16))) Lds lds;
     __shared__ __attribute__((aligned(16))) int ids[kWaves][kChunk];
-    __shared__ float top_s[kWaves][kHeads], sum_s[kWaves][kHeads];
+    __shared__ float top_s[kWaves][kHeads], sum_s[kWaves][kHeads], unit_s[kWaves][kHeads];
     __shared__ float bias_s[kHeads * DLRM_SEQ_MAX_BUCKETS];
     __shared__ int bounds_s[DLRM_SEQ_MAX_BUCKETS];
 
@@ -75,6 +75,7 @@ __global__ __launch_bounds__(kWaves * 64) void k_seq_attn_decode(const Args a, c
 #pragma unroll
     for (int m = 0; m < MB; ++m) o[m] = floatx4{0.f, 0.f, 0.f, 0.f};
     float top = -kInf, sum = 0.f;
+    float known = 0.f, share = 1.f, unit = 1.f;  // the sum, if known; what P is multiplied by; a unit of o in the sum's terms
 
     u32x4 kr[2][STEPS], vr[VN];
     const auto load = [&](int c) {
@@ -114,101 +115,123 @@ __global__ __launch_bounds__(kWaves * 64) void k_seq_attn_decode(const Args a, c
         const int c = 32 * s + 8 * quad;
         if (ln < heads && c < a.d) qf[s].q = *(const DLRM_GLOBAL u32x4 *)(a.q + b * a.q_row + (h0 + ln) * a.q_head + c);
     }
-    for (; c < v1; c += kWaves * kChunk) {
-        uint16_t *vt = lds.v[w];
-        floatx4 s[2];
+    // An output is a mean of its values and finite where they are, but sum P v before the division may not
+    // be.  Where a head's o overflowed and its sum did not, the wavefront walks its keys again with that sum as
+    // known: P / sum adds up to 1.
+#pragma unroll 1
+    for (int walk = 0;; ++walk) {
+        for (; c < v1; c += kWaves * kChunk) {
+            uint16_t *vt = lds.v[w];
+            floatx4 s[2];
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            s[g] = floatx4{0.f, 0.f, 0.f, 0.f};
+            for (int g = 0; g < 2; ++g) {
+                s[g] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < STEPS; ++i) {
-                Frag k;
-                k.q = kr[g][i];
-                s[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k.b, qf[i].b, s[g], 0, 0, 0);
+                for (int i = 0; i < STEPS; ++i) {
+                    Frag k;
+                    k.q = kr[g][i];
+                    s[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k.b, qf[i].b, s[g], 0, 0, 0);
+                }
             }
-        }
-        wave_lds_sync();  // the chunk before has been read
+            wave_lds_sync();  // the chunk before has been read
 #pragma unroll
-        for (int i = 0; i < VN; ++i) {
-            const int at = i * 64 + lane;
-            *reinterpret_cast<u32x4 *>(vt + at / CH * kPitch<LP> + at % CH * 8) = vr[i];
-        }
-        const int next = c + kWaves * kChunk;
-        if (next < v1) load(next);
+            for (int i = 0; i < VN; ++i) {
+                const int at = i * 64 + lane;
+                *reinterpret_cast<u32x4 *>(vt + at / CH * kPitch<LP> + at % CH * 8) = vr[i];
+            }
+            const int next = c + kWaves * kChunk;
+            if (next < v1) load(next);
 
-        // register r of block g: key c + 16 g + 4 quad + r (of those in a row)
-        const int last_v = min(c + kChunk, v1) - 1;
-        const int nearest = klen - 1 - (last_v < skip ? last_v : start + last_v - skip);
-        if (!a.buckets || nearest >= a.last) {
+            // register r of block g: key c + 16 g + 4 quad + r (of those in a row)
+            const int last_v = min(c + kChunk, v1) - 1;
+            const int nearest = klen - 1 - (last_v < skip ? last_v : start + last_v - skip);
+            if (!a.buckets || nearest >= a.last) {
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) s[g][r] = fmaf(s[g][r], a.scale, far);
+            } else {
+                if (lane < kChunk) {
+                    const int v = c + lane;
+                    ids[w][lane] = bucket_of(bounds_s, a.buckets, max(0, klen - 1 - (v < skip ? v : start + v - skip)));
+                }
+                wave_lds_sync();
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) s[g][r] = fmaf(s[g][r], a.scale, my_bias[ids[w][16 * g + 4 * quad + r]]);
+            }
+            if (c + kChunk > v1) {
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (c + 16 * g + 4 * quad + r >= v1) s[g][r] = -kInf;
+            }
+            float mx = s[0][0];
 #pragma unroll
             for (int g = 0; g < 2; ++g)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) s[g][r] = fmaf(s[g][r], a.scale, far);
-        } else {
-            if (lane < kChunk) {
-                const int v = c + lane;
-                ids[w][lane] = bucket_of(bounds_s, a.buckets, max(0, klen - 1 - (v < skip ? v : start + v - skip)));
+                for (int r = 0; r < 4; ++r) mx = fmaxf(mx, s[g][r]);
+            mx = fmaxf(max_quarters(mx), top);
+            if (__any(mx > top)) {
+                const float f = mx == -kInf ? 1.f : __builtin_amdgcn_exp2f((top - mx) * kLog2e);
+                sum *= f;
+#pragma unroll
+                for (int m = 0; m < MB; ++m)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) o[m][r] *= f;
+                top = mx;
+            }
+            const float ref = top == -kInf ? 0.f : top;
+            Frag p;
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    s[g][r] = __builtin_amdgcn_exp2f((s[g][r] - ref) * kLog2e) * share;
+                    sum += s[g][r];
+                }
+                p.w[2 * g] = pack_bf16(s[g][0], s[g][1]);
+                p.w[2 * g + 1] = pack_bf16(s[g][2], s[g][3]);
             }
             wave_lds_sync();
 #pragma unroll
-            for (int g = 0; g < 2; ++g)
+            for (int m = 0; m < MB; ++m) {
+                // column 16 m + ln of the keys 4 quad + {0..3} and those 16 further on
+                typedef __attribute__((address_space(3))) s16x4 *lds_t;
+                Frag v;
+                const int col = 16 * m + 4 * (ln & 3), row = 4 * quad + (ln >> 2);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) s[g][r] = fmaf(s[g][r], a.scale, my_bias[ids[w][16 * g + 4 * quad + r]]);
-        }
-        if (c + kChunk > v1) {
-#pragma unroll
-            for (int g = 0; g < 2; ++g)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (c + 16 * g + 4 * quad + r >= v1) s[g][r] = -kInf;
-        }
-        float mx = s[0][0];
-#pragma unroll
-        for (int g = 0; g < 2; ++g)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) mx = fmaxf(mx, s[g][r]);
-        mx = fmaxf(max_quarters(mx), top);
-        if (__any(mx > top)) {
-            const float f = mx == -kInf ? 1.f : __builtin_amdgcn_exp2f((top - mx) * kLog2e);
-            sum *= f;
-#pragma unroll
-            for (int m = 0; m < MB; ++m)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) o[m][r] *= f;
-            top = mx;
-        }
-        const float ref = top == -kInf ? 0.f : top;
-        Frag p;
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                s[g][r] = __builtin_amdgcn_exp2f((s[g][r] - ref) * kLog2e);
-                sum += s[g][r];
+                for (int g = 0; g < 2; ++g) {
+                    const uint16_t *at = vt + (row + 16 * g) * kPitch<LP> + col;
+                    v.h[g] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t)(at));
+                }
+                o[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v.b, p.b, o[m], 0, 0, 0);
             }
-            p.w[2 * g] = pack_bf16(s[g][0], s[g][1]);
-            p.w[2 * g + 1] = pack_bf16(s[g][2], s[g][3]);
         }
-        wave_lds_sync();
-#pragma unroll
-        for (int m = 0; m < MB; ++m) {
-            // column 16 m + ln of the keys 4 quad + {0..3} and those 16 further on
-            typedef __attribute__((address_space(3))) s16x4 *lds_t;
-            Frag v;
-            const int col = 16 * m + 4 * (ln & 3), row = 4 * quad + (ln >> 2);
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                const uint16_t *at = vt + (row + 16 * g) * kPitch<LP> + col;
-                v.h[g] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t)(at));
-            }
-            o[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v.b, p.b, o[m], 0, 0, 0);
+        sum = add_quarters(sum);
+        if (walk == 1) {
+            if (share != 1.f) unit = known / sum, sum = known;
+            break;
         }
+        float any = sum;
+#pragma unroll
+        for (int m = 0; m < MB; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) any += o[m][r];
+        const bool over = max_quarters(ln < heads && !(fabsf(any) < kInf) && sum > 0.f && sum < kInf ? 1.f : 0.f) != 0.f;
+        if (!__any(over)) break;
+        known = sum, share = over ? 1.f / sum : 1.f, top = over ? top : -kInf, sum = 0.f;
+#pragma unroll
+        for (int m = 0; m < MB; ++m) o[m] = floatx4{0.f, 0.f, 0.f, 0.f};
+        c = v0 + w * kChunk;
+        load(c);
     }
-    sum = add_quarters(sum);
 
     // join the wavefronts
     __syncthreads();
-    if (quad == 0) top_s[w][ln] = top, sum_s[w][ln] = sum;
+    if (quad == 0) top_s[w][ln] = top, sum_s[w][ln] = sum, unit_s[w][ln] = unit;
 #pragma unroll
     for (int m = 0; m < MB; ++m) *reinterpret_cast<floatx4 *>(&lds.o[w][ln][16 * m + 4 * quad]) = o[m];
     __syncthreads();
@@ -218,22 +241,26 @@ __global__ __launch_bounds__(kWaves * 64) void k_seq_attn_decode(const Args a, c
         float mx = top_s[0][hd];
 #pragma unroll
         for (int v = 1; v < kWaves; ++v) mx = fmaxf(mx, top_s[v][hd]);
-        float total = 0.f;
-        floatx4 x = {0.f, 0.f, 0.f, 0.f};
+        float total = 0.f, f[kWaves];
 #pragma unroll
         for (int v = 0; v < kWaves; ++v) {
             const float t = top_s[v][hd];
-            const float f = t == -kInf ? 0.f : __builtin_amdgcn_exp2f((t - mx) * kLog2e);
-            const floatx4 y = *reinterpret_cast<const floatx4 *>(&lds.o[v][hd][col]);
-            total += f * sum_s[v][hd];
+            f[v] = t == -kInf ? 0.f : __builtin_amdgcn_exp2f((t - mx) * kLog2e);
+            total += f[v] * sum_s[v][hd];
+        }
+        // divided before they are added: each may be near the largest number
+        const float inv = total == 0.f ? 0.f : 1.f / total;
+        floatx4 x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] += f * y[e];
+        for (int v = 0; v < kWaves; ++v) {
+            const floatx4 y = *reinterpret_cast<const floatx4 *>(&lds.o[v][hd][col]);
+            const float g = f[v] * unit_s[v][hd] * inv;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] += g * y[e];
         }
         const int64_t row = static_cast<int64_t>(b) * a.Hq + h0 + hd;
         if (splits == 1) {
-            const float inv = total == 0.f ? 0.f : 1.f / total;
-            *(DLRM_GLOBAL u32x2 *)(o_out + row * a.d + col) =
-                u32x2{pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv)};
+            *(DLRM_GLOBAL u32x2 *)(o_out + row * a.d + col) = u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
         } else {
             *(DLRM_GLOBAL floatx4 *)(part + (row * splits + split) * a.d + col) = x;
             if (col == 0) ml[row * splits + split] = make_float2(mx, total);
@@ -252,13 +279,13 @@ __global__ __launch_bounds__(256) void k_seq_decode_join(const float *part, cons
     float mx = t.x;
 #pragma unroll
     for (int i = 1; i < 64; i <<= 1) mx = fmaxf(mx, __shfl_xor(mx, i));
-    const float f = t.x == -kInf ? 0.f : __builtin_amdgcn_exp2f((t.x - mx) * kLog2e);
-    float total = f * t.y;
+    const float f = (t.x == -kInf ? 0.f : __builtin_amdgcn_exp2f((t.x - mx) * kLog2e)) * t.y;
+    float total = f;
 #pragma unroll
     for (int i = 1; i < 64; i <<= 1) total += __shfl_xor(total, i);
     float x = 0.f, y = 0.f;
     const float *p = part + row * splits * d + 2 * lane;
-    factor[w][lane] = f;
+    factor[w][lane] = total == 0.f ? 0.f : f / total;
     wave_lds_sync();
 #pragma unroll 16
     for (int s = w; s < splits; s += kWaves) {
@@ -274,8 +301,7 @@ __global__ __launch_bounds__(256) void k_seq_decode_join(const float *part, cons
     x = y = 0.f;
 #pragma unroll
     for (int v = 0; v < kWaves; ++v) x += sums[v][lane].x, y += sums[v][lane].y;
-    const float inv = total == 0.f ? 0.f : 1.f / total;
-    *reinterpret_cast<uint32_t *>(o + row * d + 2 * lane) = pack_bf16(x * inv, y * inv);
+    *reinterpret_cast<uint32_t *>(o + row * d + 2 * lane) = pack_bf16(x, y);
 }
 
 // How the keys of a sequence are split: into at most 64 runs of at least `quantum` keys.  A workgroup a

@@ -156,13 +156,15 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a
     float top, sum;
     const uint16_t *const krow = Ks + row_base<LP>(ln, half), *const vcol = Vs + column_base<LP>(lane);
     // One pass over the keys.  An infinity or NaN in a key would reach the queries that do not see it
-    // (0 * NaN in a product): where a result is NaN, the block makes a second, WILD pass that keeps
-    // the values apart.  What is finite pays nothing for it.
-    const auto attend = [&](auto is_wild) {
+    // (0 * NaN in a product): where a result is not finite, the block makes a second, WILD pass that keeps
+    // the values apart.  What is finite makes no such pass, but pays for its code in registers: 207 with
+    // it and 169 without at heads of 128, 128 and 120 at 64.  `start`: the reference that a pass
+    // begins with; `share`: what a WILD one multiplies P by.
+    const auto attend = [&](auto is_wild, float start, float share) {
         constexpr bool WILD = decltype(is_wild)::value;
 #pragma unroll
         for (int m = 0; m < MB; ++m) o[m] = f32x16{};
-        top = -kInf, sum = 0.f;
+        top = start, sum = 0.f;
         for (int it = 0; it < n; ++it) {
             const int k0 = key0(it);
             load(it);
@@ -215,8 +217,8 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a
 #pragma unroll
                 for (int r = 1; r < 16; ++r) mx = fmaxf(mx, s[r]);
                 mx = max_halves(mx);
-                // the reference is moved when the maximum is over it by 8 (P up to e^8, which bf16 and the
-                // fp32 sums bear): with 32 rows one of them has a new maximum nearly every time
+                // the reference is moved when the maximum is over it by 8 (P up to e^8: bf16 holds that as well
+                // as 1, and sums that it takes past the largest number are made again, below): with 32 rows one of them has a new maximum nearly every time
                 const bool over = mx > top + 8.f;
                 if (__any(over)) {
                     const float f = over ? __builtin_amdgcn_exp2f((top - mx) * kLog2e) : 1.f;
@@ -235,6 +237,10 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a
                     const float ref2 = ref * kLog2e;
 #pragma unroll
                     for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], kLog2e, -ref2));
+                }
+                if constexpr (WILD) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) s[r] *= share;
                 }
                 Frag p[2];
 #pragma unroll
@@ -302,18 +308,28 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a
         }
         sum = add_halves(sum);
     };
-    attend(std::false_type());
-    float any = sum;
+    attend(std::false_type(), -kInf, 1.f);
+    // An output is a mean of its values and finite where they are, but sum P v before the division may not be:
+    // P adds up to as much as e^8 a key.  Where a query's o is still not finite after a WILD pass and its sum
+    // is, a third pass takes that sum as known: P / sum adds up to 1.
+    float unit = 1.f;  // of o, in the sum's terms
+#pragma unroll 1
+    for (int again = 0; again < 2; ++again) {
+        float any = sum;
 #pragma unroll
-    for (int m = 0; m < MB; ++m)
+        for (int m = 0; m < MB; ++m)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) any += o[m][r];
-    if (__syncthreads_or(live && any != any)) {
-            attend(std::true_type());
+            for (int r = 0; r < 16; ++r) any += o[m][r];
+        const bool odd = !(fabsf(any) < kInf);
+        const bool over = max_halves(odd && again == 1 && sum > 0.f && sum < kInf ? 1.f : 0.f) != 0.f;
+        if (!__syncthreads_or(live && (again == 0 ? odd : over))) break;
+        const float top0 = top, sum0 = sum;
+        attend(std::true_type(), over ? top0 : -kInf, over ? 1.f / sum0 : 1.f);
+        if (over) unit = sum0 / sum, top = top0, sum = sum0;
     }
     if constexpr (WK == 2) {  // the second half of the keys joins the first
-        float *const part = reinterpret_cast<float *>(tiles_s) + w * (MB * 16 + 2) * 64 + lane;
-        static_assert(WQ * (MB * 16 + 2) * 64 * 4 <= 2 * TILE * 2, "the tiles' room holds the halves' results");
+        float *const part = reinterpret_cast<float *>(tiles_s) + w * (MB * 16 + 3) * 64 + lane;
+        static_assert(WQ * (MB * 16 + 3) * 64 * 4 <= 2 * TILE * 2, "the tiles' room holds the halves' results");
         __syncthreads();
         if (wk == 1) {
 #pragma unroll
@@ -322,6 +338,7 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a
                 for (int r = 0; r < 16; ++r) part[(m * 16 + r) * 64] = o[m][r];
             part[MB * 16 * 64] = top;
             part[(MB * 16 + 1) * 64] = sum;
+            part[(MB * 16 + 2) * 64] = unit;
         }
         __syncthreads();
         if (wk == 1) return;
@@ -332,14 +349,16 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a
         // maximum, as that passes NaN over, and its sum is NaN
         sum = f0 * sum + f1 * sum1;
         top = mx;
+        // divided before they are added: both may be near the largest number
+        const float inv = sum == 0.f ? 0.f : 1.f / sum, g0 = f0 * unit * inv, g1 = f1 * part[(MB * 16 + 2) * 64] * inv;
 #pragma unroll
         for (int m = 0; m < MB; ++m)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) o[m][r] = f0 * o[m][r] + f1 * part[(m * 16 + r) * 64];
+            for (int r = 0; r < 16; ++r) o[m][r] = g0 * o[m][r] + g1 * part[(m * 16 + r) * 64];
     }
 
     if (!live) return;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const float inv = WK == 2 ? 1.f : sum == 0.f ? 0.f : unit / sum;
     const int64_t row = (sp.q0 + ql) * a.Hq + h;
     if (lse_out && half == 0) lse_out[row] = sum == 0.f ? -kInf : top + __builtin_amdgcn_logf(sum) * kLn2;
 #pragma unroll

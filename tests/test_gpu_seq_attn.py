@@ -514,3 +514,50 @@ def test_lse_of_what_sees_nan(d, j):
     torch.cuda.synchronize()
     assert torch.isnan(lse[j:]).all() and torch.isnan(o[j:].float()).all()
     assert torch.equal(lse[:j], clean[2][:j]) and torch.equal(o[:j], clean[0][:j])
+
+
+@pytest.mark.parametrize("d", [32, 64, 96, 128])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (40, 3)])
+@pytest.mark.parametrize("hurt", [False, True])
+def test_values_near_the_largest(d, window, sinks, hurt):
+    """An output is a mean of its values: finite however large they are, though their sum before the
+    division is not; with a NaN in a key beside them (hurt), for the queries that do not see it."""
+    rng = rng_of("seq-big", d, window)
+    n, j = 150, 100
+    qo = offsets([n])
+    q_d, q = bf16(rng, n, 2, d)
+    k_d, k = bf16(rng, n, 1, d)
+    v_d, _ = bf16(rng, n, 1, d)
+    bits = synth.f32_to_bf16_bits((3e38 * rng.uniform(-1, 1, (n, 1, d))).astype(np.float32))
+    b_d, b = to_dev(bits), synth.bf16_bits_to_f32(bits).astype(np.float64)
+    scale = float(np.float32(2.0 / np.sqrt(d)))  # maxima that move: the reference starts up to 8 below
+    how = dict(window=window, sinks=sinks, scale=scale)
+    ref = seq.seq_attn(q, k, b, qo, qo[:-1], qo[1:], window, sinks, scale)
+    if hurt:
+        k_d[j, 0, 3] = float("nan")
+    say(f"[seq] large values d={d} window={window} hurt={hurt}")
+    o, _, lse = dlrm_seq_attn_fwd(q_d, k_d, b_d, to_dev(qo), for_backward=True, **how)
+    _, _, lse0 = dlrm_seq_attn_fwd(q_d, k_d, v_d, to_dev(qo), for_backward=True, **how)
+    torch.cuda.synchronize()
+    i = np.arange(n)
+    free = ~((i >= j) & ((window == 0) | (i - j < window))) if hurt else np.ones(n, bool)
+    gate = 2.0 ** -7 + 2 * e_of(d, ref) + 2.0 ** -16
+    assert rel_err(host(o)[free], ref["o"][free], ref["o_s"][free]) <= gate
+    assert torch.equal(lse.cpu()[torch.from_numpy(free)], lse0.cpu()[torch.from_numpy(free)])  # the values are not in it
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("longest", [1, 5000])
+def test_decode_of_values_near_the_largest(d, longest):
+    """As above for one event, unsplit and split."""
+    rng = rng_of("dec-big", d)
+    ko = offsets([1, 40, 5000])
+    q_d, q = bf16(rng, 3, 4, d)
+    k_d, k = bf16(rng, ko[-1], 2, d)
+    bits = synth.f32_to_bf16_bits((3e38 * rng.uniform(0.5, 1, (ko[-1], 2, d))).astype(np.float32))
+    v_d, v = to_dev(bits), synth.bf16_bits_to_f32(bits).astype(np.float64)
+    ref = seq.seq_attn(q, k, v, np.arange(4), ko[:-1], ko[1:], 0, 0, float(np.float32(1 / np.sqrt(d))))
+    say(f"[seq] decode of large values d={d} longest={longest}")
+    o = dlrm_seq_attn_decode(q_d, k_d, v_d, to_dev(ko[:-1]), to_dev(ko[1:]), max_kv_len=longest)
+    torch.cuda.synchronize()
+    assert rel_err(host(o), ref["o"], ref["o_s"]) <= 2.0 ** -7 + 2 * e_of(d, ref) + 2.0 ** -16
