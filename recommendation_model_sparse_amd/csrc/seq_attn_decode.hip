@@ -336,9 +336,11 @@ int launch(const Args &a, const Split &sp, uint16_t *o, void *ws, hipStream_t st
     const dim3 grid = splits_first ? dim3(splits, static_cast<uint32_t>(blocks)) : dim3(static_cast<uint32_t>(blocks), splits);
     DLRM_LAUNCH("seq_attn_decode", (k_seq_attn_decode<DP>), grid, dim3(kWaves * 64), 0, stream, a,
                 splits, sp.quantum, splits_first, head_groups, o, part, ml);
-    if (splits > 1)
-        DLRM_LAUNCH("seq_decode_join", k_seq_decode_join, dim3(static_cast<uint32_t>(rows)), dim3(256), 0, stream,
-                    static_cast<const float *>(part), static_cast<const float2 *>(ml), splits, a.d, o);
+    constexpr int64_t most = (int64_t(1) << 24) - 1;  // workgroups of 256 below 2^32 work-items
+    for (int64_t row0 = 0; splits > 1 && row0 < rows; row0 += most)
+        DLRM_LAUNCH("seq_decode_join", k_seq_decode_join, dim3(static_cast<uint32_t>(rows - row0 < most ? rows - row0 : most)), dim3(256),
+                    0, stream, static_cast<const float *>(part + row0 * splits * a.d),
+                    static_cast<const float2 *>(ml + row0 * splits), splits, a.d, o + row0 * a.d);
     return launch_status();
 }
 

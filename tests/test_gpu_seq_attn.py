@@ -561,3 +561,27 @@ def test_decode_of_values_near_the_largest(d, longest):
     o = dlrm_seq_attn_decode(q_d, k_d, v_d, to_dev(ko[:-1]), to_dev(ko[1:]), max_kv_len=longest)
     torch.cuda.synchronize()
     assert rel_err(host(o), ref["o"], ref["o_s"]) <= 2.0 ** -7 + 2 * e_of(d, ref) + 2.0 ** -16
+
+
+def test_decode_past_one_launch_of_the_join():
+    """2^24 rows of a head are 2^32 work-items in the join of a sequence's runs, and so more than one launch.
+    max_kv_len only chooses the split: unsplit, the same sequences give the same, but for the output's rounding
+    (2^-7 of it) and that of sums near 0."""
+    if torch.cuda.mem_get_info()[0] < 8 << 30:
+        pytest.skip("8 GiB of free memory")
+    rng = rng_of("dec-join")
+    B, Hq, d = (1 << 21) + 3, 8, 8
+    few, _ = bf16(rng, 1021, Hq, d)
+    q = few.repeat(B // 1021 + 1, 1, 1)[:B]
+    k, _ = bf16(rng, 64, 1, d)
+    v, _ = bf16(rng, 64, 1, d)
+    begin = torch.arange(B, device=DEV) % 50
+    end = begin + 1 + torch.arange(B, device=DEV) % 7
+    say(f"[seq] decode B={B} Hq={Hq}")
+    got = dlrm_seq_attn_decode(q, k, v, begin, end, max_kv_len=(1 << 20) + 1)
+    torch.cuda.synchronize()
+    want = dlrm_seq_attn_decode(q, k, v, begin, end, max_kv_len=10)
+    torch.cuda.synchronize()
+    most = float(v.abs().max())
+    for a, b in zip(got.split(1 << 18), want.split(1 << 18)):
+        assert ((a.float() - b.float()).abs() <= 2.0 ** -7 * b.float().abs() + 2.0 ** -16 * most).all()
