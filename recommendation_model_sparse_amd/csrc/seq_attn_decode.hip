@@ -11,6 +11,8 @@
 // Measured: 32 sequences of 32768 to 65536, 8 heads of 128 over 1: 151 us, 5.3 TB/s, the rate of a large
 // copy, and 12 for the join; 256 of 64 to 8192, 8 heads of 64 over 2: 48 us, 4.3 TB/s, and 6.6; one
 // of 150 to 200, 4 heads of 32: 8.6 us, a chain of waits for memory.
+#include <algorithm>
+
 #include "seq.h"
 
 namespace dlrm {
@@ -311,8 +313,12 @@ struct Split {
     int runs, quantum;
 };
 
+// Workgroups of a run of every sequence.
+int64_t blocks_of(int64_t B, int32_t Hq, int32_t Hkv) { return B * Hkv * ((Hq / Hkv + kHeads - 1) / kHeads); }
+constexpr int64_t kMostBlocks = (int64_t(1) << 24) - 1;  // of 256 threads: a launch holds fewer than 2^32 work-items
+
 Split split_of(int64_t B, int32_t Hq, int32_t Hkv, int32_t window, int32_t sinks, int64_t max_kv_len) {
-    const int64_t blocks = B * Hkv * ((Hq / Hkv + kHeads - 1) / kHeads);
+    const int64_t blocks = blocks_of(B, Hq, Hkv);
     int64_t seen = max_kv_len < (int64_t(1) << 30) ? max_kv_len : int64_t(1) << 30;
     if (window > 0 && static_cast<int64_t>(window) + sinks < seen) seen = static_cast<int64_t>(window) + sinks;
     int64_t quantum = (blocks * seen / 4096 + kChunk * kWaves - 1) / (kChunk * kWaves) * (kChunk * kWaves);
@@ -325,8 +331,7 @@ template <int DP>
 int launch(const Args &a, const Split &sp, uint16_t *o, void *ws, hipStream_t stream) {
     const int splits = sp.runs;
     const int head_groups = (a.group + kHeads - 1) / kHeads;
-    const int64_t rows = static_cast<int64_t>(a.B) * a.Hq, blocks = static_cast<int64_t>(a.B) * a.Hkv * head_groups;
-    if (blocks >= (int64_t(1) << 24)) return DLRM_ERR_UNSUPPORTED;  // a launch holds fewer than 2^32 work-items
+    const int64_t rows = static_cast<int64_t>(a.B) * a.Hq, blocks = blocks_of(a.B, a.Hq, a.Hkv);
     float *part = static_cast<float *>(ws);
     float2 *ml = reinterpret_cast<float2 *>(part ? part + rows * splits * a.d : nullptr);
     // Many sequences: the first runs of all start first, as every one of them has keys; the runs that only
@@ -336,9 +341,8 @@ int launch(const Args &a, const Split &sp, uint16_t *o, void *ws, hipStream_t st
     const dim3 grid = splits_first ? dim3(splits, static_cast<uint32_t>(blocks)) : dim3(static_cast<uint32_t>(blocks), splits);
     DLRM_LAUNCH("seq_attn_decode", (k_seq_attn_decode<DP>), grid, dim3(kWaves * 64), 0, stream, a,
                 splits, sp.quantum, splits_first, head_groups, o, part, ml);
-    constexpr int64_t most = (int64_t(1) << 24) - 1;  // workgroups of 256 below 2^32 work-items
-    for (int64_t row0 = 0; splits > 1 && row0 < rows; row0 += most)
-        DLRM_LAUNCH("seq_decode_join", k_seq_decode_join, dim3(static_cast<uint32_t>(rows - row0 < most ? rows - row0 : most)), dim3(256),
+    for (int64_t row0 = 0; splits > 1 && row0 < rows; row0 += kMostBlocks)
+        DLRM_LAUNCH("seq_decode_join", k_seq_decode_join, dim3(static_cast<uint32_t>(std::min(rows - row0, kMostBlocks))), dim3(256),
                     0, stream, static_cast<const float *>(part + row0 * splits * a.d),
                     static_cast<const float2 *>(ml + row0 * splits), splits, a.d, o + row0 * a.d);
     return launch_status();
@@ -352,7 +356,7 @@ extern "C" size_t dlrm_seq_attn_decode_workspace_size(int64_t B, int32_t Hq, int
                                                       int32_t sinks, int64_t max_kv_len) {
     using namespace dlrm::seq;
     if (B < 0 || B >= (1 << 24) || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Hq > 4096 || d < 1 || d > 128 || window < 0 || sinks < 0 ||
-        max_kv_len < 0)
+        max_kv_len < 0 || blocks_of(B, Hq, Hkv) > kMostBlocks)
         return 0;
     const int splits = split_of(B, Hq, Hkv, window, sinks, max_kv_len).runs;
     return 256 + (splits > 1 ? static_cast<size_t>(B) * Hq * splits * (d + 2) * 4 : 0);
@@ -368,6 +372,7 @@ extern "C" int dlrm_seq_attn_decode(const dlrm_seq_attn *desc, int64_t max_kv_le
     if (a.Nq != a.B || max_kv_len < 0) return DLRM_ERR_INVALID_ARG;
     if (a.B == 0) return DLRM_OK;
     if (!o || !aligned(o, 16)) return DLRM_ERR_INVALID_ARG;
+    if (blocks_of(a.B, a.Hq, a.Hkv) > kMostBlocks) return DLRM_ERR_UNSUPPORTED;
     const Split sp = split_of(a.B, a.Hq, a.Hkv, a.window, a.sinks, max_kv_len);
     if (sp.runs > 1 && (!workspace || !aligned(workspace, 256) ||
                        workspace_bytes < dlrm_seq_attn_decode_workspace_size(a.B, a.Hq, a.Hkv, a.d, a.window, a.sinks, max_kv_len)))

@@ -164,3 +164,14 @@ def test_backward_without_queries_takes_no_tiles(L, bias):
     assert need == L.dlrm_seq_attn_bwd_workspace_size(ctypes.byref(attn(B=0, Nq=0, Nkv=0, bias=bias)))  # no slots of queries
     if bias is None:
         assert L.dlrm_seq_attn_bwd(ctypes.byref(a), *[None] * 8, FAKE, need, None) == OK
+
+
+def test_decode_sizes_past_one_launch(L):
+    """Refused sizes have a workspace of 0, as the header says, not of what their product wraps to; they are
+    refused whatever the workspace."""
+    size = L.dlrm_seq_attn_decode_workspace_size
+    assert size((1 << 24) - 1, 1, 1, 8, 0, 0, 1 << 20) > 0
+    for B, Hq, Hkv in (((1 << 24) - 1, 4096, 4096), (1 << 20, 256, 16), (1 << 20, 17 * 8, 8)):
+        assert size(B, Hq, Hkv, 8, 0, 0, 1 << 30) == 0
+        a = attn(B=B, Nq=B, Hq=Hq, Hkv=Hkv, d=8, q_row=Hq * 8, q_head=8, k_row=Hkv * 8, k_head=8, v_row=Hkv * 8, v_head=8)
+        assert L.dlrm_seq_attn_decode(ctypes.byref(a), 1 << 30, FAKE, None, 0, None) == UNSUPPORTED
