@@ -811,8 +811,8 @@ def _head_rows(t, name: str, heads: Optional[int] = None, d: Optional[int] = Non
         raise ValueError(f"{name} must have packed heads (stride 1 in the last dimension)")
     if H == 1 or not rows:  # the stride of a dimension of one entry is of no account
         head = w
-    if rows < 2:
-        row = max(H * head, w)
+    if rows < 2:  # as is that of one row: H * head may pass the limit on row strides
+        row = w
     return rows, H, w, row, head
 
 

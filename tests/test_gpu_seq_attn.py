@@ -585,3 +585,23 @@ def test_decode_past_one_launch_of_the_join():
     most = float(v.abs().max())
     for a, b in zip(got.split(1 << 18), want.split(1 << 18)):
         assert ((a.float() - b.float()).abs() <= 2.0 ** -7 * b.float().abs() + 2.0 ** -16 * most).all()
+
+
+def test_one_row_of_heads_far_apart():
+    """A tensor of one row has no row stride to refuse: heads 2^22 elements apart, forward and for one event."""
+    rng = rng_of("seq-one-row")
+    H, d = 4, 64
+    far = torch.zeros((H, (1 << 22) // d, d), dtype=torch.bfloat16, device=DEV)
+    q_d, _ = bf16(rng, 1, H, d)
+    k_d, _ = bf16(rng, 1, H, d)
+    v_d, _ = bf16(rng, 90, H, d)
+    far[:, :1] = q_d.transpose(0, 1)
+    q2 = far.transpose(0, 1)[:1]
+    one, off = to_dev(offsets([1])), to_dev(offsets([90]))
+    say("[seq] one row of far heads")
+    a = dlrm_seq_attn_fwd(q2, v_d, v_d, one, off), dlrm_seq_attn_decode(q2, v_d, v_d, off[:1], off[1:])
+    b = dlrm_seq_attn_fwd(q_d, v_d, v_d, one, off), dlrm_seq_attn_decode(q_d, v_d, v_d, off[:1], off[1:])
+    far[:, :1] = k_d.transpose(0, 1)
+    c, e = dlrm_seq_attn_fwd(q_d, q2, q2, one), dlrm_seq_attn_fwd(q_d, k_d, k_d, one)
+    torch.cuda.synchronize()
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and torch.equal(c, e)

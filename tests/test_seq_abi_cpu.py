@@ -175,3 +175,10 @@ def test_decode_sizes_past_one_launch(L):
         assert size(B, Hq, Hkv, 8, 0, 0, 1 << 30) == 0
         a = attn(B=B, Nq=B, Hq=Hq, Hkv=Hkv, d=8, q_row=Hq * 8, q_head=8, k_row=Hkv * 8, k_head=8, v_row=Hkv * 8, v_head=8)
         assert L.dlrm_seq_attn_decode(ctypes.byref(a), 1 << 30, FAKE, None, 0, None) == UNSUPPORTED
+
+
+def test_strides_of_one_row_are_of_no_account():
+    far = torch.zeros((4, 65536, 64), dtype=torch.bfloat16)
+    assert binding._head_rows(far.transpose(0, 1)[:1], "q") == (1, 4, 64, 64, 65536 * 64)
+    assert binding._head_rows(far[:1].transpose(0, 1)[:1], "q") == (1, 1, 64, 64, 64)
+    assert binding._head_rows(far.transpose(0, 1)[:2], "q") == (2, 4, 64, 64, 65536 * 64)
