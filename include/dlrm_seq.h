@@ -159,7 +159,8 @@ int dlrm_dropout(const void *x, int32_t dtype, int64_t n, const dlrm_dropout_spe
  *   x [M][D] of x_dtype (F32 or BF16);  residual [M][D] of res_dtype or NULL (zeros);  w [D] fp32
  *   s [M][D] of res_dtype (may be residual), or NULL: not written;  rstd [M] fp32 or NULL
  *   y [M][D] of y_dtype: F32, BF16, or F8_E4M3 with y_scale [M] fp32: y = q * y_scale[row],
- *   y_scale = max_c |y| / 448 (1 for a row of zeros); y_scale is not read for the other types.
+ *   y_scale = max_c |y| / 448 (1 for a row of zeros, at least 2^-149) and q the fp32 quotient
+ *   y / y_scale, rounded to nearest even; y_scale is not written for the other types.
  *   The norm is taken of s as rounded, so that the backward, which has only that, agrees.
  *   Limits: M >= 0, 1 <= D <= 16384; buffers 16-byte aligned.
  */

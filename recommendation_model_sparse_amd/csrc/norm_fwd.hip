@@ -79,14 +79,29 @@ __global__ __launch_bounds__(256) void k_add_rmsnorm_fwd(const void *x, const vo
     }
     if constexpr (Size<Y>::bytes == 1) {
         most = over_row<L>(most, part, Max());
-        const float f = most == 0.f ? 1.f : 448.f / most;  // infinite for a row below 1.3e-36
-        if (lane == 0) y_scale[row] = most == 0.f ? 1.f : most / 448.f;
+        // divided by the scale as it is stored, which a product with 448 / most misses by an 8-bit step here and
+        // there (12 of 2^24).  One reciprocal a row and a correction by the remainder give the rounded quotient
+        // (Markstein, 1990) while nothing leaves the normal numbers (what is smaller than the scale by 2^12 is 0
+        // in 8 bits either way); a division an element took 27.3 us where this takes 24.3 (16384 of 1024).  A
+        // scale below the normal numbers is kept above 0, and its quotients within range.
+        const float scale = most == 0.f ? 1.f : fmaxf(most / 448.f, 0x1p-149f), inverse = 1.f / scale;
+        const bool normal = scale > 0x1p-90f && scale < 0x1p100f;
+        if (lane == 0) y_scale[row] = scale;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int c = column<L, N, V>(i);
             if (c >= D) continue;
 #pragma unroll
-            for (int j = 0; j < V; ++j) h[i * V + j] = f <= 3.4e38f ? h[i * V + j] * f : h[i * V + j] / most * 448.f;
+            for (int j = 0; j < V; ++j) {
+                float q = h[i * V + j] * inverse;
+                if (normal) {
+                    q = fmaf(fmaf(-q, scale, h[i * V + j]), inverse, q);
+                } else {
+                    q = h[i * V + j] / scale;
+                    q = fabsf(q) > 448.f ? copysignf(448.f, q) : q;
+                }
+                h[i * V + j] = q;
+            }
             store<F8, V>(y, row * D + c, h + i * V);
         }
     }

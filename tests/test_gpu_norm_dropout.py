@@ -296,3 +296,36 @@ def test_norm_past_one_launch():
     _, y1, rstd1, _ = dlrm_add_rmsnorm_fwd(some, None, w_d, 1e-5)
     for a in (at, M - 400):
         assert torch.equal(y[a:a + 400], y1) and torch.equal(rstd[a:a + 400], rstd1)
+
+
+@pytest.mark.parametrize("M,D,xt", [(4096, 4096, H), (16384, 1024, F), (4096, 2001, F)])
+def test_norm_8bit_is_the_quotient(M, D, xt):
+    """The 8-bit values are y / y_scale in fp32, rounded once: bit for bit, with the fp32 y that the same
+    call gives and the scale as stored."""
+    rng = rng_of("norm8-quotient", M, D)
+    x_d, _ = draw(rng, xt, M, D)
+    w_d, _ = draw(rng, F, D)
+    say(f"[norm8] quotient M={M} D={D} {xt}")
+    _, q, _, scale = dlrm_add_rmsnorm_fwd(x_d, None, w_d, 1e-5, y_dtype=E)
+    _, y, _, _ = dlrm_add_rmsnorm_fwd(x_d, None, w_d, 1e-5, y_dtype=F)
+    torch.cuda.synchronize()
+    want = (y.cpu() / scale.cpu()[:, None]).to(E)
+    off = (q.cpu().view(torch.uint8) != want.view(torch.uint8)).sum().item()
+    say(f"   {off} of {M * D} differ")
+    assert off == 0
+
+
+@pytest.mark.parametrize("size", [1e-40, 1e-42, 1e-44])
+def test_norm_8bit_rows_below_the_normal_numbers(size):
+    """Scales that are a few times the smallest number, or would round to 0: every value is within half of
+    448 such steps (the scale's rounding) and an 8-bit step."""
+    rng = rng_of("tiny8", size)
+    x = rng.standard_normal((5, 256)).astype(np.float32)
+    w = np.full(256, size, np.float32)
+    say(f"[norm8 below normal] size={size}")
+    _, y, _, scale = dlrm_add_rmsnorm_fwd(to_dev(x), None, to_dev(w), 1e-6, y_dtype=E)
+    _, y32, _, _ = dlrm_add_rmsnorm_fwd(to_dev(x), None, to_dev(w), 1e-6, y_dtype=F)
+    torch.cuda.synchronize()
+    sc, ref = scale.cpu().numpy().astype(np.float64), host(y32)
+    assert (sc >= 2.0 ** -149).all() and np.isfinite(host(y)).all()
+    assert (np.abs(host(y) * sc[:, None] - ref) <= 2.0 ** -4 * np.abs(ref) + 225 * 2.0 ** -149).all()
