@@ -195,7 +195,17 @@ class HistoryCache:
 
     def prefill(self, ids: torch.Tensor, offsets: torch.Tensor, longest_new: int) -> torch.Tensor:
         """Encodes the users' new events (jagged, offsets [users + 1], at most longest_new each) against
-        what the cache holds; returns each user's vector [users, D] (of a user with no new event: nothing)."""
+        what the cache holds; returns each user's vector [users, D] (of a user with no new event: nothing).
+        The lengths are checked on the host, which waits for the device once: a count past longest_new or a
+        region's end would be written into the next user's."""
+        if offsets.shape != (self.users + 1,):
+            raise ValueError(f"offsets must have {self.users + 1} entries, got {tuple(offsets.shape)}")
+        off = offsets.cpu().numpy()
+        count = np.diff(off)
+        if off[0] != 0 or off[-1] != ids.numel() or (count < 0).any():
+            raise ValueError(f"offsets must rise from 0 to the number of events, {ids.numel()}")
+        if count.max(initial=0) > longest_new:
+            raise ValueError(f"longest_new is {longest_new}, but a user has {count.max()} new events")
         if self.longest + longest_new > self.capacity:
             raise ValueError(f"{self.longest} + {longest_new} events do not fit a capacity of {self.capacity}")
         enc, count = self.enc, offsets.diff()

@@ -126,3 +126,41 @@ def test_it_learns():
     """Guessing the base rate gives the clicks' entropy (0.69 at most); a model that finds the event goes below."""
     first, last = main()
     assert last < 0.75 * first
+
+
+def serving(rng, users, capacity, **over):
+    enc = HistoryEncoder(Shape(events=500, D=64, layers=2, **over), DEV, 5)
+    return enc, enc.cache(users, capacity)
+
+
+def visit(rng, counts, dtype=np.int64):
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(dtype)
+    return torch.from_numpy(rng.integers(0, 500, off[-1])).to(DEV), torch.from_numpy(off).to(DEV)
+
+
+def test_prefill_refuses_what_would_leave_a_region():
+    """More new events than longest_new says, or than a user's region holds: refused, and no other
+    user's keys are touched."""
+    rng = np.random.default_rng(11)
+    enc, cache = serving(rng, 3, 64)
+    cache.prefill(*visit(rng, [10, 20, 30]), 30)
+    held = lambda: [t.view(torch.int16).clone() for t in cache.k + cache.v] + [cache.end]  # noqa: E731
+    before = held()
+    say("[history] prefill past a region")
+    for counts, longest in (([60, 1, 1], 1), ([1, 50, 1], 49), ([1, 50, 1], 50)):
+        with pytest.raises(ValueError):
+            cache.prefill(*visit(rng, counts), longest)
+    torch.cuda.synchronize()
+    for x, y in zip(before, held()):
+        assert torch.equal(x, y)
+
+
+def test_prefill_refuses_offsets_that_are_not_the_events():
+    rng = np.random.default_rng(15)
+    enc, cache = serving(rng, 3, 64)
+    ids, off = visit(rng, [10, 20, 30])
+    say("[history] prefill refusals")
+    for i, o in ((ids[:-1], off), (ids, off + 1), (ids, off[:-1]), (ids, off[[0, 2, 1, 3]])):
+        with pytest.raises(ValueError):
+            cache.prefill(i, o, 30)
+    assert torch.equal(cache.end, cache.begin)
