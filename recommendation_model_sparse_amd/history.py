@@ -200,14 +200,16 @@ class HistoryCache:
         region's end would be written into the next user's."""
         if offsets.shape != (self.users + 1,):
             raise ValueError(f"offsets must have {self.users + 1} entries, got {tuple(offsets.shape)}")
-        off = offsets.cpu().numpy()
+        host = torch.cat((self.end - self.begin, offsets)).cpu().numpy()
+        held, off = host[:self.users], host[self.users:]
         count = np.diff(off)
         if off[0] != 0 or off[-1] != ids.numel() or (count < 0).any():
             raise ValueError(f"offsets must rise from 0 to the number of events, {ids.numel()}")
         if count.max(initial=0) > longest_new:
             raise ValueError(f"longest_new is {longest_new}, but a user has {count.max()} new events")
-        if self.longest + longest_new > self.capacity:
-            raise ValueError(f"{self.longest} + {longest_new} events do not fit a capacity of {self.capacity}")
+        longest = int((held + count).max(initial=0))
+        if longest > self.capacity:
+            raise ValueError(f"a history of {longest} events does not fit a capacity of {self.capacity}")
         enc, count = self.enc, offsets.diff()
         at = torch.arange(ids.numel(), device=enc.dev) + torch.repeat_interleave(self.end - offsets[:-1], count, output_size=ids.numel())
         end = self.end + count
@@ -217,7 +219,7 @@ class HistoryCache:
             return L.dlrm_seq_attn_fwd(q, self.k[i], self.v[i], offsets, (self.begin, end), **enc._how(layer)), None
 
         x, s, _ = enc._layers(enc._events(ids), attend)
-        self.end, self.longest = end, self.longest + longest_new
+        self.end, self.longest = end, longest
         last = (offsets[1:] - 1).clamp(min=0)
         return enc._norm(x[last], s[last], enc.w, False)[1]
 

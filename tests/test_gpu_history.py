@@ -164,3 +164,17 @@ def test_prefill_refuses_offsets_that_are_not_the_events():
         with pytest.raises(ValueError):
             cache.prefill(i, o, 30)
     assert torch.equal(cache.end, cache.begin)
+
+
+def test_prefill_takes_what_fits():
+    """The longest history is that of a user, not the sum of the visits' longest."""
+    rng = np.random.default_rng(12)
+    enc, cache = serving(rng, 2, 64)
+    say("[history] prefill of what fits")
+    cache.prefill(*visit(rng, [50, 5]), 50)
+    cache.prefill(*visit(rng, [5, 50]), 50)
+    assert cache.longest == 55
+    for _ in range(9):
+        cache.append(torch.from_numpy(rng.integers(0, 500, 2)).to(DEV))
+    with pytest.raises(ValueError):
+        cache.append(torch.from_numpy(rng.integers(0, 500, 2)).to(DEV))
