@@ -195,7 +195,7 @@ class HistoryCache:
 
     def prefill(self, ids: torch.Tensor, offsets: torch.Tensor, longest_new: int) -> torch.Tensor:
         """Encodes the users' new events (jagged, offsets [users + 1], at most longest_new each) against
-        what the cache holds; returns each user's vector [users, D] (of a user with no new event: nothing).
+        what the cache holds; returns each user's vector [users, D] (zeros for a user with no new event).
         The lengths are checked on the host, which waits for the device once: a count past longest_new or a
         region's end would be written into the next user's."""
         if offsets.shape != (self.users + 1,):
@@ -210,6 +210,8 @@ class HistoryCache:
         longest = int((held + count).max(initial=0))
         if longest > self.capacity:
             raise ValueError(f"a history of {longest} events does not fit a capacity of {self.capacity}")
+        if ids.numel() == 0:
+            return torch.zeros((self.users, self.enc.c.D), dtype=torch.bfloat16, device=self.enc.dev)
         enc, count = self.enc, offsets.diff()
         at = torch.arange(ids.numel(), device=enc.dev) + torch.repeat_interleave(self.end - offsets[:-1], count, output_size=ids.numel())
         end = self.end + count
@@ -221,7 +223,8 @@ class HistoryCache:
         x, s, _ = enc._layers(enc._events(ids), attend)
         self.end, self.longest = end, longest
         last = (offsets[1:] - 1).clamp(min=0)
-        return enc._norm(x[last], s[last], enc.w, False)[1]
+        y = enc._norm(x[last], s[last], enc.w, False)[1]
+        return torch.where(count[:, None] > 0, y, 0)
 
     def append(self, ids: torch.Tensor, eight_bit: bool = False):
         """One new event of every user; returns their vectors [users, D] bf16, or with eight_bit 8-bit

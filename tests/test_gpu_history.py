@@ -178,3 +178,26 @@ def test_prefill_takes_what_fits():
         cache.append(torch.from_numpy(rng.integers(0, 500, 2)).to(DEV))
     with pytest.raises(ValueError):
         cache.append(torch.from_numpy(rng.integers(0, 500, 2)).to(DEV))
+
+
+def test_users_without_a_new_event():
+    """Their vectors are 0, not another user's; the others' are as without them."""
+    rng = np.random.default_rng(13)
+    enc, cache = serving(rng, 4, 64)
+    first = visit(rng, [10, 20, 30, 5])
+    cache.prefill(*first, 30)
+    ids, off = visit(rng, [0, 7, 0, 3])
+    say("[history] users without a new event")
+    got = cache.prefill(ids, off, 7)
+    assert (got[[0, 2]] == 0).all() and (got[[1, 3]] != 0).any(1).all()
+    assert torch.equal((cache.end - cache.begin).cpu(), torch.tensor([10, 27, 30, 8]))
+
+
+def test_no_new_event_at_all():
+    rng = np.random.default_rng(14)
+    enc, cache = serving(rng, 3, 64)
+    cache.prefill(*visit(rng, [10, 20, 30]), 30)
+    end = cache.end.clone()
+    say("[history] no new event at all")
+    got = cache.prefill(*visit(rng, [0, 0, 0]), 0)
+    assert got.shape == (3, 64) and got.dtype == torch.bfloat16 and (got == 0).all() and torch.equal(cache.end, end)
