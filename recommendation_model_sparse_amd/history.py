@@ -107,9 +107,9 @@ class HistoryEncoder:
         x = qkv.view(-1, self.c.Hq + 2 * self.c.Hkv, self.d)
         return x[:, :self.c.Hq], x[:, self.c.Hq:self.c.Hq + self.c.Hkv], x[:, self.c.Hq + self.c.Hkv:]
 
-    def _layers(self, x, attend, drop=False):
+    def _layers(self, x, attend, drop=False, keep=False):
         """The layers over event rows x; attend(i, layer, q, k, v) gives the attention's output and what
-        its backward wants.  Returns the last sum's branch, the sum, and what each layer saved."""
+        its backward wants.  Returns the last sum's branch, the sum, and (keep) what each layer's backward wants."""
         s, saved = None, []
         for i, layer in enumerate(self.layers):
             s, y1, n1, _ = self._norm(x, s, layer["w1"], drop)
@@ -119,7 +119,8 @@ class HistoryEncoder:
             s, y2, n2, _ = self._norm(layer["out"].fwd(o), s, layer["w2"], drop)
             h = layer["up"].fwd(y2, L.DLRM_ACT_RELU)
             x = layer["down"].fwd(h)
-            saved.append((y1, n1, qkv, o, kept, y2, n2, h))
+            if keep:
+                saved.append((y1, n1, qkv, o, kept, y2, n2, h))
         return x, s, saved
 
     # ------------------------------------------------------------------ training
@@ -131,7 +132,7 @@ class HistoryEncoder:
             o, tiles, lse = L.dlrm_seq_attn_fwd(q, k, v, offsets, for_backward=True, **self._how(layer))
             return o, (o, tiles, lse)
 
-        x, s, saved = self._layers(self._events(ids), attend, drop)
+        x, s, saved = self._layers(self._events(ids), attend, drop, keep=True)
         _, y, n, _ = self._norm(x, s, self.w, drop)
         last = offsets[1:] - 1
         return y[last], (ids, offsets, last, saved, n)

@@ -201,3 +201,23 @@ def test_no_new_event_at_all():
     say("[history] no new event at all")
     got = cache.prefill(*visit(rng, [0, 0, 0]), 0)
     assert got.shape == (3, 64) and got.dtype == torch.bfloat16 and (got == 0).all() and torch.equal(cache.end, end)
+
+
+def test_serving_keeps_no_activations():
+    """Twelve layers need no more room for a visit than two: nothing reads a layer's activations again."""
+    rng = np.random.default_rng(16)
+    room = []
+    for layers in (2, 12):
+        enc = HistoryEncoder(Shape(events=500, D=128, layers=layers), DEV, 5)
+        cache = enc.cache(16, 512)
+        ids, off = visit(rng, [256] * 16)
+        say(f"[history] room of {layers} layers")
+        cache.prefill(ids, off, 256)
+        torch.cuda.synchronize()
+        held = torch.cuda.memory_allocated()
+        torch.cuda.reset_peak_memory_stats()
+        cache.prefill(ids, off, 256)
+        torch.cuda.synchronize()
+        room.append(torch.cuda.max_memory_allocated() - held)
+    say(f"   {room}")
+    assert room[1] <= 1.1 * room[0]
