@@ -201,6 +201,7 @@ class HistoryCache:
         region's end would be written into the next user's."""
         if offsets.shape != (self.users + 1,):
             raise ValueError(f"offsets must have {self.users + 1} entries, got {tuple(offsets.shape)}")
+        offsets = offsets.to(torch.int64)  # the type of the regions'
         host = torch.cat((self.end - self.begin, offsets)).cpu().numpy()
         held, off = host[:self.users], host[self.users:]
         count = np.diff(off)

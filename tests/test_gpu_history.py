@@ -221,3 +221,14 @@ def test_serving_keeps_no_activations():
         room.append(torch.cuda.max_memory_allocated() - held)
     say(f"   {room}")
     assert room[1] <= 1.1 * room[0]
+
+
+def test_prefill_takes_int32_offsets():
+    """As training does; the same vectors."""
+    rng = np.random.default_rng(17)
+    enc, cache = serving(rng, 3, 64)
+    ids, off = visit(rng, [10, 20, 30])
+    say("[history] int32 offsets")
+    want = cache.prefill(ids, off, 30)
+    got = enc.cache(3, 64).prefill(ids, off.int(), 30)
+    assert torch.equal(got, want)
