@@ -26,8 +26,7 @@ struct Args {
     int32_t B, Hq, Hkv, group, d;
     int32_t idx32;
     int32_t window, sinks;
-    float scale;       // of <q, k>
-    float scale_log2;  // scale * log2(e): the softmax is computed in base 2
+    float scale;  // of <q, k>
     const float *bias;
     int32_t buckets;   // 0 without a bias
     int32_t last;      // first distance of the last bucket: from there on the bias is one value
@@ -38,7 +37,6 @@ struct Args {
 int check_attn(const dlrm_seq_attn *a, bool need_q_offsets, Args *out);
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));

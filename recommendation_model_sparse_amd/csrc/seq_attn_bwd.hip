@@ -791,7 +791,6 @@ extern "C" int dlrm_seq_attn_bwd(const dlrm_seq_attn *desc, const uint16_t *dout
     // the keys' tiles are found by the same offsets as the sequences' ends
     const uintptr_t ib = a.idx32 ? 4 : 8;
     if (a.B > 0 && static_cast<const char *>(a.kv_end) != static_cast<const char *>(a.kv_begin) + ib) return DLRM_ERR_INVALID_ARG;
-    if (static_cast<int64_t>(a.Hq) * a.d >= (1 << 24)) return DLRM_ERR_UNSUPPORTED;
     const Layout l = layout_of(a);
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < l.bytes) return DLRM_ERR_WORKSPACE;
     if (l.qslots == 0 && l.kslots == 0 && !a.buckets) return DLRM_OK;

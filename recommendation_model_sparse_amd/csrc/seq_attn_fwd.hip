@@ -62,7 +62,7 @@ int check_attn(const dlrm_seq_attn *a, bool need_q_offsets, Args *out) {
     constexpr int32_t kFar = 1 << 30;  // past every distance; keeps the kernels' differences in 32 bits
     out->window = a->window < kFar ? a->window : kFar;
     out->sinks = !a->window ? 0 : a->sinks < kFar ? a->sinks : kFar;
-    out->scale = a->scale, out->scale_log2 = a->scale * kLog2e;
+    out->scale = a->scale;
     out->bias = a->bias, out->buckets = a->bias ? a->buckets : 0;
     for (int t = 0; t < out->buckets; ++t) out->bounds[t] = a->bounds[t];
     out->last = out->buckets ? out->bounds[out->buckets - 1] : 0;
