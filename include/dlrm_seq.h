@@ -106,7 +106,7 @@ size_t dlrm_seq_attn_bwd_workspace_size(const dlrm_seq_attn *a);
  *   rows outside every sequence not at all);
  *   dbias [Hq][buckets] fp32 (with a bias; else NULL)
  *   Infinities and NaN in a key that a query does not see have no effect on its dq, and a key that
- *   no query sees has gradients of zero; those of q and dout reach every key near by.
+ *   no query sees has gradients of zero; those of q, dout and lse reach every key near by.
  */
 int dlrm_seq_attn_bwd(const dlrm_seq_attn *a, const uint16_t *dout, const uint16_t *o,
                       const float *lse, const int32_t *tiles, uint16_t *dq, uint16_t *dk,
@@ -162,7 +162,8 @@ int dlrm_dropout(const void *x, int32_t dtype, int64_t n, const dlrm_dropout_spe
  *   y_scale = max_c |y| / 448 (1 for a row of zeros, at least 2^-149) and q the fp32 quotient
  *   y / y_scale, rounded to nearest even; y_scale is not written for the other types.
  *   The norm is taken of s as rounded, so that the backward, which has only that, agrees.
- *   Limits: M >= 0, 1 <= D <= 16384; buffers 16-byte aligned.
+ *   Limits: 0 <= M < 2^31; D from 1 to 16384 in steps of 8, other widths to 4096; buffers 16-byte
+ *   aligned.
  */
 int dlrm_add_rmsnorm_fwd(const void *x, int32_t x_dtype, const void *residual, int32_t res_dtype,
                          const float *w, float eps, const dlrm_dropout_spec *drop, int64_t M, int32_t D,

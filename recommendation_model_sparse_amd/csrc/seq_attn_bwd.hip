@@ -6,10 +6,12 @@
 // P is computed again from Q, K and the saved log-sums.  Two kernels, so that every sum has an owner
 // and no gradient is added to by atomics: one over blocks of queries (delta, dQ, dbias), one over
 // blocks of keys (dK, dV; it walks the query heads that share the key head one after the other).
-// That computes S and dP twice: 7 products of Q x K x d instead of the 5 that one kernel with atomic
-// dQ would need.  Both work on the tiles of the forward: the accumulator of S and dP becomes the
+// That computes S and dP twice, with a bias three times (delta, below): 7 products of Q x K x d, or 9,
+// instead of the 5 that one kernel with atomic dQ would need.  Both work on the tiles of the forward: the accumulator of S and dP becomes the
 // next product's operand in registers, and the transposed operands (K^T; Q^T and dO^T) are read from
-// row-major tiles by transposing LDS loads.
+// row-major tiles by transposing LDS loads.  As operands P and ds are rounded to bf16, as the matrix
+// instruction takes them (fp32's 24 bits would be three products): the gradients are 2.4e-3 from the formulas
+// in 64 bits, of which their own rounding to bf16 is 1.7e-3.
 //
 // delta.  Without a bias it is <dO, o> from the forward's output.  That o is rounded to bf16, which
 // the gradients, rounded to bf16 too, bear; dbias does not: it sums ds over up to every pair, where
@@ -385,9 +387,9 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_bwd_q(const Args
 // key head, and which run of the queries (of all heads that share it) where they are split.
 //
 // OWN: the block's values are read from LDS at every step instead of kept in registers: at heads of 128
-// 47 fewer registers spill (252 -> 224 us on 4 sequences of 2000 to 4096, 8 heads over 2; the keys in
-// LDS too: 228), at heads of 64 a third wavefront fits a SIMD (114 -> 110 us on 1024 sequences of 16
-// to 512, 2 heads).  Heads of 32 fit as they are.
+// 47 fewer registers spill, which leaves 22 (252 -> 224 us on 4 sequences of 2000 to 4096, 8 heads over 2;
+// the keys in LDS too: 228), at heads of 64 a third wavefront fits a SIMD, with 12 (114 -> 110 us on 1024
+// sequences of 16 to 512, 2 heads).  Heads of 32 fit as they are.
 //
 // FAR: the few first keys that every later query sees, and only the queries past the window: a key
 // block of its own would walk all queries of a long sequence after the others are done (4 sequences of

@@ -6,7 +6,8 @@
 // chunks of 32 keys with its own running maximum and sum; their results are joined at the end, those
 // of several runs by a second kernel.  The products are 16x16x32 matrix instructions on transposed
 // tiles, as in the forward: K goes from memory straight into the first operand, P^T stays in
-// registers, and V passes through LDS, each wavefront's own, for the transposed read.
+// registers, and V passes through LDS, each wavefront's own, for the transposed read.  P is rounded to bf16
+// for its product, as there.
 //
 // Measured: 32 sequences of 32768 to 65536, 8 heads of 128 over 1: 151 us, 5.3 TB/s, the rate of a large
 // copy, and 12 for the join; 256 of 64 to 8192, 8 heads of 64 over 2: 48 us, 4.3 TB/s, and 6.6; one
@@ -22,6 +23,10 @@ namespace {
 constexpr int kHeads = 16;  // query heads a workgroup: the columns of a product
 constexpr int kWaves = 4;
 constexpr int kChunk = 32;  // keys a wavefront takes at once
+// Wavefronts a SIMD that the registers have to leave room for: unbound, heads of 64 took 150 and three
+// fitted (256 of 64 to 8192, 8 heads over 2: 48.8 us, with four 47.4).
+template <int DP>
+constexpr int kOcc = DP == 32 ? 5 : DP == 64 ? 4 : 2;
 
 __device__ __forceinline__ float max_quarters(float x) {  // over lanes l, l ^ 16, l ^ 32, l ^ 48
     const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -34,7 +39,7 @@ __device__ __forceinline__ float add_quarters(float x) {
 
 // part: [B][Hq][splits] rows of d floats, the runs' outputs; ml: their (maximum, sum)
 template <int DP>
-__global__ __launch_bounds__(kWaves * 64, DP == 32 ? 5 : DP == 64 ? 4 : 2) void k_seq_attn_decode(const Args a, const int splits, const int quantum, const bool splits_first,
+__global__ __launch_bounds__(kWaves * 64, kOcc<DP>) void k_seq_attn_decode(const Args a, const int splits, const int quantum, const bool splits_first,
                                                                  const int head_groups,
                                                                  uint16_t *o_out, float *part, float2 *ml) {
     constexpr int LP = DP, CH = LP / 8, STEPS = DP / 32, MB = DP / 16, VN = kChunk * CH / 64;

@@ -8,11 +8,13 @@
 // accumulator's column), so the maximum and the sum of a row are sums over registers and one
 // exchange between lanes l and l + 32, and P^T is, as it stands in the registers, the second
 // operand of O^T = V^T P^T.  P never goes through LDS; V^T is read from the row-major tile of V by
-// transposing LDS loads.
+// transposing LDS loads.  P is rounded to bf16 there, as the matrix instruction takes it (fp32's 24 bits would
+// be three products): o is 2.0e-3 from the formula in 64 bits, of which its own rounding to bf16 is 1.6e-3.
 //
-// Bound by waits, half of the wavefronts' cycles: no unit is busy for a third of the time (heads of 64: VALU 30 %, MFMA 7 %, LDS
-// 13 %; of 128: 22, 12, 22).  Measured: 1024 sequences of 16 to 512, 2 heads of 64, 62 us (150 TFLOP/s of
-// the visible pairs' products); 4 of 2000 to 4096, window 1024, 8 heads of 128 over 2, 120 us (305).
+// Bound by waits, half of the wavefronts' cycles: no unit is busy for a third of the time (heads of 64:
+// VALU 30 %, MFMA 7 %, LDS 13 %; of 128: 22, 12, 23).  Measured: 1024 sequences of 16 to 512, 2 heads of
+// 64, 64 us (145 TFLOP/s of the visible pairs' products); 4 of 2000 to 4096, window 1024, 8 heads of 128
+// over 2, 121 us (302).
 #include <type_traits>
 
 #include "seq.h"

@@ -11,13 +11,14 @@ sigmoid head here, or one more row of the dot-product interaction.
     user = norm(s)[last event]
 
 Like dlrm_step, it only orders the calls and owns the weights: every step runs in the library's
-kernels (plain torch indexing moves rows).  The residual stream is fp32, activations and the dense
-layers' weights bf16 with fp32 masters (SGD), the table is updated by row-wise Adagrad.  Histories are
-jagged: event rows laid end to end, with offsets [B + 1].
+kernels, but for what moves data: torch indexes rows, and in the backward joins dq, dk and dv and
+casts them.  The residual stream is fp32, activations and the dense layers' weights bf16 with fp32
+masters (SGD), the table is updated by row-wise Adagrad.  Histories are jagged: event rows laid end
+to end, with offsets [B + 1].
 
 Serving keeps each layer's keys and values in a region of `capacity` rows a user: `prefill` encodes the
-events since the last visit against them, `append` one new event a user, and `append(eight_bit=True)` gives the
-users' vectors as 8-bit rows with scales for a store of candidates.
+events since the last visit against them, `append` one new event a user, and `append(eight_bit=True)`
+gives the users' vectors as 8-bit rows with scales for a store of candidates.
 """
 from __future__ import annotations
 
