@@ -605,3 +605,106 @@ def test_one_row_of_heads_far_apart():
     c, e = dlrm_seq_attn_fwd(q_d, q2, q2, one), dlrm_seq_attn_fwd(q_d, k_d, k_d, one)
     torch.cuda.synchronize()
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and torch.equal(c, e)
+
+
+@pytest.mark.parametrize("d,buckets", [(32, 8), (64, 0), (64, 8), (96, 8), (128, 0), (128, 8)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (40, 3)])
+def test_gradients_beside_hidden_keys(d, buckets, window, sinks):
+    """NaN and infinities in a key change nothing in dq of the queries that do not see it."""
+    rng = rng_of("seq-hidden-grad", d, buckets, window)
+    n = 200
+    qo = to_dev(offsets([n]))
+    q_d, _ = bf16(rng, n, 2, d)
+    k_d, _ = bf16(rng, n, 1, d)
+    v_d, _ = bf16(rng, n, 1, d)
+    g_d, _ = bf16(rng, n, 2, d)
+    how = dict(window=window, sinks=sinks)
+    if buckets:
+        how.update(bias=to_dev(rng.standard_normal((2, buckets)).astype(np.float32)), bounds=dlrm_seq_bucket_bounds(buckets, 32))
+    clean = dlrm_seq_attn_fwd(q_d, k_d, v_d, qo, for_backward=True, **how)
+    dq0 = dlrm_seq_attn_bwd(g_d, q_d, k_d, v_d, *clean, qo, **how)[0]
+    i = np.arange(n)
+    for j, what in ((130, float("nan")), (70, float("inf")), (32, float("-inf")), (199, float("nan"))):
+        for hurt_k in (False, True):
+            k2, v2 = k_d.clone(), v_d.clone()
+            (k2 if hurt_k else v2)[j, 0, 3] = what
+            say(f"[seq] hidden gradients d={d} buckets={buckets} window={window} j={j} {what} k={hurt_k}")
+            kept = dlrm_seq_attn_fwd(q_d, k2, v2, qo, for_backward=True, **how)
+            dq = dlrm_seq_attn_bwd(g_d, q_d, k2, v2, *kept, qo, **how)[0]
+            torch.cuda.synchronize()
+            free = torch.from_numpy(~((i >= j) & ((window == 0) | (i - j < window) | (j < sinks))))
+            assert torch.equal(dq.cpu()[free], dq0.cpu()[free]), (j, what, hurt_k)
+
+
+def test_rows_past_32_bits():
+    """Keys and queries past 2^31 elements of their tensors."""
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("60 GiB of free memory")
+    rng = rng_of("seq-far-rows")
+    Hq, Hkv, d, n = 2, 2, 64, 300
+    rows = (1 << 31) // (Hkv * d) + 1000
+    k = torch.zeros((rows, Hkv, d), dtype=torch.bfloat16, device=DEV)
+    v = torch.zeros((rows, Hkv, d), dtype=torch.bfloat16, device=DEV)
+    q_d, q = bf16(rng, n, Hq, d)
+    k_d, kh = bf16(rng, n, Hkv, d)
+    v_d, vh = bf16(rng, n, Hkv, d)
+    g_d, g = bf16(rng, n, Hq, d)
+    k[rows - n:], v[rows - n:] = k_d, v_d
+    ref = seq.seq_attn(q, kh, vh, [0, n], [0], [n], 50, 3, float(np.float32(d ** -0.5)), do=g)
+    e = e_of(d, ref)
+
+    def check(o, dq, dk, dv):
+        torch.cuda.synchronize()
+        assert rel_err(host(o), ref["o"], ref["o_s"]) <= 2.0 ** -7 + 2 * e + 2.0 ** -16
+        for name, x in (("dq", dq), ("dk", dk), ("dv", dv)):
+            gate = 2.0 ** -7 + 2.0 ** -14 + 4 * e + (2.0 ** -8 if name != "dv" else 0)
+            assert rel_err(host(x), ref[name], ref[name + "_s"]) <= gate, name
+
+    say(f"[seq] rows past 32 bits: {rows}")
+    how = dict(window=50, sinks=3)
+    qo, one = to_dev(offsets([n])), to_dev(np.array([rows - n, rows]))
+    kept = dlrm_seq_attn_fwd(q_d, k, v, qo, one, for_backward=True, **how)
+    dq, dk, dv, _ = dlrm_seq_attn_bwd(g_d, q_d, k, v, *kept, qo, one, **how)
+    check(kept[0], dq, dk[rows - n:], dv[rows - n:])
+    last = dlrm_seq_attn_decode(q_d[-1:], k, v, one[:1], one[1:], max_kv_len=n, **how)
+    torch.cuda.synchronize()
+    assert rel_err(host(last), ref["o"][-1:], ref["o_s"][-1:]) <= 2.0 ** -7 + 2 * e + 2.0 ** -16
+    del dk, dv
+    wide = torch.zeros((rows, Hq, d), dtype=torch.bfloat16, device=DEV)
+    grad = torch.zeros_like(wide)
+    wide[rows - n:], grad[rows - n:] = q_d, g_d
+    kept = dlrm_seq_attn_fwd(wide, k_d, v_d, one, qo, for_backward=True, **how)
+    dq, dk, dv, _ = dlrm_seq_attn_bwd(grad, wide, k_d, v_d, *kept, one, qo, **how)
+    check(kept[0][rows - n:], dq[rows - n:], dk, dv)
+
+
+def test_graph_replays():
+    """A training pass and a step of serving, captured; every replay is the eager result for the inputs as they
+    are then, with eager work and other lengths between the replays."""
+    rng = rng_of("seq-graph")
+    total, H, d = 500, 4, 64
+    q, k, v, g = (bf16(rng, total, H, d)[0] for _ in range(4))
+    bias, bounds = to_dev(rng.standard_normal((H, 8)).astype(np.float32)), dlrm_seq_bucket_bounds(8, 64)
+    off = to_dev(offsets([300, 120, 80]))
+    how = dict(window=100, sinks=2, bias=bias, bounds=bounds)
+
+    def train():
+        kept = dlrm_seq_attn_fwd(q, k, v, off, for_backward=True, **how)
+        return kept + dlrm_seq_attn_bwd(g, q, k, v, *kept, off, **how) + (
+            dlrm_seq_attn_decode(q[:3], k, v, off[:-1], off[1:], max_kv_len=total, **how),)
+
+    train()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = train()
+    for lens in ([300, 120, 80], [10, 490, 0], [1, 2, 497], [300, 120, 80]):
+        off.copy_(to_dev(offsets(lens)))
+        say(f"[seq] replay {lens}")
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in out]
+        want = train()
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            assert torch.equal(x, y)
