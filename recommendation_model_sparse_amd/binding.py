@@ -39,6 +39,9 @@ class DlrmError(RuntimeError):
 
 # dlrm_seq_attn (dlrm_seq.h), field by field
 _SEQ_ATTN = struct.Struct("@3q4i6Q6q2ifi2Q")
+# dlrm_seq_pages (dlrm_seq_pages.h) and dlrm_seq_decay (dlrm_seq_decay.h)
+_SEQ_PAGES = struct.Struct("@3q2i4Q")
+_SEQ_DECAY = struct.Struct("@2q4iQq3Q6qQqf4x")
 
 
 class _Dropout(ctypes.Structure):
@@ -99,6 +102,21 @@ def lib() -> ctypes.CDLL:
             f.restype = ctypes.c_int
         for f in (L.dlrm_seq_attn_bwd_workspace_size, L.dlrm_seq_attn_tiles, L.dlrm_seq_attn_decode_workspace_size,
                   L.dlrm_add_rmsnorm_bwd_workspace_size):
+            f.restype = sz
+        L.dlrm_seq_pages_update_workspace_size.argtypes = [i64, i64]
+        L.dlrm_seq_pages_update.argtypes = [p, p, i32, i64, p, p, p, p, sz, p]
+        L.dlrm_seq_pages_write.argtypes = [p, i64, i64, p, i64, i64, i64, i32, i32, p, p, i64, i64, p, i64, i64, i64, p]
+        L.dlrm_seq_attn_paged_fwd.argtypes = [p, p, p, p]
+        L.dlrm_seq_attn_paged_decode.argtypes = [p, p, i64, p, p, sz, p]
+        L.dlrm_seq_decay_fwd_workspace_size.argtypes = [p]
+        L.dlrm_seq_decay_fwd.argtypes = [p, p, p, p, p, sz, p]
+        L.dlrm_seq_decay_bwd_workspace_size.argtypes = [p]
+        L.dlrm_seq_decay_bwd.argtypes = [p, p, p, p, p, p, p, sz, p]
+        L.dlrm_seq_decay_step.argtypes = [p, p, p, p]
+        for f in (L.dlrm_seq_pages_update, L.dlrm_seq_pages_write, L.dlrm_seq_attn_paged_fwd, L.dlrm_seq_attn_paged_decode,
+                  L.dlrm_seq_decay_fwd, L.dlrm_seq_decay_bwd, L.dlrm_seq_decay_step):
+            f.restype = ctypes.c_int
+        for f in (L.dlrm_seq_pages_update_workspace_size, L.dlrm_seq_decay_fwd_workspace_size, L.dlrm_seq_decay_bwd_workspace_size):
             f.restype = sz
         L.dlrm_status_string.argtypes = [ctypes.c_int]
         L.dlrm_status_string.restype = ctypes.c_char_p
@@ -842,7 +860,8 @@ def _seq_attn(q, k, v, q_offsets, begin, end, B, window, sinks, scale, bias, bou
         raise ValueError(f"q's heads must be a multiple of k's, got {Hq} and {Hkv}")
     if d % 8 or d > 128:
         raise ValueError(f"a head must have a multiple of 8 columns, at most 128, got {d}")
-    if (q_offsets is not None and begin.dtype != q_offsets.dtype) or end.dtype != begin.dtype:
+    index = q_offsets if begin is None else begin  # without ranges the keys are in pages
+    if (q_offsets is not None and index.dtype != q_offsets.dtype) or (begin is not None and end.dtype != begin.dtype):
         raise ValueError("all offsets must have one type")
     if (bias is None) != (bounds is None):
         raise ValueError("bias and bounds go together")
@@ -857,9 +876,9 @@ def _seq_attn(q, k, v, q_offsets, begin, end, B, window, sinks, scale, bias, bou
         edges = array.array("i", bounds)
         at = edges.buffer_info()[0]
     dev = _device(q, k, v, q_offsets, begin, end, bias)
-    code = DLRM_INDEX_I32 if begin.dtype is torch.int32 else DLRM_INDEX_I64
-    desc = _SEQ_ATTN.pack(B, Nq, Nkv, Hq, Hkv, d, code, 0 if q_offsets is None else q_offsets.data_ptr(), begin.data_ptr(),
-                          end.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), q_row, q_head, k_row, k_head, v_row, v_head,
+    code = DLRM_INDEX_I32 if index is not None and index.dtype is torch.int32 else DLRM_INDEX_I64
+    desc = _SEQ_ATTN.pack(B, Nq, Nkv, Hq, Hkv, d, code, 0 if q_offsets is None else q_offsets.data_ptr(),
+                          0 if begin is None else begin.data_ptr(), 0 if end is None else end.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), q_row, q_head, k_row, k_head, v_row, v_head,
                           _count(window, "window"), _count(sinks, "sinks"), d ** -0.5 if scale is None else float(scale), n,
                           0 if bias is None else bias.data_ptr(), at)
     return desc, edges, dev, (Nq, Hq, d), n
@@ -1049,6 +1068,213 @@ def dlrm_add_rmsnorm_bwd(dy: torch.Tensor, ds: Optional[torch.Tensor], s: torch.
                                       _ptr(rstd), ctypes.byref(spec), M, D, _ptr(dx), _TORCH_CODE[xt], _ptr(dresidual),
                                       _ptr(dw), _ptr(ws), ws.numel(), _stream(dev)), "dlrm_add_rmsnorm_bwd")
     return dx, dresidual, dw
+
+
+# ---------------------------------------------------------------- paged histories (dlrm_seq_pages.h)
+
+def _seq_pages(table, lengths, page: int, rows: int, free=None, free_count=None, pages: Optional[int] = None):
+    """The checked description of the users' pages, its device's tensors."""
+    if not isinstance(table, torch.Tensor) or table.dim() != 2 or table.dtype is not torch.int32:
+        raise ValueError("table must be a 2-D tensor of torch.int32 [users, pages of a user]")
+    B, width = table.shape
+    if width > 1 and table.stride(1) != 1:
+        raise ValueError("table must have packed rows")
+    _is(lengths, "lengths", torch.int32, (B,))
+    page = int(page)
+    if page < 8 or page > 4096 or page & (page - 1):
+        raise ValueError(f"page must be a power of two from 8 to 4096, got {page}")
+    if pages is None:
+        pages = rows // page
+        if rows % page or pages < 1:
+            raise ValueError(f"the pool must be whole pages of {page} rows, at least one, got {rows} rows")
+    row = table.stride(0) if B > 1 else width
+    if row < width:
+        raise ValueError("table must have rows of its own for each user")
+    return _SEQ_PAGES.pack(B, pages, row, width, page, table.data_ptr(), lengths.data_ptr(),
+                           0 if free is None else free.data_ptr(), 0 if free_count is None else free_count.data_ptr())
+
+
+def dlrm_seq_pages_update(table: torch.Tensor, lengths: torch.Tensor, free: torch.Tensor, free_count: torch.Tensor, page: int,
+                          offsets: torch.Tensor, n: int, leave: Optional[torch.Tensor] = None, *,
+                          slots: Optional[torch.Tensor] = None, refused: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(slots [n] int64, refused [1] int32): users who leave give their pages back, new events get theirs
+    (C: dlrm_seq_pages_update).  table [users, width], lengths [users], free [pages], free_count [1], all int32, are
+    updated in place; offsets [users+1] of the new events, n at least their last; leave [users] bool.  A refused
+    user's slots are -1."""
+    _offsets(offsets, "offsets")
+    free = _need(free, "free", torch.int32)
+    _is(free_count, "free_count", torch.int32, (1,))
+    if free.dim() != 1 or free.numel() < 1:
+        raise ValueError("free must be 1-D with an entry for each page of the pool, at least one")
+    desc = _seq_pages(table, lengths, page, 0, free, free_count, free.numel())
+    B = lengths.numel()
+    if offsets.numel() != B + 1:
+        raise ValueError(f"offsets must have {B + 1} entries, got {offsets.numel()}")
+    n = _count(n, "n")
+    leave = _opt(leave, "leave", (torch.bool, torch.uint8), (B,))
+    dev = _device(table, lengths, free, free_count, offsets, leave)
+    slots, refused = _out(slots, "slots", torch.int64, (n,), dev), _out(refused, "refused", torch.int32, (1,), dev)
+    ws = _ws(lib().dlrm_seq_pages_update_workspace_size(B, n), dev, workspace)
+    code = DLRM_INDEX_I32 if offsets.dtype is torch.int32 else DLRM_INDEX_I64
+    _check(lib().dlrm_seq_pages_update(desc, _ptr(offsets), code, n, _ptr(leave), _ptr(slots), _ptr(refused), _ptr(ws), ws.numel(),
+                                       _stream(dev)), "dlrm_seq_pages_update")
+    return slots, refused
+
+
+def dlrm_seq_pages_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor) -> None:
+    """Rows of k and v [N, heads, d] to the rows slots [N] of k_pool and v_pool [rows, heads, d]; slots outside
+    are passed over, no two others may be equal (C: dlrm_seq_pages_write)."""
+    N, H, d, k_row, k_head = _head_rows(k, "k")
+    Nv, _, _, v_row, v_head = _head_rows(v, "v", H, d)
+    rows, _, _, kp_row, kp_head = _head_rows(k_pool, "k_pool", H, d)
+    rows_v, _, _, vp_row, vp_head = _head_rows(v_pool, "v_pool", H, d)
+    if Nv != N or rows_v != rows:
+        raise ValueError(f"k and v must have the same rows, and their pools, got {N} and {Nv}, {rows} and {rows_v}")
+    _is(slots, "slots", torch.int64, (N,))
+    dev = _device(k, v, slots, k_pool, v_pool)
+    _check(lib().dlrm_seq_pages_write(_ptr(k), k_row, k_head, _ptr(v), v_row, v_head, N, H, d, _ptr(slots), _ptr(k_pool), kp_row,
+                                      kp_head, _ptr(v_pool), vp_row, vp_head, rows, _stream(dev)), "dlrm_seq_pages_write")
+
+
+def dlrm_seq_attn_paged_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: torch.Tensor, table: torch.Tensor,
+                            lengths: torch.Tensor, page: int, *, window: int = 0, sinks: int = 0, scale: Optional[float] = None,
+                            bias: Optional[torch.Tensor] = None, bounds: Optional[Sequence[int]] = None,
+                            out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dlrm_seq_attn_fwd with keys and values in pages (C: dlrm_seq_attn_paged_fwd): k and v are the pool
+    [pages * page, Hkv, d], table and lengths as dlrm_seq_pages_update left them; the queries are the users'
+    last events."""
+    _offsets(q_offsets, "q_offsets")
+    B = q_offsets.numel() - 1
+    a, edges, dev, shape, _ = _seq_attn(q, k, v, q_offsets, None, None, B, window, sinks, scale, bias, bounds)
+    pg = _seq_pages(table, lengths, page, k.shape[0])
+    if lengths.numel() != B:
+        raise ValueError(f"table and lengths must be of the {B} users of q_offsets, got {lengths.numel()}")
+    _device(q, table, lengths)
+    out = _out(out, "out", torch.bfloat16, shape, dev)
+    _check(lib().dlrm_seq_attn_paged_fwd(a, pg, _ptr(out), _stream(dev)), "dlrm_seq_attn_paged_fwd")
+    return out
+
+
+def dlrm_seq_attn_paged_decode(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lengths: torch.Tensor,
+                               page: int, *, window: int = 0, sinks: int = 0, scale: Optional[float] = None,
+                               bias: Optional[torch.Tensor] = None, bounds: Optional[Sequence[int]] = None,
+                               max_kv_len: Optional[int] = None, out: Optional[torch.Tensor] = None,
+                               workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dlrm_seq_attn_decode with keys and values in pages (C: dlrm_seq_attn_paged_decode): q [B, Hq, d] is one
+    event of each user, the last of those that lengths counts; max_kv_len (None: what the table can hold) only
+    chooses how far a history is split."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be [B, heads, d]")
+    B = q.shape[0]
+    a, edges, dev, shape, _ = _seq_attn(q, k, v, None, None, None, B, window, sinks, scale, bias, bounds)
+    pg = _seq_pages(table, lengths, page, k.shape[0])
+    if lengths.numel() != B:
+        raise ValueError(f"table and lengths must be of q's {B} users, got {lengths.numel()}")
+    _device(q, table, lengths)
+    longest = table.shape[1] * int(page) if max_kv_len is None else int(max_kv_len)
+    if longest < 0:
+        raise ValueError(f"max_kv_len must not be negative, got {longest}")
+    out = _out(out, "out", torch.bfloat16, shape, dev)
+    ws = _ws(lib().dlrm_seq_attn_decode_workspace_size(B, shape[1], k.shape[1], shape[2], window, sinks, longest), dev, workspace)
+    _check(lib().dlrm_seq_attn_paged_decode(a, pg, longest, _ptr(out), _ptr(ws), ws.numel(), _stream(dev)),
+           "dlrm_seq_attn_paged_decode")
+    return out
+
+
+# ---------------------------------------------------------------- linear attention with a decay (dlrm_seq_decay.h)
+
+def _seq_decay(q, k, v, g, offsets, B: int, scale, max_len):
+    """The checked description of a call: (its bytes, device, (N, Hq, d), Hkv)."""
+    N, Hq, d, q_row, q_head = _head_rows(q, "q")
+    Nk, Hkv, _, k_row, k_head = _head_rows(k, "k", None, d)
+    Nv, _, _, v_row, v_head = _head_rows(v, "v", Hkv, d)
+    if Nk != N or Nv != N:
+        raise ValueError(f"q, k and v must have the same rows, got {N}, {Nk} and {Nv}")
+    if Hq % Hkv:
+        raise ValueError(f"q's heads must be a multiple of k's, got {Hq} and {Hkv}")
+    if d % 8 or d > 128:
+        raise ValueError(f"a head must have a multiple of 8 columns, at most 128, got {d}")
+    if not isinstance(g, torch.Tensor) or g.dtype is not torch.float32:
+        raise ValueError("g must be a tensor of torch.float32")
+    if tuple(g.shape) == (Hkv,) and g.is_contiguous():
+        g_row = 0
+    elif tuple(g.shape) == (N, Hkv) and (Hkv == 1 or N == 0 or g.stride(1) == 1):
+        g_row = g.stride(0) if N > 1 else Hkv
+        if g_row < Hkv:
+            raise ValueError("g must have rows of its own for each event; one decay for a head is [heads]")
+    else:
+        raise ValueError(f"g must be [{N}, {Hkv}] with packed rows, or [{Hkv}], got {tuple(g.shape)}")
+    if max_len is not None and max_len < 0:
+        raise ValueError(f"max_len must not be negative, got {max_len}")
+    dev = _device(q, k, v, g, offsets)
+    code = DLRM_INDEX_I32 if offsets is not None and offsets.dtype is torch.int32 else DLRM_INDEX_I64
+    desc = _SEQ_DECAY.pack(B, N, Hq, Hkv, d, code, 0 if offsets is None else offsets.data_ptr(), N if max_len is None else int(max_len),
+                           q.data_ptr(), k.data_ptr(), v.data_ptr(), q_row, q_head, k_row, k_head, v_row, v_head, g.data_ptr(), g_row,
+                           d ** -0.5 if scale is None else float(scale))
+    return desc, dev, (N, Hq, d), Hkv
+
+
+def dlrm_seq_decay_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, offsets: torch.Tensor, *,
+                       scale: Optional[float] = None, state: Optional[torch.Tensor] = None, want_state: bool = False,
+                       max_len: Optional[int] = None, out: Optional[torch.Tensor] = None,
+                       state_out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """Linear attention with a decay over jagged sequences (C: dlrm_seq_decay_fwd): o [N, Hq, d] bf16, or with
+    want_state or state_out (o, the states after each sequence).  q [N, Hq, d], k and v [N, Hkv, d]; g, the logarithms
+    of the decays, <= 0: [N, Hkv], or [Hkv]; state [B, Hkv, d, d] fp32: what sequences begin with, None: zeros;
+    state_out may be state.  max_len: the longest sequence, None: not known; it only chooses how a call works."""
+    _offsets(offsets, "offsets")
+    B = offsets.numel() - 1
+    a, dev, shape, Hkv = _seq_decay(q, k, v, g, offsets, B, scale, max_len)
+    ss = (B, Hkv, shape[2], shape[2])
+    if state is not None:
+        _is(state, "state", torch.float32, ss)
+        _device(q, state)
+    out = _out(out, "out", torch.bfloat16, shape, dev)
+    want_state = want_state or state_out is not None
+    if want_state:
+        state_out = _out(state_out, "state_out", torch.float32, ss, dev)
+    ws = _ws(lib().dlrm_seq_decay_fwd_workspace_size(a), dev, workspace)
+    _check(lib().dlrm_seq_decay_fwd(a, _ptr(state), _ptr(state_out), _ptr(out), _ptr(ws), ws.numel(), _stream(dev)),
+           "dlrm_seq_decay_fwd")
+    return (out, state_out) if want_state else out
+
+
+def dlrm_seq_decay_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, offsets: torch.Tensor, *,
+                       scale: Optional[float] = None, max_len: Optional[int] = None, want_dg: bool = True,
+                       dq: Optional[torch.Tensor] = None, dk: Optional[torch.Tensor] = None, dv: Optional[torch.Tensor] = None,
+                       dg: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """(dq, dk, dv, dg or None) of dlrm_seq_decay_fwd without states (C: dlrm_seq_decay_bwd); dg has g's shape, and is
+    left out without want_dg, at less work."""
+    _offsets(offsets, "offsets")
+    B = offsets.numel() - 1
+    a, dev, qs, Hkv = _seq_decay(q, k, v, g, offsets, B, scale, max_len)
+    ks, bf = (qs[0], Hkv, qs[2]), torch.bfloat16
+    _is(dout, "dout", bf, qs)
+    _device(q, dout)
+    dq, dk, dv = _out(dq, "dq", bf, qs, dev), _out(dk, "dk", bf, ks, dev), _out(dv, "dv", bf, ks, dev)
+    if dg is not None and not want_dg:
+        raise ValueError("dg without want_dg")
+    if want_dg:
+        dg = _out(dg, "dg", torch.float32, tuple(g.shape), dev)
+    ws = _ws(lib().dlrm_seq_decay_bwd_workspace_size(a), dev, workspace)
+    _check(lib().dlrm_seq_decay_bwd(a, _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(ws), ws.numel(), _stream(dev)),
+           "dlrm_seq_decay_bwd")
+    return dq, dk, dv, dg
+
+
+def dlrm_seq_decay_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, state: torch.Tensor, *,
+                        scale: Optional[float] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One event of each of B sequences (C: dlrm_seq_decay_step): o [B, Hq, d] bf16; q [B, Hq, d], k and v
+    [B, Hkv, d], g [B, Hkv] or [Hkv]; state [B, Hkv, d, d] fp32 is updated in place."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be [B, heads, d]")
+    a, dev, shape, Hkv = _seq_decay(q, k, v, g, None, q.shape[0], scale, 1)
+    _is(state, "state", torch.float32, (shape[0], Hkv, shape[2], shape[2]))
+    _device(q, state)
+    out = _out(out, "out", torch.bfloat16, shape, dev)
+    _check(lib().dlrm_seq_decay_step(a, _ptr(state), _ptr(out), _stream(dev)), "dlrm_seq_decay_step")
+    return out
 
 
 def dlrm_trace_enable(on: bool = True) -> None:

@@ -4,6 +4,7 @@
 
 #include "common.h"
 #include "dlrm_seq.h"
+#include "dlrm_seq_pages.h"
 
 namespace dlrm {
 namespace seq {
@@ -33,8 +34,26 @@ struct Args {
     int32_t bounds[DLRM_SEQ_MAX_BUCKETS];
 };
 
-// Checks the description and fills Args (host).
-int check_attn(const dlrm_seq_attn *a, bool need_q_offsets, Args *out);
+// Checks the description and fills Args (host).  `paged`: the keys are in pages, and have no offsets.
+int check_attn(const dlrm_seq_attn *a, bool need_q_offsets, Args *out, bool paged = false);
+
+// Which rows of a pool hold the events of a sequence (dlrm_seq_pages.h).
+struct Pages {
+    const int32_t *table, *lengths;
+    int64_t row;  // of the table
+    int32_t width, shift, last;  // pages of a sequence, log2 of a page's events, the pool's last page
+};
+
+// Checks the tables against the description and fills Pages (host).
+int check_pages(const dlrm_seq_attn *a, const dlrm_seq_pages *p, Pages *out);
+
+__device__ __forceinline__ int paged_length(const Pages &pg, int b) { return min(max(pg.lengths[b], 0), pg.width << pg.shift); }
+
+// The pool's row of event x; `table`: the sequence's.  What is no page counts as the last one.
+__device__ __forceinline__ int paged_row(const Pages &pg, const int32_t *table, int x) {
+    const uint32_t page = min(static_cast<uint32_t>(table[x >> pg.shift]), static_cast<uint32_t>(pg.last));
+    return static_cast<int>((page << pg.shift) + (x & ((1 << pg.shift) - 1)));
+}
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -56,7 +75,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 // Entry i of an offset array, brought into [0, limit] (limit < 2^31; what is negative is limit).
-__device__ __forceinline__ int offset_at(const Args &a, const void *p, int64_t i, int64_t limit) {
+// `a`: Args, or another kernel's with its idx32.
+template <typename A>
+__device__ __forceinline__ int offset_at(const A &a, const void *p, int64_t i, int64_t limit) {
     if (a.idx32) {
         const uint32_t x = static_cast<const uint32_t *>(p)[i];
         return static_cast<int>(min(x, static_cast<uint32_t>(limit)));
@@ -72,7 +93,8 @@ __host__ __device__ __forceinline__ int64_t slot_count(int64_t rows, int64_t B, 
 
 // The sequence that owns a slot, by one wavefront, as every probe waits for memory: 64 probes at
 // once, twice for up to 4096 sequences.
-__device__ __forceinline__ int find_sequence(const Args &a, const void *off, int64_t limit, int slot, int T) {
+template <typename A>
+__device__ __forceinline__ int find_sequence(const A &a, const void *off, int64_t limit, int slot, int T) {
     int lo = 0, n = a.B;
     while (n > 1) {
         const int step = (n + 63) / 64;
@@ -98,6 +120,15 @@ __device__ __forceinline__ Span span_of(const Args &a, int b) {
     Span s;
     s.q0 = q0, s.k0 = k0;
     s.qlen = max(q1 - q0, 0), s.klen = max(k1 - k0, 0);
+    s.shift = s.klen - s.qlen;
+    return s;
+}
+
+__device__ __forceinline__ Span span_of(const Args &a, const Pages &pg, int b) {
+    const int q0 = offset_at(a, a.q_off, b, a.Nq), q1 = offset_at(a, a.q_off, b + 1, a.Nq);
+    Span s;
+    s.q0 = q0, s.k0 = 0;
+    s.qlen = max(q1 - q0, 0), s.klen = paged_length(pg, b);
     s.shift = s.klen - s.qlen;
     return s;
 }
@@ -177,6 +208,23 @@ struct Stage {
             const int x = row0 + i * R + row;
             r[i] = u32x4{0, 0, 0, 0};
             if (col && x < end && (x >= first || x < sinks)) r[i] = *(const DLRM_GLOBAL u32x4 *)(p + at);
+        }
+    }
+    // The rows of a thread's pieces in a pool of pages, and the pieces from there.
+    __device__ __forceinline__ void paged_rows(int (&at)[N], const Pages &pg, const int32_t *table, int row0, int first, int end,
+                                               int sinks) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int x = row0 + i * R + row;
+            at[i] = x < end && (x >= first || x < sinks) ? paged_row(pg, table, x) : -1;
+        }
+    }
+    __device__ __forceinline__ void load_rows(const uint16_t *base, int64_t stride, const int (&at)[N]) {
+        const int c = threadIdx.x % CH;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            r[i] = u32x4{0, 0, 0, 0};
+            if (col && at[i] >= 0) r[i] = *(const DLRM_GLOBAL u32x4 *)(base + at[i] * stride + 8 * c);
         }
     }
     __device__ __forceinline__ void store(uint16_t *tile) const {

@@ -38,8 +38,9 @@ __device__ __forceinline__ float add_quarters(float x) {
 }
 
 // part: [B][Hq][splits] rows of d floats, the runs' outputs; ml: their (maximum, sum)
-template <int DP>
-__global__ __launch_bounds__(kWaves * 64, kOcc<DP>) void k_seq_attn_decode(const Args a, const int splits, const int quantum, const bool splits_first,
+// PAGED: a key's row comes from the table of its sequence's pages
+template <int DP, bool PAGED>
+__global__ __launch_bounds__(kWaves * 64, kOcc<DP>) void k_seq_attn_decode(const Args a, const Pages pg, const int splits, const int quantum, const bool splits_first,
                                                                  const int head_groups,
                                                                  uint16_t *o_out, float *part, float2 *ml) {
     constexpr int LP = DP, CH = LP / 8, STEPS = DP / 32, MB = DP / 16, VN = kChunk * CH / 64;
@@ -62,8 +63,8 @@ __global__ __launch_bounds__(kWaves * 64, kOcc<DP>) void k_seq_attn_decode(const
     const int tid = threadIdx.x, lane = tid & 63, ln = lane & 15, quad = lane >> 4;
     const int w = static_cast<int>(wave_id());
 
-    const int64_t row0 = offset_at(a, a.kv_begin, b, a.Nkv);
-    const int klen = max(offset_at(a, a.kv_end, b, a.Nkv) - static_cast<int>(row0), 0);
+    const int64_t row0 = PAGED ? 0 : offset_at(a, a.kv_begin, b, a.Nkv);
+    const int klen = PAGED ? paged_length(pg, b) : max(offset_at(a, a.kv_end, b, a.Nkv) - static_cast<int>(row0), 0);
     // the visible keys in a row: the first `skip` ones, then those from `start` on
     const int start = a.window ? max(0, klen - a.window) : 0;
     const int skip = min(a.sinks, start);
@@ -84,12 +85,19 @@ __global__ __launch_bounds__(kWaves * 64, kOcc<DP>) void k_seq_attn_decode(const
     float top = -kInf, sum = 0.f;
     float known = 0.f, share = 1.f, unit = 1.f;  // the sum, if known; what P is multiplied by; a unit of o in the sum's terms
 
+    // The rows of a chunk's keys, one a lane, looked up a chunk before they are needed.
+    const int32_t *const table = PAGED ? pg.table + b * pg.row : nullptr;
+    int rows = 0;
+    const auto look_up = [&](int c) {
+        const int v = c + (lane & 31);
+        if (PAGED && v < v1) rows = paged_row(pg, table, v < skip ? v : start + v - skip);
+    };
     u32x4 kr[2][STEPS], vr[VN];
     const auto load = [&](int c) {
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
             const int v = c + 16 * g + ln;
-            const int64_t key = v < skip ? v : start + v - skip;
+            const int64_t key = PAGED ? __shfl(rows, 16 * g + ln) : v < skip ? v : start + v - skip;
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
                 kr[g][s] = u32x4{0, 0, 0, 0};
@@ -100,14 +108,16 @@ __global__ __launch_bounds__(kWaves * 64, kOcc<DP>) void k_seq_attn_decode(const
 #pragma unroll
         for (int i = 0; i < VN; ++i) {
             const int at = i * 64 + lane, v = c + at / CH, col = at % CH * 8;
-            const int64_t key = v < skip ? v : start + v - skip;
+            const int64_t key = PAGED ? __shfl(rows, at / CH) : v < skip ? v : start + v - skip;
             vr[i] = u32x4{0, 0, 0, 0};
             if (v < v1 && col < a.d) vr[i] = *(const DLRM_GLOBAL u32x4 *)(vb + key * a.v_row + col);
         }
+        look_up(c + kWaves * kChunk);
     };
 
     // the first chunk and the queries are on their way while the bias is fetched
     int c = v0 + w * kChunk;
+    look_up(c);
     if (c < v1) load(c);
     for (int i = tid; i < a.buckets; i += kWaves * 64) bounds_s[i] = a.bounds[i];
     for (int i = tid; i < a.buckets * heads; i += kWaves * 64) bias_s[i] = a.bias[static_cast<int64_t>(h0) * a.buckets + i];
@@ -233,6 +243,7 @@ __global__ __launch_bounds__(kWaves * 64, kOcc<DP>) void k_seq_attn_decode(const
 #pragma unroll
         for (int m = 0; m < MB; ++m) o[m] = floatx4{0.f, 0.f, 0.f, 0.f};
         c = v0 + w * kChunk;
+        look_up(c);
         load(c);
     }
 
@@ -333,7 +344,7 @@ Split split_of(int64_t B, int32_t Hq, int32_t Hkv, int32_t window, int32_t sinks
 }
 
 template <int DP>
-int launch(const Args &a, const Split &sp, uint16_t *o, void *ws, hipStream_t stream) {
+int launch(const Args &a, const Pages *pg, const Split &sp, uint16_t *o, void *ws, hipStream_t stream) {
     const int splits = sp.runs;
     const int head_groups = (a.group + kHeads - 1) / kHeads;
     const int64_t rows = static_cast<int64_t>(a.B) * a.Hq, blocks = blocks_of(a.B, a.Hq, a.Hkv);
@@ -344,7 +355,11 @@ int launch(const Args &a, const Split &sp, uint16_t *o, void *ws, hipStream_t st
     // by side, as neighbours in memory (32 of up to 65536: 166 -> 152 us).
     const bool splits_first = blocks < 256;
     const dim3 grid = splits_first ? dim3(splits, static_cast<uint32_t>(blocks)) : dim3(static_cast<uint32_t>(blocks), splits);
-    DLRM_LAUNCH("seq_attn_decode", (k_seq_attn_decode<DP>), grid, dim3(kWaves * 64), 0, stream, a,
+    if (pg)
+        DLRM_LAUNCH("seq_attn_paged_decode", (k_seq_attn_decode<DP, true>), grid, dim3(kWaves * 64), 0, stream, a, *pg,
+                splits, sp.quantum, splits_first, head_groups, o, part, ml);
+    else
+        DLRM_LAUNCH("seq_attn_decode", (k_seq_attn_decode<DP, false>), grid, dim3(kWaves * 64), 0, stream, a, Pages{},
                 splits, sp.quantum, splits_first, head_groups, o, part, ml);
     for (int64_t row0 = 0; splits > 1 && row0 < rows; row0 += kMostBlocks)
         DLRM_LAUNCH("seq_decode_join", k_seq_decode_join, dim3(static_cast<uint32_t>(std::min(rows - row0, kMostBlocks))), dim3(256),
@@ -367,13 +382,11 @@ extern "C" size_t dlrm_seq_attn_decode_workspace_size(int64_t B, int32_t Hq, int
     return 256 + (splits > 1 ? static_cast<size_t>(B) * Hq * splits * (d + 2) * 4 : 0);
 }
 
-extern "C" int dlrm_seq_attn_decode(const dlrm_seq_attn *desc, int64_t max_kv_len, uint16_t *o, void *workspace,
-                                    size_t workspace_bytes, dlrm_stream_t stream_) {
-    using namespace dlrm;
-    using namespace dlrm::seq;
-    Args a;
-    const int rc = check_attn(desc, false, &a);
-    if (rc != DLRM_OK) return rc;
+namespace dlrm {
+namespace seq {
+namespace {
+
+int decode(const Args &a, const Pages *pg, int64_t max_kv_len, uint16_t *o, void *workspace, size_t workspace_bytes, hipStream_t stream) {
     if (a.Nq != a.B || max_kv_len < 0) return DLRM_ERR_INVALID_ARG;
     if (a.B == 0) return DLRM_OK;
     if (!o || !aligned(o, 16)) return DLRM_ERR_INVALID_ARG;
@@ -382,8 +395,33 @@ extern "C" int dlrm_seq_attn_decode(const dlrm_seq_attn *desc, int64_t max_kv_le
     if (sp.runs > 1 && (!workspace || !aligned(workspace, 256) ||
                        workspace_bytes < dlrm_seq_attn_decode_workspace_size(a.B, a.Hq, a.Hkv, a.d, a.window, a.sinks, max_kv_len)))
         return DLRM_ERR_WORKSPACE;
-    hipStream_t stream = reinterpret_cast<hipStream_t>(stream_);
-    if (a.d <= 32) return launch<32>(a, sp, o, workspace, stream);
-    if (a.d <= 64) return launch<64>(a, sp, o, workspace, stream);
-    return launch<128>(a, sp, o, workspace, stream);
+    if (a.d <= 32) return launch<32>(a, pg, sp, o, workspace, stream);
+    if (a.d <= 64) return launch<64>(a, pg, sp, o, workspace, stream);
+    return launch<128>(a, pg, sp, o, workspace, stream);
+}
+
+}  // namespace
+}  // namespace seq
+}  // namespace dlrm
+
+extern "C" int dlrm_seq_attn_decode(const dlrm_seq_attn *desc, int64_t max_kv_len, uint16_t *o, void *workspace,
+                                    size_t workspace_bytes, dlrm_stream_t stream) {
+    using namespace dlrm;
+    using namespace dlrm::seq;
+    Args a;
+    const int rc = check_attn(desc, false, &a);
+    if (rc != DLRM_OK) return rc;
+    return decode(a, nullptr, max_kv_len, o, workspace, workspace_bytes, reinterpret_cast<hipStream_t>(stream));
+}
+
+extern "C" int dlrm_seq_attn_paged_decode(const dlrm_seq_attn *desc, const dlrm_seq_pages *pages, int64_t max_kv_len, uint16_t *o,
+                                          void *workspace, size_t workspace_bytes, dlrm_stream_t stream) {
+    using namespace dlrm;
+    using namespace dlrm::seq;
+    Args a;
+    Pages pg;
+    int rc = check_attn(desc, false, &a, true);
+    if (rc == DLRM_OK) rc = check_pages(desc, pages, &pg);
+    if (rc != DLRM_OK) return rc;
+    return decode(a, &pg, max_kv_len, o, workspace, workspace_bytes, reinterpret_cast<hipStream_t>(stream));
 }

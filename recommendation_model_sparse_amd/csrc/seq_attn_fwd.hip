@@ -22,7 +22,7 @@
 namespace dlrm {
 namespace seq {
 
-int check_attn(const dlrm_seq_attn *a, bool need_q_offsets, Args *out) {
+int check_attn(const dlrm_seq_attn *a, bool need_q_offsets, Args *out, bool paged) {
     if (!a) return DLRM_ERR_INVALID_ARG;
     if (a->B < 0 || a->Nq < 0 || a->Nkv < 0 || a->Hq < 1 || a->Hkv < 1 || a->Hq % a->Hkv != 0 || a->d < 1)
         return DLRM_ERR_INVALID_ARG;
@@ -38,11 +38,11 @@ int check_attn(const dlrm_seq_attn *a, bool need_q_offsets, Args *out) {
     if (a->Nq >= (int64_t(1) << 31) || a->Nkv >= (int64_t(1) << 31)) return DLRM_ERR_UNSUPPORTED;
     if (need_q_offsets) {  // a launch holds fewer than 2^32 work-items
         const int64_t most = (int64_t(1) << 32) / (a->d <= 64 ? 128 : 256) - kNumXcd;
-        if (slot_count(a->Nq > a->Nkv ? a->Nq : a->Nkv, a->B, kQT) > most) return DLRM_ERR_UNSUPPORTED;
+        if (slot_count(a->Nq > a->Nkv || paged ? a->Nq : a->Nkv, a->B, kQT) > most) return DLRM_ERR_UNSUPPORTED;
     }
     const uintptr_t ib = a->index_type == DLRM_INDEX_I32 ? 4 : 8;
     if (a->B > 0) {
-        if (!a->kv_begin || !a->kv_end || !aligned(a->kv_begin, ib) || !aligned(a->kv_end, ib)) return DLRM_ERR_INVALID_ARG;
+        if (!paged && (!a->kv_begin || !a->kv_end || !aligned(a->kv_begin, ib) || !aligned(a->kv_end, ib))) return DLRM_ERR_INVALID_ARG;
         if (need_q_offsets && (!a->q_offsets || !aligned(a->q_offsets, ib))) return DLRM_ERR_INVALID_ARG;
     }
     if ((a->Nq > 0 && !a->q) || (a->Nkv > 0 && (!a->k || !a->v))) return DLRM_ERR_INVALID_ARG;
@@ -71,13 +71,25 @@ int check_attn(const dlrm_seq_attn *a, bool need_q_offsets, Args *out) {
     return DLRM_OK;
 }
 
+int check_pages(const dlrm_seq_attn *a, const dlrm_seq_pages *p, Pages *out) {
+    if (!a || !p || p->B != a->B || p->pages < 1 || p->width < 0 || p->table_row < p->width) return DLRM_ERR_INVALID_ARG;
+    if (p->page < 8 || p->page > 4096 || (p->page & (p->page - 1)) != 0) return DLRM_ERR_UNSUPPORTED;
+    if (p->pages >= (int64_t(1) << 31) / p->page || static_cast<int64_t>(p->width) * p->page >= (int64_t(1) << 30)) return DLRM_ERR_UNSUPPORTED;
+    if (a->Nkv != p->pages * p->page) return DLRM_ERR_INVALID_ARG;
+    if (p->B > 0 && (!p->lengths || (!p->table && p->width > 0) || !aligned(p->lengths, 4) || !aligned(p->table, 4)))
+        return DLRM_ERR_INVALID_ARG;
+    *out = Pages{p->table, p->lengths, p->table_row, p->width, __builtin_ctz(p->page), static_cast<int32_t>(p->pages - 1)};
+    return DLRM_OK;
+}
+
 namespace {
 
 // DP: the head's width rounded up (the products run over DP columns, those from d on are zeros);
 // LP: columns of a row in LDS.  WQ wavefronts of 32 queries each, by WK that share a tile's keys:
-// each then takes one of its two halves, and their results are joined at the end.
-template <int DP, int LP, int WQ, int WK, int OCC, int NEAR>
-__global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a, uint16_t *o_out, float *lse_out,
+// each then takes one of its two halves, and their results are joined at the end.  PAGED: a key's row comes
+// from the table of its sequence's pages.
+template <int DP, int LP, int WQ, int WK, int OCC, int NEAR, bool PAGED>
+__global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a, const Pages pg, uint16_t *o_out, float *lse_out,
                                                                     int32_t *tiles_out) {
     constexpr int QT = WQ * 32, STEPS = DP / 16, MB = DP / 32, THREADS = WQ * WK * 64;
     constexpr int TAB = QT + kBK, TILE = kBK * kPitch<LP>;
@@ -89,7 +101,7 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a
     const int slot = static_cast<int>(xcd_contiguous(blockIdx.x, gridDim.x));
     const int h = blockIdx.y;
     const int b = find_sequence(a, a.q_off, a.Nq, slot, QT);
-    const Span sp = span_of(a, b);
+    const Span sp = PAGED ? span_of(a, pg, b) : span_of(a, b);
     if (tiles_out && h == 0 && threadIdx.x == 0 && slot < slot_count(a.Nq, a.B, QT)) tiles_out[slot] = b;
     const int t = slot - (static_cast<int>(sp.q0) / QT + b);
     const int tiles = (sp.qlen + QT - 1) / QT;
@@ -113,7 +125,15 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a
 
     Stage<LP, THREADS> ks(a.k_row, a.d), vs(a.v_row, a.d);
     const auto key0 = [&](int it) { return (it < nsink ? it : t0 + it - nsink) * kBK; };
+    const int32_t *const mine = PAGED ? pg.table + b * pg.row : nullptr;
     const auto load = [&](int it) {
+        if constexpr (PAGED) {
+            int at[decltype(ks)::N];
+            ks.paged_rows(at, pg, mine, key0(it), first, end, a.sinks);
+            ks.load_rows(kb, a.k_row, at);
+            vs.load_rows(vb, a.v_row, at);
+            return;
+        }
         ks.load(kb, a.k_row, a.d, key0(it), first, end, a.sinks);
         vs.load(vb, a.v_row, a.d, key0(it), first, end, a.sinks);
     };
@@ -378,10 +398,23 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a
 }
 
 template <int DP, int LP, int WQ, int WK, int OCC, int NEAR>
-int launch(const Args &a, uint16_t *o, float *lse, int32_t *tiles, hipStream_t stream) {
+int launch(const Args &a, const Pages *pg, uint16_t *o, float *lse, int32_t *tiles, hipStream_t stream) {
     const dim3 grid(round_up_xcd(slot_count(a.Nq, a.B, WQ * 32)), a.Hq);
-    DLRM_LAUNCH("seq_attn_fwd", (k_seq_attn_fwd<DP, LP, WQ, WK, OCC, NEAR>), grid, dim3(WQ * WK * 64), 0, stream, a, o, lse, tiles);
+    if (pg) DLRM_LAUNCH("seq_attn_paged_fwd", (k_seq_attn_fwd<DP, LP, WQ, WK, OCC, NEAR, true>), grid, dim3(WQ * WK * 64), 0, stream, a, *pg, o, lse, tiles);
+    else DLRM_LAUNCH("seq_attn_fwd", (k_seq_attn_fwd<DP, LP, WQ, WK, OCC, NEAR, false>), grid, dim3(WQ * WK * 64), 0, stream, a, Pages{}, o, lse, tiles);
     return launch_status();
+}
+
+// Wavefronts (queries x halves of a tile's keys) and their number a SIMD, at each width the best of
+// those tried.  Heads of 64: 2 x 1 took 78 us where 2 x 2 took 93 (the 1024 sequences above, before later
+// steps).  Of 128: 2 x 2 took 38 us where 4 x 1 took 50 and 2 x 1 with three a SIMD 53 (16 sequences of up
+// to 300 queries after up to 2048 keys).  The near biases: 2048 distances against 896 at heads of 32, 74 -> 70
+// us, and against 1280 at 128, 99 -> 97 (8 sequences of 2048, a bias that differs up to 2048); at 64 the
+// longer table costs a workgroup a CU: 86 -> 87, and 18.7 -> 20.5 for 64 sequences of 256.
+int launch_for(const Args &a, const Pages *pg, uint16_t *o, float *lse, int32_t *tiles, hipStream_t stream) {
+    if (a.d <= 32) return launch<32, 32, 2, 1, 4, 2048>(a, pg, o, lse, tiles, stream);
+    if (a.d <= 64) return launch<64, 64, 2, 1, 4, 640>(a, pg, o, lse, tiles, stream);
+    return launch<128, 128, 2, 2, 2, 2048>(a, pg, o, lse, tiles, stream);
 }
 
 }  // namespace
@@ -402,14 +435,18 @@ extern "C" int dlrm_seq_attn_fwd(const dlrm_seq_attn *desc, uint16_t *o, float *
     if (a.B > 0 && a.Nq > 0 && (lse == nullptr) != (tiles == nullptr)) return DLRM_ERR_INVALID_ARG;
     if (a.Nq > 0 && (!o || !aligned(o, 16) || !aligned(lse, 4) || !aligned(tiles, 4))) return DLRM_ERR_INVALID_ARG;
     if (a.B == 0 || a.Nq == 0) return DLRM_OK;
-    hipStream_t stream = reinterpret_cast<hipStream_t>(stream_);
-    // Wavefronts (queries x halves of a tile's keys) and their number a SIMD, at each width the best of
-    // those tried.  Heads of 64: 2 x 1 took 78 us where 2 x 2 took 93 (the 1024 sequences above, before later
-    // steps).  Of 128: 2 x 2 took 38 us where 4 x 1 took 50 and 2 x 1 with three a SIMD 53 (16 sequences of up
-    // to 300 queries after up to 2048 keys).  The near biases: 2048 distances against 896 at heads of 32, 74 -> 70
-    // us, and against 1280 at 128, 99 -> 97 (8 sequences of 2048, a bias that differs up to 2048); at 64 the
-    // longer table costs a workgroup a CU: 86 -> 87, and 18.7 -> 20.5 for 64 sequences of 256.
-    if (a.d <= 32) return launch<32, 32, 2, 1, 4, 2048>(a, o, lse, tiles, stream);
-    if (a.d <= 64) return launch<64, 64, 2, 1, 4, 640>(a, o, lse, tiles, stream);
-    return launch<128, 128, 2, 2, 2, 2048>(a, o, lse, tiles, stream);
+    return launch_for(a, nullptr, o, lse, tiles, reinterpret_cast<hipStream_t>(stream_));
+}
+
+extern "C" int dlrm_seq_attn_paged_fwd(const dlrm_seq_attn *desc, const dlrm_seq_pages *pages, uint16_t *o, dlrm_stream_t stream_) {
+    using namespace dlrm;
+    using namespace dlrm::seq;
+    Args a;
+    Pages pg;
+    int rc = check_attn(desc, true, &a, true);
+    if (rc == DLRM_OK) rc = check_pages(desc, pages, &pg);
+    if (rc != DLRM_OK) return rc;
+    if (a.Nq > 0 && (!o || !aligned(o, 16))) return DLRM_ERR_INVALID_ARG;
+    if (a.B == 0 || a.Nq == 0) return DLRM_OK;
+    return launch_for(a, &pg, o, nullptr, nullptr, reinterpret_cast<hipStream_t>(stream_));
 }
