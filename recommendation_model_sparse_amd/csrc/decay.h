@@ -13,10 +13,12 @@
 //
 // and in reverse e^{G_n - G_j} on the way out and e^{G_i} on the way in.
 //
-// A workgroup walks the chunks of one sequence and key head.  Each of its LP / 32 wavefronts has 32
-// columns of the state in its accumulators (32x32x16 matrix instructions: rows of y, columns of z), and
-// those columns of the outputs, as transposed tiles: out^T = S^T x^T + z^T P^T.  The state's accumulators are,
-// rounded, the first operand as they stand; P^T goes through LDS, as every wavefront needs all of it.
+// A workgroup walks the chunks of one sequence and key head.  Each of its LP / 16 wavefronts has 16 columns of
+// the state in its accumulators (16x16x32 matrix instructions: rows of y, columns of z), and those columns of the
+// outputs, as transposed tiles: out^T = S^T x^T + z^T P^T.  The state's accumulators are, rounded, the first operand
+// as they stand; P^T goes through LDS, as every wavefront needs all of it.  (With 32 columns a wavefront, on
+// 32x32x16, half as many wavefronts waited twice as long: a chunk of heads of 128 took 8100 cycles of a workgroup
+// by itself, of 64 7200.)
 #pragma once
 
 #include "dlrm_seq_decay.h"
@@ -44,25 +46,35 @@ struct Walk {
     int32_t idx32, B, Hq, Hkv, group, d;
     float scale;
     int32_t run;         // chunks of a run, a workgroup's share of a sequence; 0: the whole of it
+    int32_t splits;      // workgroups that share a group's query heads (forward)
     uint32_t slots;      // runs, or sequences
     const float *start;  // states: of runs [slots][Hkv][d][d], or [B][Hkv][d][d]; NULL: zeros
     float *last;         // [B][Hkv][d][d] or NULL
     float *fade;         // e^(sum of g) of each run, [slots][Hkv]
     uint16_t *out, *out2;
-    float *terms;  // [Hkv][N]
+    // for the decays' gradient
+    float *terms;        // [parts][Hkv][N]: <t, out> of the walk for dq, for each of its splits, by way of the state
+    float *pairs;        // and by way of the chunk's pairs
+    int32_t parts;
+    float *marks;        // the forward state (dq's) before every `mark`th chunk, as its wavefronts hold it
+    int32_t mark;
+    float *dg;           // [N][Hkv]
+    double *sums;        // or over each slot's events, [Hkv][slots]
 };
 
-// Which chunks of which sequence a workgroup walks.
+// Which chunks of which sequence a workgroup walks, and for which query heads of a group.
 struct Part {
     int64_t row0;
-    int b, len, chunks, c0, c1, kvh;
+    int b, len, chunks, c0, c1, kvh, split;
     uint32_t slot;
     bool any;
 };
 
 __device__ __forceinline__ Part part_of(const Walk &a, uint32_t id) {
     Part p;
-    p.slot = id / static_cast<uint32_t>(a.Hkv), p.kvh = static_cast<int>(id - p.slot * a.Hkv);
+    const uint32_t one = id / static_cast<uint32_t>(a.splits);
+    p.split = static_cast<int>(id - one * a.splits);
+    p.slot = one / static_cast<uint32_t>(a.Hkv), p.kvh = static_cast<int>(one - p.slot * a.Hkv);
     p.any = p.slot < a.slots;
     if (!p.any) return p;
     const int T = kC * a.run;
@@ -77,10 +89,34 @@ __device__ __forceinline__ Part part_of(const Walk &a, uint32_t id) {
     return p;
 }
 
+// A sum over the lanes up to each, in fp64.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double from_lanes_below(double x) {
+    const int64_t v = __double_as_longlong(x);
+    const int lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, ROWS, 0xf, false);
+    const int hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(v >> 32), CTRL, ROWS, 0xf, false);
+    return __longlong_as_double(static_cast<int64_t>(hi) << 32 | static_cast<uint32_t>(lo));
+}
+__device__ __forceinline__ double prefix_sum(double s) {
+    s += from_lanes_below<0x111, 0xf>(s);  // the lane 1, 2, 4, 8 below, within 16
+    s += from_lanes_below<0x112, 0xf>(s);
+    s += from_lanes_below<0x114, 0xf>(s);
+    s += from_lanes_below<0x118, 0xf>(s);
+    s += from_lanes_below<0x142, 0xa>(s);  // the last of the 16 below; of the 32 below
+    s += from_lanes_below<0x143, 0xc>(s);
+    return s;
+}
+__device__ __forceinline__ double last_lane(double x) {
+    const int64_t v = __double_as_longlong(x);
+    const int lo = __builtin_amdgcn_readlane(static_cast<int>(v), 63), hi = __builtin_amdgcn_readlane(static_cast<int>(v >> 32), 63);
+    return __longlong_as_double(static_cast<int64_t>(hi) << 32 | static_cast<uint32_t>(lo));
+}
+
 // What a chunk's decays come to, for each event: its sum G as two fp32 numbers (their sum holds 48 bits:
-// differences are exact to fp32 whatever pauses lie between), e^G and e^{G_n - G}, in base 2.
+// differences are exact to fp32 whatever pauses lie between), e^G and e^{G_n - G}, in base 2; e^{G_n}.
 struct Decays {
     float hi[kC], lo[kC], from[kC], to[kC];
+    float fade;
 };
 
 __device__ __forceinline__ float decay_load(const Walk &a, const Part &p, int c, int lane) {
@@ -88,29 +124,71 @@ __device__ __forceinline__ float decay_load(const Walk &a, const Part &p, int c,
     return i < p.len ? a.g[(p.row0 + i) * a.g_row + p.kvh] : 0.f;
 }
 
-// By one wavefront, lane = event; returns e^{G_n} to all lanes and adds G_n to *total.
-__device__ __forceinline__ float decays(Decays &out, float g, int lane, double *total) {
+// 2^x to fp32's precision: what is lost of x in fp32 would be up to 2^-20 of the result.
+__device__ __forceinline__ float exp2_of(double x) {
+    const float hi = static_cast<float>(x);
+    return __builtin_amdgcn_exp2f(hi) * fmaf(static_cast<float>(x - hi), 0.6931471805599453f, 1.f);
+}
+
+// By one wavefront, lane = event; adds G_n to *total.
+__device__ __forceinline__ void decays(Decays &out, float g, int lane, double *total) {
     g = g > 0.f ? 0.f : g < kLeast ? kLeast : g;  // NaN stays
-    double s = static_cast<double>(g) * 1.4426950408889634;
-#pragma unroll
-    for (int i = 1; i < 64; i <<= 1) {
-        const double up = __shfl_up(s, i);
-        if (lane >= i) s += up;
-    }
-    const double n = __shfl(s, 63);
+    const double s = prefix_sum(static_cast<double>(g) * 1.4426950408889634);
+    const double n = last_lane(s);
     *total += n;
     const float hi = static_cast<float>(s);
     out.hi[lane] = hi;
     out.lo[lane] = static_cast<float>(s - hi);
-    out.from[lane] = __builtin_amdgcn_exp2f(hi);
-    out.to[lane] = __builtin_amdgcn_exp2f(static_cast<float>(n - s));
-    return __builtin_amdgcn_exp2f(static_cast<float>(n));
+    out.from[lane] = exp2_of(s);
+    out.to[lane] = exp2_of(n - s);
+    if (lane == 0) out.fade = exp2_of(n);
 }
 
+// The lane's number, worked out anew: addresses made from it are not kept in registers from one chunk to the next.
+__device__ __forceinline__ int fresh(int lane) {
+    asm volatile("" : "+v"(lane));
+    return lane;
+}
+
+// The decays' gradient: none; for each event; for each head (summed over the events).
+enum { kNone = 0, kEach = 1, kHead = 2 };
+
+// A barrier for what the wavefronts share in LDS: loads and stores of memory stay under way across it.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// The sum over lanes l, l ^ 16, l ^ 32, l ^ 48.
+__device__ __forceinline__ float add_quarters(float x) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return add_halves(__uint_as_float(r[0]) + __uint_as_float(r[1]));
+}
+
+// NB: blocks of 16 columns a wavefront.  Two of them read each tile from LDS half as often.
 template <int LP>
 struct Of {
-    static constexpr int WAVES = LP / 32, CT = LP / 32, STEPS = LP / 16, TILE = kC * kPitch<LP>;
+    static constexpr int NB = LP == 128 ? 2 : 1, WAVES = LP / 16 / NB, CT = LP / 16, STEPS = LP / 32, TILE = kC * kPitch<LP>;
+    typedef floatx4 State[NB][CT];  // block b, tile ct, register r: row 16 ct + 4 quad + r, column 16 (NB w + b) + ln
+    typedef floatx4 Out[NB][4];     // block b, rows 16 ib on, register r: column 16 (NB w + b) + 4 quad + r of row 16 ib + ln
 };
+
+// Tiles hold each row's columns in the order in which an accumulator holds its rows: of 32, the four from 4 q on
+// and those 16 further on are side by side.  So a lane's eight values of an operand are one read, whether the
+// other operand comes from a tile or from the accumulators; the order of a product's sum is of no account.
+__device__ __forceinline__ constexpr int place_of(int col) { return (col & ~31) + 2 * (col & 12) + (col & 16) / 4 + (col & 3); }
+
+template <int LP, int THREADS>
+__device__ __forceinline__ void tile_store(const Stage<LP, THREADS> &s, uint16_t *tile) {
+    const int col = 8 * (fresh(threadIdx.x) % Stage<LP, THREADS>::CH);
+    uint16_t *const at = tile + s.row * kPitch<LP> + place_of(col);
+#pragma unroll
+    for (int i = 0; i < Stage<LP, THREADS>::N; ++i) {
+        *reinterpret_cast<u32x2 *>(at + i * Stage<LP, THREADS>::R * kPitch<LP>) = u32x2{s.r[i].x, s.r[i].y};
+        *reinterpret_cast<u32x2 *>(at + i * Stage<LP, THREADS>::R * kPitch<LP> + 8) = u32x2{s.r[i].z, s.r[i].w};
+    }
+}
 
 // The high halves of two words.
 __device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
@@ -142,163 +220,213 @@ __device__ __forceinline__ void parts_of(const float (&x)[8], Frag (&out)[N]) {
 
 // S from memory (rows y, columns z; TRANSPOSED: the other way round) or zeros.
 template <int LP, bool TRANSPOSED>
-__device__ __forceinline__ void state_load(f32x16 (&S)[Of<LP>::CT], const float *p, int d, int w, int lane) {
-    const int ln = lane & 31, half = lane >> 5, e = 32 * w + ln;
+__device__ __forceinline__ void state_load(typename Of<LP>::State &S, const float *p, int d, int w, int lane) {
+    const int ln = lane & 15, quad = lane >> 4;
 #pragma unroll
-    for (int ct = 0; ct < Of<LP>::CT; ++ct) S[ct] = f32x16{};
-    if (!p || e >= d) return;
+    for (int b = 0; b < Of<LP>::NB; ++b) {
+        const int e = 16 * (Of<LP>::NB * w + b) + ln;
 #pragma unroll
-    for (int ct = 0; ct < Of<LP>::CT; ++ct)
+        for (int ct = 0; ct < Of<LP>::CT; ++ct) {
+            const int c = 16 * ct + 4 * quad;
+            S[b][ct] = floatx4{0.f, 0.f, 0.f, 0.f};
+            if (!p || e >= d || c >= d) continue;
+            if constexpr (TRANSPOSED) {
+                S[b][ct] = *(const DLRM_GLOBAL floatx4 *)(p + e * d + c);
+            } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (32 * ct + 8 * k >= d) continue;  // d is a multiple of 8
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int c = 32 * ct + 8 * k + 4 * half + r;
-                S[ct][4 * k + r] = p[TRANSPOSED ? e * d + c : c * d + e];
+                for (int r = 0; r < 4; ++r) S[b][ct][r] = p[(c + r) * d + e];
             }
         }
+    }
 }
 
 template <int LP>
-__device__ __forceinline__ void state_store(const f32x16 (&S)[Of<LP>::CT], float *p, int d, int w, int lane) {
-    const int ln = lane & 31, half = lane >> 5, e = 32 * w + ln;
-    if (e >= d) return;
+__device__ __forceinline__ void state_store(const typename Of<LP>::State &S, float *p, int d, int w, int lane) {
+    const int ln = lane & 15, quad = lane >> 4;
 #pragma unroll
-    for (int ct = 0; ct < Of<LP>::CT; ++ct)
+    for (int b = 0; b < Of<LP>::NB; ++b) {
+        const int e = 16 * (Of<LP>::NB * w + b) + ln;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (32 * ct + 8 * k >= d) continue;
+        for (int ct = 0; ct < Of<LP>::CT; ++ct) {
+            const int c = 16 * ct + 4 * quad;
+            if (e >= d || c >= d) continue;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) p[(32 * ct + 8 * k + 4 * half + r) * d + e] = S[ct][4 * k + r];
+            for (int r = 0; r < 4; ++r) p[(c + r) * d + e] = S[b][ct][r];
         }
+    }
 }
 
-// S <- fade S + sum_j w_j y_j z_j^T
+template <int LP>
+__device__ __forceinline__ void state_fade(typename Of<LP>::State &S, float f) {
+#pragma unroll
+    for (int b = 0; b < Of<LP>::NB; ++b)
+#pragma unroll
+        for (int ct = 0; ct < Of<LP>::CT; ++ct)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) S[b][ct][r] *= f;
+}
+
+// Transposed operand of v_mfma_f32_16x16x32_bf16 from a tile: a lane gets column 16 block + ln of the rows
+// row0 + 4 quad + {0..3} and those 16 further on.  Within 16 lanes ds_read_b64_tr_b16 takes 4 rows of 16 columns, lane i
+// reading 4 columns of row i / 4, and gives lane i column i of the 4 rows.
+template <int LP>
+__device__ __forceinline__ int columns_base(int lane) {
+    return (4 * (lane >> 4) + ((lane & 15) >> 2)) * kPitch<LP> + 8 * (lane & 3);
+}
+template <int LP>
+__device__ __forceinline__ void columns(Frag &f, const uint16_t *at, int row0, int block) {
+    typedef __attribute__((address_space(3))) s16x4 *lds_t;
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+        f.h[g] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t)(at + (row0 + 16 * g) * kPitch<LP> + 32 * (block / 2) + 4 * (block % 2)));
+}
+
+// S <- S + sum_j w_j y_j z_j^T
 template <int LP, int UP>
-__device__ __forceinline__ void state_grow(f32x16 (&S)[Of<LP>::CT], const uint16_t *ys, const uint16_t *zs, const float *weight, int w,
+__device__ __forceinline__ void state_grow(typename Of<LP>::State &S, const uint16_t *ys, const uint16_t *zs, const float *weight, int w,
                                            int lane) {
-    const uint16_t *ycol = ys + column_base<LP>(lane), *zcol = zs + column_base<LP>(lane);
-    const int half = lane >> 5;
+    constexpr int NB = Of<LP>::NB;
+    lane = fresh(lane);
+    const uint16_t *const ycol = ys + columns_base<LP>(lane), *const zcol = zs + columns_base<LP>(lane);
+    const float *const wj = weight + 4 * (lane >> 4);
 #pragma unroll
-    for (int u = 0; u < kC / 16; ++u) {
-        Frag z, zw[UP];
-        read_columns<LP>(z, zcol, 16 * u, 32 * w);
-        const floatx4 w0 = *reinterpret_cast<const floatx4 *>(weight + 16 * u + 4 * half);
-        const floatx4 w1 = *reinterpret_cast<const floatx4 *>(weight + 16 * u + 8 + 4 * half);
-        float x[8];
+    for (int s = 0; s < kC / 32; ++s) {
+        Frag zw[NB][UP];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            x[2 * e] = bf16_lo(z.w[e]) * (e < 2 ? w0[2 * e % 4] : w1[2 * e % 4]);
-            x[2 * e + 1] = bf16_hi(z.w[e]) * (e < 2 ? w0[2 * e % 4 + 1] : w1[2 * e % 4 + 1]);
+        for (int b = 0; b < NB; ++b) {
+            Frag z;
+            columns<LP>(z, zcol, 32 * s, NB * w + b);
+            float x[8];
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const floatx4 f = *reinterpret_cast<const floatx4 *>(wj + 32 * s + 16 * g);
+                x[4 * g] = bf16_lo(z.w[2 * g]) * f[0], x[4 * g + 1] = bf16_hi(z.w[2 * g]) * f[1];
+                x[4 * g + 2] = bf16_lo(z.w[2 * g + 1]) * f[2], x[4 * g + 3] = bf16_hi(z.w[2 * g + 1]) * f[3];
+            }
+            parts_of<UP>(x, zw[b]);
         }
-        parts_of<UP>(x, zw);
 #pragma unroll
         for (int ct = 0; ct < Of<LP>::CT; ++ct) {
             Frag y;
-            read_columns<LP>(y, ycol, 16 * u, 32 * ct);
+            columns<LP>(y, ycol, 32 * s, ct);
 #pragma unroll
-            for (int n = 0; n < UP; ++n) S[ct] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(y.b, zw[n].b, S[ct], 0, 0, 0);
+            for (int n = 0; n < UP; ++n)
+#pragma unroll
+                for (int b = 0; b < NB; ++b) S[b][ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(y.b, zw[b][n].b, S[b][ct], 0, 0, 0);
         }
     }
 }
 
-// A lane's eight values of row `row`, columns 16 s + 4 half + {0..3} and those 8 further on: the order of an
-// accumulator's rows.
-template <int LP>
-__device__ __forceinline__ void read_row_as_rows(Frag &f, const uint16_t *tile, int row, int half, int s) {
-    const uint16_t *at = tile + row * kPitch<LP> + 4 * half + 16 * s;
-    const u32x2 a = *reinterpret_cast<const u32x2 *>(at), b = *reinterpret_cast<const u32x2 *>(at + 8);
-    f.w[0] = a.x, f.w[1] = a.y, f.w[2] = b.x, f.w[3] = b.y;
-}
-
-// o^T = S^T x^T for both halves of the chunk's rows.
+// o^T = S^T x^T
 template <int LP, int PR>
-__device__ __forceinline__ void through_state(f32x16 (&o)[2], const f32x16 (&S)[Of<LP>::CT], const uint16_t *xs, int lane) {
-    const int ln = lane & 31, half = lane >> 5;
-    o[0] = o[1] = f32x16{};
+__device__ __forceinline__ void through_state(typename Of<LP>::Out &o, const typename Of<LP>::State &S, const uint16_t *xs, int lane) {
+    constexpr int NB = Of<LP>::NB;
+    lane = fresh(lane);
+    const uint16_t *const row = xs + (lane & 15) * kPitch<LP> + 8 * (lane >> 4);
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int ib = 0; ib < 4; ++ib) o[b][ib] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int s = 0; s < Of<LP>::STEPS; ++s) {
-        float v[8];
+        Frag f[NB][PR];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = S[s / 2][8 * (s % 2) + e];
-        Frag f[PR];
-        parts_of<PR>(v, f);
+        for (int b = 0; b < NB; ++b) {
+            float v[8];
 #pragma unroll
-        for (int ib = 0; ib < 2; ++ib) {
+            for (int e = 0; e < 8; ++e) v[e] = S[b][2 * s + e / 4][e % 4];
+            parts_of<PR>(v, f[b]);
+        }
+#pragma unroll
+        for (int ib = 0; ib < 4; ++ib) {
             Frag x;
-            read_row_as_rows<LP>(x, xs, 32 * ib + ln, half, s);
+            x.q = *reinterpret_cast<const u32x4 *>(row + 16 * ib * kPitch<LP> + 32 * s);
 #pragma unroll
-            for (int n = 0; n < PR; ++n) o[ib] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[n].b, x.b, o[ib], 0, 0, 0);
+            for (int n = 0; n < PR; ++n)
+#pragma unroll
+                for (int b = 0; b < NB; ++b) o[b][ib] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[b][n].b, x.b, o[b][ib], 0, 0, 0);
         }
     }
 }
 
-// Tile t of the three that hold pairs that see each other: rows jb of y, ib of x.
+// Of the 16 tiles of 16 x 16 pairs, the ten that hold some that see each other: tile t has rows 16 jb on of y and 16 ib on
+// of x.
+constexpr int kTiles = 10;
 template <bool REV>
 __device__ __forceinline__ void tile_of(int t, int *jb, int *ib) {
-    *ib = REV ? t == 2 : t > 0;
-    *jb = REV ? t > 0 : t == 2;
+    const int a = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3, b = t - a * (a + 1) / 2;
+    *ib = REV ? b : a, *jb = REV ? a : b;
 }
 
-// P^T = <y_j, x_i> e^{..}, rounded to bf16, one tile, to LDS: row i, its j in the order of an operand's
-// lanes.  MORE: also sums over j of P times the product of a second pair of rows, for each i (kept unrounded: the
-// decays' gradient is fp32); x2(s) gives a lane's share of the second x at step s.
-template <int LP, bool REV, bool MORE, typename X2>
+// Where P holds row i and column j: a row's columns in the order that an operand's lanes take them.
+__device__ __forceinline__ int pair_at(int i, int j) { return i * kPP + (j & 32) + 2 * (j & 12) + (j & 16) / 4 + (j & 3); }
+
+// The tiles beside the diagonal that a product of 32 columns takes along are zeros, once and for all.
+template <bool REV>
+__device__ __forceinline__ void pair_zeros(uint16_t *P, int t) {
+    if (t >= 128) return;
+    const int i = (t & 64 ? 32 : 0) + (REV ? 16 : 0) + (t & 15), j = (t & 64 ? 32 : 0) + (REV ? 0 : 16) + (t & 48) / 4;
+    *reinterpret_cast<u32x2 *>(P + pair_at(i, j)) = u32x2{0, 0};
+}
+
+// P^T = <y_j, x_i> e^{..}, rounded to bf16, one tile, to LDS.  GRAD: also sums over j of P times the product of a
+// second pair of rows, for each i (kept unrounded: the decays' gradient is fp32), for each head times the events between
+// the two; x2(s) gives a lane's share of the second x at step s.
+template <int LP, bool REV, int GRAD, typename X2>
 __device__ __forceinline__ float pair_tile(uint16_t *P, const Decays &dec, const uint16_t *xs, const uint16_t *ys, X2 x2,
                                            const uint16_t *y2s, int jb, int ib, int lane) {
-    const int ln = lane & 31, half = lane >> 5;
-    f32x16 s = f32x16{}, m = f32x16{};
+    lane = fresh(lane);
+    const int ln = lane & 15, quad = lane >> 4;
+    const int xat = (16 * ib + ln) * kPitch<LP> + 8 * quad, yat = (16 * jb + ln) * kPitch<LP> + 8 * quad;
+    floatx4 s = {0.f, 0.f, 0.f, 0.f}, m = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < Of<LP>::STEPS; ++i) {
         Frag x, y;
-        read_row(x, xs + row_base<LP>(32 * ib + ln, half), i);
-        read_row(y, ys + row_base<LP>(32 * jb + ln, half), i);
-        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(y.b, x.b, s, 0, 0, 0);
-        if constexpr (MORE) {
+        x.q = *reinterpret_cast<const u32x4 *>(xs + xat + 32 * i);
+        y.q = *reinterpret_cast<const u32x4 *>(ys + yat + 32 * i);
+        s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(y.b, x.b, s, 0, 0, 0);
+        if constexpr (GRAD != kNone) {
             const Frag u = x2(i);
             Frag v;
-            read_row(v, y2s + row_base<LP>(32 * jb + ln, half), i);
-            m = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v.b, u.b, m, 0, 0, 0);
+            v.q = *reinterpret_cast<const u32x4 *>(y2s + yat + 32 * i);
+            m = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v.b, u.b, m, 0, 0, 0);
         }
     }
-    const int i = 32 * ib + ln;
+    const int i = 16 * ib + ln, j0 = 16 * jb + 4 * quad;
     const float hi = dec.hi[i], lo = dec.lo[i];
-    float sum = 0.f;
+    const floatx4 hj = *reinterpret_cast<const floatx4 *>(dec.hi + j0), lj = *reinterpret_cast<const floatx4 *>(dec.lo + j0);
+    float p[4], sum = 0.f;
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        const int j0 = 32 * jb + 8 * g + 4 * half;
-        const floatx4 hj = *reinterpret_cast<const floatx4 *>(dec.hi + j0), lj = *reinterpret_cast<const floatx4 *>(dec.lo + j0);
-        float p[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const float diff = REV ? (hj[r] - hi) + (lj[r] - lo) : (hi - hj[r]) + (lo - lj[r]);
-            const bool sees = REV ? j0 + r >= i : j0 + r <= i;
-            const float x = s[4 * g + r] * __builtin_amdgcn_exp2f(diff);
-            p[r] = sees ? x : 0.f;
-            if constexpr (MORE) sum += sees ? x * m[4 * g + r] : 0.f;
-        }
-        *reinterpret_cast<u32x2 *>(P + i * kPP + 32 * jb + 16 * (g / 2) + 8 * half + 4 * (g % 2)) =
-            u32x2{pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3])};
+    for (int r = 0; r < 4; ++r) {
+        const float diff = REV ? (hj[r] - hi) + (lj[r] - lo) : (hi - hj[r]) + (lo - lj[r]);
+        const bool sees = REV ? j0 + r >= i : j0 + r <= i;
+        const float x = s[r] * __builtin_amdgcn_exp2f(diff);
+        p[r] = sees ? x : 0.f;
+        if constexpr (GRAD != kNone) sum += sees ? x * m[r] * (GRAD == kHead ? static_cast<float>(REV ? j0 + r - i : i - j0 - r) : 1.f) : 0.f;
     }
-    return MORE ? add_halves(sum) : 0.f;
+    *reinterpret_cast<u32x2 *>(P + pair_at(i, j0)) = u32x2{pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3])};
+    return GRAD != kNone ? add_quarters(sum) : 0.f;
 }
 
 // o^T += z^T P^T
 template <int LP, bool REV>
-__device__ __forceinline__ void through_pairs(f32x16 (&o)[2], const uint16_t *P, const uint16_t *zs, int w, int lane) {
-    const uint16_t *zcol = zs + column_base<LP>(lane);
-    const uint16_t *row = P + (lane & 31) * kPP + 8 * (lane >> 5);
+__device__ __forceinline__ void through_pairs(typename Of<LP>::Out &o, const uint16_t *P, const uint16_t *zs, int w, int lane) {
+    constexpr int NB = Of<LP>::NB;
+    lane = fresh(lane);
+    const uint16_t *const zcol = zs + columns_base<LP>(lane);
+    const uint16_t *const row = P + (lane & 15) * kPP + 8 * (lane >> 4);
 #pragma unroll
-    for (int u = 0; u < kC / 16; ++u) {
-        Frag z;
-        read_columns<LP>(z, zcol, 16 * u, 32 * w);
+    for (int s = 0; s < kC / 32; ++s) {
+        Frag z[NB];
 #pragma unroll
-        for (int ib = 0; ib < 2; ++ib) {
-            if (REV ? ib == 1 && u < 2 : ib == 0 && u >= 2) continue;  // none of its pairs see each other
+        for (int b = 0; b < NB; ++b) columns<LP>(z[b], zcol, 32 * s, NB * w + b);
+#pragma unroll
+        for (int ib = 0; ib < 4; ++ib) {
+            if (REV ? ib / 2 > s : ib / 2 < s) continue;  // none of its pairs see each other
             Frag p;
-            p.q = *reinterpret_cast<const u32x4 *>(row + 32 * ib * kPP + 16 * u);
-            o[ib] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(z.b, p.b, o[ib], 0, 0, 0);
+            p.q = *reinterpret_cast<const u32x4 *>(row + 16 * ib * kPP + 32 * s);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) o[b][ib] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(z[b].b, p.b, o[b][ib], 0, 0, 0);
         }
     }
 }
@@ -306,48 +434,85 @@ __device__ __forceinline__ void through_pairs(f32x16 (&o)[2], const uint16_t *P,
 // The same one row of z at a time, added where it is seen: what a row after it holds does not reach an output,
 // though 0 * infinity is NaN.
 template <int LP>
-__device__ __forceinline__ void through_pairs_apart(f32x16 (&o)[2], const uint16_t *P, const uint16_t *zs, int w, int lane) {
-    const uint16_t *zcol = zs + column_base<LP>(lane);
-    const uint16_t *row = P + (lane & 31) * kPP + 8 * (lane >> 5);
+__device__ __forceinline__ void through_pairs_apart(typename Of<LP>::Out &o, const uint16_t *P, const uint16_t *zs, int w, int lane) {
+    lane = fresh(lane);
+    const uint16_t *const zcol = zs + columns_base<LP>(lane);
+    const uint16_t *const row = P + (lane & 15) * kPP + 8 * (lane >> 4);
 #pragma unroll 1
     for (int j = 0; j < kC; ++j) {
-        const int u = j / 16, mine = j % 16 - 4 * (lane >> 5);  // which of a lane's rows 0..3 and 8..11
-        Frag z;
-        read_columns<LP>(z, zcol, 16 * u, 32 * w);
+        const int m = (lane >> 4) == (j & 12) / 4 ? j & 19 : -1;  // which of a lane's rows 0..3 and 16..19
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int first = 8 * (e / 2) + 2 * (e % 2);
-            z.w[e] = mine == first ? z.w[e] & 0xffffu : mine == first + 1 ? z.w[e] & 0xffff0000u : 0u;
-        }
+        for (int b = 0; b < Of<LP>::NB; ++b) {
+            Frag z;
+            columns<LP>(z, zcol, j & 32, Of<LP>::NB * w + b);
 #pragma unroll
-        for (int ib = 0; ib < 2; ++ib) {
-            Frag p;
-            p.q = *reinterpret_cast<const u32x4 *>(row + 32 * ib * kPP + 16 * u);
-            if (j > 32 * ib + (lane & 31)) p.q = u32x4{0, 0, 0, 0};  // the tile that nobody sees is not written
-            const f32x16 add = __builtin_amdgcn_mfma_f32_32x32x16_bf16(z.b, p.b, f32x16{}, 0, 0, 0);
+            for (int e = 0; e < 4; ++e) {
+                const int first = 16 * (e / 2) + 2 * (e % 2);
+                z.w[e] = m == first ? z.w[e] & 0xffffu : m == first + 1 ? z.w[e] & 0xffff0000u : 0u;
+            }
 #pragma unroll
-            for (int r = 0; r < 16; ++r)
-                if (j <= 32 * ib + (lane & 31)) o[ib][r] += add[r];
+            for (int ib = 0; ib < 4; ++ib) {
+                const bool sees = j <= 16 * ib + (lane & 15);
+                Frag p;
+                p.q = *reinterpret_cast<const u32x4 *>(row + 16 * ib * kPP + (j & 32));
+                if (!sees) p.q = u32x4{0, 0, 0, 0};  // a tile that nobody sees is not written
+                const floatx4 add = __builtin_amdgcn_mfma_f32_16x16x32_bf16(z.b, p.b, floatx4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (sees) o[b][ib][r] += add[r];
+            }
         }
     }
 }
 
-// Rows of one chunk's outputs, columns 32 w on.
-template <int LP>
-__device__ __forceinline__ void out_rows(const f32x16 (&o)[2], uint16_t *out, int64_t stride, int rows, int d, float scale, int w,
-                                         int lane) {
-    const int ln = lane & 31, half = lane >> 5;
+// o times f of each row; MORE: *sums of o's columns times those of the row of t, for rows 16 ib + ln.
+template <int LP, bool MORE>
+__device__ __forceinline__ void weigh(typename Of<LP>::Out &o, const float *f, const uint16_t *ts, float *sums, int w, int lane) {
+    lane = fresh(lane);
+    const int ln = lane & 15, quad = lane >> 4;
 #pragma unroll
-    for (int ib = 0; ib < 2; ++ib) {
-        if (32 * ib + ln >= rows) continue;
-        uint16_t *at = out + (32 * ib + ln) * stride;
+    for (int ib = 0; ib < 4; ++ib) {
+        const int row = 16 * ib + ln;
+        const float x = f[row];
+        float sum = 0.f;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const int c = 32 * w + 8 * g + 4 * half;
-            if (32 * w + 8 * g < d)
-                *(DLRM_GLOBAL u32x2 *)(at + c) = u32x2{pack_bf16(o[ib][4 * g] * scale, o[ib][4 * g + 1] * scale),
-                                                       pack_bf16(o[ib][4 * g + 2] * scale, o[ib][4 * g + 3] * scale)};
+        for (int b = 0; b < Of<LP>::NB; ++b) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) o[b][ib][r] *= x;
+            if constexpr (MORE) {
+                const u32x2 t = *reinterpret_cast<const u32x2 *>(ts + row * kPitch<LP> + place_of(16 * (Of<LP>::NB * w + b)) + 8 * quad);
+                sum += o[b][ib][0] * bf16_lo(t.x) + o[b][ib][1] * bf16_hi(t.x) + (o[b][ib][2] * bf16_lo(t.y) + o[b][ib][3] * bf16_hi(t.y));
+            }
         }
+        if constexpr (MORE) {
+            sum = add_quarters(sum);
+            if (quad == 0) sums[row] = sum;
+        }
+    }
+}
+
+// Rows of one chunk's outputs, a wavefront's columns, by way of that part of a tile that nobody reads any more
+// (from the accumulators a store would write 8 bytes of each of 16 rows).
+template <int LP>
+__device__ __forceinline__ void out_rows(const typename Of<LP>::Out &o, uint16_t *tile, uint16_t *out, int64_t stride, int rows, int d,
+                                         float scale, int w, int lane) {
+    constexpr int NB = Of<LP>::NB, LANES = 2 * NB, AT_ONCE = 64 / LANES;  // lanes a row
+    lane = fresh(lane);
+    const int ln = lane & 15, quad = lane >> 4;
+    uint16_t *const part = tile + 16 * NB * w;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int ib = 0; ib < 4; ++ib)
+            *reinterpret_cast<u32x2 *>(part + (16 * ib + ln) * kPitch<LP> + 16 * b + 4 * quad) =
+                u32x2{pack_bf16(o[b][ib][0] * scale, o[b][ib][1] * scale), pack_bf16(o[b][ib][2] * scale, o[b][ib][3] * scale)};
+    wave_lds_sync();
+    const int col = 8 * (lane % LANES);
+#pragma unroll
+    for (int i = 0; i < kC / AT_ONCE; ++i) {
+        const int row = AT_ONCE * i + lane / LANES;
+        if (row < rows && 16 * NB * w + col < d)
+            *(DLRM_GLOBAL u32x4 *)(out + row * stride + 16 * NB * w + col) = *reinterpret_cast<const u32x4 *>(part + row * kPitch<LP> + col);
     }
 }
 
@@ -365,12 +530,17 @@ Cut cut_of(const Walk &a, int64_t max_len);
 
 int64_t state_floats(const Walk &a, const Cut &c);  // of the runs' states and fades
 
+constexpr int padded(int d) { return d <= 32 ? 32 : d <= 64 ? 64 : 128; }
+
 // The states at the start of every run, forward (y and z of `a`) or reversed, into `states`.
 // `first`: what sequences begin with, or NULL.
 int run_states(const Walk &a, const Cut &c, bool reversed, int up, const float *first, float *states, hipStream_t stream);
 
-// The forward walk; `up` and `more` as the kernel's.
-int walk(const Walk &a, int up, bool more, hipStream_t stream);
+// Workgroups that share a group's query heads in the forward walk.
+int splits_of(const Walk &a);
+
+// The forward walk; `up`, `grad`: the kernel's.
+int walk(const Walk &a, int up, int grad, hipStream_t stream);
 
 }  // namespace decay
 }  // namespace seq
