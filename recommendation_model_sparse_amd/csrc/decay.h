@@ -48,6 +48,7 @@ struct Walk {
     int32_t run;         // chunks of a run, a workgroup's share of a sequence; 0: the whole of it
     int32_t splits;      // workgroups that share a group's query heads (forward)
     uint32_t slots;      // runs, or sequences
+    const int32_t *order;  // [B] the sequences, those of the most chunks first; NULL: as they come
     const float *start;  // states: of runs [slots][Hkv][d][d], or [B][Hkv][d][d]; NULL: zeros
     float *last;         // [B][Hkv][d][d] or NULL
     float *fade;         // e^(sum of g) of each run, [slots][Hkv]
@@ -70,15 +71,18 @@ struct Part {
     bool any;
 };
 
-__device__ __forceinline__ Part part_of(const Walk &a, uint32_t id) {
+// A slot's workgroups, which read the same rows, go to one XCD, and the slots to the XCDs in turn.
+__device__ __forceinline__ Part part_of(const Walk &a) {
     Part p;
+    const uint32_t of_slot = a.Hkv * a.splits, turn = blockIdx.x / (kNumXcd * of_slot), at = blockIdx.x - turn * kNumXcd * of_slot;
+    const uint32_t id = (turn * kNumXcd + at % kNumXcd) * of_slot + at / kNumXcd;
     const uint32_t one = id / static_cast<uint32_t>(a.splits);
     p.split = static_cast<int>(id - one * a.splits);
     p.slot = one / static_cast<uint32_t>(a.Hkv), p.kvh = static_cast<int>(one - p.slot * a.Hkv);
     p.any = p.slot < a.slots;
     if (!p.any) return p;
     const int T = kC * a.run;
-    p.b = a.run ? find_sequence(a, a.off, a.N, static_cast<int>(p.slot), T) : static_cast<int>(p.slot);
+    p.b = a.run ? find_sequence(a, a.off, a.N, static_cast<int>(p.slot), T) : a.order ? a.order[p.slot] : static_cast<int>(p.slot);
     const int r0 = offset_at(a, a.off, p.b, a.N), r1 = offset_at(a, a.off, p.b + 1, a.N);
     p.row0 = r0, p.len = max(r1 - r0, 0);
     p.chunks = (p.len + kC - 1) / kC;
@@ -114,7 +118,7 @@ __device__ __forceinline__ double last_lane(double x) {
 
 // What a chunk's decays come to, for each event: its sum G as two fp32 numbers (their sum holds 48 bits:
 // differences are exact to fp32 whatever pauses lie between), e^G and e^{G_n - G}, in base 2; e^{G_n}.
-struct Decays {
+struct __attribute__((aligned(16))) Decays {
     float hi[kC], lo[kC], from[kC], to[kC];
     float fade;
 };
@@ -166,12 +170,11 @@ __device__ __forceinline__ float add_quarters(float x) {
     return add_halves(__uint_as_float(r[0]) + __uint_as_float(r[1]));
 }
 
-// NB: blocks of 16 columns a wavefront.  Two of them read each tile from LDS half as often.
 template <int LP>
 struct Of {
-    static constexpr int NB = LP == 128 ? 2 : 1, WAVES = LP / 16 / NB, CT = LP / 16, STEPS = LP / 32, TILE = kC * kPitch<LP>;
-    typedef floatx4 State[NB][CT];  // block b, tile ct, register r: row 16 ct + 4 quad + r, column 16 (NB w + b) + ln
-    typedef floatx4 Out[NB][4];     // block b, rows 16 ib on, register r: column 16 (NB w + b) + 4 quad + r of row 16 ib + ln
+    static constexpr int WAVES = LP / 16, CT = LP / 16, STEPS = LP / 32, TILE = kC * kPitch<LP>;
+    typedef floatx4 State[CT];  // tile ct, register r: row 16 ct + 4 quad + r, column 16 w + ln
+    typedef floatx4 Out[4];     // rows 16 ib on, register r: column 16 w + 4 quad + r of row 16 ib + ln
 };
 
 // Tiles hold each row's columns in the order in which an accumulator holds its rows: of 32, the four from 4 q on
@@ -179,16 +182,38 @@ struct Of {
 // other operand comes from a tile or from the accumulators; the order of a product's sum is of no account.
 __device__ __forceinline__ constexpr int place_of(int col) { return (col & ~31) + 2 * (col & 12) + (col & 16) / 4 + (col & 3); }
 
+// The 64 rows of a chunk on their way to LDS.  The reads go through a buffer descriptor that ends with the last
+// row: past it they give zeros, so that they need no branch (one would wait for reads under way, to carry
+// their registers through it), and where nothing is wanted there are no rows.
 template <int LP, int THREADS>
-__device__ __forceinline__ void tile_store(const Stage<LP, THREADS> &s, uint16_t *tile) {
-    const int col = 8 * (fresh(threadIdx.x) % Stage<LP, THREADS>::CH);
-    uint16_t *const at = tile + s.row * kPitch<LP> + place_of(col);
-#pragma unroll
-    for (int i = 0; i < Stage<LP, THREADS>::N; ++i) {
-        *reinterpret_cast<u32x2 *>(at + i * Stage<LP, THREADS>::R * kPitch<LP>) = u32x2{s.r[i].x, s.r[i].y};
-        *reinterpret_cast<u32x2 *>(at + i * Stage<LP, THREADS>::R * kPitch<LP> + 8) = u32x2{s.r[i].z, s.r[i].w};
+struct Loader {
+    static constexpr int CH = LP / 8, N = kC * CH / THREADS, R = THREADS / CH;
+    u32x4 r[N];
+    uint32_t at, step;
+
+    __device__ __forceinline__ Loader(int64_t stride, int d) {
+        const int row = threadIdx.x / CH, col = 8 * (threadIdx.x % CH);
+        const uint32_t row_bytes = 2 * static_cast<uint32_t>(stride);  // < 2^25
+        at = col < d ? row * row_bytes + 2 * col : 0x80000000u;        // columns past the head: past every descriptor
+        step = R * row_bytes;
     }
-}
+    __device__ __forceinline__ void load(const uint16_t *base, int64_t stride, int d, int rows) {
+        rows = min(rows, kC);
+        const int64_t bytes = rows > 0 ? 2 * ((rows - 1) * stride + d) : 0;
+        const auto desc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(base), 0, static_cast<int>(bytes), 0x00027000);
+#pragma unroll
+        for (int i = 0; i < N; ++i) r[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(desc, at + i * step, 0, 0));
+    }
+    __device__ __forceinline__ void store(uint16_t *tile) const {
+        const int thread = fresh(threadIdx.x);
+        uint16_t *const to = tile + thread / CH * kPitch<LP> + place_of(8 * (thread % CH));
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            *reinterpret_cast<u32x2 *>(to + i * R * kPitch<LP>) = u32x2{r[i].x, r[i].y};
+            *reinterpret_cast<u32x2 *>(to + i * R * kPitch<LP> + 8) = u32x2{r[i].z, r[i].w};
+        }
+    }
+};
 
 // The high halves of two words.
 __device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
@@ -221,49 +246,39 @@ __device__ __forceinline__ void parts_of(const float (&x)[8], Frag (&out)[N]) {
 // S from memory (rows y, columns z; TRANSPOSED: the other way round) or zeros.
 template <int LP, bool TRANSPOSED>
 __device__ __forceinline__ void state_load(typename Of<LP>::State &S, const float *p, int d, int w, int lane) {
-    const int ln = lane & 15, quad = lane >> 4;
+    const int e = 16 * w + (lane & 15);
 #pragma unroll
-    for (int b = 0; b < Of<LP>::NB; ++b) {
-        const int e = 16 * (Of<LP>::NB * w + b) + ln;
+    for (int ct = 0; ct < Of<LP>::CT; ++ct) {
+        const int c = 16 * ct + 4 * (lane >> 4);
+        S[ct] = floatx4{0.f, 0.f, 0.f, 0.f};
+        if (!p || e >= d || c >= d) continue;
+        if constexpr (TRANSPOSED) {
+            S[ct] = *(const DLRM_GLOBAL floatx4 *)(p + e * d + c);
+        } else {
 #pragma unroll
-        for (int ct = 0; ct < Of<LP>::CT; ++ct) {
-            const int c = 16 * ct + 4 * quad;
-            S[b][ct] = floatx4{0.f, 0.f, 0.f, 0.f};
-            if (!p || e >= d || c >= d) continue;
-            if constexpr (TRANSPOSED) {
-                S[b][ct] = *(const DLRM_GLOBAL floatx4 *)(p + e * d + c);
-            } else {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) S[b][ct][r] = p[(c + r) * d + e];
-            }
+            for (int r = 0; r < 4; ++r) S[ct][r] = p[(c + r) * d + e];
         }
     }
 }
 
 template <int LP>
 __device__ __forceinline__ void state_store(const typename Of<LP>::State &S, float *p, int d, int w, int lane) {
-    const int ln = lane & 15, quad = lane >> 4;
+    const int e = 16 * w + (lane & 15);
 #pragma unroll
-    for (int b = 0; b < Of<LP>::NB; ++b) {
-        const int e = 16 * (Of<LP>::NB * w + b) + ln;
+    for (int ct = 0; ct < Of<LP>::CT; ++ct) {
+        const int c = 16 * ct + 4 * (lane >> 4);
+        if (e >= d || c >= d) continue;
 #pragma unroll
-        for (int ct = 0; ct < Of<LP>::CT; ++ct) {
-            const int c = 16 * ct + 4 * quad;
-            if (e >= d || c >= d) continue;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) p[(c + r) * d + e] = S[b][ct][r];
-        }
+        for (int r = 0; r < 4; ++r) p[(c + r) * d + e] = S[ct][r];
     }
 }
 
 template <int LP>
 __device__ __forceinline__ void state_fade(typename Of<LP>::State &S, float f) {
 #pragma unroll
-    for (int b = 0; b < Of<LP>::NB; ++b)
+    for (int ct = 0; ct < Of<LP>::CT; ++ct)
 #pragma unroll
-        for (int ct = 0; ct < Of<LP>::CT; ++ct)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) S[b][ct][r] *= f;
+        for (int r = 0; r < 4; ++r) S[ct][r] *= f;
 }
 
 // Transposed operand of v_mfma_f32_16x16x32_bf16 from a tile: a lane gets column 16 block + ln of the rows
@@ -285,34 +300,27 @@ __device__ __forceinline__ void columns(Frag &f, const uint16_t *at, int row0, i
 template <int LP, int UP>
 __device__ __forceinline__ void state_grow(typename Of<LP>::State &S, const uint16_t *ys, const uint16_t *zs, const float *weight, int w,
                                            int lane) {
-    constexpr int NB = Of<LP>::NB;
     lane = fresh(lane);
     const uint16_t *const ycol = ys + columns_base<LP>(lane), *const zcol = zs + columns_base<LP>(lane);
     const float *const wj = weight + 4 * (lane >> 4);
 #pragma unroll
     for (int s = 0; s < kC / 32; ++s) {
-        Frag zw[NB][UP];
+        Frag z, zw[UP];
+        columns<LP>(z, zcol, 32 * s, w);
+        float x[8];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            Frag z;
-            columns<LP>(z, zcol, 32 * s, NB * w + b);
-            float x[8];
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                const floatx4 f = *reinterpret_cast<const floatx4 *>(wj + 32 * s + 16 * g);
-                x[4 * g] = bf16_lo(z.w[2 * g]) * f[0], x[4 * g + 1] = bf16_hi(z.w[2 * g]) * f[1];
-                x[4 * g + 2] = bf16_lo(z.w[2 * g + 1]) * f[2], x[4 * g + 3] = bf16_hi(z.w[2 * g + 1]) * f[3];
-            }
-            parts_of<UP>(x, zw[b]);
+        for (int g = 0; g < 2; ++g) {
+            const floatx4 f = *reinterpret_cast<const floatx4 *>(wj + 32 * s + 16 * g);
+            x[4 * g] = bf16_lo(z.w[2 * g]) * f[0], x[4 * g + 1] = bf16_hi(z.w[2 * g]) * f[1];
+            x[4 * g + 2] = bf16_lo(z.w[2 * g + 1]) * f[2], x[4 * g + 3] = bf16_hi(z.w[2 * g + 1]) * f[3];
         }
+        parts_of<UP>(x, zw);
 #pragma unroll
         for (int ct = 0; ct < Of<LP>::CT; ++ct) {
             Frag y;
             columns<LP>(y, ycol, 32 * s, ct);
 #pragma unroll
-            for (int n = 0; n < UP; ++n)
-#pragma unroll
-                for (int b = 0; b < NB; ++b) S[b][ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(y.b, zw[b][n].b, S[b][ct], 0, 0, 0);
+            for (int n = 0; n < UP; ++n) S[ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(y.b, zw[n].b, S[ct], 0, 0, 0);
         }
     }
 }
@@ -320,31 +328,23 @@ __device__ __forceinline__ void state_grow(typename Of<LP>::State &S, const uint
 // o^T = S^T x^T
 template <int LP, int PR>
 __device__ __forceinline__ void through_state(typename Of<LP>::Out &o, const typename Of<LP>::State &S, const uint16_t *xs, int lane) {
-    constexpr int NB = Of<LP>::NB;
     lane = fresh(lane);
     const uint16_t *const row = xs + (lane & 15) * kPitch<LP> + 8 * (lane >> 4);
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int ib = 0; ib < 4; ++ib) o[b][ib] = floatx4{0.f, 0.f, 0.f, 0.f};
+    for (int ib = 0; ib < 4; ++ib) o[ib] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int s = 0; s < Of<LP>::STEPS; ++s) {
-        Frag f[NB][PR];
+        float v[8];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = S[b][2 * s + e / 4][e % 4];
-            parts_of<PR>(v, f[b]);
-        }
+        for (int e = 0; e < 8; ++e) v[e] = S[2 * s + e / 4][e % 4];
+        Frag f[PR];
+        parts_of<PR>(v, f);
 #pragma unroll
         for (int ib = 0; ib < 4; ++ib) {
             Frag x;
             x.q = *reinterpret_cast<const u32x4 *>(row + 16 * ib * kPitch<LP> + 32 * s);
 #pragma unroll
-            for (int n = 0; n < PR; ++n)
-#pragma unroll
-                for (int b = 0; b < NB; ++b) o[b][ib] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[b][n].b, x.b, o[b][ib], 0, 0, 0);
+            for (int n = 0; n < PR; ++n) o[ib] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[n].b, x.b, o[ib], 0, 0, 0);
         }
     }
 }
@@ -369,13 +369,15 @@ __device__ __forceinline__ void pair_zeros(uint16_t *P, int t) {
     *reinterpret_cast<u32x2 *>(P + pair_at(i, j)) = u32x2{0, 0};
 }
 
-// P^T = <y_j, x_i> e^{..}, rounded to bf16, one tile, to LDS.  GRAD: also sums over j of P times the product of a
-// second pair of rows, for each i (kept unrounded: the decays' gradient is fp32), for each head times the events between
-// the two; x2(s) gives a lane's share of the second x at step s.
-template <int LP, bool REV, int GRAD, typename X2>
-__device__ __forceinline__ float pair_tile(uint16_t *P, const Decays &dec, const uint16_t *xs, const uint16_t *ys, X2 x2,
-                                           const uint16_t *y2s, int jb, int ib, int lane) {
+// P^T = <y_j, x_i> e^{..}, rounded to bf16, one tile, to LDS.  With a second pair of rows: the same of it to P2 (BOTH);
+// GRAD: sums over j of both products times e^{..}, for each i (kept unrounded: the decays' gradient is fp32), for each head
+// times the events between the two.
+template <int LP, bool REV, bool BOTH, int GRAD>
+__device__ __forceinline__ float pair_tile(uint16_t *P, uint16_t *P2, const Decays &dec, const uint16_t *xs, const uint16_t *ys,
+                                           const uint16_t *x2s, const uint16_t *y2s, int t, int lane) {
     lane = fresh(lane);
+    int jb, ib;
+    tile_of<REV>(t, &jb, &ib);
     const int ln = lane & 15, quad = lane >> 4;
     const int xat = (16 * ib + ln) * kPitch<LP> + 8 * quad, yat = (16 * jb + ln) * kPitch<LP> + 8 * quad;
     floatx4 s = {0.f, 0.f, 0.f, 0.f}, m = {0.f, 0.f, 0.f, 0.f};
@@ -385,9 +387,9 @@ __device__ __forceinline__ float pair_tile(uint16_t *P, const Decays &dec, const
         x.q = *reinterpret_cast<const u32x4 *>(xs + xat + 32 * i);
         y.q = *reinterpret_cast<const u32x4 *>(ys + yat + 32 * i);
         s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(y.b, x.b, s, 0, 0, 0);
-        if constexpr (GRAD != kNone) {
-            const Frag u = x2(i);
-            Frag v;
+        if constexpr (BOTH || GRAD != kNone) {
+            Frag u, v;
+            u.q = *reinterpret_cast<const u32x4 *>(x2s + xat + 32 * i);
             v.q = *reinterpret_cast<const u32x4 *>(y2s + yat + 32 * i);
             m = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v.b, u.b, m, 0, 0, 0);
         }
@@ -395,38 +397,38 @@ __device__ __forceinline__ float pair_tile(uint16_t *P, const Decays &dec, const
     const int i = 16 * ib + ln, j0 = 16 * jb + 4 * quad;
     const float hi = dec.hi[i], lo = dec.lo[i];
     const floatx4 hj = *reinterpret_cast<const floatx4 *>(dec.hi + j0), lj = *reinterpret_cast<const floatx4 *>(dec.lo + j0);
-    float p[4], sum = 0.f;
+    float p[4], p2[4], sum = 0.f;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         const float diff = REV ? (hj[r] - hi) + (lj[r] - lo) : (hi - hj[r]) + (lo - lj[r]);
         const bool sees = REV ? j0 + r >= i : j0 + r <= i;
-        const float x = s[r] * __builtin_amdgcn_exp2f(diff);
+        const float e = __builtin_amdgcn_exp2f(diff), x = s[r] * e;
         p[r] = sees ? x : 0.f;
+        if constexpr (BOTH) p2[r] = sees ? m[r] * e : 0.f;
         if constexpr (GRAD != kNone) sum += sees ? x * m[r] * (GRAD == kHead ? static_cast<float>(REV ? j0 + r - i : i - j0 - r) : 1.f) : 0.f;
     }
-    *reinterpret_cast<u32x2 *>(P + pair_at(i, j0)) = u32x2{pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3])};
+    const int at = pair_at(i, j0);
+    *reinterpret_cast<u32x2 *>(P + at) = u32x2{pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3])};
+    if constexpr (BOTH) *reinterpret_cast<u32x2 *>(P2 + at) = u32x2{pack_bf16(p2[0], p2[1]), pack_bf16(p2[2], p2[3])};
     return GRAD != kNone ? add_quarters(sum) : 0.f;
 }
 
 // o^T += z^T P^T
 template <int LP, bool REV>
 __device__ __forceinline__ void through_pairs(typename Of<LP>::Out &o, const uint16_t *P, const uint16_t *zs, int w, int lane) {
-    constexpr int NB = Of<LP>::NB;
     lane = fresh(lane);
     const uint16_t *const zcol = zs + columns_base<LP>(lane);
     const uint16_t *const row = P + (lane & 15) * kPP + 8 * (lane >> 4);
 #pragma unroll
     for (int s = 0; s < kC / 32; ++s) {
-        Frag z[NB];
-#pragma unroll
-        for (int b = 0; b < NB; ++b) columns<LP>(z[b], zcol, 32 * s, NB * w + b);
+        Frag z;
+        columns<LP>(z, zcol, 32 * s, w);
 #pragma unroll
         for (int ib = 0; ib < 4; ++ib) {
             if (REV ? ib / 2 > s : ib / 2 < s) continue;  // none of its pairs see each other
             Frag p;
             p.q = *reinterpret_cast<const u32x4 *>(row + 16 * ib * kPP + 32 * s);
-#pragma unroll
-            for (int b = 0; b < NB; ++b) o[b][ib] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(z[b].b, p.b, o[b][ib], 0, 0, 0);
+            o[ib] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(z.b, p.b, o[ib], 0, 0, 0);
         }
     }
 }
@@ -441,26 +443,23 @@ __device__ __forceinline__ void through_pairs_apart(typename Of<LP>::Out &o, con
 #pragma unroll 1
     for (int j = 0; j < kC; ++j) {
         const int m = (lane >> 4) == (j & 12) / 4 ? j & 19 : -1;  // which of a lane's rows 0..3 and 16..19
+        Frag z;
+        columns<LP>(z, zcol, j & 32, w);
 #pragma unroll
-        for (int b = 0; b < Of<LP>::NB; ++b) {
-            Frag z;
-            columns<LP>(z, zcol, j & 32, Of<LP>::NB * w + b);
+        for (int e = 0; e < 4; ++e) {
+            const int first = 16 * (e / 2) + 2 * (e % 2);
+            z.w[e] = m == first ? z.w[e] & 0xffffu : m == first + 1 ? z.w[e] & 0xffff0000u : 0u;
+        }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int first = 16 * (e / 2) + 2 * (e % 2);
-                z.w[e] = m == first ? z.w[e] & 0xffffu : m == first + 1 ? z.w[e] & 0xffff0000u : 0u;
-            }
+        for (int ib = 0; ib < 4; ++ib) {
+            const bool sees = j <= 16 * ib + (lane & 15);
+            Frag p;
+            p.q = *reinterpret_cast<const u32x4 *>(row + 16 * ib * kPP + (j & 32));
+            if (!sees) p.q = u32x4{0, 0, 0, 0};  // a tile that nobody sees is not written
+            const floatx4 add = __builtin_amdgcn_mfma_f32_16x16x32_bf16(z.b, p.b, floatx4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
 #pragma unroll
-            for (int ib = 0; ib < 4; ++ib) {
-                const bool sees = j <= 16 * ib + (lane & 15);
-                Frag p;
-                p.q = *reinterpret_cast<const u32x4 *>(row + 16 * ib * kPP + (j & 32));
-                if (!sees) p.q = u32x4{0, 0, 0, 0};  // a tile that nobody sees is not written
-                const floatx4 add = __builtin_amdgcn_mfma_f32_16x16x32_bf16(z.b, p.b, floatx4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (sees) o[b][ib][r] += add[r];
-            }
+            for (int r = 0; r < 4; ++r)
+                if (sees) o[ib][r] += add[r];
         }
     }
 }
@@ -474,18 +473,12 @@ __device__ __forceinline__ void weigh(typename Of<LP>::Out &o, const float *f, c
     for (int ib = 0; ib < 4; ++ib) {
         const int row = 16 * ib + ln;
         const float x = f[row];
-        float sum = 0.f;
 #pragma unroll
-        for (int b = 0; b < Of<LP>::NB; ++b) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) o[b][ib][r] *= x;
-            if constexpr (MORE) {
-                const u32x2 t = *reinterpret_cast<const u32x2 *>(ts + row * kPitch<LP> + place_of(16 * (Of<LP>::NB * w + b)) + 8 * quad);
-                sum += o[b][ib][0] * bf16_lo(t.x) + o[b][ib][1] * bf16_hi(t.x) + (o[b][ib][2] * bf16_lo(t.y) + o[b][ib][3] * bf16_hi(t.y));
-            }
-        }
+        for (int r = 0; r < 4; ++r) o[ib][r] *= x;
         if constexpr (MORE) {
-            sum = add_quarters(sum);
+            const u32x2 t = *reinterpret_cast<const u32x2 *>(ts + row * kPitch<LP> + place_of(16 * w) + 8 * quad);
+            const float sum = add_quarters(o[ib][0] * bf16_lo(t.x) + o[ib][1] * bf16_hi(t.x) +
+                                           (o[ib][2] * bf16_lo(t.y) + o[ib][3] * bf16_hi(t.y)));
             if (quad == 0) sums[row] = sum;
         }
     }
@@ -496,23 +489,20 @@ __device__ __forceinline__ void weigh(typename Of<LP>::Out &o, const float *f, c
 template <int LP>
 __device__ __forceinline__ void out_rows(const typename Of<LP>::Out &o, uint16_t *tile, uint16_t *out, int64_t stride, int rows, int d,
                                          float scale, int w, int lane) {
-    constexpr int NB = Of<LP>::NB, LANES = 2 * NB, AT_ONCE = 64 / LANES;  // lanes a row
     lane = fresh(lane);
     const int ln = lane & 15, quad = lane >> 4;
-    uint16_t *const part = tile + 16 * NB * w;
+    uint16_t *const part = tile + 16 * w;
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int ib = 0; ib < 4; ++ib)
-            *reinterpret_cast<u32x2 *>(part + (16 * ib + ln) * kPitch<LP> + 16 * b + 4 * quad) =
-                u32x2{pack_bf16(o[b][ib][0] * scale, o[b][ib][1] * scale), pack_bf16(o[b][ib][2] * scale, o[b][ib][3] * scale)};
+    for (int ib = 0; ib < 4; ++ib)
+        *reinterpret_cast<u32x2 *>(part + (16 * ib + ln) * kPitch<LP> + 4 * quad) =
+            u32x2{pack_bf16(o[ib][0] * scale, o[ib][1] * scale), pack_bf16(o[ib][2] * scale, o[ib][3] * scale)};
     wave_lds_sync();
-    const int col = 8 * (lane % LANES);
+    const int col = 8 * (lane & 1);
 #pragma unroll
-    for (int i = 0; i < kC / AT_ONCE; ++i) {
-        const int row = AT_ONCE * i + lane / LANES;
-        if (row < rows && 16 * NB * w + col < d)
-            *(DLRM_GLOBAL u32x4 *)(out + row * stride + 16 * NB * w + col) = *reinterpret_cast<const u32x4 *>(part + row * kPitch<LP> + col);
+    for (int i = 0; i < 2; ++i) {
+        const int row = 32 * i + (lane >> 1);
+        if (row < rows && 16 * w + col < d)
+            *(DLRM_GLOBAL u32x4 *)(out + row * stride + 16 * w + col) = *reinterpret_cast<const u32x4 *>(part + row * kPitch<LP> + col);
     }
 }
 
@@ -521,20 +511,29 @@ __device__ __forceinline__ void out_rows(const typename Of<LP>::Out &o, uint16_t
 // Checks the description and fills what all walks share.
 int check(const dlrm_seq_decay *a, bool offsets, Walk *out);
 
+inline uint32_t workgroups_of(const Walk &a) { return (a.slots + kNumXcd - 1) / kNumXcd * kNumXcd * a.Hkv * a.splits; }
+
 // How sequences are cut: chunks of a run (0: not), and the workgroups' places.
 struct Cut {
     int32_t run;
     int64_t slots;
+    bool order;  // sequences go by their length
 };
 Cut cut_of(const Walk &a, int64_t max_len);
 
-int64_t state_floats(const Walk &a, const Cut &c);  // of the runs' states and fades
-
 constexpr int padded(int d) { return d <= 32 ? 32 : d <= 64 ? 64 : 128; }
+constexpr size_t whole(size_t bytes) { return (bytes + 255) / 256 * 256; }
 
-// The states at the start of every run, forward (y and z of `a`) or reversed, into `states`.
-// `first`: what sequences begin with, or NULL.
-int run_states(const Walk &a, const Cut &c, bool reversed, int up, const float *first, float *states, hipStream_t stream);
+// Bytes of one direction's states and fades of runs, and of the order.
+size_t states_bytes(const Walk &a, const Cut &c);
+size_t order_bytes(const Walk &a, const Cut &c);
+
+// The order of the sequences, into `order`.
+int order_by_length(const Walk &a, int32_t *order, hipStream_t stream);
+
+// The states at the start of every run: of `f` (its y and z) forward, from `first` or zeros, and, unless it is NULL, of
+// `r` reversed, into the states that each has as its start.
+int run_states(const Walk &f, const Walk *r, int up, const float *first, hipStream_t stream);
 
 // Workgroups that share a group's query heads in the forward walk.
 int splits_of(const Walk &a);

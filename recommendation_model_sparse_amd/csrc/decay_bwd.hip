@@ -23,7 +23,7 @@ namespace {
 // from the states themselves.  Over all events of a head: n Z + sum (i + 1) (x_i - y_i) + the pairs times the events between
 // them, i and n within the chunk.
 template <int LP, int UP, int PR, int GRAD>
-__global__ __launch_bounds__(Of<LP>::WAVES * 128, LP == 128 ? 2 : LP == 64 ? 4 : 3) void k_decay_back(const Walk a) {
+__global__ __launch_bounds__(Of<LP>::WAVES * 128, LP == 32 ? 3 : 4) void k_decay_back(const Walk a) {
     using O = Of<LP>;
     constexpr bool MORE = GRAD != kNone;
     constexpr int TEAM = 64 * O::WAVES, THREADS = 2 * TEAM;
@@ -33,7 +33,7 @@ __global__ __launch_bounds__(Of<LP>::WAVES * 128, LP == 128 ? 2 : LP == 64 ? 4 :
     __shared__ double across[MORE ? O::WAVES : 1];
 
     const int tid = threadIdx.x, lane = tid & 63, ln = lane & 15, quad = lane >> 4;
-    const Part p = part_of(a, xcd_contiguous(blockIdx.x, gridDim.x));
+    const Part p = part_of(a);
     if (!p.any) {
         if (GRAD == kHead && p.slot < a.slots && tid == 0) a.sums[static_cast<int64_t>(p.kvh) * a.slots + p.slot] = 0.0;
         return;
@@ -48,22 +48,22 @@ __global__ __launch_bounds__(Of<LP>::WAVES * 128, LP == 128 ? 2 : LP == 64 ? 4 :
     const uint16_t *const yt = team ? Ds : Qs, *const zt = team ? Qs : Ds;
     uint16_t *const P = Ps[team];
 
-    Stage<LP, THREADS> ks(a.x.row, a.d), vs(a.t.row, a.d), qs(a.y.row, a.d), ds(a.z.row, a.d);
-    const auto load_kv = [&](int c) {
-        ks.load(kb, a.x.row, a.d, c * kC, 0, p.len, 0);
-        vs.load(vb, a.t.row, a.d, c * kC, 0, p.len, 0);
-    };
-    const auto load_q = [&](int c, int h) {
-        qs.load(qb + h * a.y.head, a.y.row, a.d, c * kC, 0, p.len, 0);
-        ds.load(db + h * a.z.head, a.z.row, a.d, c * kC, 0, p.len, 0);
+    Loader<LP, THREADS> ks(a.x.row, a.d), vs(a.t.row, a.d), qs(a.y.row, a.d), ds(a.z.row, a.d);
+    const auto load = [&](int c, int h) {  // of k and v with the first head
+        const int rows = c >= p.c0 ? p.len - c * kC : 0;
+        const int64_t row = static_cast<int64_t>(c) * kC;
+        ks.load(kb + row * a.x.row, a.x.row, a.d, h == 0 ? rows : 0);
+        vs.load(vb + row * a.t.row, a.t.row, a.d, h == 0 ? rows : 0);
+        qs.load(qb + row * a.y.row + h * a.y.head, a.y.row, a.d, rows);
+        ds.load(db + row * a.z.row + h * a.z.head, a.z.row, a.d, rows);
     };
     const bool clock = team == 0 && w == O::WAVES - 1;
     float g = 0.f;
     double total = 0.0, carry = 0.0, all = 0.0;
     if (p.c0 < p.c1) {
         if (clock) g = decay_load(a, p, p.c1 - 1, lane);
-        load_kv(p.c1 - 1), load_q(p.c1 - 1, 0);
     }
+    load(p.c1 - 1, 0);
     typename O::State S;
     const float *start = a.start ? a.start + (p.slot * static_cast<int64_t>(a.Hkv) + p.kvh) * a.d * a.d : nullptr;
     if (team) state_load<LP, true>(S, start, a.d, w, lane);
@@ -79,9 +79,10 @@ __global__ __launch_bounds__(Of<LP>::WAVES * 128, LP == 128 ? 2 : LP == 64 ? 4 :
             const float *at = a.marks + ((p.row0 / (kC * a.mark) + p.b + c / a.mark) * a.Hkv + p.kvh) * (LP * LP) + 4 * (tid - TEAM);
             double sum = 0.0;
 #pragma unroll
-            for (int i = 0; i < O::NB * O::CT; ++i) {
-                const floatx4 f = *(const DLRM_GLOBAL floatx4 *)(at + i * 4 * TEAM), s = S[i / O::CT][i % O::CT];
-                for (int r = 0; r < 4; ++r) sum += static_cast<double>(f[r]) * s[r];
+            for (int ct = 0; ct < O::CT; ++ct) {
+                const floatx4 f = *(const DLRM_GLOBAL floatx4 *)(at + ct * 4 * TEAM);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) sum += static_cast<double>(f[r]) * S[ct][r];
             }
 #pragma unroll
             for (int i = 1; i < 64; i <<= 1) sum += __shfl_xor(sum, i);
@@ -101,11 +102,10 @@ __global__ __launch_bounds__(Of<LP>::WAVES * 128, LP == 128 ? 2 : LP == 64 ? 4 :
         float term = 0.f, pairs = 0.f, plus = 0.f, plus_pairs = 0.f, here = 0.f;
         for (int h = 0; h < a.group; ++h) {
             lds_barrier();  // the tiles before have been read
-            if (h == 0) tile_store(ks, Ks), tile_store(vs, Vs);
-            tile_store(qs, Qs), tile_store(ds, Ds);
+            if (h == 0) ks.store(Ks), vs.store(Vs);
+            qs.store(Qs), ds.store(Ds);
             lds_barrier();
-            if (h + 1 < a.group) load_q(c, h + 1);
-            else if (c > p.c0) load_kv(c - 1), load_q(c - 1, 0);
+            load(h + 1 < a.group ? c : c - 1, h + 1 < a.group ? h + 1 : 0);
             if (clock && h == 0 && c > p.c0) {
                 decays(decs[~c & 1], g, lane, &total);
                 if (c - 2 >= p.c0) g = decay_load(a, p, c - 2, lane);
@@ -119,20 +119,13 @@ __global__ __launch_bounds__(Of<LP>::WAVES * 128, LP == 128 ? 2 : LP == 64 ? 4 :
                     if constexpr (GRAD == kEach) plus_pairs += a.pairs[at];
                 }
             }
-#pragma unroll 1
-            for (int t = w; t < kTiles; t += O::WAVES) {
-                int jb, ib;
-                tile_of<true>(t, &jb, &ib);
-                const auto k_row = [&](int s) {
-                    Frag f;
-                    f.q = *reinterpret_cast<const u32x4 *>(Ks + (16 * ib + ln) * kPitch<LP> + 8 * quad + 32 * s);
-                    return f;
-                };
-                if (MORE && team == 1) {
-                    const float sum = pair_tile<LP, true, GRAD>(P, dec, xt, yt, k_row, Qs, jb, ib, lane);
+            // both teams' pairs, tile by tile: they have their decays in common, and dg takes the product of both
+#pragma unroll
+            for (int n = 0; n < (kTiles + 2 * O::WAVES - 1) / (2 * O::WAVES); ++n) {
+                const int t = min(static_cast<int>(wave_id()) + n * 2 * O::WAVES, kTiles - 1);
+                const float sum = pair_tile<LP, true, true, GRAD>(Ps[0], Ps[1], dec, Ks, Qs, Vs, Ds, t, lane);
+                if constexpr (MORE) {
                     if (quad == 0) by_tile[t][ln] = sum;
-                } else {
-                    pair_tile<LP, true, kNone>(P, dec, xt, yt, k_row, nullptr, jb, ib, lane);
                 }
             }
             if (h == 0) {
@@ -174,7 +167,7 @@ __global__ __launch_bounds__(Of<LP>::WAVES * 128, LP == 128 ? 2 : LP == 64 ? 4 :
     }
     if (GRAD == kHead && tid < 64) {
         all = last_lane(prefix_sum(all));
-        if (lane == 0) a.sums[static_cast<int64_t>(p.kvh) * a.slots + p.slot] = all;
+        if (lane == 0) a.sums[static_cast<int64_t>(p.kvh) * a.slots + (a.run ? p.slot : p.b)] = all;  // not by their order, which is left to chance
     }
 }
 
@@ -193,7 +186,7 @@ __global__ __launch_bounds__(256) void k_decay_dg_join(const double *sums, uint3
 
 template <int LP>
 int back(const Walk &a, int grad, hipStream_t stream) {
-    const dim3 grid(round_up_xcd(static_cast<uint64_t>(a.slots) * a.Hkv)), block(Of<LP>::WAVES * 128);
+    const dim3 grid(workgroups_of(a)), block(Of<LP>::WAVES * 128);
     if (grad == kEach) DLRM_LAUNCH("seq_decay_dkv", (k_decay_back<LP, 3, 3, kEach>), grid, block, 0, stream, a);
     else if (grad == kHead) DLRM_LAUNCH("seq_decay_dkv", (k_decay_back<LP, 3, 3, kHead>), grid, block, 0, stream, a);
     else DLRM_LAUNCH("seq_decay_dkv", (k_decay_back<LP, 2, 1, kNone>), grid, block, 0, stream, a);
@@ -205,16 +198,17 @@ int back(const Walk &a, int grad, hipStream_t stream) {
 // without the marks between, as the events' own errors are 6e-7.)
 int mark_of(const Cut &c, bool by_head) { return by_head ? 2 : c.run && c.run < 8 ? c.run : 8; }
 
-// Bytes: the runs' states; for dg, the terms from dq, the states at the marks, the slots' sums.
+// Bytes: the runs' states, forward and reversed, or the order; for dg, the terms from dq, the states at the marks, the
+// slots' sums.
 struct Room {
-    size_t states, terms, marks, sums;
+    size_t states, order, terms, marks, sums;
 };
 Room room_of(Walk a, const Cut &c) {
-    const auto whole = [](size_t n) { return (n + 255) / 256 * 256; };
     a.slots = static_cast<uint32_t>(c.slots);
     const size_t lp = padded(a.d);
-    return Room{whole(4 * static_cast<size_t>(state_floats(a, c))), whole(8 * static_cast<size_t>(a.N) * a.Hkv * splits_of(a)),
-                4 * lp * lp * a.Hkv * static_cast<size_t>(slot_count(a.N, a.B, kC * mark_of(c, a.g_row == 0))), whole(8 * static_cast<size_t>(c.slots) * a.Hkv)};
+    return Room{states_bytes(a, c), order_bytes(a, c), whole(8 * static_cast<size_t>(a.N) * a.Hkv * splits_of(a)),
+                4 * lp * lp * a.Hkv * static_cast<size_t>(slot_count(a.N, a.B, kC * mark_of(c, a.g_row == 0))),
+                whole(8 * static_cast<size_t>(c.slots) * a.Hkv)};
 }
 
 }  // namespace
@@ -227,7 +221,7 @@ extern "C" size_t dlrm_seq_decay_bwd_workspace_size(const dlrm_seq_decay *desc) 
     Walk a;
     if (check(desc, true, &a) != DLRM_OK) return 0;
     const Room r = room_of(a, cut_of(a, desc->max_len));
-    return 256 + r.states + r.terms + r.marks + r.sums;
+    return 256 + 2 * r.states + r.order + r.terms + r.marks + r.sums;
 }
 
 extern "C" int dlrm_seq_decay_bwd(const dlrm_seq_decay *desc, const uint16_t *dout, uint16_t *dq, uint16_t *dk, uint16_t *dv, float *dg,
@@ -242,37 +236,42 @@ extern "C" int dlrm_seq_decay_bwd(const dlrm_seq_decay *desc, const uint16_t *do
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < dlrm_seq_decay_bwd_workspace_size(desc)) return DLRM_ERR_WORKSPACE;
     hipStream_t stream = reinterpret_cast<hipStream_t>(stream_);
     const bool by_head = dg && a.g_row == 0, any = a.N > 0 && a.B > 0;
-    const int grad = !dg ? kNone : by_head ? kHead : kEach;
+    const int grad = !dg ? kNone : by_head ? kHead : kEach, up = dg ? 3 : 2;
     const Cut c = cut_of(a, desc->max_len);
     const Room room = room_of(a, c);
     char *ws = static_cast<char *>(workspace);
-    float *states = reinterpret_cast<float *>(ws);
-    const Heads q = a.x, k = a.y, v = a.z, d = {dout, static_cast<int64_t>(a.Hq) * a.d, a.d};
-    a.run = c.run, a.slots = static_cast<uint32_t>(c.slots);
-    const int up = dg ? 3 : 2, splits = splits_of(a);
-    double *sums = reinterpret_cast<double *>(ws + room.states + room.terms + room.marks);
+    const auto take = [&](size_t bytes) {
+        char *p = ws;
+        ws += bytes;
+        return p;
+    };
+    float *forward = reinterpret_cast<float *>(take(room.states)), *reversed = reinterpret_cast<float *>(take(room.states));
+    int32_t *order = reinterpret_cast<int32_t *>(take(room.order));
+    a.terms = reinterpret_cast<float *>(take(room.terms)), a.marks = reinterpret_cast<float *>(take(room.marks));
+    double *sums = reinterpret_cast<double *>(take(room.sums));
+    a.run = c.run, a.slots = static_cast<uint32_t>(c.slots), a.mark = mark_of(c, by_head);
+    const int splits = splits_of(a);
+    a.pairs = a.terms + a.N * a.Hkv * splits;
     if (any) {
-        a.terms = reinterpret_cast<float *>(ws + room.states), a.pairs = a.terms + a.N * a.Hkv * splits;
-        a.marks = reinterpret_cast<float *>(ws + room.states + room.terms);
-        a.mark = mark_of(c, by_head);
-        a.x = d, a.y = v, a.z = k, a.t = q;
-        a.out = dq;
+        const Heads q = a.x, k = a.y, v = a.z, d = {dout, static_cast<int64_t>(a.Hq) * a.d, a.d};
+        Walk r = a;
+        a.x = d, a.y = v, a.z = k, a.t = q, a.out = dq;
+        r.x = k, r.y = q, r.z = d, r.t = v, r.out = dv, r.out2 = dk;
+        r.parts = splits, r.dg = dg, r.sums = sums;
         if (c.run) {
-            rc = run_states(a, c, false, up, nullptr, states, stream);
-            if (rc != DLRM_OK) return rc;
-            a.start = states;
+            const int64_t states = c.slots * a.Hkv * a.d * a.d;
+            a.start = forward, a.fade = forward + states;
+            r.start = reversed, r.fade = reversed + states;
+            rc = run_states(a, &r, up, nullptr, stream);
+        } else if (c.order) {
+            rc = order_by_length(a, order, stream);
+            a.order = r.order = order;
         }
+        if (rc != DLRM_OK) return rc;
         a.splits = splits;
         rc = walk(a, up, grad, stream);
         if (rc != DLRM_OK) return rc;
-        a.splits = 1, a.parts = splits;
-        a.x = k, a.y = q, a.z = d, a.t = v;
-        a.out = dv, a.out2 = dk, a.dg = dg, a.sums = by_head ? sums : nullptr;
-        if (c.run) {
-            rc = run_states(a, c, true, up, nullptr, states, stream);
-            if (rc != DLRM_OK) return rc;
-        }
-        rc = a.d <= 32 ? back<32>(a, grad, stream) : a.d <= 64 ? back<64>(a, grad, stream) : back<128>(a, grad, stream);
+        rc = a.d <= 32 ? back<32>(r, grad, stream) : a.d <= 64 ? back<64>(r, grad, stream) : back<128>(r, grad, stream);
         if (rc != DLRM_OK) return rc;
     }
     if (by_head)

@@ -40,6 +40,9 @@ int check(const dlrm_seq_decay *a, bool offsets, Walk *out) {
     return DLRM_OK;
 }
 
+// Most sequences that one workgroup puts in order.
+constexpr int kOrdered = 16384;
+
 // Workgroups that fill the GPU.
 static int64_t places_of(int32_t d) { return d <= 32 ? 1536 : d <= 64 ? 1024 : 512; }
 
@@ -48,16 +51,20 @@ static int64_t places_of(int32_t d) { return d <= 32 ? 1536 : d <= 64 ? 1024 : 5
 Cut cut_of(const Walk &a, int64_t max_len) {
     const int64_t longest = std::min(max_len, a.N), chunks = (longest + kC - 1) / kC;
     const int64_t all = slot_count(a.N, a.B, kC) * a.Hkv, places = places_of(a.d);
-    int64_t share = std::max<int64_t>(4, (all + places - 1) / places);  // chunks for each place
+    int64_t share = std::max<int64_t>(2, (all + places - 1) / places);  // chunks for each place
     if (share > 8) share = (share + 7) / 8 * 8;
-    const bool many = a.B * static_cast<int64_t>(a.Hkv) * 16 >= (int64_t(1) << 24);  // more than a launch of k_decay_join holds
+    const bool many = a.B * static_cast<int64_t>(a.Hkv) * 64 >= (int64_t(1) << 24);  // more than a launch of k_decay_join holds
     Cut c;
     c.run = chunks > 2 * share && !many ? static_cast<int32_t>(share) : 0;
     c.slots = c.run ? slot_count(a.N, a.B, kC * c.run) : a.B;
+    c.order = !c.run && chunks > 1 && a.B <= kOrdered && static_cast<int64_t>(a.B) * a.Hkv > places / 2;
     return c;
 }
 
-int64_t state_floats(const Walk &a, const Cut &c) { return c.run ? c.slots * a.Hkv * (static_cast<int64_t>(a.d) * a.d + 1) : 0; }
+size_t states_bytes(const Walk &a, const Cut &c) {
+    return c.run ? whole(4 * static_cast<size_t>(c.slots) * a.Hkv * (static_cast<size_t>(a.d) * a.d + 1)) : 0;
+}
+size_t order_bytes(const Walk &a, const Cut &c) { return c.order ? whole(4 * static_cast<size_t>(a.B)) : 0; }
 
 int splits_of(const Walk &a) {
     int n = 1;
@@ -71,7 +78,7 @@ int splits_of(const Walk &a) {
 namespace {
 
 template <int LP, int UP, int PR, int GRAD>
-__global__ __launch_bounds__(Of<LP>::WAVES * 64, LP == 128 ? (GRAD ? 1 : 2) : LP == 64 ? (GRAD ? 3 : 4) : GRAD ? 2 : 3) void k_decay_walk(const Walk a) {
+__global__ __launch_bounds__(Of<LP>::WAVES * 64, LP == 128 ? (GRAD ? 2 : 4) : LP == 64 ? (GRAD ? 3 : 4) : GRAD ? 2 : 3) void k_decay_walk(const Walk a) {
     constexpr bool MORE = GRAD != kNone;
     using O = Of<LP>;
     constexpr int THREADS = 64 * O::WAVES;
@@ -80,7 +87,7 @@ __global__ __launch_bounds__(Of<LP>::WAVES * 64, LP == 128 ? (GRAD ? 1 : 2) : LP
     __shared__ __attribute__((aligned(16))) uint16_t Ts[MORE ? O::TILE : 8];
     __shared__ float by_wave[MORE ? O::WAVES : 1][kC], by_tile[GRAD == kEach ? kTiles : 1][16];
 
-    const Part p = part_of(a, xcd_contiguous(blockIdx.x, gridDim.x));
+    const Part p = part_of(a);
     if (!p.any) return;
     const int tid = threadIdx.x, lane = tid & 63, ln = lane & 15, quad = lane >> 4;
     const int w = static_cast<int>(wave_id());
@@ -90,22 +97,22 @@ __global__ __launch_bounds__(Of<LP>::WAVES * 64, LP == 128 ? (GRAD ? 1 : 2) : LP
     const uint16_t *zb = a.z.p + p.row0 * a.z.row + p.kvh * a.z.head;
     const uint16_t *tb = MORE ? a.t.p + p.row0 * a.t.row + h0 * a.t.head : nullptr;
 
-    Stage<LP, THREADS> xs(a.x.row, a.d), ys(a.y.row, a.d), zs(a.z.row, a.d), ts(MORE ? a.t.row : 0, a.d);
-    const auto load_yz = [&](int c) {
-        ys.load(yb, a.y.row, a.d, c * kC, 0, p.len, 0);
-        zs.load(zb, a.z.row, a.d, c * kC, 0, p.len, 0);
-    };
-    const auto load_x = [&](int c, int h) {
-        xs.load(xb + h * a.x.head, a.x.row, a.d, c * kC, 0, p.len, 0);
-        if constexpr (MORE) ts.load(tb + h * a.t.head, a.t.row, a.d, c * kC, 0, p.len, 0);
+    Loader<LP, THREADS> xs(a.x.row, a.d), ys(a.y.row, a.d), zs(a.z.row, a.d), ts(MORE ? a.t.row : 0, a.d);
+    const auto load = [&](int c, int h) {  // of y and z with the first head
+        const int rows = c < p.c1 ? p.len - c * kC : 0;
+        const int64_t row = static_cast<int64_t>(c) * kC;
+        ys.load(yb + row * a.y.row, a.y.row, a.d, h == 0 ? rows : 0);
+        zs.load(zb + row * a.z.row, a.z.row, a.d, h == 0 ? rows : 0);
+        xs.load(xb + row * a.x.row + h * a.x.head, a.x.row, a.d, rows);
+        if constexpr (MORE) ts.load(tb + row * a.t.row + h * a.t.head, a.t.row, a.d, rows);
     };
     const bool clock = w == O::WAVES - 1;  // the wavefront that works out the next chunk's decays: it has the fewest tiles
     float g = 0.f;
     double total = 0.0;
     if (p.c0 < p.c1) {
         if (clock) g = decay_load(a, p, p.c0, lane);
-        load_yz(p.c0), load_x(p.c0, 0);
     }
+    load(p.c0, 0);
     typename O::State S;
     const int64_t dd = static_cast<int64_t>(a.d) * a.d;
     state_load<LP, false>(S, a.start ? a.start + ((a.run ? p.slot : p.b) * static_cast<int64_t>(a.Hkv) + p.kvh) * dd : nullptr, a.d, w, lane);
@@ -123,31 +130,25 @@ __global__ __launch_bounds__(Of<LP>::WAVES * 64, LP == 128 ? (GRAD ? 1 : 2) : LP
             if (c > 0 && c % a.mark == 0 && p.split == 0) {
                 float *at = a.marks + ((p.row0 / (kC * a.mark) + p.b + c / a.mark) * a.Hkv + p.kvh) * (LP * LP) + 4 * tid;
 #pragma unroll
-                for (int i = 0; i < O::NB * O::CT; ++i) *(DLRM_GLOBAL floatx4 *)(at + i * 4 * THREADS) = S[i / O::CT][i % O::CT];
+                for (int ct = 0; ct < O::CT; ++ct) *(DLRM_GLOBAL floatx4 *)(at + ct * 4 * THREADS) = S[ct];
             }
         }
         for (int h = 0; h < heads; ++h) {
             lds_barrier();  // the tiles before have been read
-            if (h == 0) tile_store(ys, Ys), tile_store(zs, Zs);
-            tile_store(xs, Xs);
-            if constexpr (MORE) tile_store(ts, Ts);
+            if (h == 0) ys.store(Ys), zs.store(Zs);
+            xs.store(Xs);
+            if constexpr (MORE) ts.store(Ts);
             lds_barrier();
-            if (h + 1 < heads) load_x(c, h + 1);
-            else if (c + 1 < p.c1) load_yz(c + 1), load_x(c + 1, 0);
+            load(h + 1 < heads ? c : c + 1, h + 1 < heads ? h + 1 : 0);
             if (clock && h == 0 && c + 1 < p.c1) {
                 decays(decs[~c & 1], g, lane, &total);
                 if (c + 2 < p.c1) g = decay_load(a, p, c + 2, lane);
             }
-#pragma unroll 1
-            for (int t = w; t < kTiles; t += O::WAVES) {
-                int jb, ib;
-                tile_of<false>(t, &jb, &ib);
-                const auto t_row = [&](int s) {
-                    Frag f;
-                    f.q = *reinterpret_cast<const u32x4 *>(Ts + (16 * ib + ln) * kPitch<LP> + 8 * quad + 32 * s);
-                    return f;
-                };
-                const float sum = pair_tile<LP, false, GRAD == kEach ? kEach : kNone>(P, dec, Xs, Ys, t_row, Zs, jb, ib, lane);
+            // (a wavefront without a last tile makes one that another makes too)
+#pragma unroll
+            for (int n = 0; n < (kTiles + O::WAVES - 1) / O::WAVES; ++n) {
+                const int t = min(w + n * O::WAVES, kTiles - 1);
+                const float sum = pair_tile<LP, false, false, GRAD == kEach ? kEach : kNone>(P, nullptr, dec, Xs, Ys, Ts, Zs, t, lane);
                 if constexpr (GRAD == kEach) {
                     if (quad == 0) by_tile[t][ln] = sum;
                 }
@@ -156,20 +157,15 @@ __global__ __launch_bounds__(Of<LP>::WAVES * 64, LP == 128 ? (GRAD ? 1 : 2) : LP
             through_state<LP, PR>(o, S, Xs, lane);
             weigh<LP, MORE>(o, dec.from, Ts, by_wave[MORE ? w : 0], w, lane);
             lds_barrier();
-            typename O::Out before;
-#pragma unroll
-            for (int i = 0; i < O::NB * 4; ++i) before[i / 4][i % 4] = o[i / 4][i % 4];
+            const floatx4 before[4] = {o[0], o[1], o[2], o[3]};
             through_pairs<LP, false>(o, P, Zs, w, lane);
             float any = 0.f;
 #pragma unroll
-            for (int i = 0; i < O::NB * 4; ++i) {
-                const floatx4 x = o[i / 4][i % 4];
-                any += (x[0] + x[1]) + (x[2] + x[3]);
-            }
+            for (int ib = 0; ib < 4; ++ib) any += (o[ib][0] + o[ib][1]) + (o[ib][2] + o[ib][3]);
             if (__any(!(fabsf(any) < kInf))) {
                 // an infinity or NaN in z reaches the rows before it (0 * NaN in a product): once more, with its rows apart
 #pragma unroll
-                for (int i = 0; i < O::NB * 4; ++i) o[i / 4][i % 4] = before[i / 4][i % 4];
+                for (int ib = 0; ib < 4; ++ib) o[ib] = before[ib];
                 through_pairs_apart<LP>(o, P, Zs, w, lane);
             }
             out_rows<LP>(o, Xs, a.out + ((p.row0 + c * kC) * a.Hq + h0 + h) * a.d, static_cast<int64_t>(a.Hq) * a.d, rows, a.d, a.scale, w,
@@ -199,13 +195,10 @@ __global__ __launch_bounds__(Of<LP>::WAVES * 64, LP == 128 ? (GRAD ? 1 : 2) : LP
 // What each run adds to the state, and how far it fades what was there.  REV: from the sequence's end, y and z
 // the query heads' (all of a group add to one state).
 template <int LP, bool REV, int UP>
-__global__ __launch_bounds__(Of<LP>::WAVES * 64, LP == 128 ? 2 : 4) void k_decay_runs(const Walk a, float *states) {
+__device__ __forceinline__ void run_state(const Walk &a, uint16_t *Ys, uint16_t *Zs, Decays (&decs)[2]) {
     using O = Of<LP>;
     constexpr int THREADS = 64 * O::WAVES;
-    __shared__ __attribute__((aligned(16))) uint16_t Ys[O::TILE], Zs[O::TILE];
-    __shared__ __attribute__((aligned(16))) Decays decs[2];
-
-    const Part p = part_of(a, xcd_contiguous(blockIdx.x, gridDim.x));
+    const Part p = part_of(a);
     if (!p.any || p.chunks == 0 || (REV ? p.c0 == 0 : p.c1 == p.chunks)) return;  // what the last run adds is of no use
     const int lane = threadIdx.x & 63, w = static_cast<int>(wave_id());
     const int heads = REV ? a.group : 1, h0 = p.kvh * heads, n = p.c1 - p.c0;
@@ -214,11 +207,13 @@ __global__ __launch_bounds__(Of<LP>::WAVES * 64, LP == 128 ? 2 : 4) void k_decay
 
     typename O::State S;
     state_load<LP, false>(S, nullptr, a.d, w, lane);
-    Stage<LP, THREADS> ys(a.y.row, a.d), zs(a.z.row, a.d);
+    Loader<LP, THREADS> ys(a.y.row, a.d), zs(a.z.row, a.d);
     const auto chunk = [&](int i) { return REV ? p.c1 - 1 - i : p.c0 + i; };
     const auto load = [&](int i, int h) {
-        ys.load(yb + h * a.y.head, a.y.row, a.d, chunk(i) * kC, 0, p.len, 0);
-        zs.load(zb + h * a.z.head, a.z.row, a.d, chunk(i) * kC, 0, p.len, 0);
+        const int64_t row = static_cast<int64_t>(chunk(i)) * kC;
+        const int rows = i < n ? p.len - chunk(i) * kC : 0;
+        ys.load(yb + row * a.y.row + h * a.y.head, a.y.row, a.d, rows);
+        zs.load(zb + row * a.z.row + h * a.z.head, a.z.row, a.d, rows);
     };
     double total = 0.0;
     float g = 0.f;
@@ -232,10 +227,9 @@ __global__ __launch_bounds__(Of<LP>::WAVES * 64, LP == 128 ? 2 : 4) void k_decay
         const Decays &dec = decs[i & 1];
         for (int h = 0; h < heads; ++h) {
             lds_barrier();
-            tile_store(ys, Ys), tile_store(zs, Zs);
+            ys.store(Ys), zs.store(Zs);
             lds_barrier();
-            if (h + 1 < heads) load(i, h + 1);
-            else if (i + 1 < n) load(i + 1, 0);
+            load(h + 1 < heads ? i : i + 1, h + 1 < heads ? h + 1 : 0);
             if (h == 0) {
                 if (w == 0 && i + 1 < n) {
                     decays(decs[~i & 1], g, lane, &total);
@@ -247,44 +241,90 @@ __global__ __launch_bounds__(Of<LP>::WAVES * 64, LP == 128 ? 2 : 4) void k_decay
         }
     }
     const int64_t at = p.slot * static_cast<int64_t>(a.Hkv) + p.kvh;
-    state_store<LP>(S, states + at * a.d * a.d, a.d, w, lane);
+    state_store<LP>(S, const_cast<float *>(a.start) + at * a.d * a.d, a.d, w, lane);
     if (w == 0 && lane == 0) a.fade[at] = __builtin_amdgcn_exp2f(static_cast<float>(total));
 }
 
-// The states at the runs' starts, in place of what the runs add: four elements a thread.
+template <int LP, int UP, bool BACK>
+__global__ __launch_bounds__(Of<LP>::WAVES * 64, 4) void k_decay_runs(const Walk f, const Walk r) {
+    __shared__ __attribute__((aligned(16))) uint16_t Ys[Of<LP>::TILE], Zs[Of<LP>::TILE];
+    __shared__ __attribute__((aligned(16))) Decays decs[2];
+    if (BACK && blockIdx.y == 0) run_state<LP, true, UP>(r, Ys, Zs, decs);  // the longer one first
+    else run_state<LP, false, UP>(f, Ys, Zs, decs);
+}
+
+// The states at the runs' starts, in place of what the runs add, four elements a thread; sixteen runs are read at once.
 template <bool REV>
-__global__ __launch_bounds__(256) void k_decay_join(const Walk a, const float *first, float *states, uint32_t blocks) {
+__device__ __forceinline__ void join(const Walk &a, const float *first, uint32_t blocks) {
     const uint32_t id = blockIdx.x / blocks, part = blockIdx.x % blocks;
     const int b = static_cast<int>(id / a.Hkv), kvh = static_cast<int>(id % a.Hkv);
-    const int64_t dd = static_cast<int64_t>(a.d) * a.d, e = (part * 256 + threadIdx.x) * int64_t(4);
+    const int64_t dd = static_cast<int64_t>(a.d) * a.d, e = (part * 64 + threadIdx.x) * int64_t(4);
     if (e >= dd) return;
     const int T = kC * a.run;
     const int r0 = offset_at(a, a.off, b, a.N), r1 = offset_at(a, a.off, b + 1, a.N);
-    const int runs = (max(r1 - r0, 0) + T - 1) / T;
+    const int runs = max((max(r1 - r0, 0) + T - 1) / T, 1);  // a sequence without events has a slot all the same
     const int64_t slot0 = r0 / T + b;
+    float *const states = const_cast<float *>(a.start) + e;
     floatx4 s = {0.f, 0.f, 0.f, 0.f};
     if (first) s = *reinterpret_cast<const floatx4 *>(first + id * dd + e);
-#pragma unroll 4
-    for (int i = 0; i < max(runs, 1); ++i) {
-        const int64_t at = (slot0 + (REV ? runs - 1 - i : i)) * a.Hkv + kvh;
-        floatx4 *p = reinterpret_cast<floatx4 *>(states + at * dd + e);
-        if (i + 1 < runs) {
-            const floatx4 add = *p;
-            const float f = a.fade[at];
-            *p = s;
+    constexpr int AT_ONCE = 16;
+    for (int i0 = 0; i0 < runs; i0 += AT_ONCE) {
+        floatx4 add[AT_ONCE];
+        float f[AT_ONCE];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) s[k] = fmaf(f, s[k], add[k]);
-        } else if (!REV || runs > 0) {
-            *p = s;
+        for (int i = 0; i < AT_ONCE; ++i) {
+            const int64_t at = (slot0 + (REV ? runs - 1 - i0 - i : i0 + i)) * a.Hkv + kvh;
+            if (i0 + i + 1 < runs) add[i] = *reinterpret_cast<const floatx4 *>(states + at * dd), f[i] = a.fade[at];
+        }
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) {
+            const int64_t at = (slot0 + (REV ? runs - 1 - i0 - i : i0 + i)) * a.Hkv + kvh;
+            if (i0 + i < runs) *reinterpret_cast<floatx4 *>(states + at * dd) = s;
+            if (i0 + i + 1 < runs) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) s[k] = fmaf(f[i], s[k], add[i][k]);
+            }
         }
     }
 }
 
-uint32_t grid_of(const Walk &a) { return round_up_xcd(static_cast<uint64_t>(a.slots) * a.Hkv * a.splits); }
+__global__ __launch_bounds__(64) void k_decay_join(const Walk f, const Walk r, const float *first, uint32_t blocks) {
+    if (blockIdx.y == 0) join<false>(f, first, blocks);
+    else join<true>(r, nullptr, blocks);
+}
+
+// The sequences by their chunks, the most first: a counting sort by one workgroup.  (Which of two equal ones comes
+// first is left to chance: nothing but the time goes by it.)
+__global__ __launch_bounds__(1024) void k_decay_order(const Walk a, int32_t *order) {
+    constexpr int CLASSES = 1024;
+    __shared__ int32_t count[CLASSES], wave[16];
+    const int t = threadIdx.x, lane = t & 63, w = static_cast<int>(wave_id());
+    const auto class_of = [&](int b) {
+        const int n = max(offset_at(a, a.off, b + 1, a.N) - offset_at(a, a.off, b, a.N), 0);
+        return CLASSES - 1 - min((n + kC - 1) / kC, CLASSES - 1);
+    };
+    count[t] = 0;
+    __syncthreads();
+    for (int b = t; b < a.B; b += 1024) atomicAdd(&count[class_of(b)], 1);
+    __syncthreads();
+    const int mine = count[t];
+    int upto = mine;
+#pragma unroll
+    for (int i = 1; i < 64; i <<= 1) {
+        const int up = __shfl_up(upto, i);
+        if (lane >= i) upto += up;
+    }
+    if (lane == 63) wave[w] = upto;
+    __syncthreads();
+    for (int v = 0; v < w; ++v) upto += wave[v];
+    count[t] = upto - mine;
+    __syncthreads();
+    for (int b = t; b < a.B; b += 1024) order[atomicAdd(&count[class_of(b)], 1)] = b;
+}
 
 template <int LP>
 int walk_lp(const Walk &a, int up, int grad, hipStream_t stream) {
-    const dim3 grid(grid_of(a)), block(Of<LP>::WAVES * 64);
+    const dim3 grid(workgroups_of(a)), block(Of<LP>::WAVES * 64);
     if (grad == kEach) DLRM_LAUNCH("seq_decay_dq", (k_decay_walk<LP, 3, 3, kEach>), grid, block, 0, stream, a);
     else if (grad == kHead) DLRM_LAUNCH("seq_decay_dq", (k_decay_walk<LP, 3, 3, kHead>), grid, block, 0, stream, a);
     else if (up == 3) DLRM_LAUNCH("seq_decay_walk", (k_decay_walk<LP, 3, 1, kNone>), grid, block, 0, stream, a);
@@ -292,32 +332,30 @@ int walk_lp(const Walk &a, int up, int grad, hipStream_t stream) {
     return launch_status();
 }
 
-template <int LP, bool REV>
-void runs_lp(const Walk &a, int up, float *states, hipStream_t stream) {
-    const dim3 grid(grid_of(a)), block(Of<LP>::WAVES * 64);
-    if (up == 3) DLRM_LAUNCH("seq_decay_runs", (k_decay_runs<LP, REV, 3>), grid, block, 0, stream, a, states);
-    else DLRM_LAUNCH("seq_decay_runs", (k_decay_runs<LP, REV, 2>), grid, block, 0, stream, a, states);
-}
-
-template <bool REV>
-int run_states_of(const Walk &a, int up, const float *first, float *states, hipStream_t stream) {
-    if (a.d <= 32) runs_lp<32, REV>(a, up, states, stream);
-    else if (a.d <= 64) runs_lp<64, REV>(a, up, states, stream);
-    else runs_lp<128, REV>(a, up, states, stream);
-    const uint32_t blocks = (static_cast<uint32_t>(a.d * a.d) / 4 + 255) / 256;
-    const int64_t all = static_cast<int64_t>(a.B) * a.Hkv * blocks;
-    DLRM_LAUNCH("seq_decay_join", (k_decay_join<REV>), dim3(static_cast<uint32_t>(all)), dim3(256), 0, stream, a, first, states, blocks);
-    return launch_status();
+template <int LP>
+void runs_lp(const Walk &f, const Walk *r, int up, hipStream_t stream) {
+    const dim3 grid(workgroups_of(f), r ? 2 : 1), block(Of<LP>::WAVES * 64);
+    if (r && up == 3) DLRM_LAUNCH("seq_decay_runs", (k_decay_runs<LP, 3, true>), grid, block, 0, stream, f, *r);
+    else if (r) DLRM_LAUNCH("seq_decay_runs", (k_decay_runs<LP, 2, true>), grid, block, 0, stream, f, *r);
+    else if (up == 3) DLRM_LAUNCH("seq_decay_runs", (k_decay_runs<LP, 3, false>), grid, block, 0, stream, f, f);
+    else DLRM_LAUNCH("seq_decay_runs", (k_decay_runs<LP, 2, false>), grid, block, 0, stream, f, f);
 }
 
 }  // namespace
 
-int run_states(const Walk &a, const Cut &c, bool reversed, int up, const float *first, float *states, hipStream_t stream) {
-    Walk r = a;
-    r.splits = 1;
-    r.run = c.run, r.slots = static_cast<uint32_t>(c.slots);
-    r.fade = states + c.slots * a.Hkv * a.d * a.d;
-    return reversed ? run_states_of<true>(r, up, first, states, stream) : run_states_of<false>(r, up, first, states, stream);
+int run_states(const Walk &f, const Walk *r, int up, const float *first, hipStream_t stream) {
+    if (f.d <= 32) runs_lp<32>(f, r, up, stream);
+    else if (f.d <= 64) runs_lp<64>(f, r, up, stream);
+    else runs_lp<128>(f, r, up, stream);
+    const uint32_t blocks = (static_cast<uint32_t>(f.d * f.d) / 4 + 63) / 64;
+    DLRM_LAUNCH("seq_decay_join", k_decay_join, dim3(static_cast<uint32_t>(f.B) * f.Hkv * blocks, r ? 2 : 1), dim3(64), 0, stream, f, r ? *r : f,
+                first, blocks);
+    return launch_status();
+}
+
+int order_by_length(const Walk &a, int32_t *order, hipStream_t stream) {
+    DLRM_LAUNCH("seq_decay_order", k_decay_order, dim3(1), dim3(1024), 0, stream, a, order);
+    return launch_status();
 }
 
 int walk(const Walk &a, int up, int grad, hipStream_t stream) {
@@ -334,7 +372,8 @@ extern "C" size_t dlrm_seq_decay_fwd_workspace_size(const dlrm_seq_decay *desc) 
     using namespace dlrm::seq::decay;
     Walk a;
     if (check(desc, true, &a) != DLRM_OK) return 0;
-    return 256 + 4 * static_cast<size_t>(state_floats(a, cut_of(a, desc->max_len)));
+    const Cut c = cut_of(a, desc->max_len);
+    return 256 + states_bytes(a, c) + order_bytes(a, c);
 }
 
 extern "C" int dlrm_seq_decay_fwd(const dlrm_seq_decay *desc, const float *state_in, float *state_out, uint16_t *o, void *workspace,
@@ -347,18 +386,22 @@ extern "C" int dlrm_seq_decay_fwd(const dlrm_seq_decay *desc, const float *state
     if ((a.N > 0 && !o) || !aligned(o, 16) || !aligned(state_in, 16) || !aligned(state_out, 16)) return DLRM_ERR_INVALID_ARG;
     if (a.B == 0) return DLRM_OK;
     const Cut c = cut_of(a, desc->max_len);
-    if (c.run && (!workspace || !aligned(workspace, 256) || workspace_bytes < dlrm_seq_decay_fwd_workspace_size(desc)))
+    if ((c.run || c.order) && (!workspace || !aligned(workspace, 256) || workspace_bytes < dlrm_seq_decay_fwd_workspace_size(desc)))
         return DLRM_ERR_WORKSPACE;
     hipStream_t stream = reinterpret_cast<hipStream_t>(stream_);
     const int up = state_out ? 3 : 2;
     a.run = c.run, a.slots = static_cast<uint32_t>(c.slots);
     a.start = state_in, a.last = state_out, a.out = o;
     if (c.run) {
-        float *states = static_cast<float *>(workspace);
-        rc = run_states(a, c, false, up, state_in, states, stream);
-        if (rc != DLRM_OK) return rc;
-        a.start = states;
+        a.start = static_cast<const float *>(workspace);
+        a.fade = static_cast<float *>(workspace) + c.slots * a.Hkv * a.d * a.d;
+        rc = run_states(a, nullptr, up, state_in, stream);
+    } else if (c.order) {
+        int32_t *order = static_cast<int32_t *>(workspace);
+        rc = order_by_length(a, order, stream);
+        a.order = order;
     }
+    if (rc != DLRM_OK) return rc;
     a.splits = splits_of(a);
     return walk(a, up, kNone, stream);
 }
