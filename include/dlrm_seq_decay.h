@@ -64,7 +64,7 @@ size_t dlrm_seq_decay_fwd_workspace_size(const dlrm_seq_decay *a);
 /*
  * Forward.  o [N][Hq][d] bf16; rows outside every sequence are not written.
  *   state_in   [B][Hkv][d][d] fp32 (key's element, value's element), or NULL: zeros
- *   state_out  the same after each sequence's last event (may be state_in), or NULL: not wanted.
+ *   state_out  the same after each sequence's last event (may be state_in, else apart from it), or NULL: not wanted.
  *              A sequence without events leaves its state as it is.
  *   What an event holds has no effect on the outputs before it, NaN and infinities included; after it,
  *   what they reach is not finite.  o takes the products within 64 events, and the state's with q,

@@ -49,7 +49,9 @@ struct Walk {
     int32_t splits;      // workgroups that share a group's query heads (forward)
     uint32_t slots;      // runs, or sequences
     const int32_t *order;  // [B] the sequences, those of the most chunks first; NULL: as they come
-    const float *start;  // states: of runs [slots][Hkv][d][d], or [B][Hkv][d][d]; NULL: zeros
+    const float *first;  // what sequences begin with, [B][Hkv][d][d], or NULL: zeros
+    float *start;        // the states at the start of the runs after a sequence's first, [slots][Hkv][d][d]
+    bool all_start;      // and of its first: `last` is `first`, which other workgroups may write before one has read it
     float *last;         // [B][Hkv][d][d] or NULL
     float *fade;         // e^(sum of g) of each run, [slots][Hkv]
     uint16_t *out, *out2;
@@ -531,9 +533,9 @@ size_t order_bytes(const Walk &a, const Cut &c);
 // The order of the sequences, into `order`.
 int order_by_length(const Walk &a, int32_t *order, hipStream_t stream);
 
-// The states at the start of every run: of `f` (its y and z) forward, from `first` or zeros, and, unless it is NULL, of
-// `r` reversed, into the states that each has as its start.
-int run_states(const Walk &f, const Walk *r, int up, const float *first, hipStream_t stream);
+// The states at the start of every run after a sequence's first one: of `f` (its y and z) forward and, unless it is NULL,
+// of `r` reversed, into the `start` of each.
+int run_states(const Walk &f, const Walk *r, int up, hipStream_t stream);
 
 // Workgroups that share a group's query heads in the forward walk.
 int splits_of(const Walk &a);

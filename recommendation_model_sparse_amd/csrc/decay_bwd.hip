@@ -65,7 +65,7 @@ __global__ __launch_bounds__(Of<LP>::WAVES * 128, LP == 32 ? 3 : 4) void k_decay
     }
     load(p.c1 - 1, 0);
     typename O::State S;
-    const float *start = a.start ? a.start + (p.slot * static_cast<int64_t>(a.Hkv) + p.kvh) * a.d * a.d : nullptr;
+    const float *start = p.c1 < p.chunks ? a.start + (p.slot * static_cast<int64_t>(a.Hkv) + p.kvh) * a.d * a.d : nullptr;
     if (team) state_load<LP, true>(S, start, a.d, w, lane);
     else state_load<LP, false>(S, start, a.d, w, lane);
     pair_zeros<true>(P, tid - team * TEAM);
@@ -262,7 +262,7 @@ extern "C" int dlrm_seq_decay_bwd(const dlrm_seq_decay *desc, const uint16_t *do
             const int64_t states = c.slots * a.Hkv * a.d * a.d;
             a.start = forward, a.fade = forward + states;
             r.start = reversed, r.fade = reversed + states;
-            rc = run_states(a, &r, up, nullptr, stream);
+            rc = run_states(a, &r, up, stream);
         } else if (c.order) {
             rc = order_by_length(a, order, stream);
             a.order = r.order = order;

@@ -115,7 +115,9 @@ __global__ __launch_bounds__(Of<LP>::WAVES * 64, LP == 128 ? (GRAD ? 2 : 4) : LP
     load(p.c0, 0);
     typename O::State S;
     const int64_t dd = static_cast<int64_t>(a.d) * a.d;
-    state_load<LP, false>(S, a.start ? a.start + ((a.run ? p.slot : p.b) * static_cast<int64_t>(a.Hkv) + p.kvh) * dd : nullptr, a.d, w, lane);
+    const float *start = a.first ? a.first + (static_cast<int64_t>(p.b) * a.Hkv + p.kvh) * dd : nullptr;
+    if (p.c0 > 0 || a.all_start) start = a.start + (p.slot * static_cast<int64_t>(a.Hkv) + p.kvh) * dd;
+    state_load<LP, false>(S, start, a.d, w, lane);
     pair_zeros<false>(P, tid);
     if (clock && p.c0 < p.c1) {
         decays(decs[p.c0 & 1], g, lane, &total);
@@ -241,7 +243,7 @@ __device__ __forceinline__ void run_state(const Walk &a, uint16_t *Ys, uint16_t 
         }
     }
     const int64_t at = p.slot * static_cast<int64_t>(a.Hkv) + p.kvh;
-    state_store<LP>(S, const_cast<float *>(a.start) + at * a.d * a.d, a.d, w, lane);
+    state_store<LP>(S, a.start + at * a.d * a.d, a.d, w, lane);
     if (w == 0 && lane == 0) a.fade[at] = __builtin_amdgcn_exp2f(static_cast<float>(total));
 }
 
@@ -255,42 +257,45 @@ __global__ __launch_bounds__(Of<LP>::WAVES * 64, 4) void k_decay_runs(const Walk
 
 // The states at the runs' starts, in place of what the runs add, four elements a thread; sixteen runs are read at once.
 template <bool REV>
-__device__ __forceinline__ void join(const Walk &a, const float *first, uint32_t blocks) {
+__device__ __forceinline__ void join(const Walk &a, uint32_t blocks) {
     const uint32_t id = blockIdx.x / blocks, part = blockIdx.x % blocks;
     const int b = static_cast<int>(id / a.Hkv), kvh = static_cast<int>(id % a.Hkv);
     const int64_t dd = static_cast<int64_t>(a.d) * a.d, e = (part * 64 + threadIdx.x) * int64_t(4);
-    if (e >= dd) return;
     const int T = kC * a.run;
     const int r0 = offset_at(a, a.off, b, a.N), r1 = offset_at(a, a.off, b + 1, a.N);
-    const int runs = max((max(r1 - r0, 0) + T - 1) / T, 1);  // a sequence without events has a slot all the same
+    const int runs = (max(r1 - r0, 0) + T - 1) / T;
+    if ((runs < 2 && !a.all_start) || e >= dd) return;
     const int64_t slot0 = r0 / T + b;
-    float *const states = const_cast<float *>(a.start) + e;
+    const auto at = [&](int i) { return (slot0 + (REV ? runs - 1 - i : i)) * a.Hkv + kvh; };
+    float *const states = a.start + e;
     floatx4 s = {0.f, 0.f, 0.f, 0.f};
-    if (first) s = *reinterpret_cast<const floatx4 *>(first + id * dd + e);
+    if (!REV && a.first) s = *reinterpret_cast<const floatx4 *>(a.first + id * dd + e);
+    if (runs < 2) {
+        *reinterpret_cast<floatx4 *>(states + (slot0 * a.Hkv + kvh) * dd) = s;
+        return;
+    }
     constexpr int AT_ONCE = 16;
-    for (int i0 = 0; i0 < runs; i0 += AT_ONCE) {
+    for (int i0 = 0; i0 + 1 < runs; i0 += AT_ONCE) {
         floatx4 add[AT_ONCE];
         float f[AT_ONCE];
 #pragma unroll
-        for (int i = 0; i < AT_ONCE; ++i) {
-            const int64_t at = (slot0 + (REV ? runs - 1 - i0 - i : i0 + i)) * a.Hkv + kvh;
-            if (i0 + i + 1 < runs) add[i] = *reinterpret_cast<const floatx4 *>(states + at * dd), f[i] = a.fade[at];
-        }
+        for (int i = 0; i < AT_ONCE; ++i)
+            if (i0 + i + 1 < runs) add[i] = *reinterpret_cast<const floatx4 *>(states + at(i0 + i) * dd), f[i] = a.fade[at(i0 + i)];
+        // (run i's place takes its start, the last one's, which adds nothing that is wanted, too)
 #pragma unroll
         for (int i = 0; i < AT_ONCE; ++i) {
-            const int64_t at = (slot0 + (REV ? runs - 1 - i0 - i : i0 + i)) * a.Hkv + kvh;
-            if (i0 + i < runs) *reinterpret_cast<floatx4 *>(states + at * dd) = s;
-            if (i0 + i + 1 < runs) {
+            if (i0 + i + 1 >= runs) continue;
+            if (i0 + i > 0 || a.all_start) *reinterpret_cast<floatx4 *>(states + at(i0 + i) * dd) = s;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) s[k] = fmaf(f[i], s[k], add[i][k]);
-            }
+            for (int k = 0; k < 4; ++k) s[k] = fmaf(f[i], s[k], add[i][k]);
         }
     }
+    *reinterpret_cast<floatx4 *>(states + at(runs - 1) * dd) = s;
 }
 
-__global__ __launch_bounds__(64) void k_decay_join(const Walk f, const Walk r, const float *first, uint32_t blocks) {
-    if (blockIdx.y == 0) join<false>(f, first, blocks);
-    else join<true>(r, nullptr, blocks);
+__global__ __launch_bounds__(64) void k_decay_join(const Walk f, const Walk r, uint32_t blocks) {
+    if (blockIdx.y == 0) join<false>(f, blocks);
+    else join<true>(r, blocks);
 }
 
 // The sequences by their chunks, the most first: a counting sort by one workgroup.  (Which of two equal ones comes
@@ -343,13 +348,12 @@ void runs_lp(const Walk &f, const Walk *r, int up, hipStream_t stream) {
 
 }  // namespace
 
-int run_states(const Walk &f, const Walk *r, int up, const float *first, hipStream_t stream) {
+int run_states(const Walk &f, const Walk *r, int up, hipStream_t stream) {
     if (f.d <= 32) runs_lp<32>(f, r, up, stream);
     else if (f.d <= 64) runs_lp<64>(f, r, up, stream);
     else runs_lp<128>(f, r, up, stream);
     const uint32_t blocks = (static_cast<uint32_t>(f.d * f.d) / 4 + 63) / 64;
-    DLRM_LAUNCH("seq_decay_join", k_decay_join, dim3(static_cast<uint32_t>(f.B) * f.Hkv * blocks, r ? 2 : 1), dim3(64), 0, stream, f, r ? *r : f,
-                first, blocks);
+    DLRM_LAUNCH("seq_decay_join", k_decay_join, dim3(static_cast<uint32_t>(f.B) * f.Hkv * blocks, r ? 2 : 1), dim3(64), 0, stream, f, r ? *r : f, blocks);
     return launch_status();
 }
 
@@ -391,17 +395,19 @@ extern "C" int dlrm_seq_decay_fwd(const dlrm_seq_decay *desc, const float *state
     hipStream_t stream = reinterpret_cast<hipStream_t>(stream_);
     const int up = state_out ? 3 : 2;
     a.run = c.run, a.slots = static_cast<uint32_t>(c.slots);
-    a.start = state_in, a.last = state_out, a.out = o;
+    a.first = state_in, a.last = state_out, a.out = o;
     if (c.run) {
-        a.start = static_cast<const float *>(workspace);
-        a.fade = static_cast<float *>(workspace) + c.slots * a.Hkv * a.d * a.d;
-        rc = run_states(a, nullptr, up, state_in, stream);
+        a.start = static_cast<float *>(workspace);
+        a.fade = a.start + c.slots * a.Hkv * a.d * a.d;
+        a.all_start = state_in && state_in == state_out;
+        rc = run_states(a, nullptr, up, stream);
     } else if (c.order) {
         int32_t *order = static_cast<int32_t *>(workspace);
         rc = order_by_length(a, order, stream);
         a.order = order;
     }
     if (rc != DLRM_OK) return rc;
-    a.splits = splits_of(a);
+    // in place, one workgroup reads and writes a whole sequence's state
+    a.splits = state_in && state_in == state_out && !c.run ? 1 : splits_of(a);
     return walk(a, up, kNone, stream);
 }

@@ -88,19 +88,24 @@ __device__ __forceinline__ int owner(const int64_t *sums, int64_t k) {
     return lo;
 }
 
-// What the workgroups before this one have of entry `which` of sums, of all workgroups in *all.
-__device__ __forceinline__ int64_t before(const Visit &a, Scan &lds, int which, int64_t *all) {
-    const int blocks = (a.B + kUsers - 1) / kUsers, i = static_cast<int>(threadIdx.x);
-    const int64_t x = i < blocks ? a.sums[2 * i + which] : 0;
-    int64_t mine;
-    scan(lds, i < static_cast<int>(blockIdx.x) ? x : 0, &mine);
-    scan(lds, x, all);
+// What the workgroups before this one have of entry `which` of sums, and all of them in *all; each wavefront by itself.
+__device__ __forceinline__ int64_t before(const Visit &a, int which, int64_t *all) {
+    const int blocks = (a.B + kUsers - 1) / kUsers;
+    int64_t mine = 0, total = 0;
+    for (int i = static_cast<int>(__lane_id()); i < blocks; i += 64) {
+        const int64_t x = a.sums[2 * i + which];
+        total += x;
+        if (i < static_cast<int>(blockIdx.x)) mine += x;
+    }
+#pragma unroll
+    for (int i = 1; i < 64; i <<= 1) mine += __shfl_xor(mine, i), total += __shfl_xor(total, i);
+    *all = total;
     return mine;
 }
 
 struct Lds {
     Scan scan;
-    int64_t sums[kUsers + 1], start[kUsers];
+    int64_t sums[kUsers], start[kUsers];
     int32_t have[kUsers];
 };
 
@@ -121,24 +126,22 @@ __device__ __forceinline__ void give_back(const Visit &a, Lds &lds, const User &
 }
 
 // Pages from the stack's top for those whom it has them for; `first`: wanted in the workgroups before.  Returns
-// how far the stack is taken to, the largest over the threads; *upto: of this user.
-__device__ __forceinline__ bool take(const Visit &a, Lds &lds, const User &u, int64_t top, int64_t first, int64_t *taken) {
+// whether it has them for this thread's user; in all, *taken pages, and users *refused.
+__device__ __forceinline__ bool take(const Visit &a, Lds &lds, const User &u, int64_t top, int64_t first, int64_t *taken, int64_t *refused) {
     const int t = static_cast<int>(threadIdx.x), b0 = static_cast<int>(blockIdx.x) * kUsers;
     int64_t all;
-    const int64_t upto = first + scan(lds.scan, u.want, &all);
-    const bool fits = u.wide && (u.want == 0 || upto <= top);
-    const int got = fits ? u.want : 0;
-    lds.start[t] = upto - u.want, lds.have[t] = u.have;
-    const int64_t mine = scan(lds.scan, got, &all);  // its barriers are behind the reads of lds.sums
-    lds.sums[t] = mine - got;
-    __syncthreads();
-    for (int64_t k = t; k < all; k += kUsers) {
+    const int64_t upto = scan(lds.scan, u.want, &all);  // its barriers are behind the reads of lds.sums
+    const bool fits = u.wide && (u.want == 0 || first + upto <= top);
+    // who is refused wants pages that are not there, or none: those who get some are the first ones who want any
+    lds.sums[t] = upto - u.want, lds.have[t] = fits ? u.have : -1;
+    int64_t both;
+    scan(lds.scan, (fits ? static_cast<int64_t>(u.want) << 20 : 0) + (b0 + t < a.B && !fits ? 1 : 0), &both);
+    *taken = both >> 20, *refused = both & ((1 << 20) - 1);
+    for (int64_t k = t; k < *taken; k += kUsers) {
         const int i = owner(lds.sums, k);
-        const int64_t c = k - lds.sums[i];
-        a.table[(b0 + i) * a.row + lds.have[i] + c] = a.free_list[top - 1 - lds.start[i] - c];
+        a.table[(b0 + i) * a.row + lds.have[i] + (k - lds.sums[i])] = a.free_list[top - 1 - first - k];
     }
     if (b0 + t < a.B && fits && u.n) a.lengths[b0 + t] = static_cast<int32_t>(u.held + u.n);
-    *taken = all;
     return fits;
 }
 
@@ -163,8 +166,7 @@ __global__ __launch_bounds__(kUsers) void k_pages_visit(const Visit a) {
     if (gone) give_back(a, lds, u, top0);
     const int64_t top = min(top0 + gone, a.pages);
     __syncthreads();  // the stack as it is now
-    const bool fits = take(a, lds, u, top, 0, &taken);
-    scan(lds.scan, t < a.B && !fits ? 1 : 0, &refused);
+    const bool fits = take(a, lds, u, top, 0, &taken, &refused);
     if (t == 0) *a.free_count = static_cast<int32_t>(top - taken), *a.refused = static_cast<int32_t>(refused);
     if constexpr (PLACE) {
         // sums over the users' events; their rows begin at the first offset
@@ -199,7 +201,7 @@ __global__ __launch_bounds__(kUsers) void k_pages_give_back(const Visit a) {
     const int b = static_cast<int>(blockIdx.x * kUsers + threadIdx.x);
     const User u = user_of(a, b);
     int64_t all;
-    const int64_t first = before(a, lds.scan, 0, &all);
+    const int64_t first = before(a, 0, &all);
     // `taken` of the next launch needs what each user held: its length is not what it was from here on
     if (b < a.B) a.base[b] = u.held;
     if (all) give_back(a, lds, u, a.tops[0] + first);
@@ -212,11 +214,10 @@ __global__ __launch_bounds__(kUsers) void k_pages_take(const Visit a) {
     now.leave = nullptr;  // they are empty by now
     const User u = user_of(now, b);
     int64_t gone, want, taken, refused;
-    before(a, lds.scan, 0, &gone);
-    const int64_t first = before(a, lds.scan, 1, &want);
-    const bool fits = take(a, lds, u, min(a.tops[0] + gone, a.pages), first, &taken);
+    before(a, 0, &gone);
+    const int64_t first = before(a, 1, &want);
+    const bool fits = take(a, lds, u, min(a.tops[0] + gone, a.pages), first, &taken, &refused);
     if (b < a.B && !fits) a.base[b] = -1;
-    scan(lds.scan, b < a.B && !fits ? 1 : 0, &refused);
     if (threadIdx.x != 0) return;
     if (refused) atomicAdd(a.refused, static_cast<int32_t>(refused));
     if (taken) atomicAdd(reinterpret_cast<unsigned long long *>(a.tops + 1), static_cast<unsigned long long>(taken));
