@@ -36,7 +36,8 @@ extern "C" {
  *              outside are brought inside: no foreign memory is read.  Not read by the step.
  *   max_len    an upper bound of the sequences' lengths, by which a call chooses whether to cut
  *              sequences into runs that are worked on side by side; N where it is not known.
- *              Longer sequences give results as exact, slower.  (The bits may differ with it.)
+ *              Longer sequences give results as exact, slower.  (The bits may differ with it, and with
+              the number of sequences and rows.)
  *   q, k, v    bf16; element e of head h of row r at r * row_stride + h * head_stride + e, strides
  *              in elements, multiples of 8, >= d; 16-byte aligned
  *   g          fp32 logarithms of the decays, <= 0: that of row r and head c at r * g_row + c; g_row >= Hkv,
@@ -88,7 +89,7 @@ size_t dlrm_seq_decay_bwd_workspace_size(const dlrm_seq_decay *a);
  *   dg   [N][Hkv] fp32 (rows outside every sequence are not written), [Hkv] where g_row == 0, or NULL:
  *        not wanted
  *   Infinities and NaN in k and v have no effect on dq before them; those of q and dout reach dk and
- *   dv of the events near by, and any reaches dg of its sequence.
+ *   dv of the events near by; dg of a sequence that holds any means nothing (nor does that of a head).
  */
 int dlrm_seq_decay_bwd(const dlrm_seq_decay *a, const uint16_t *dout, uint16_t *dq, uint16_t *dk,
                        uint16_t *dv, float *dg, void *workspace, size_t workspace_bytes,

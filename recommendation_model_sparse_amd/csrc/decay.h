@@ -206,6 +206,27 @@ struct Loader {
 #pragma unroll
         for (int i = 0; i < N; ++i) r[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(desc, at + i * step, 0, 0));
     }
+    // Infinities and NaN become zeros, as 0 times them would reach rows that do not see them: `first` takes the first row of
+    // each column that holds one, *any whether there is one.
+    __device__ __forceinline__ void tame(int *first, int *any) {
+        bool wild = false;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) wild |= (r[i][e] & 0x7f80u) == 0x7f80u || (r[i][e] & 0x7f800000u) == 0x7f800000u;
+        if (!wild) return;
+        *any = 1;
+        const int thread = fresh(threadIdx.x), col = 8 * (thread % CH);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int row = thread / CH + i * R;
+                if ((r[i][e] & 0x7f80u) == 0x7f80u) atomicMin(first + col + 2 * e, row);
+                if ((r[i][e] & 0x7f800000u) == 0x7f800000u) atomicMin(first + col + 2 * e + 1, row);
+                r[i][e] = only_finite(r[i][e]);
+            }
+    }
     __device__ __forceinline__ void store(uint16_t *tile) const {
         const int thread = fresh(threadIdx.x);
         uint16_t *const to = tile + thread / CH * kPitch<LP> + place_of(8 * (thread % CH));
@@ -435,35 +456,19 @@ __device__ __forceinline__ void through_pairs(typename Of<LP>::Out &o, const uin
     }
 }
 
-// The same one row of z at a time, added where it is seen: what a row after it holds does not reach an output,
-// though 0 * infinity is NaN.
-template <int LP>
-__device__ __forceinline__ void through_pairs_apart(typename Of<LP>::Out &o, const uint16_t *P, const uint16_t *zs, int w, int lane) {
-    lane = fresh(lane);
-    const uint16_t *const zcol = zs + columns_base<LP>(lane);
-    const uint16_t *const row = P + (lane & 15) * kPP + 8 * (lane >> 4);
-#pragma unroll 1
-    for (int j = 0; j < kC; ++j) {
-        const int m = (lane >> 4) == (j & 12) / 4 ? j & 19 : -1;  // which of a lane's rows 0..3 and 16..19
-        Frag z;
-        columns<LP>(z, zcol, j & 32, w);
+// NaN for what z held infinities or NaN for (Loader::tame): the rows from the first such one on, and the state.
+__device__ __forceinline__ void out_wild(floatx4 (&o)[4], const int *first, int w, int lane) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int first = 16 * (e / 2) + 2 * (e % 2);
-            z.w[e] = m == first ? z.w[e] & 0xffffu : m == first + 1 ? z.w[e] & 0xffff0000u : 0u;
-        }
+    for (int r = 0; r < 4; ++r) {
+        const int from = first[16 * w + 4 * (lane >> 4) + r];
 #pragma unroll
-        for (int ib = 0; ib < 4; ++ib) {
-            const bool sees = j <= 16 * ib + (lane & 15);
-            Frag p;
-            p.q = *reinterpret_cast<const u32x4 *>(row + 16 * ib * kPP + (j & 32));
-            if (!sees) p.q = u32x4{0, 0, 0, 0};  // a tile that nobody sees is not written
-            const floatx4 add = __builtin_amdgcn_mfma_f32_16x16x32_bf16(z.b, p.b, floatx4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                if (sees) o[ib][r] += add[r];
-        }
+        for (int ib = 0; ib < 4; ++ib)
+            if (16 * ib + (lane & 15) >= from) o[ib][r] = __builtin_nanf("");
     }
+}
+template <int LP>
+__device__ __forceinline__ void state_wild(typename Of<LP>::State &S, const int *first, int w, int lane) {
+    if (first[16 * w + (lane & 15)] < kC) state_fade<LP>(S, __builtin_nanf(""));
 }
 
 // o times f of each row; MORE: *sums of o's columns times those of the row of t, for rows 16 ib + ln.

@@ -86,6 +86,7 @@ __global__ __launch_bounds__(Of<LP>::WAVES * 64, LP == 128 ? (GRAD ? 2 : 4) : LP
     __shared__ __attribute__((aligned(16))) Decays decs[2];
     __shared__ __attribute__((aligned(16))) uint16_t Ts[MORE ? O::TILE : 8];
     __shared__ float by_wave[MORE ? O::WAVES : 1][kC], by_tile[GRAD == kEach ? kTiles : 1][16];
+    __shared__ int wild[2], first_wild[2][LP];  // infinities and NaN in z (Loader::tame), in even and odd chunks
 
     const Part p = part_of(a);
     if (!p.any) return;
@@ -119,6 +120,8 @@ __global__ __launch_bounds__(Of<LP>::WAVES * 64, LP == 128 ? (GRAD ? 2 : 4) : LP
     if (p.c0 > 0 || a.all_start) start = a.start + (p.slot * static_cast<int64_t>(a.Hkv) + p.kvh) * dd;
     state_load<LP, false>(S, start, a.d, w, lane);
     pair_zeros<false>(P, tid);
+    if (tid < 2) wild[tid] = 0;
+    if (tid < LP) first_wild[0][tid] = first_wild[1][tid] = kC;
     if (clock && p.c0 < p.c1) {
         decays(decs[p.c0 & 1], g, lane, &total);
         if (p.c0 + 1 < p.c1) g = decay_load(a, p, p.c0 + 1, lane);
@@ -137,12 +140,17 @@ __global__ __launch_bounds__(Of<LP>::WAVES * 64, LP == 128 ? (GRAD ? 2 : 4) : LP
         }
         for (int h = 0; h < heads; ++h) {
             lds_barrier();  // the tiles before have been read
-            if (h == 0) ys.store(Ys), zs.store(Zs);
+            if (h == 0) {
+                zs.tame(first_wild[c & 1], &wild[c & 1]);
+                ys.store(Ys), zs.store(Zs);
+            }
             xs.store(Xs);
             if constexpr (MORE) ts.store(Ts);
             lds_barrier();
             load(h + 1 < heads ? c : c + 1, h + 1 < heads ? h + 1 : 0);
             if (clock && h == 0 && c + 1 < p.c1) {
+                if (lane == 0) wild[~c & 1] = 0;
+                for (int i = lane; i < LP; i += 64) first_wild[~c & 1][i] = kC;
                 decays(decs[~c & 1], g, lane, &total);
                 if (c + 2 < p.c1) g = decay_load(a, p, c + 2, lane);
             }
@@ -159,17 +167,8 @@ __global__ __launch_bounds__(Of<LP>::WAVES * 64, LP == 128 ? (GRAD ? 2 : 4) : LP
             through_state<LP, PR>(o, S, Xs, lane);
             weigh<LP, MORE>(o, dec.from, Ts, by_wave[MORE ? w : 0], w, lane);
             lds_barrier();
-            const floatx4 before[4] = {o[0], o[1], o[2], o[3]};
             through_pairs<LP, false>(o, P, Zs, w, lane);
-            float any = 0.f;
-#pragma unroll
-            for (int ib = 0; ib < 4; ++ib) any += (o[ib][0] + o[ib][1]) + (o[ib][2] + o[ib][3]);
-            if (__any(!(fabsf(any) < kInf))) {
-                // an infinity or NaN in z reaches the rows before it (0 * NaN in a product): once more, with its rows apart
-#pragma unroll
-                for (int ib = 0; ib < 4; ++ib) o[ib] = before[ib];
-                through_pairs_apart<LP>(o, P, Zs, w, lane);
-            }
+            if (__builtin_amdgcn_readfirstlane(wild[c & 1])) out_wild(o, first_wild[c & 1], w, lane);
             out_rows<LP>(o, Xs, a.out + ((p.row0 + c * kC) * a.Hq + h0 + h) * a.d, static_cast<int64_t>(a.Hq) * a.d, rows, a.d, a.scale, w,
                          lane);
             if (MORE && w == 0) {
@@ -189,6 +188,7 @@ __global__ __launch_bounds__(Of<LP>::WAVES * 64, LP == 128 ? (GRAD ? 2 : 4) : LP
         if (c + 1 == p.c1 && !a.last) break;  // nobody reads the state any more
         state_fade<LP>(S, dec.fade);
         state_grow<LP, UP>(S, Ys, Zs, dec.to, w, lane);
+        if (__builtin_amdgcn_readfirstlane(wild[c & 1])) state_wild<LP>(S, first_wild[c & 1], w, lane);
     }
     if (a.last && p.c1 == p.chunks && p.split == 0)
         state_store<LP>(S, a.last + (static_cast<int64_t>(p.b) * a.Hkv + p.kvh) * dd, a.d, w, lane);
