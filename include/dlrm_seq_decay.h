@@ -37,7 +37,7 @@ extern "C" {
  *   max_len    an upper bound of the sequences' lengths, by which a call chooses whether to cut
  *              sequences into runs that are worked on side by side; N where it is not known.
  *              Longer sequences give results as exact, slower.  (The bits may differ with it, and with
-              the number of sequences and rows.)
+ *              the number of sequences and rows.)
  *   q, k, v    bf16; element e of head h of row r at r * row_stride + h * head_stride + e, strides
  *              in elements, multiples of 8, >= d; 16-byte aligned
  *   g          fp32 logarithms of the decays, <= 0: that of row r and head c at r * g_row + c; g_row >= Hkv,

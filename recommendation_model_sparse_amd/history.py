@@ -115,8 +115,11 @@ class HistoryEncoder:
         return dict(window=self.c.window, sinks=self.c.sinks, bias=layer["bias"], bounds=self.bounds)
 
     def _heads_norm(self, o, layer):
-        """The norm of a linear layer's heads, and what its backward wants."""
-        s, y, rstd, _ = L.dlrm_add_rmsnorm_fwd(o.view(-1, self.d), None, layer["wo"], res_dtype=torch.bfloat16)
+        """The norm of a linear layer's heads, and what its backward wants.  eps: a head's output is as small as q . k
+        of a first event may be, and the norm passes an error on enlarged up to 1 / sqrt(eps) times.  q . k / sqrt(d)
+        of bf16 values of about 0.6 is off by 1e-3: times v and 1 / sqrt(1e-3) 2 % of a normed head at most, where
+        1e-6 would leave a gradient of any size."""
+        s, y, rstd, _ = L.dlrm_add_rmsnorm_fwd(o.view(-1, self.d), None, layer["wo"], eps=1e-3, res_dtype=torch.bfloat16)
         return y, (s, rstd)
 
     def _split(self, qkv):
@@ -343,8 +346,10 @@ class PagedHistoryCache(_States):
 
     def release(self, users) -> None:
         """Users (their numbers) leave: their pages go back, and they are without a history."""
-        leave = np.zeros(self.users, bool)
-        leave[np.asarray(users, np.int64)] = True
+        leave, users = np.zeros(self.users, bool), np.asarray(users, np.int64)
+        if ((users < 0) | (users >= self.users)).any():
+            raise ValueError(f"users must be 0 to {self.users - 1}, got {users}")
+        leave[users] = True
         none = torch.zeros(self.users + 1, dtype=torch.int64, device=self.enc.dev)
         self._update(np.zeros(self.users, np.int64), none, 0, leave)
         for state in self.state:
