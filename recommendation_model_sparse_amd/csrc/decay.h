@@ -421,14 +421,20 @@ __device__ __forceinline__ float pair_tile(uint16_t *P, uint16_t *P2, const Deca
     const float hi = dec.hi[i], lo = dec.lo[i];
     const floatx4 hj = *reinterpret_cast<const floatx4 *>(dec.hi + j0), lj = *reinterpret_cast<const floatx4 *>(dec.lo + j0);
     float p[4], p2[4], sum = 0.f;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
+    const auto pair = [&](int r, bool sees) {
         const float diff = REV ? (hj[r] - hi) + (lj[r] - lo) : (hi - hj[r]) + (lo - lj[r]);
-        const bool sees = REV ? j0 + r >= i : j0 + r <= i;
-        const float e = __builtin_amdgcn_exp2f(diff), x = s[r] * e;
-        p[r] = sees ? x : 0.f;
+        const float e = __builtin_amdgcn_exp2f(diff);
+        p[r] = sees ? s[r] * e : 0.f;
         if constexpr (BOTH) p2[r] = sees ? m[r] * e : 0.f;
-        if constexpr (GRAD != kNone) sum += sees ? x * m[r] * (GRAD == kHead ? static_cast<float>(REV ? j0 + r - i : i - j0 - r) : 1.f) : 0.f;
+        if constexpr (GRAD == kEach) sum = fmaf(p[r], m[r], sum);
+        if constexpr (GRAD == kHead) sum = fmaf(p[r] * static_cast<float>(REV ? j0 + r - i : i - j0 - r), m[r], sum);
+    };
+    if (ib == jb) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) pair(r, REV ? j0 + r >= i : j0 + r <= i);
+    } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) pair(r, true);
     }
     const int at = pair_at(i, j0);
     *reinterpret_cast<u32x2 *>(P + at) = u32x2{pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3])};

@@ -122,7 +122,8 @@ __global__ __launch_bounds__(Of<LP>::WAVES * 128, LP == 32 ? 3 : 4) void k_decay
             // both teams' pairs, tile by tile: they have their decays in common, and dg takes the product of both
 #pragma unroll
             for (int n = 0; n < (kTiles + 2 * O::WAVES - 1) / (2 * O::WAVES); ++n) {
-                const int t = min(static_cast<int>(wave_id()) + n * 2 * O::WAVES, kTiles - 1);
+                const int t = static_cast<int>(wave_id()) + n * 2 * O::WAVES;
+                if (t >= kTiles) break;
                 const float sum = pair_tile<LP, true, true, GRAD>(Ps[0], Ps[1], dec, Ks, Qs, Vs, Ds, t, lane);
                 if constexpr (MORE) {
                     if (quad == 0) by_tile[t][ln] = sum;

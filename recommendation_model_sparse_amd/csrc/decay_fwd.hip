@@ -154,10 +154,10 @@ __global__ __launch_bounds__(Of<LP>::WAVES * 64, LP == 128 ? (GRAD ? 2 : 4) : LP
                 decays(decs[~c & 1], g, lane, &total);
                 if (c + 2 < p.c1) g = decay_load(a, p, c + 2, lane);
             }
-            // (a wavefront without a last tile makes one that another makes too)
 #pragma unroll
             for (int n = 0; n < (kTiles + O::WAVES - 1) / O::WAVES; ++n) {
-                const int t = min(w + n * O::WAVES, kTiles - 1);
+                const int t = w + n * O::WAVES;
+                if (t >= kTiles) break;
                 const float sum = pair_tile<LP, false, false, GRAD == kEach ? kEach : kNone>(P, nullptr, dec, Xs, Ys, Ts, Zs, t, lane);
                 if constexpr (GRAD == kEach) {
                     if (quad == 0) by_tile[t][ln] = sum;
