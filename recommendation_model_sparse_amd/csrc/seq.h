@@ -210,22 +210,24 @@ struct Stage {
             if (col && x < end && (x >= first || x < sinks)) r[i] = *(const DLRM_GLOBAL u32x4 *)(p + at);
         }
     }
-    // The rows of a thread's pieces in a pool of pages, and the pieces from there.
-    __device__ __forceinline__ void paged_rows(int (&at)[N], const Pages &pg, const int32_t *table, int row0, int first, int end,
-                                               int sinks) const {
+    // The rows of a thread's pieces in a pool of pages, and the pieces from there.  Nothing branches, as each branch
+    // waits: a row past the end reads the last one, and what is not wanted is left out on its way to the tile.
+    __device__ __forceinline__ void paged_rows(int (&at)[N], const Pages &pg, const int32_t *table, int row0, int end) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) at[i] = paged_row(pg, table, min(row0 + i * R + row, end - 1));
+    }
+    __device__ __forceinline__ void load_rows(const uint16_t *base, int64_t stride, const int (&at)[N]) {
+        const int c = col ? 8 * (threadIdx.x % CH) : 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) r[i] = *(const DLRM_GLOBAL u32x4 *)(base + at[i] * stride + c);
+    }
+    __device__ __forceinline__ void store_rows(uint16_t *tile, int row0, int first, int end, int sinks) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int x = row0 + i * R + row;
-            at[i] = x < end && (x >= first || x < sinks) ? paged_row(pg, table, x) : -1;
+            if (!(col && x < end && (x >= first || x < sinks))) r[i] = u32x4{0, 0, 0, 0};
         }
-    }
-    __device__ __forceinline__ void load_rows(const uint16_t *base, int64_t stride, const int (&at)[N]) {
-        const int c = threadIdx.x % CH;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            r[i] = u32x4{0, 0, 0, 0};
-            if (col && at[i] >= 0) r[i] = *(const DLRM_GLOBAL u32x4 *)(base + at[i] * stride + 8 * c);
-        }
+        store(tile);
     }
     __device__ __forceinline__ void store(uint16_t *tile) const {
 #pragma unroll

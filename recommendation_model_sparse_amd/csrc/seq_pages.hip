@@ -4,7 +4,7 @@
 // workgroup, one a thread: how many pages each gives back and wants, and the sums before it; then all pages of
 // the 1024, and all new events, are spread over the threads, each of which finds its user in the sums.  Up to 1024
 // users and 16384 events are one launch of one workgroup, which is bound by its chain of reads (a launch
-// and five of them); more take four launches, as pages that are taken may have come back in another workgroup.
+// and five of them); more take four launches, as pages that are taken may have come back in another workgroup, or three if nobody leaves.
 #include "seq.h"
 
 namespace dlrm {
@@ -198,12 +198,9 @@ __global__ __launch_bounds__(kUsers) void k_pages_count(const Visit a) {
 
 __global__ __launch_bounds__(kUsers) void k_pages_give_back(const Visit a) {
     __shared__ Lds lds;
-    const int b = static_cast<int>(blockIdx.x * kUsers + threadIdx.x);
-    const User u = user_of(a, b);
+    const User u = user_of(a, static_cast<int>(blockIdx.x * kUsers + threadIdx.x));
     int64_t all;
     const int64_t first = before(a, 0, &all);
-    // `taken` of the next launch needs what each user held: its length is not what it was from here on
-    if (b < a.B) a.base[b] = u.held;
     if (all) give_back(a, lds, u, a.tops[0] + first);
 }
 
@@ -217,7 +214,7 @@ __global__ __launch_bounds__(kUsers) void k_pages_take(const Visit a) {
     before(a, 0, &gone);
     const int64_t first = before(a, 1, &want);
     const bool fits = take(a, lds, u, min(a.tops[0] + gone, a.pages), first, &taken, &refused);
-    if (b < a.B && !fits) a.base[b] = -1;
+    if (b < a.B) a.base[b] = fits ? u.held : -1;
     if (threadIdx.x != 0) return;
     if (refused) atomicAdd(a.refused, static_cast<int32_t>(refused));
     if (taken) atomicAdd(reinterpret_cast<unsigned long long *>(a.tops + 1), static_cast<unsigned long long>(taken));
@@ -312,7 +309,7 @@ extern "C" int dlrm_seq_pages_update(const dlrm_seq_pages *p, const void *offset
     } else {
         const dim3 blocks(static_cast<uint32_t>((p->B + kUsers - 1) / kUsers));
         DLRM_LAUNCH("seq_pages_count", k_pages_count, blocks, dim3(kUsers), 0, stream, a);
-        DLRM_LAUNCH("seq_pages_give_back", k_pages_give_back, blocks, dim3(kUsers), 0, stream, a);
+        if (leave) DLRM_LAUNCH("seq_pages_give_back", k_pages_give_back, blocks, dim3(kUsers), 0, stream, a);
         DLRM_LAUNCH("seq_pages_take", k_pages_take, blocks, dim3(kUsers), 0, stream, a);
     }
     if (place && p->B > 0) {
