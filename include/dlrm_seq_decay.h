@@ -44,7 +44,7 @@ extern "C" {
  *              or 0: one decay for a head, [Hkv].  What is above 0 counts as 0 (with a gradient of 0),
  *              what is below -104, -infinity too, as -104, where e^g is 0 in fp32.
  *   Limits: d % 8 == 0, 8 <= d <= 128; Hq <= 4096; B < 2^24; N < 2^31; row strides < 2^24 elements; a
- *   sequence < 2^30 rows; (N / 64 + B) * Hkv <= 2^23.
+ *   sequence < 2^30 rows; (N / 64 + B + 8) * Hkv < 2^23, for d > 64 < 2^22.
  */
 typedef struct {
     int64_t B, N;

@@ -526,13 +526,13 @@ int check(const dlrm_seq_decay *a, bool offsets, Walk *out);
 
 inline uint32_t workgroups_of(const Walk &a) { return (a.slots + kNumXcd - 1) / kNumXcd * kNumXcd * a.Hkv * a.splits; }
 
-// How sequences are cut: chunks of a run (0: not), and the workgroups' places.
+// How sequences are cut: chunks of a run (0: not), and slots; `back`: for the backward.
 struct Cut {
     int32_t run;
     int64_t slots;
     bool order;  // sequences go by their length
 };
-Cut cut_of(const Walk &a, int64_t max_len);
+Cut cut_of(const Walk &a, int64_t max_len, bool back);
 
 constexpr int padded(int d) { return d <= 32 ? 32 : d <= 64 ? 64 : 128; }
 constexpr size_t whole(size_t bytes) { return (bytes + 255) / 256 * 256; }
@@ -549,7 +549,7 @@ int order_by_length(const Walk &a, int32_t *order, hipStream_t stream);
 int run_states(const Walk &f, const Walk *r, int up, hipStream_t stream);
 
 // Workgroups that share a group's query heads in the forward walk.
-int splits_of(const Walk &a);
+int splits_of(const Walk &a, bool back);
 
 // The forward walk; `up`, `grad`: the kernel's.
 int walk(const Walk &a, int up, int grad, hipStream_t stream);

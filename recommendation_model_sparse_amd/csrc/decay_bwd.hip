@@ -195,9 +195,9 @@ int back(const Walk &a, int grad, hipStream_t stream) {
 }
 
 // Marks are eight chunks apart, or two where dg is summed over the events, which leaves an error of Z in every event of
-// a chunk; or a run's length: at every run's start there is one.  (Two decays over 29000 events: an error of 7e-5 of the sum
+// a chunk; or a run's length, or one: at every run's start there is one.  (Two decays over 29000 events: an error of 7e-5 of the sum
 // without the marks between, as the events' own errors are 6e-7.)
-int mark_of(const Cut &c, bool by_head) { return by_head ? 2 : c.run && c.run < 8 ? c.run : 8; }
+int mark_of(const Cut &c, bool by_head) { return by_head ? 2 - c.run % 2 : c.run && c.run < 8 ? c.run : 8; }
 
 // Bytes: the runs' states, forward and reversed, or the order; for dg, the terms from dq, the states at the marks, the
 // slots' sums.
@@ -207,7 +207,7 @@ struct Room {
 Room room_of(Walk a, const Cut &c) {
     a.slots = static_cast<uint32_t>(c.slots);
     const size_t lp = padded(a.d);
-    return Room{states_bytes(a, c), order_bytes(a, c), whole(8 * static_cast<size_t>(a.N) * a.Hkv * splits_of(a)),
+    return Room{states_bytes(a, c), order_bytes(a, c), whole(8 * static_cast<size_t>(a.N) * a.Hkv * splits_of(a, true)),
                 4 * lp * lp * a.Hkv * static_cast<size_t>(slot_count(a.N, a.B, kC * mark_of(c, a.g_row == 0))),
                 whole(8 * static_cast<size_t>(c.slots) * a.Hkv)};
 }
@@ -221,7 +221,7 @@ extern "C" size_t dlrm_seq_decay_bwd_workspace_size(const dlrm_seq_decay *desc) 
     using namespace dlrm::seq::decay;
     Walk a;
     if (check(desc, true, &a) != DLRM_OK) return 0;
-    const Room r = room_of(a, cut_of(a, desc->max_len));
+    const Room r = room_of(a, cut_of(a, desc->max_len, true));
     return 256 + 2 * r.states + r.order + r.terms + r.marks + r.sums;
 }
 
@@ -238,7 +238,7 @@ extern "C" int dlrm_seq_decay_bwd(const dlrm_seq_decay *desc, const uint16_t *do
     hipStream_t stream = reinterpret_cast<hipStream_t>(stream_);
     const bool by_head = dg && a.g_row == 0, any = a.N > 0 && a.B > 0;
     const int grad = !dg ? kNone : by_head ? kHead : kEach, up = dg ? 3 : 2;
-    const Cut c = cut_of(a, desc->max_len);
+    const Cut c = cut_of(a, desc->max_len, true);
     const Room room = room_of(a, c);
     char *ws = static_cast<char *>(workspace);
     const auto take = [&](size_t bytes) {
@@ -251,7 +251,7 @@ extern "C" int dlrm_seq_decay_bwd(const dlrm_seq_decay *desc, const uint16_t *do
     a.terms = reinterpret_cast<float *>(take(room.terms)), a.marks = reinterpret_cast<float *>(take(room.marks));
     double *sums = reinterpret_cast<double *>(take(room.sums));
     a.run = c.run, a.slots = static_cast<uint32_t>(c.slots), a.mark = mark_of(c, by_head);
-    const int splits = splits_of(a);
+    const int splits = splits_of(a, true);
     a.pairs = a.terms + a.N * a.Hkv * splits;
     if (any) {
         const Heads q = a.x, k = a.y, v = a.z, d = {dout, static_cast<int64_t>(a.Hq) * a.d, a.d};

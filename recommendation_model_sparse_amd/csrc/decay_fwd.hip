@@ -18,7 +18,7 @@ int check(const dlrm_seq_decay *a, bool offsets, Walk *out) {
         const uintptr_t ib = a->index_type == DLRM_INDEX_I32 ? 4 : 8;
         if (a->B > 0 && (!a->offsets || !aligned(a->offsets, ib))) return DLRM_ERR_INVALID_ARG;
         // a launch holds fewer than 2^32 work-items
-        if (slot_count(a->N, a->B, kC) * a->Hkv > (int64_t(1) << 23)) return DLRM_ERR_UNSUPPORTED;
+        if ((slot_count(a->N, a->B, kC) + kNumXcd) * a->Hkv >= (int64_t(1) << (a->d <= 64 ? 23 : 22))) return DLRM_ERR_UNSUPPORTED;
     }
     if (a->N > 0 && (!a->q || !a->k || !a->v || !a->g)) return DLRM_ERR_INVALID_ARG;
     if (!aligned(a->q, 16) || !aligned(a->k, 16) || !aligned(a->v, 16) || !aligned(a->g, 4)) return DLRM_ERR_INVALID_ARG;
@@ -40,24 +40,58 @@ int check(const dlrm_seq_decay *a, bool offsets, Walk *out) {
     return DLRM_OK;
 }
 
-// Most sequences that one workgroup puts in order.
-constexpr int kOrdered = 16384;
+// Most sequences that one workgroup puts in order; chunks of the longest run, whose rows are an int's.
+constexpr int kOrdered = 16384, kMostChunks = 1 << 20;
+constexpr int kCUs = 256;
 
-// Workgroups that fill the GPU.
-static int64_t places_of(int32_t d) { return d <= 32 ? 1536 : d <= 64 ? 1024 : 512; }
+// Workgroups that are resident at once, as their LDS leaves room for them: of the forward walk, of k_decay_back.
+static int places_of(int32_t d, bool back) {
+    const int lp = padded(d);
+    return kCUs * (back ? (lp == 32 ? 3 : lp == 64 ? 2 : 1) : (lp == 32 ? 5 : lp == 64 ? 4 : 2));
+}
+
+// Heads of a group are split where there are so few workgroups that two times as many would still have places (4 long
+// histories, 8 heads of 128 over 2: without 47 us, split until all places are taken 50, like this 43; one of 400, 16 heads over
+// 2: 51, 21, 21).
+static int splits_for(int64_t workgroups, int group, int places) {
+    int n = 1;
+    while (n < group && workgroups * n < places / 2) {
+        do ++n;
+        while (group % n != 0);
+    }
+    return n;
+}
 
 // A sequence and key head a workgroup is enough where there are many; where few are long, they are cut into
-// runs, whose states at the start are made first from k and v alone.
-Cut cut_of(const Walk &a, int64_t max_len) {
-    const int64_t longest = std::min(max_len, a.N), chunks = (longest + kC - 1) / kC;
-    const int64_t all = slot_count(a.N, a.B, kC) * a.Hkv, places = places_of(a.d);
-    int64_t share = std::max<int64_t>(2, (all + places - 1) / places);  // chunks for each place
-    if (share > 8) share = (share + 7) / 8 * 8;
+// runs, whose states at the start are made first from y and z alone.  What takes least is worked out, in chunks of one head:
+// a workgroup begins in the time of 2 and takes its heads' chunks and, cut, one more for the states; workgroups past
+// the places wait for others, and the last of them ends three quarters of its own time after the mean; joining the states
+// takes 1 for each 16 runs of the longest sequence, and the two launches 2.  Of the runs of 1 to 8 and 16 chunks and none, on
+// 17 shapes forward and backward (1 to 1024 sequences of 1 to 8192, heads of 32, 64, 128, groups of 1 to 16), this choice
+// was 0.5 % slower than the best in the mean, 9 % at worst.
+Cut cut_of(const Walk &a, int64_t max_len, bool back) {
+    const int64_t longest = (std::min(max_len, a.N) + kC - 1) / kC;
+    const int places = places_of(a.d, back);
+    const double total = static_cast<double>(slot_count(a.N, a.B, kC) * a.Hkv);
+    const auto time_of = [&](int64_t run) {
+        const int64_t groups = (run ? slot_count(a.N, a.B, kC * static_cast<int>(run)) : a.B) * a.Hkv;
+        const double heads = back ? a.group : a.group / splits_for(groups, a.group, places), each = heads + (run ? 1 : 0);
+        const double own = (run ? run : longest) * each;
+        const double shared = (total * each + 2.0 * groups) / places;
+        if (!run) return std::max(own + 2, shared);
+        return (groups <= places ? own + 2 : shared + 0.75 * own) + 2 + (longest / run + 15) / 16;
+    };
+    Cut c = {};
+    double least = time_of(0);
     const bool many = a.B * static_cast<int64_t>(a.Hkv) * 64 >= (int64_t(1) << 24);  // more than a launch of k_decay_join holds
-    Cut c;
-    c.run = chunks > 2 * share && !many ? static_cast<int32_t>(share) : 0;
+    // (from 8 on, multiples of 8: the marks are that far apart)
+    for (int64_t run = 1; run < longest && run <= kMostChunks && !many; run += run < 8 ? 1 : run) {
+        const double t = time_of(run);
+        if (t < least) least = t, c.run = static_cast<int32_t>(run);
+    }
     c.slots = c.run ? slot_count(a.N, a.B, kC * c.run) : a.B;
-    c.order = !c.run && chunks > 1 && a.B <= kOrdered && static_cast<int64_t>(a.B) * a.Hkv > places / 2;
+    // the longest first: with 1024 sequences of 16 to 512, 2 heads of 64, 42 us instead of 56, the backward 143 instead of 202
+    c.order = !c.run && longest > 1 && a.B <= kOrdered && static_cast<int64_t>(a.B) * a.Hkv > places / 2;
     return c;
 }
 
@@ -66,13 +100,8 @@ size_t states_bytes(const Walk &a, const Cut &c) {
 }
 size_t order_bytes(const Walk &a, const Cut &c) { return c.order ? whole(4 * static_cast<size_t>(a.B)) : 0; }
 
-int splits_of(const Walk &a) {
-    int n = 1;
-    while (n < a.group && static_cast<int64_t>(a.slots) * a.Hkv * n < places_of(a.d)) {
-        do ++n;
-        while (a.group % n != 0);
-    }
-    return n;
+int splits_of(const Walk &a, bool back) {
+    return splits_for(static_cast<int64_t>(a.slots) * a.Hkv, a.group, places_of(a.d, back));
 }
 
 namespace {
@@ -376,7 +405,7 @@ extern "C" size_t dlrm_seq_decay_fwd_workspace_size(const dlrm_seq_decay *desc) 
     using namespace dlrm::seq::decay;
     Walk a;
     if (check(desc, true, &a) != DLRM_OK) return 0;
-    const Cut c = cut_of(a, desc->max_len);
+    const Cut c = cut_of(a, desc->max_len, false);
     return 256 + states_bytes(a, c) + order_bytes(a, c);
 }
 
@@ -389,7 +418,7 @@ extern "C" int dlrm_seq_decay_fwd(const dlrm_seq_decay *desc, const float *state
     if (rc != DLRM_OK) return rc;
     if ((a.N > 0 && !o) || !aligned(o, 16) || !aligned(state_in, 16) || !aligned(state_out, 16)) return DLRM_ERR_INVALID_ARG;
     if (a.B == 0) return DLRM_OK;
-    const Cut c = cut_of(a, desc->max_len);
+    const Cut c = cut_of(a, desc->max_len, false);
     if ((c.run || c.order) && (!workspace || !aligned(workspace, 256) || workspace_bytes < dlrm_seq_decay_fwd_workspace_size(desc)))
         return DLRM_ERR_WORKSPACE;
     hipStream_t stream = reinterpret_cast<hipStream_t>(stream_);
@@ -408,6 +437,6 @@ extern "C" int dlrm_seq_decay_fwd(const dlrm_seq_decay *desc, const float *state
     }
     if (rc != DLRM_OK) return rc;
     // in place, one workgroup reads and writes a whole sequence's state
-    a.splits = state_in && state_in == state_out && !c.run ? 1 : splits_of(a);
+    a.splits = state_in && state_in == state_out && !c.run ? 1 : splits_of(a, false);
     return walk(a, up, kNone, stream);
 }

@@ -120,6 +120,36 @@ def test_forward_backward(lens, Hq, Hkv, d, each, longest, itype):
     check_dg(got[3].cpu().numpy().astype(np.float64), want, full["dg"], gate["dg"], each)
 
 
+# sequences, their lengths, Hq, Hkv, d: cut into runs of one chunk to many (and a length a call is told that leaves them whole)
+CUTS = [(26, 1100, 1500, 2, 2, 128), (8, 500, 2000, 4, 4, 128), (4, 2000, 4096, 8, 2, 128), (64, 500, 1500, 2, 2, 64), (200, 100, 2000, 4, 2, 64),
+        (16, 300, 600, 4, 4, 32), (1, 8192, 8192, 4, 4, 64), (64, 200, 1500, 8, 2, 128), (3, 20000, 30000, 1, 1, 64), (100, 1000, 2000, 1, 1, 24)]
+
+
+@pytest.mark.parametrize("B,lo,hi,Hq,Hkv,d", CUTS)
+def test_runs_of_every_length(B, lo, hi, Hq, Hkv, d):
+    """Cut and whole the results agree to twice the gates (of the values themselves: their norms are below the scales'), and one
+    decay a head has the events' gradients' sum."""
+    rng = rng_of("cuts", B, lo, hi, d)
+    lens = rng.integers(lo, hi + 1, B)
+    off, dev, _, g, (do, _) = problem(rng, lens, Hq, Hkv, d, False)
+    off, g, n = to_dev(off), to_dev(g), int(lens.max())
+    each = g.expand(dev[0].shape[0], Hkv).contiguous()
+    gate = gates(n, d)
+    cut, whole = (dlrm_seq_decay_bwd(do, *dev, each, off, max_len=m) for m in (n, 1))
+    head, head_whole = (dlrm_seq_decay_bwd(do, *dev, g, off, max_len=m) for m in (n, 1))
+    o, o_whole = (dlrm_seq_decay_fwd(*dev, each, off, want_state=True, max_len=m) for m in (n, 1))
+    torch.cuda.synchronize()
+    far = lambda x, y: float((x.double() - y.double()).norm() / y.double().norm())  # noqa: E731
+    say(f"[decay] {B} of {lo}..{hi} d={d}: dg {far(cut[3], whole[3]):.1e}, a head's {far(head[3], cut[3].double().sum(0)):.1e}")
+    for x, y in zip(cut[:3] + head[:3] + o[:1], whole[:3] + head_whole[:3] + o_whole[:1]):
+        assert far(x, y) <= 2 * gate["bf16"]
+    assert far(o[1], o_whole[1]) <= 2 * gate["state"]
+    assert far(cut[3], whole[3]) <= 2 * gate["dg"]
+    want, room = cut[3].double().sum(0), 2 * np.sqrt(128) * gate["dg"] * cut[3].double().norm(dim=0)
+    for x in (head[3], head_whole[3]):
+        assert ((x.double() - want).abs() <= room).all()
+
+
 def test_gradients_against_differences():
     """The loss <do, o> along a direction of each input: the kernels' gradients against central differences of the oracle's
     forward in fp64."""

@@ -122,7 +122,8 @@ BAD_DECAY = [(dict(B=-1), INVALID), (dict(N=-1), INVALID), (dict(Hq=0), INVALID)
              (dict(q=0), INVALID), (dict(k=FAKE + 8), INVALID), (dict(g=0), INVALID), (dict(g=FAKE + 2), INVALID), (dict(g_row=1), INVALID),
              (dict(g_row=-2), INVALID), (dict(q_row=129), INVALID), (dict(v_head=24), INVALID), (dict(k_row=1 << 24), UNSUPPORTED),
              (dict(g_row=1 << 24), UNSUPPORTED), (dict(scale=float("nan")), INVALID)]
-BAD_OFFSETS = [(dict(offsets=0), INVALID), (dict(offsets=FAKE + 4), INVALID), (dict(N=(1 << 29) + 64), UNSUPPORTED)]
+BAD_OFFSETS = [(dict(offsets=0), INVALID), (dict(offsets=FAKE + 4), INVALID), (dict(N=(1 << 29) + 64), UNSUPPORTED),
+               (dict(N=1 << 28, Hq=1, Hkv=1, d=128, q_row=128, q_head=128, k_row=128, k_head=128, v_row=128, v_head=128), UNSUPPORTED)]
 
 
 @pytest.mark.parametrize("over,want", BAD_DECAY + BAD_OFFSETS)
