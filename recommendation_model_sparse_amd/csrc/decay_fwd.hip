@@ -282,7 +282,7 @@ __device__ __forceinline__ void run_state(const Walk &a, uint16_t *Ys, uint16_t 
     }
     const int64_t at = p.slot * static_cast<int64_t>(a.Hkv) + p.kvh;
     state_store<LP>(S, a.start + at * a.d * a.d, a.d, w, lane);
-    if (w == 0 && lane == 0) a.fade[at] = __builtin_amdgcn_exp2f(static_cast<float>(total));
+    if (w == 0 && lane == 0) a.fade[at] = exp2_of(total);
 }
 
 template <int LP, int UP, bool BACK>
