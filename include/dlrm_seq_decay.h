@@ -59,7 +59,7 @@ typedef struct {
     float scale;
 } dlrm_seq_decay;
 
-/* Bytes of workspace dlrm_seq_decay_fwd needs (0 on an invalid description). */
+/* Bytes of workspace dlrm_seq_decay_fwd needs (0 on an invalid description; 256: it uses none, which may be NULL). */
 size_t dlrm_seq_decay_fwd_workspace_size(const dlrm_seq_decay *a);
 
 /*

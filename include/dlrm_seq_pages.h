@@ -81,7 +81,7 @@ int dlrm_seq_pages_write(const uint16_t *k, int64_t k_row, int64_t k_head, const
 int dlrm_seq_attn_paged_fwd(const dlrm_seq_attn *a, const dlrm_seq_pages *p, uint16_t *o,
                             dlrm_stream_t stream);
 
-/* dlrm_seq_attn_decode over the pages, likewise; its workspace has the same size. */
+/* dlrm_seq_attn_decode over the pages, likewise; its workspace has the same size (256: it uses none, which may be NULL). */
 int dlrm_seq_attn_paged_decode(const dlrm_seq_attn *a, const dlrm_seq_pages *p, int64_t max_kv_len,
                                uint16_t *o, void *workspace, size_t workspace_bytes,
                                dlrm_stream_t stream);

@@ -650,6 +650,14 @@ def _ws(nbytes: int, dev, workspace: Optional[torch.Tensor]) -> torch.Tensor:
     return workspace
 
 
+def _ws_if(nbytes: int, dev, workspace: Optional[torch.Tensor]):
+    """_ws of a call that uses none where its size is 256: (its address, its bytes) and the tensor, which keeps it."""
+    if nbytes <= 256 and workspace is None:
+        return None, 0, None
+    workspace = _ws(nbytes, dev, workspace)
+    return workspace.data_ptr(), workspace.numel(), workspace
+
+
 def _mat(t, name: str, dtype) -> torch.Tensor:
     _need(t, name, dtype)
     if t.dim() != 2:
@@ -809,6 +817,13 @@ def _out(t, name: str, dtype: torch.dtype, shape, dev: torch.device) -> torch.Te
     if t.device != dev:
         raise ValueError(f"all tensors must be on {dev}, found one on {t.device}")
     return t
+
+
+def _out_like(t, name: str, like: torch.Tensor, shape, dev: torch.device) -> torch.Tensor:
+    """_out of `like`'s type, which costs two thirds where it has the shape."""
+    if t is None and like.is_contiguous() and like.shape == shape:
+        return torch.empty_like(like)
+    return _out(t, name, like.dtype, shape, dev)
 
 
 def _head_rows(t, name: str, heads: Optional[int] = None, d: Optional[int] = None):
@@ -1151,7 +1166,7 @@ def dlrm_seq_attn_paged_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q
     if lengths.numel() != B:
         raise ValueError(f"table and lengths must be of the {B} users of q_offsets, got {lengths.numel()}")
     _device(q, table, lengths)
-    out = _out(out, "out", torch.bfloat16, shape, dev)
+    out = _out_like(out, "out", q, shape, dev)
     _check(lib().dlrm_seq_attn_paged_fwd(a, pg, _ptr(out), _stream(dev)), "dlrm_seq_attn_paged_fwd")
     return out
 
@@ -1175,10 +1190,9 @@ def dlrm_seq_attn_paged_decode(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor
     longest = table.shape[1] * int(page) if max_kv_len is None else int(max_kv_len)
     if longest < 0:
         raise ValueError(f"max_kv_len must not be negative, got {longest}")
-    out = _out(out, "out", torch.bfloat16, shape, dev)
-    ws = _ws(lib().dlrm_seq_attn_decode_workspace_size(B, shape[1], k.shape[1], shape[2], window, sinks, longest), dev, workspace)
-    _check(lib().dlrm_seq_attn_paged_decode(a, pg, longest, _ptr(out), _ptr(ws), ws.numel(), _stream(dev)),
-           "dlrm_seq_attn_paged_decode")
+    out = _out_like(out, "out", q, shape, dev)
+    at, n, workspace = _ws_if(lib().dlrm_seq_attn_decode_workspace_size(B, shape[1], k.shape[1], shape[2], window, sinks, longest), dev, workspace)
+    _check(lib().dlrm_seq_attn_paged_decode(a, pg, longest, _ptr(out), at, n, _stream(dev)), "dlrm_seq_attn_paged_decode")
     return out
 
 
@@ -1197,9 +1211,9 @@ def _seq_decay(q, k, v, g, offsets, B: int, scale, max_len):
         raise ValueError(f"a head must have a multiple of 8 columns, at most 128, got {d}")
     if not isinstance(g, torch.Tensor) or g.dtype is not torch.float32:
         raise ValueError("g must be a tensor of torch.float32")
-    if tuple(g.shape) == (Hkv,) and g.is_contiguous():
+    if g.shape == (Hkv,) and g.is_contiguous():
         g_row = 0
-    elif tuple(g.shape) == (N, Hkv) and (Hkv == 1 or N == 0 or g.stride(1) == 1):
+    elif g.shape == (N, Hkv) and (Hkv == 1 or N == 0 or g.stride(1) == 1):
         g_row = g.stride(0) if N > 1 else Hkv
         if g_row < Hkv:
             raise ValueError("g must have rows of its own for each event; one decay for a head is [heads]")
@@ -1230,13 +1244,12 @@ def dlrm_seq_decay_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: tor
     if state is not None:
         _is(state, "state", torch.float32, ss)
         _device(q, state)
-    out = _out(out, "out", torch.bfloat16, shape, dev)
+    out = _out_like(out, "out", q, shape, dev)
     want_state = want_state or state_out is not None
     if want_state:
         state_out = _out(state_out, "state_out", torch.float32, ss, dev)
-    ws = _ws(lib().dlrm_seq_decay_fwd_workspace_size(a), dev, workspace)
-    _check(lib().dlrm_seq_decay_fwd(a, _ptr(state), _ptr(state_out), _ptr(out), _ptr(ws), ws.numel(), _stream(dev)),
-           "dlrm_seq_decay_fwd")
+    at, n, workspace = _ws_if(lib().dlrm_seq_decay_fwd_workspace_size(a), dev, workspace)
+    _check(lib().dlrm_seq_decay_fwd(a, _ptr(state), _ptr(state_out), _ptr(out), at, n, _stream(dev)), "dlrm_seq_decay_fwd")
     return (out, state_out) if want_state else out
 
 
@@ -1252,11 +1265,11 @@ def dlrm_seq_decay_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
     ks, bf = (qs[0], Hkv, qs[2]), torch.bfloat16
     _is(dout, "dout", bf, qs)
     _device(q, dout)
-    dq, dk, dv = _out(dq, "dq", bf, qs, dev), _out(dk, "dk", bf, ks, dev), _out(dv, "dv", bf, ks, dev)
+    dq, dk, dv = _out_like(dq, "dq", q, qs, dev), _out_like(dk, "dk", k, ks, dev), _out_like(dv, "dv", v, ks, dev)
     if dg is not None and not want_dg:
         raise ValueError("dg without want_dg")
     if want_dg:
-        dg = _out(dg, "dg", torch.float32, tuple(g.shape), dev)
+        dg = _out_like(dg, "dg", g, g.shape, dev)
     ws = _ws(lib().dlrm_seq_decay_bwd_workspace_size(a), dev, workspace)
     _check(lib().dlrm_seq_decay_bwd(a, _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(ws), ws.numel(), _stream(dev)),
            "dlrm_seq_decay_bwd")
@@ -1272,7 +1285,7 @@ def dlrm_seq_decay_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: to
     a, dev, shape, Hkv = _seq_decay(q, k, v, g, None, q.shape[0], scale, 1)
     _is(state, "state", torch.float32, (shape[0], Hkv, shape[2], shape[2]))
     _device(q, state)
-    out = _out(out, "out", torch.bfloat16, shape, dev)
+    out = _out_like(out, "out", q, shape, dev)
     _check(lib().dlrm_seq_decay_step(a, _ptr(state), _ptr(out), _stream(dev)), "dlrm_seq_decay_step")
     return out
 
