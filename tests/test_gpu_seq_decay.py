@@ -127,8 +127,8 @@ CUTS = [(26, 1100, 1500, 2, 2, 128), (8, 500, 2000, 4, 4, 128), (4, 2000, 4096, 
 
 @pytest.mark.parametrize("B,lo,hi,Hq,Hkv,d", CUTS)
 def test_runs_of_every_length(B, lo, hi, Hq, Hkv, d):
-    """Cut and whole the results agree to twice the gates (of the values themselves: their norms are below the scales'), and one
-    decay a head has the events' gradients' sum."""
+    """Cut and whole the results agree to twice the gates, in the norm of the values themselves (roundings of either sign add up
+    as the terms do), and one decay a head has the events' gradients' sum."""
     rng = rng_of("cuts", B, lo, hi, d)
     lens = rng.integers(lo, hi + 1, B)
     off, dev, _, g, (do, _) = problem(rng, lens, Hq, Hkv, d, False)
