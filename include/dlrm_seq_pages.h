@@ -76,7 +76,8 @@ int dlrm_seq_pages_write(const uint16_t *k, int64_t k_row, int64_t k_head, const
 /*
  * dlrm_seq_attn_fwd over the pages: `a` as there, but that k and v are the pool (Nkv == pages * page rows),
  * kv_begin and kv_end are not read, and sequence b's keys are user b's events, lengths[b] of them, the
- * new ones among them (the update has counted them, the write has put them there).  B == p->B.
+ * new ones among them (the update has counted them, the write has put them there).  B == p->B.  (Sums over
+ * keys may be taken in another order than there: the bits may differ.)
  */
 int dlrm_seq_attn_paged_fwd(const dlrm_seq_attn *a, const dlrm_seq_pages *p, uint16_t *o,
                             dlrm_stream_t stream);

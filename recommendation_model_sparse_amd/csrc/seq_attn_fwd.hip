@@ -405,10 +405,16 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a
 }
 
 template <int DP, int LP, int WQ, int WK, int OCC, int NEAR>
-int launch(const Args &a, const Pages *pg, uint16_t *o, float *lse, int32_t *tiles, hipStream_t stream) {
+int launch(const Args &a, uint16_t *o, float *lse, int32_t *tiles, hipStream_t stream) {
     const dim3 grid(round_up_xcd(slot_count(a.Nq, a.B, WQ * 32)), a.Hq);
-    if (pg) DLRM_LAUNCH("seq_attn_paged_fwd", (k_seq_attn_fwd<DP, LP, WQ, WK, OCC, NEAR, true>), grid, dim3(WQ * WK * 64), 0, stream, a, *pg, o, lse, tiles);
-    else DLRM_LAUNCH("seq_attn_fwd", (k_seq_attn_fwd<DP, LP, WQ, WK, OCC, NEAR, false>), grid, dim3(WQ * WK * 64), 0, stream, a, Pages{}, o, lse, tiles);
+    DLRM_LAUNCH("seq_attn_fwd", (k_seq_attn_fwd<DP, LP, WQ, WK, OCC, NEAR, false>), grid, dim3(WQ * WK * 64), 0, stream, a, Pages{}, o, lse, tiles);
+    return launch_status();
+}
+
+template <int DP, int LP, int WQ, int WK, int OCC, int NEAR>
+int launch_paged(const Args &a, const Pages &pg, uint16_t *o, hipStream_t stream) {
+    const dim3 grid(round_up_xcd(slot_count(a.Nq, a.B, WQ * 32)), a.Hq);
+    DLRM_LAUNCH("seq_attn_paged_fwd", (k_seq_attn_fwd<DP, LP, WQ, WK, OCC, NEAR, true>), grid, dim3(WQ * WK * 64), 0, stream, a, pg, o, nullptr, nullptr);
     return launch_status();
 }
 
@@ -418,10 +424,21 @@ int launch(const Args &a, const Pages *pg, uint16_t *o, float *lse, int32_t *til
 // to 300 queries after up to 2048 keys).  The near biases: 2048 distances against 896 at heads of 32, 74 -> 70
 // us, and against 1280 at 128, 99 -> 97 (8 sequences of 2048, a bias that differs up to 2048); at 64 the
 // longer table costs a workgroup a CU: 86 -> 87, and 18.7 -> 20.5 for 64 sequences of 256.
-int launch_for(const Args &a, const Pages *pg, uint16_t *o, float *lse, int32_t *tiles, hipStream_t stream) {
-    if (a.d <= 32) return launch<32, 32, 2, 1, 4, 2048>(a, pg, o, lse, tiles, stream);
-    if (a.d <= 64) return launch<64, 64, 2, 1, 4, 640>(a, pg, o, lse, tiles, stream);
-    return launch<128, 128, 2, 2, 2, 2048>(a, pg, o, lse, tiles, stream);
+int launch_for(const Args &a, uint16_t *o, float *lse, int32_t *tiles, hipStream_t stream) {
+    if (a.d <= 32) return launch<32, 32, 2, 1, 4, 2048>(a, o, lse, tiles, stream);
+    if (a.d <= 64) return launch<64, 64, 2, 1, 4, 640>(a, o, lse, tiles, stream);
+    return launch<128, 128, 2, 2, 2, 2048>(a, o, lse, tiles, stream);
+}
+
+// Over pages heads of up to 64 take 2 x 2 where there are up to ten workgroups a CU, as a visit of few users has, since
+// more wavefronts wait side by side.  16 users of 100 to 2048 with up to 300 new events, 8 heads of 64 (32): 78 -> 46 us
+// (65 -> 39); 32 of 1000 to 4000 with up to 1000, 2224 workgroups: 269 -> 198 (199 -> 152); 512 of 100 to 512, 3692: 60 -> 57
+// (44 -> 47); 1024, 7380: 98 -> 101 (73 -> 84).
+int launch_for_paged(const Args &a, const Pages &pg, uint16_t *o, hipStream_t stream) {
+    const bool few = slot_count(a.Nq, a.B, kQT) * a.Hq <= 10 * 256;
+    if (a.d <= 32) return few ? launch_paged<32, 32, 2, 2, 4, 2048>(a, pg, o, stream) : launch_paged<32, 32, 2, 1, 4, 2048>(a, pg, o, stream);
+    if (a.d <= 64) return few ? launch_paged<64, 64, 2, 2, 4, 640>(a, pg, o, stream) : launch_paged<64, 64, 2, 1, 4, 640>(a, pg, o, stream);
+    return launch_paged<128, 128, 2, 2, 2, 2048>(a, pg, o, stream);
 }
 
 }  // namespace
@@ -442,7 +459,7 @@ extern "C" int dlrm_seq_attn_fwd(const dlrm_seq_attn *desc, uint16_t *o, float *
     if (a.B > 0 && a.Nq > 0 && (lse == nullptr) != (tiles == nullptr)) return DLRM_ERR_INVALID_ARG;
     if (a.Nq > 0 && (!o || !aligned(o, 16) || !aligned(lse, 4) || !aligned(tiles, 4))) return DLRM_ERR_INVALID_ARG;
     if (a.B == 0 || a.Nq == 0) return DLRM_OK;
-    return launch_for(a, nullptr, o, lse, tiles, reinterpret_cast<hipStream_t>(stream_));
+    return launch_for(a, o, lse, tiles, reinterpret_cast<hipStream_t>(stream_));
 }
 
 extern "C" int dlrm_seq_attn_paged_fwd(const dlrm_seq_attn *desc, const dlrm_seq_pages *pages, uint16_t *o, dlrm_stream_t stream_) {
@@ -455,5 +472,5 @@ extern "C" int dlrm_seq_attn_paged_fwd(const dlrm_seq_attn *desc, const dlrm_seq
     if (rc != DLRM_OK) return rc;
     if (a.Nq > 0 && (!o || !aligned(o, 16))) return DLRM_ERR_INVALID_ARG;
     if (a.B == 0 || a.Nq == 0) return DLRM_OK;
-    return launch_for(a, &pg, o, nullptr, nullptr, reinterpret_cast<hipStream_t>(stream_));
+    return launch_for_paged(a, pg, o, reinterpret_cast<hipStream_t>(stream_));
 }

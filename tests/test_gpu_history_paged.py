@@ -1,10 +1,11 @@
 """The history encoder's pages and linear layers (history.py; needs an MI355X): a paged cache against one with a
-region for each user, bit for bit; the encoder with linear layers against the same model in fp64 through torch
+region for each user; the encoder with linear layers against the same model in fp64 through torch
 autograd, and its serving against its training.
 
 Gates: those of test_gpu_history.py.  A linear layer rounds its state's part of an output to bf16 once more and
 its heads' norm twice: two roundings a layer on top of seven, sqrt(19) 2^-9 = 0.85 %, within the same fourfold.
-Two caches' vectors may differ by bits of the linear layers' alone, and those do the same sums here.
+Two caches do the same roundings; over heads of up to 64 a visit's sums over keys may be taken in two halves, another order of
+sums: 3 %, as serving has against training there.  Over larger heads the sums are the same, and the vectors.
 """
 import numpy as np
 import pytest
@@ -125,21 +126,27 @@ def test_a_step_moves_every_weight():
 
 
 @pytest.mark.parametrize("page", [8, 64])
-@pytest.mark.parametrize("over", [dict(), dict(window=20, sinks=3), dict(linear=1), dict(linear=2), dict(Hq=8, Hkv=1, linear=1)])
+@pytest.mark.parametrize("over", [dict(), dict(window=20, sinks=3), dict(linear=1), dict(linear=2), dict(Hq=8, Hkv=1, linear=1),
+                                  dict(D=512), dict(D=384, window=20, sinks=3, linear=1)])
 def test_pages_give_the_regions_vectors(page, over):
     """Visits with users that come, stay away and come again, then single events, 8-bit ones too."""
     rng = np.random.default_rng(23)
     enc = encoder(**over)
     one, other = enc.cache(5, 160), enc.paged_cache(5, 160, -(-160 // page) * 5, page)
     say(f"[history] pages of {page}, {over}")
+    alike = torch.equal if enc.d > 64 else lambda x, y: far(x, y) <= 0.03 and torch.equal((x != 0).any(1), (y != 0).any(1))
     for counts in ([30, 1, 0, 64, 100], [0, 7, 65, 1, 0], [0, 0, 0, 0, 0], [1, 0, 8, 0, 9]):
         v = visit(rng, counts, np.int32 if counts[0] else np.int64)
-        assert torch.equal(one.prefill(*v, 100), other.prefill(*v, 100)), counts
+        x, y = one.prefill(*v, 100), other.prefill(*v, 100)
+        assert alike(x, y) or not y.any() and torch.equal(x, y), counts
     for i in range(9):
         ids = put(rng.integers(0, 500, 5))
         a, b = one.append(ids, eight_bit=i == 4), other.append(ids, eight_bit=i == 4)
-        for x, y in zip(*((a, b) if i == 4 else ((a,), (b,)))):
-            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8)), i
+        if i == 4:  # 8 bits: 2^-5 in the mean square, of two rounded values
+            (x, s), (y, t) = a, b
+            assert far(x.float() * s[:, None], y.float() * t[:, None]) <= (0.0 if enc.d > 64 else 0.08)
+        else:
+            assert alike(a, b), i
     assert torch.equal((one.end - one.begin).cpu(), other.lengths.cpu().long())
     assert (other.held == other.lengths.cpu().numpy()).all()
 

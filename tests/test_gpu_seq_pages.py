@@ -1,6 +1,9 @@
 """GPU parity of the paged cache (dlrm_seq_pages.h; needs an MI355X): the visit's tables, lengths and slots against
 oracle/pages.py, entry by entry; attention over pages against the calls over rows that lie together, bit by bit (the
-same products in the same order)."""
+same products in the same order).
+
+Over heads of up to 64 a few users' new events take the keys of a tile in two halves, another order: either side rounds P and its
+output to bf16 (2^-8 each of sum P |v|, which the call over |v| gives to 2^-6), so they are at most 2^-6 (1 + 2^-6) of it apart."""
 import zlib
 
 import numpy as np
@@ -180,11 +183,20 @@ def how_of(rng, Hq, window, sinks, buckets):
     return how
 
 
+def check_several(got, want, call, v):
+    """`call`: the attention over rows that lie together, of v."""
+    if got.shape[2] > 64:
+        assert torch.equal(got, want)
+        return
+    room = 2.0 ** -6 * (1 + 2.0 ** -6) * call(v.abs()).float()
+    assert ((got.float() - want.float()).abs() <= room).all()
+
+
 CASES = [
     # lens, page, Hq, Hkv, d, window, sinks, buckets
     ([1], 8, 1, 1, 8, 0, 0, 0), ([5, 0, 17, 64], 8, 4, 2, 32, 0, 0, 8), ([63, 64, 65, 1], 64, 2, 1, 64, 0, 0, 8), ([300, 7, 129], 16, 8, 2, 128, 0, 0, 32),
     ([300, 7, 129], 32, 4, 4, 40, 50, 3, 16), ([700, 1000], 256, 6, 2, 96, 300, 70, 0), ([2000, 3, 900], 8, 40, 2, 64, 0, 0, 32), ([5000, 10], 512, 2, 1, 64, 0, 0, 0),
-    ([40] * 300, 16, 2, 1, 32, 0, 0, 8), ([0, 0], 16, 2, 1, 32, 0, 0, 0)]
+    ([40] * 300, 16, 2, 1, 32, 0, 0, 8), ([0, 0], 16, 2, 1, 32, 0, 0, 0), ([130, 3, 40] * 500, 16, 2, 1, 64, 0, 0, 8), ([70] * 1400, 32, 2, 2, 32, 30, 2, 8)]
 
 
 @pytest.mark.parametrize("lens,page,Hq,Hkv,d,window,sinks,buckets", CASES)
@@ -216,7 +228,10 @@ def test_new_events_over_pages(lens, page, Hq, Hkv, d, window, sinks, buckets):
     got = dlrm_seq_attn_paged_fwd(q, *pools, qo, table, lengths, page, **how)
     narrow = dlrm_seq_attn_paged_fwd(q, *pools, qo.int(), table[:, :], lengths, page, **how)
     torch.cuda.synchronize()
-    assert torch.equal(got, want) and torch.equal(narrow, want)
+    assert torch.equal(got, narrow)
+    if len(lens) > 1000:  # many users: no halves
+        assert torch.equal(got, want)
+    check_several(got, want, lambda x: dlrm_seq_attn_fwd(q, k, x, qo, to_dev(off), **how), v)
 
 
 def test_heads_that_lie_apart_and_a_wider_pool():
@@ -234,7 +249,8 @@ def test_heads_that_lie_apart_and_a_wider_pool():
     got = dlrm_seq_attn_paged_decode(q, joint[:, :2], joint[:, 2:], part, lengths, 16)
     assert torch.equal(got, want)
     qo = to_dev(offsets([1, 1]))
-    assert torch.equal(dlrm_seq_attn_paged_fwd(q, joint[:, :2], joint[:, 2:], qo, part, lengths, 16), dlrm_seq_attn_fwd(q, k, v, qo, off))
+    check_several(dlrm_seq_attn_paged_fwd(q, joint[:, :2], joint[:, 2:], qo, part, lengths, 16), dlrm_seq_attn_fwd(q, k, v, qo, off),
+                  lambda x: dlrm_seq_attn_fwd(q, k, x, qo, off), v)
 
 
 def test_tables_that_cannot_be():
