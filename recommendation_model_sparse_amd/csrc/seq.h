@@ -178,10 +178,10 @@ __device__ __forceinline__ void read_columns(Frag &f, const uint16_t *at, int ro
 // columns from d on), `store` writes it.  The next tile is not read ahead: its 16 to 32 registers a
 // matrix cost a wavefront a SIMD, which hides more (heads of 128: 361 -> 318 us for the backward's
 // first kernel; of 64: no difference).
-template <int LP, int THREADS>
+template <int LP, int THREADS, int BK = kBK>
 struct Stage {
     static constexpr int CH = LP / 8;
-    static constexpr int N = kBK * CH / THREADS;  // 16-byte pieces a thread
+    static constexpr int N = BK * CH / THREADS;  // 16-byte pieces a thread
     static constexpr int R = THREADS / CH;        // rows that are read at once
     u32x4 r[N];
     int row, lds;
@@ -198,7 +198,7 @@ struct Stage {
     __device__ __forceinline__ void load(const uint16_t *base, int64_t stride, int d, int row0, int first, int end, int sinks) {
         const char *p = reinterpret_cast<const char *>(base + row0 * stride);
         const int64_t step = R * stride * 2;
-        if (d == LP && row0 >= first && row0 + kBK <= end) {
+        if (d == LP && row0 >= first && row0 + BK <= end) {
 #pragma unroll
             for (int i = 0; i < N; ++i, p += step) r[i] = *(const DLRM_GLOBAL u32x4 *)(p + at);
             return;

@@ -86,7 +86,7 @@ namespace {
 
 // DP: the head's width rounded up (the products run over DP columns, those from d on are zeros);
 // LP: columns of a row in LDS.  WQ wavefronts of 32 queries each, by WK that share a tile's keys:
-// each then takes one of its two halves, and their results are joined at the end.  PAGED: a key's row comes
+// each then takes 32 of them, and their results are joined at the end.  PAGED: a key's row comes
 // from the table of its sequence's pages.  (Four histories of 3000 to 4096, heads of 128, all events new: 118 us, where reads
 // of wanted rows alone, with a branch each, took 134; a tile's reads begun while the one before is worked on, 115, but
 // 52.0 where 51.0 for 256 histories of up to 512: not kept.)
@@ -94,7 +94,8 @@ template <int DP, int LP, int WQ, int WK, int OCC, int NEAR, bool PAGED>
 __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a, const Pages pg, uint16_t *o_out, float *lse_out,
                                                                     int32_t *tiles_out) {
     constexpr int QT = WQ * 32, STEPS = DP / 16, MB = DP / 32, THREADS = WQ * WK * 64;
-    constexpr int TAB = QT + kBK, TILE = kBK * kPitch<LP>;
+    constexpr int BK = WK > 2 ? 32 * WK : kBK;  // keys of a tile
+    constexpr int TAB = QT + BK, TILE = BK * kPitch<LP>;
     __shared__ __attribute__((aligned(16))) uint16_t tiles_s[2 * TILE];
     __shared__ float near_s[kPad + NEAR], tab[TAB], bias_s[DLRM_SEQ_MAX_BUCKETS];
     __shared__ int bounds_s[DLRM_SEQ_MAX_BUCKETS];
@@ -120,13 +121,13 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a
     const int pmin = q0 + sp.shift, pmax = min(q0 + QT, sp.qlen) - 1 + sp.shift;
     const int end = min(sp.klen, pmax + 1);
     const int first = a.window ? max(0, pmin - a.window + 1) : 0;
-    const int t1 = end > 0 ? (end + kBK - 1) / kBK : 0;
-    const int t0 = min(first / kBK, t1);
-    const int nsink = min((a.sinks + kBK - 1) / kBK, t0);
+    const int t1 = end > 0 ? (end + BK - 1) / BK : 0;
+    const int t0 = min(first / BK, t1);
+    const int nsink = min((a.sinks + BK - 1) / BK, t0);
     const int n = nsink + t1 - t0;
 
-    Stage<LP, THREADS> ks(a.k_row, a.d), vs(a.v_row, a.d);
-    const auto key0 = [&](int it) { return (it < nsink ? it : t0 + it - nsink) * kBK; };
+    Stage<LP, THREADS, BK> ks(a.k_row, a.d), vs(a.v_row, a.d);
+    const auto key0 = [&](int it) { return (it < nsink ? it : t0 + it - nsink) * BK; };
     const int32_t *const mine = PAGED ? pg.table + b * pg.row : nullptr;
     const auto load = [&](int it) {
         if constexpr (PAGED) {
@@ -141,13 +142,13 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a
     };
     // Every query of the block sees every key of the tile at one bias: no table.
     const auto even = [&](int k0) {
-        const int nearest = pmin - (k0 + kBK - 1);
-        return nearest >= a.last && (!a.window || q0 + QT - 1 + sp.shift - k0 < a.window || k0 + kBK <= a.sinks);
+        const int nearest = pmin - (k0 + BK - 1);
+        return nearest >= a.last && (!a.window || q0 + QT - 1 + sp.shift - k0 < a.window || k0 + BK <= a.sinks);
     };
     const auto close = [&](int k0) { return pmin - k0 + QT - 1 < NEAR && k0 >= a.sinks; };
     const auto table = [&](int k0) {
         if (even(k0) || close(k0)) return;
-        const int n0 = pmin - (k0 + kBK - 1);
+        const int n0 = pmin - (k0 + BK - 1);
         int bucket;
         for (int i = tid; i < TAB - 1; i += THREADS) tab[i] = bias_at(a, bounds_s, bias_s, n0 + i, k0 < a.sinks, &bucket);
     };
@@ -170,7 +171,7 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a
 
     __syncthreads();
     {
-        const int reach = n > 0 ? min(NEAR, pmin + QT - t0 * kBK) : 0;  // past the furthest but for first keys'
+        const int reach = n > 0 ? min(NEAR, pmin + QT - t0 * BK) : 0;  // past the furthest but for first keys'
         int bucket;
         for (int i = tid; i < reach; i += THREADS) near_s[kPad + i] = bias_at(a, bounds_s, bias_s, i, false, &bucket);
         for (int i = tid; i < kPad; i += THREADS) near_s[i] = -kInf;
@@ -205,7 +206,7 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a
             const int wpos = pmin + w * 32;  // position of the wavefront's first query
             // 32 keys at a time: S, P and their operands for 64 would cost a wavefront a SIMD
 #pragma unroll 1
-            for (int g = WK == 2 ? wk : 0; g < (WK == 2 ? wk + 1 : 2); ++g) {
+            for (int g = WK > 1 ? wk : 0; g < (WK > 1 ? wk + 1 : 2); ++g) {
                 const int k1 = k0 + 32 * g;
                 if (wpos + 31 < k1 || q0 + w * 32 >= sp.qlen || (a.window && wpos - (k1 + 31) >= a.window && k1 >= a.sinks))
                     continue;  // seen by none of the wavefront's queries
@@ -225,7 +226,7 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a
                 } else {
                     // distance wpos + ln - k1 - 4 half - (key): entry 63 - that of tab's
                     const float *tb = close(k0) ? near_s + kPad + wpos - k1 + ln - 4 * half
-                                                : tab + w * 32 + ln + kBK - 1 - 32 * g - 4 * half;
+                                                : tab + w * 32 + ln + BK - 1 - 32 * g - 4 * half;
 #pragma unroll
                     for (int r = 0; r < 16; ++r) s[r] = fmaf(s[r], a.scale, tb[-(8 * (r / 4) + r % 4)]);
                     if constexpr (WILD) {  // NaN - infinity is no -infinity
@@ -356,11 +357,13 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a
         attend(std::true_type(), over ? top0 : -kInf, over ? 1.f / sum0 : 1.f);
         if (over) unit = sum0 / sum, top = top0, sum = sum0;
     }
-    if constexpr (WK == 2) {  // the second half of the keys joins the first
-        float *const part = reinterpret_cast<float *>(tiles_s) + w * (MB * 16 + 3) * 64 + lane;
-        static_assert(WQ * (MB * 16 + 3) * 64 * 4 <= 2 * TILE * 2, "the tiles' room holds the halves' results");
+    // The parts of the keys are joined two by two: the upper wavefronts' results go to the lower ones.
+#pragma unroll
+    for (int n = WK / 2; n >= 1; n /= 2) {
+        float *const part = reinterpret_cast<float *>(tiles_s) + (wk % n * WQ + w) * (MB * 16 + 3) * 64 + lane;
+        static_assert(WK < 2 || WK / 2 * WQ * (MB * 16 + 3) * 64 * 4 <= 2 * TILE * 2, "the tiles' room holds the parts' results");
         __syncthreads();
-        if (wk == 1) {
+        if (wk >= n && wk < 2 * n) {
 #pragma unroll
             for (int m = 0; m < MB; ++m)
 #pragma unroll
@@ -370,11 +373,11 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a
             part[(MB * 16 + 2) * 64] = unit;
         }
         __syncthreads();
-        if (wk == 1) return;
+        if (wk >= n) continue;
         const float top1 = part[MB * 16 * 64], sum1 = part[(MB * 16 + 1) * 64], mx = fmaxf(top, top1);
         const float f0 = top == -kInf ? 0.f : top == mx ? 1.f : __builtin_amdgcn_exp2f((top - mx) * kLog2e);
         const float f1 = top1 == -kInf ? 0.f : top1 == mx ? 1.f : __builtin_amdgcn_exp2f((top1 - mx) * kLog2e);
-        // a half without a key that the query sees holds a sum of 0; one whose every logit is NaN has the same
+        // a part without a key that the query sees holds a sum of 0; one whose every logit is NaN has the same
         // maximum, as that passes NaN over, and its sum is NaN
         sum = f0 * sum + f1 * sum1;
         top = mx;
@@ -384,10 +387,12 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a
         for (int m = 0; m < MB; ++m)
 #pragma unroll
             for (int r = 0; r < 16; ++r) o[m][r] = g0 * o[m][r] + g1 * part[(m * 16 + r) * 64];
+        unit = sum;  // o is the mean by now
     }
+    if (WK > 1 && wk > 0) return;
 
     if (!live) return;
-    const float inv = WK == 2 ? 1.f : sum == 0.f ? 0.f : unit / sum;
+    const float inv = WK > 1 ? 1.f : sum == 0.f ? 0.f : unit / sum;
     const int64_t row = (sp.q0 + ql) * a.Hq + h;
     if (lse_out && half == 0) lse_out[row] = sum == 0.f ? -kInf : top + __builtin_amdgcn_logf(sum) * kLn2;
 #pragma unroll
@@ -430,15 +435,21 @@ int launch_for(const Args &a, uint16_t *o, float *lse, int32_t *tiles, hipStream
     return launch<128, 128, 2, 2, 2, 2048>(a, o, lse, tiles, stream);
 }
 
-// Over pages heads of up to 64 take 2 x 2 where there are up to ten workgroups a CU, as a visit of few users has, since
-// more wavefronts wait side by side.  16 users of 100 to 2048 with up to 300 new events, 8 heads of 64 (32): 78 -> 46 us
-// (65 -> 39); 32 of 1000 to 4000 with up to 1000, 2224 workgroups: 269 -> 198 (199 -> 152); 512 of 100 to 512, 3692: 60 -> 57
-// (44 -> 47); 1024, 7380: 98 -> 101 (73 -> 84).
+// Over pages, where a visit of few users has few workgroups, more wavefronts share a tile's keys, as each waits for chains of
+// its own: 2 x 4 over tiles of 128 while all workgroups are resident, two a CU, one of heads past 64; heads of up to 64 take 2 x 2
+// up to ten a CU.  Heads of 128 (64, 32): 4 users of 3000 to 4000, 100 to 4000 new events, 248 workgroups, 2 x 4 78 us (50, 39) and
+// 2 x 2 116 (72, 55); 16 of 100 to 2048, 448: 84 (38, 30) and 76 (47, 38), and 2 x 1 (78, 65); 128 of 100 to 512, 940: 59 (27,
+// 22) and 42 (22, 17); 32 of 1000 to 4000, 2224: 2 x 2 (198, 152), 2 x 1 (269, 199); 512 of 100 to 512, 3692: (57, 47), (60, 44).
 int launch_for_paged(const Args &a, const Pages &pg, uint16_t *o, hipStream_t stream) {
-    const bool few = slot_count(a.Nq, a.B, kQT) * a.Hq <= 10 * 256;
-    if (a.d <= 32) return few ? launch_paged<32, 32, 2, 2, 4, 2048>(a, pg, o, stream) : launch_paged<32, 32, 2, 1, 4, 2048>(a, pg, o, stream);
-    if (a.d <= 64) return few ? launch_paged<64, 64, 2, 2, 4, 640>(a, pg, o, stream) : launch_paged<64, 64, 2, 1, 4, 640>(a, pg, o, stream);
-    return launch_paged<128, 128, 2, 2, 2, 2048>(a, pg, o, stream);
+    const int64_t groups = slot_count(a.Nq, a.B, kQT) * a.Hq;
+    if (a.d > 64) return groups <= 256 ? launch_paged<128, 128, 2, 4, 2, 2048>(a, pg, o, stream) : launch_paged<128, 128, 2, 2, 2, 2048>(a, pg, o, stream);
+    const int wk = groups <= 2 * 256 ? 4 : groups <= 10 * 256 ? 2 : 1;
+    if (a.d <= 32) {
+        if (wk == 4) return launch_paged<32, 32, 2, 4, 4, 2048>(a, pg, o, stream);
+        return wk == 2 ? launch_paged<32, 32, 2, 2, 4, 2048>(a, pg, o, stream) : launch_paged<32, 32, 2, 1, 4, 2048>(a, pg, o, stream);
+    }
+    if (wk == 4) return launch_paged<64, 64, 2, 4, 4, 640>(a, pg, o, stream);
+    return wk == 2 ? launch_paged<64, 64, 2, 2, 4, 640>(a, pg, o, stream) : launch_paged<64, 64, 2, 1, 4, 640>(a, pg, o, stream);
 }
 
 }  // namespace
