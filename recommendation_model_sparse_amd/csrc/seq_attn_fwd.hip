@@ -357,13 +357,14 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a
         attend(std::true_type(), over ? top0 : -kInf, over ? 1.f / sum0 : 1.f);
         if (over) unit = sum0 / sum, top = top0, sum = sum0;
     }
-    // The parts of the keys are joined two by two: the upper wavefronts' results go to the lower ones.
-#pragma unroll
-    for (int n = WK / 2; n >= 1; n /= 2) {
-        float *const part = reinterpret_cast<float *>(tiles_s) + (wk % n * WQ + w) * (MB * 16 + 3) * 64 + lane;
-        static_assert(WK < 2 || WK / 2 * WQ * (MB * 16 + 3) * 64 * 4 <= 2 * TILE * 2, "the tiles' room holds the parts' results");
+    // Parts of the keys are joined two by two: the results of the wavefronts n to 2 n - 1 go to those below.  Says whether this
+    // one's are with another now.
+    const auto join = [&](auto number) {
+        constexpr int n = decltype(number)::value;
+        static_assert(n * WQ * (MB * 16 + 3) * 64 * 4 <= 2 * TILE * 2, "the tiles' room holds the parts' results");
+        float *const part = reinterpret_cast<float *>(tiles_s) + (n == 1 ? w : wk % n * WQ + w) * (MB * 16 + 3) * 64 + lane;
         __syncthreads();
-        if (wk >= n && wk < 2 * n) {
+        if (n == 1 ? wk == 1 : wk >= n) {
 #pragma unroll
             for (int m = 0; m < MB; ++m)
 #pragma unroll
@@ -373,7 +374,7 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a
             part[(MB * 16 + 2) * 64] = unit;
         }
         __syncthreads();
-        if (wk >= n) continue;
+        if (n == 1 ? wk >= 1 : wk >= n) return true;
         const float top1 = part[MB * 16 * 64], sum1 = part[(MB * 16 + 1) * 64], mx = fmaxf(top, top1);
         const float f0 = top == -kInf ? 0.f : top == mx ? 1.f : __builtin_amdgcn_exp2f((top - mx) * kLog2e);
         const float f1 = top1 == -kInf ? 0.f : top1 == mx ? 1.f : __builtin_amdgcn_exp2f((top1 - mx) * kLog2e);
@@ -388,8 +389,11 @@ __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a
 #pragma unroll
             for (int r = 0; r < 16; ++r) o[m][r] = g0 * o[m][r] + g1 * part[(m * 16 + r) * 64];
         unit = sum;  // o is the mean by now
-    }
-    if (WK > 1 && wk > 0) return;
+        return false;
+    };
+    if constexpr (WK == 4) join(std::integral_constant<int, 2>());
+    if constexpr (WK > 1)
+        if (join(std::integral_constant<int, 1>())) return;
 
     if (!live) return;
     const float inv = WK > 1 ? 1.f : sum == 0.f ? 0.f : unit / sum;
