@@ -11,10 +11,10 @@ sigmoid head here, or one more row of the dot-product interaction.
     user = norm(s)[last event]
 
 Like dlrm_step, it only orders the calls and owns the weights: every step runs in the library's
-kernels, but for what moves data: torch indexes rows, and in the backward joins dq, dk and dv and
-casts them.  The residual stream is fp32, activations and the dense layers' weights bf16 with fp32
-masters (SGD), the table is updated by row-wise Adagrad.  Histories are jagged: event rows laid end
-to end, with offsets [B + 1].
+kernels, but for what moves data: torch indexes rows, in the backward joins dq, dk and dv and
+casts them, and keeps the learned decays at 0 or below.  The residual stream is fp32, activations and
+the dense layers' weights bf16 with fp32 masters (SGD), the table is updated by row-wise Adagrad.
+Histories are jagged: event rows laid end to end, with offsets [B + 1].
 
 Serving keeps each layer's keys and values in a region of `capacity` rows a user (`cache`), or in pages of
 a pool that all users share (`paged_cache`): `prefill` encodes the events since the last visit against them,
@@ -189,7 +189,8 @@ class HistoryEncoder:
         return dx, grads[::-1], dw
 
     def step(self, ids: torch.Tensor, offsets: torch.Tensor, clicks: torch.Tensor, longest: Optional[int] = None) -> torch.Tensor:
-        """One training step on B histories and their clicks [B] (0 or 1); returns the loss [1]."""
+        """One training step on B histories and their clicks [B] (0 or 1); returns the loss [1].  A linear layer's decays
+        stay at 0 or below: a step past 0 ends there."""
         users, kept = self.forward(ids, offsets, longest=longest)
         head = L.dlrm_bce_head(users, self.head.W16.view(-1), self.head.b, clicks)
         rows, grads, dw = self.backward(head["dx"], kept)
@@ -200,6 +201,8 @@ class HistoryEncoder:
             params += [(layer[name], None, g[name]) for name in g]
         for i in range(0, len(params), 64):
             L.dlrm_sgd_dense_multi(params[i:i + 64], self.lr)
+        for layer in self.layers[:self.c.linear]:  # above 0 a decay counts as 0 without a gradient, and would stay there; at 0 it has one
+            layer["g"].clamp_(max=0)
         one = torch.arange(ids.numel() + 1, dtype=torch.int64, device=self.dev)
         L.emb_bag_bwd_adagrad([self.table], [self.state], ids, one, None, rows.view(-1, 1, self.c.D), self.lr_emb, self.eps_emb)
         return head["loss"]

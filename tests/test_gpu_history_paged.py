@@ -11,7 +11,7 @@ import numpy as np
 import pytest
 import torch
 
-from recommendation_model_sparse_amd import dlrm_dropout
+from recommendation_model_sparse_amd import dlrm_bce_head, dlrm_dropout
 from recommendation_model_sparse_amd.history import HistoryEncoder, Shape
 
 from gpu_util import DEV, say
@@ -123,6 +123,30 @@ def test_a_step_moves_every_weight():
     assert {name for name, _, _ in before} == {"w1", "w2", "bias", "g", "wo"}
     for name, i, x in before:
         assert torch.isfinite(enc.layers[i][name]).all() and not torch.equal(enc.layers[i][name], x), (name, i)
+
+
+def test_a_decay_pushed_against_0_learns_again():
+    """A step that would take decays past 0 leaves them at 0; there they have a gradient, and the next step goes by it.
+    (A step is w - lr dw in fp32: lr's rounding, the product's and the sum's, 2^-22 of both terms.)"""
+    rng = np.random.default_rng(29)
+    enc = encoder(linear=2, Hkv=4, p=0.0)
+    ids, off = visit(rng, [30, 40, 64, 65, 10, 100])
+    clicks = np.array([0, 1, 1, 0, 1, 0], np.float32)
+    decays = lambda: torch.cat([layer["g"].clone() for layer in enc.layers])  # noqa: E731
+    for layer in enc.layers:
+        layer["g"].fill_(-1e-7)
+    enc.step(ids, off, put(clicks))
+    first = decays()
+    say(f"[history] decays after a step past 0: {first.tolist()}")
+    assert (first <= 0).all() and (first == 0).any() and (first < -1e-7).any()
+    users, kept = enc.forward(ids, off)
+    dx = dlrm_bce_head(users, enc.head.W16.view(-1), enc.head.b, put(1 - clicks))["dx"]
+    dg = torch.cat([grads["g"] for grads in enc.backward(dx, kept)[1]])
+    assert (dg != 0).all() and (dg[first == 0] > 0).any()
+    enc.step(ids, off, put(1 - clicks))
+    second = decays()
+    say(f"[history] and after the opposite one: {second.tolist()}")
+    assert ((second - (first - enc.lr * dg).clamp(max=0)).abs() <= 2.0 ** -22 * (first.abs() + enc.lr * dg.abs())).all()
 
 
 @pytest.mark.parametrize("page", [8, 64])
