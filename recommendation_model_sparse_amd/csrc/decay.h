@@ -65,7 +65,7 @@ struct Walk {
     float *terms;        // [parts][Hkv][N]: <t, out> of the walk for dq, for each of its splits, by way of the state
     float *pairs;        // and by way of the chunk's pairs
     int32_t parts;
-    float *marks;        // the forward state (dq's) before every `mark`th chunk, as its wavefronts hold it
+    float *marks;        // the forward state (dq's) before every `mark`th chunk but the first, as its wavefronts hold it (mark_at)
     int32_t mark;
     float *dg;           // [N][Hkv]
     double *sums;        // or over each slot's events, [Hkv][slots]
@@ -99,6 +99,12 @@ __device__ __forceinline__ Part part_of(const Walk &a) {
     p.c1 = a.run ? min(p.c0 + a.run, p.chunks) : p.chunks;
     p.any = r >= 0 && (r == 0 || p.c0 < p.chunks);
     return p;
+}
+
+// The place of the state before chunk c > 0, a multiple of `mark`.  c / mark whole marks of the sequence's rows lie before it, so
+// that no two sequences meet in a place, and N / (64 mark) places a key head are enough however many sequences there are.
+__device__ __forceinline__ int64_t mark_at(const Walk &a, const Part &p, int c) {
+    return (p.row0 / (kC * a.mark) + c / a.mark - 1) * a.Hkv + p.kvh;
 }
 
 // A sum over the lanes up to each, in fp64.

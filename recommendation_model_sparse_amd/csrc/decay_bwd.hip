@@ -82,7 +82,7 @@ __global__ __launch_bounds__(Of<LP>::WAVES * 128, LP == 32 ? 3 : 4) void k_decay
     // The pairs across the beginning of chunk c, in the state that the chunks from it on have left.
     const auto begin_anew = [&](int c) {
         if (team) {
-            const float *at = a.marks + ((p.row0 / (kC * a.mark) + p.b + c / a.mark) * a.Hkv + p.kvh) * (LP * LP) + 4 * (tid - TEAM);
+            const float *at = a.marks + mark_at(a, p, c) * (LP * LP) + 4 * (tid - TEAM);
             double sum = 0.0;
 #pragma unroll
             for (int ct = 0; ct < O::CT; ++ct) {
@@ -214,7 +214,7 @@ Room room_of(Walk a, const Cut &c) {
     a.slots = static_cast<uint32_t>(c.slots);
     const size_t lp = padded(a.d);
     return Room{states_bytes(a, c), order_bytes(a, c), whole(8 * static_cast<size_t>(a.N) * a.Hkv * splits_of(a, true)),
-                4 * lp * lp * a.Hkv * static_cast<size_t>(slot_count(a.N, a.B, kC * mark_of(c, a.g_row == 0))),
+                4 * lp * lp * a.Hkv * static_cast<size_t>(a.N / (kC * mark_of(c, a.g_row == 0))),
                 whole(8 * static_cast<size_t>(c.slots) * a.Hkv)};
 }
 

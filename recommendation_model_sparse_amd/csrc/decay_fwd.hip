@@ -170,7 +170,7 @@ __global__ __launch_bounds__(Of<LP>::WAVES * 64, LP == 128 ? (GRAD ? 2 : 4) : LP
         float term = 0.f, pairs = 0.f;
         if constexpr (MORE) {
             if (c > 0 && c % a.mark == 0 && p.split == 0) {
-                float *at = a.marks + ((p.row0 / (kC * a.mark) + p.b + c / a.mark) * a.Hkv + p.kvh) * (LP * LP) + 4 * tid;
+                float *at = a.marks + mark_at(a, p, c) * (LP * LP) + 4 * tid;
 #pragma unroll
                 for (int ct = 0; ct < O::CT; ++ct) *(DLRM_GLOBAL floatx4 *)(at + ct * 4 * THREADS) = S[ct];
             }

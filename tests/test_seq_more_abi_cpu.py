@@ -164,6 +164,17 @@ def test_decay_refuses_outputs(L):
     assert L.dlrm_seq_decay_step(ctypes.byref(many), FAKE, FAKE, None) == UNSUPPORTED
 
 
+@pytest.mark.parametrize("B,each_len", [(65536, 64), (200000, 8)])
+@pytest.mark.parametrize("each", [True, False])
+def test_backward_workspace_of_many_short_sequences(L, B, each_len, each):
+    """States at marks (64 d d bytes for 512 events of a key head, or 128 with one decay a head) go by the rows, not by the
+    sequences; beside them two floats an event and what goes by the sequences, an order and a sum each."""
+    N, H, d = B * each_len, 4, 128
+    a = decay(B=B, N=N, Hq=H, Hkv=H, d=d, max_len=each_len, q_row=H * d, q_head=d, k_row=H * d, k_head=d, v_row=H * d, v_head=d, g_row=H if each else 0)
+    size = L.dlrm_seq_decay_bwd_workspace_size(ctypes.byref(a))
+    assert 0 < size <= 4 * d * d * H * (N // (512 if each else 128)) + 8 * N * H + 12 * B * H + 4096
+
+
 def test_nothing_to_do(L):
     assert L.dlrm_seq_decay_fwd(ctypes.byref(decay(B=0, N=0)), None, None, None, None, 0, None) == OK
     assert L.dlrm_seq_decay_step(ctypes.byref(decay(B=0, N=0)), None, None, None) == OK
