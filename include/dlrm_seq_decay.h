@@ -35,8 +35,9 @@ extern "C" {
  *   offsets    [B+1] int64 (DLRM_INDEX_I64) or int32, non-decreasing, within [0, N].  Offsets
  *              outside are brought inside: no foreign memory is read.  Not read by the step.
  *   max_len    an upper bound of the sequences' lengths, by which a call chooses whether to cut
- *              sequences into runs that are worked on side by side; N where it is not known.
- *              Longer sequences give results as exact, slower.  (The bits may differ with it, and with
+ *              sequences into runs that are worked on side by side, with a state for each in the workspace (up to
+ *              256 MB, or as much as q, k, v and o take); N where it is not known: one sequence may then be
+ *              all of them, and batches of short ones are slower.  Longer sequences give results as exact, slower.  (The bits may differ with it, and with
  *              the number of sequences and rows.)
  *   q, k, v    bf16; element e of head h of row r at r * row_stride + h * head_stride + e, strides
  *              in elements, multiples of 8, >= d; 16-byte aligned

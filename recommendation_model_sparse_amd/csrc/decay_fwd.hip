@@ -69,6 +69,10 @@ static int splits_for(int64_t workgroups, int group, int places) {
 // takes 1 for each 16 runs of the longest sequence, and the two launches 2.  Of the runs of 1 to 8 and 16 chunks and none, on
 // 17 shapes forward and backward (1 to 1024 sequences of 1 to 8192, heads of 32, 64, 128, groups of 1 to 16), this choice
 // was 0.5 % slower than the best in the mean, 9 % at worst.
+// The states of the runs, one a sequence among them, are held to what the rows of q, k, v and o take, or to what the 256 MB behind
+// the L2s hold: with an unknown longest history the time alone would cut any batch, as one sequence might be all of it (20000
+// histories of 60 events, 4 heads of 128, are left whole, where runs would take 5.4 GB of states beside 4.9 GB of rows; of 1 to 120,
+// 0.49 million events: 2693 -> 1153 us, the backward 9980 -> 6584).
 Cut cut_of(const Walk &a, int64_t max_len, bool back) {
     const int64_t longest = (std::min(max_len, a.N) + kC - 1) / kC;
     const int places = places_of(a.d, back);
@@ -81,13 +85,15 @@ Cut cut_of(const Walk &a, int64_t max_len, bool back) {
         if (!run) return std::max(own + 2, shared);
         return (groups <= places ? own + 2 : shared + 0.75 * own) + 2 + (longest / run + 15) / 16;
     };
+    const int64_t room = std::max(int64_t(1) << 28, 4 * a.N * a.d * (a.Hq + a.Hkv));
+    const auto fits = [&](int64_t run) { return slot_count(a.N, a.B, kC * static_cast<int>(run)) * a.Hkv <= room / (4 * a.d * a.d); };
     Cut c = {};
     double least = time_of(0);
     const bool many = a.B * static_cast<int64_t>(a.Hkv) * 64 >= (int64_t(1) << 24);  // more than a launch of k_decay_join holds
     // (from 8 on, multiples of 8: the marks are that far apart)
     for (int64_t run = 1; run < longest && run <= kMostChunks && !many; run += run < 8 ? 1 : run) {
         const double t = time_of(run);
-        if (t < least) least = t, c.run = static_cast<int32_t>(run);
+        if (t < least && fits(run)) least = t, c.run = static_cast<int32_t>(run);
     }
     c.slots = c.run ? slot_count(a.N, a.B, kC * c.run) : a.B;
     // the longest first: with 1024 sequences of 16 to 512, 2 heads of 64, 42 us instead of 56, the backward 143 instead of 202

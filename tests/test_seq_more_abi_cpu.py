@@ -175,6 +175,20 @@ def test_backward_workspace_of_many_short_sequences(L, B, each_len, each):
     assert 0 < size <= 4 * d * d * H * (N // (512 if each else 128)) + 8 * N * H + 12 * B * H + 4096
 
 
+@pytest.mark.parametrize("B,each_len,H,d", [(20000, 60, 4, 128), (65536, 64, 4, 128), (200000, 8, 4, 128), (1024, 256, 4, 128), (4096, 30, 16, 64), (3000, 100, 32, 96)])
+def test_workspace_where_the_longest_is_not_known(L, B, each_len, H, d):
+    """Told that one of many sequences may be all rows, a call keeps its runs' states, each direction's, to 256 MB or to the rows of
+    q, k, v and o (with a float a state beside); the backward's marks, terms, order and sums come on top."""
+    N = B * each_len
+    rows = max(1 << 28, 8 * N * H * d)
+    for g_row in (0, H):
+        a = decay(B=B, N=N, Hq=H, Hkv=H, d=d, max_len=N, q_row=H * d, q_head=d, k_row=H * d, k_head=d, v_row=H * d, v_head=d, g_row=g_row)
+        states = rows + rows // (d * d) + 4096
+        assert 0 < L.dlrm_seq_decay_fwd_workspace_size(ctypes.byref(a)) <= states
+        marks = 4 * 128 * 128 * H * (N // 64)  # one a chunk at most
+        assert 0 < L.dlrm_seq_decay_bwd_workspace_size(ctypes.byref(a)) <= 2 * states + marks + 8 * N * H + 8 * H * (N // 64 + B) + 4 * B + 4096
+
+
 def test_nothing_to_do(L):
     assert L.dlrm_seq_decay_fwd(ctypes.byref(decay(B=0, N=0)), None, None, None, None, 0, None) == OK
     assert L.dlrm_seq_decay_step(ctypes.byref(decay(B=0, N=0)), None, None, None) == OK
