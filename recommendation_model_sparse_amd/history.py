@@ -26,6 +26,7 @@ of each head's output: what they keep of a user is one d x d state a key head, h
 """
 from __future__ import annotations
 
+import contextlib
 from dataclasses import dataclass
 from typing import Dict, List, Optional, Tuple
 
@@ -218,11 +219,28 @@ class HistoryEncoder:
 
 
 class _States:
-    """The states of `users` histories in the linear layers, and what both caches do with them."""
+    """The states of `users` histories in the linear layers, and what both caches do with them.
+
+    A visit updates states layer by layer, in place.  Where it ends half way (no memory for a layer, for instance), its
+    users' histories are neither with its events nor without: `torn` says whose, and until they have left every visit is refused."""
 
     def __init__(self, enc: HistoryEncoder, users: int):
         self.enc, self.users = enc, users
+        self.torn = np.zeros(users, bool)
         self.state = [torch.zeros((users, enc.c.Hkv, enc.d, enc.d), device=enc.dev) for _ in range(enc.c.linear)]
+
+    def _whole(self):
+        if self.torn.any():
+            raise RuntimeError(f"a visit of users {np.flatnonzero(self.torn).tolist()} ended half way: their histories cannot be used")
+
+    @contextlib.contextmanager
+    def _half_way(self, users):
+        """What changes the histories of `users` (a mask) bit by bit."""
+        try:
+            yield
+        except BaseException:
+            self.torn |= users
+            raise
 
     def _linear(self, i, layer, q, k, v, offsets, longest_new):
         """New events (offsets None: one of each user) through linear layer i."""
@@ -275,16 +293,18 @@ class HistoryCache(_States):
         """Encodes the users' new events (jagged, offsets [users + 1], at most longest_new each) against
         what the cache holds; returns each user's vector [users, D] (zeros for a user with no new event).
         The lengths are checked on the host, which waits for the device once: a count past longest_new or a
-        region's end would be written into the next user's."""
+        region's end would be written into the next user's.  (A visit that ends half way can be made again, but with linear
+        layers: then the cache refuses any further one.)"""
+        self._whole()
         offsets, count, (held,) = self._offsets(ids, offsets, longest_new, self.end - self.begin)
         longest = int((held + count).max(initial=0))
         if longest > self.capacity:
             raise ValueError(f"a history of {longest} events does not fit a capacity of {self.capacity}")
         if ids.numel() == 0:
             return torch.zeros((self.users, self.enc.c.D), dtype=torch.bfloat16, device=self.enc.dev)
-        enc, count = self.enc, offsets.diff()
+        enc, fresh, count = self.enc, count > 0, offsets.diff()
         at = torch.arange(ids.numel(), device=enc.dev) + torch.repeat_interleave(self.end - offsets[:-1], count, output_size=ids.numel())
-        end = self.end + count
+        end, events = self.end + count, enc._events(ids)
 
         def attend(i, layer, q, k, v):
             if "g" in layer:
@@ -292,17 +312,22 @@ class HistoryCache(_States):
             self.k[i][at], self.v[i][at] = k, v
             return L.dlrm_seq_attn_fwd(q, self.k[i], self.v[i], offsets, (self.begin, end), **enc._how(layer)), None
 
-        x, s, _ = enc._layers(enc._events(ids), attend)
+        with self._half_way(fresh & bool(self.state)):
+            x, s, _ = enc._layers(events, attend)
+            users = self._users(x, s, offsets)
         self.end, self.longest = end, longest
-        return self._users(x, s, offsets)
+        return users
 
     def append(self, ids: torch.Tensor, eight_bit: bool = False):
         """One new event of every user; returns their vectors [users, D] bf16, or with eight_bit 8-bit
         rows and their scales [users]."""
+        self._whole()
         if self.longest + 1 > self.capacity:
             raise ValueError(f"the cache holds {self.capacity} events a user")
+        if ids.shape != (self.users,):
+            raise ValueError(f"ids must be one event of each of {self.users} users, got {tuple(ids.shape)}")
         enc, at = self.enc, self.end
-        end = at + 1
+        end, events = at + 1, enc._events(ids)
 
         def attend(i, layer, q, k, v):
             if "g" in layer:
@@ -311,15 +336,18 @@ class HistoryCache(_States):
             return L.dlrm_seq_attn_decode(q, self.k[i], self.v[i], self.begin, end, max_kv_len=self.longest + 1,
                                           **enc._how(layer)), None
 
-        x, s, _ = enc._layers(enc._events(ids), attend)
+        with self._half_way(np.full(self.users, bool(self.state))):
+            x, s, _ = enc._layers(events, attend)
+            users = self._appended(x, s, eight_bit)
         self.end, self.longest = end, self.longest + 1
-        return self._appended(x, s, eight_bit)
+        return users
 
 
 class PagedHistoryCache(_States):
     """Keys and values of `users` histories of up to `longest` events in a pool of `pages` pages of `page` events each,
     which the users share: a history takes the pages that it fills, and gives them back when its user leaves.
-    The host knows the histories' lengths, so that a call that does not fit is refused before anything changes."""
+    The host knows the histories' lengths, so that a call that does not fit is refused before anything changes.  Events are
+    counted before the layers write their rows: users whose visit ends half way have to leave (`release`)."""
 
     def __init__(self, enc: HistoryEncoder, users: int, longest: int, pages: int, page: int = 64):
         super().__init__(enc, users)
@@ -349,23 +377,27 @@ class PagedHistoryCache(_States):
         return slots
 
     def release(self, users) -> None:
-        """Users (their numbers) leave: their pages go back, and they are without a history."""
+        """Users (their numbers) leave: their pages go back, and they are without a history, also those whose last visit
+        ended half way."""
         leave, users = np.zeros(self.users, bool), np.asarray(users, np.int64)
         if ((users < 0) | (users >= self.users)).any():
             raise ValueError(f"users must be 0 to {self.users - 1}, got {users}")
         leave[users] = True
         none = torch.zeros(self.users + 1, dtype=torch.int64, device=self.enc.dev)
-        self._update(np.zeros(self.users, np.int64), none, 0, leave)
-        for state in self.state:
-            state[torch.from_numpy(leave).to(self.enc.dev)] = 0
+        with self._half_way(leave):
+            self._update(np.zeros(self.users, np.int64), none, 0, leave)
+            for state in self.state:
+                state[torch.from_numpy(leave).to(self.enc.dev)] = 0
+        self.torn &= ~leave
 
     def prefill(self, ids: torch.Tensor, offsets: torch.Tensor, longest_new: int) -> torch.Tensor:
         """HistoryCache.prefill, over the pages."""
+        self._whole()
         enc = self.enc
         offsets, count, _ = self._offsets(ids, offsets, longest_new)
         if ids.numel() == 0:
             return torch.zeros((self.users, enc.c.D), dtype=torch.bfloat16, device=enc.dev)
-        slots = self._update(count, offsets, ids.numel())
+        events, slots = enc._events(ids), self._update(count, offsets, ids.numel())
 
         def attend(i, layer, q, k, v):
             if "g" in layer:
@@ -373,16 +405,18 @@ class PagedHistoryCache(_States):
             L.dlrm_seq_pages_write(k, v, slots, self.k[i], self.v[i])
             return L.dlrm_seq_attn_paged_fwd(q, self.k[i], self.v[i], offsets, self.table, self.lengths, self.page, **enc._how(layer)), None
 
-        x, s, _ = enc._layers(enc._events(ids), attend)
-        return self._users(x, s, offsets)
+        with self._half_way(count > 0):
+            x, s, _ = enc._layers(events, attend)
+            return self._users(x, s, offsets)
 
     def append(self, ids: torch.Tensor, eight_bit: bool = False):
         """HistoryCache.append, over the pages."""
+        self._whole()
         enc = self.enc
         if ids.shape != (self.users,):
             raise ValueError(f"ids must be one event of each of {self.users} users, got {tuple(ids.shape)}")
         one = torch.arange(self.users + 1, dtype=torch.int64, device=enc.dev)
-        slots = self._update(np.ones(self.users, np.int64), one, self.users)
+        events, slots = enc._events(ids), self._update(np.ones(self.users, np.int64), one, self.users)
         longest = int(self.held.max(initial=0))
 
         def attend(i, layer, q, k, v):
@@ -392,8 +426,9 @@ class PagedHistoryCache(_States):
             return L.dlrm_seq_attn_paged_decode(q, self.k[i], self.v[i], self.table, self.lengths, self.page, max_kv_len=longest,
                                                 **enc._how(layer)), None
 
-        x, s, _ = enc._layers(enc._events(ids), attend)
-        return self._appended(x, s, eight_bit)
+        with self._half_way(np.ones(self.users, bool)):
+            x, s, _ = enc._layers(events, attend)
+            return self._appended(x, s, eight_bit)
 
 
 def main(steps: int = 800, users: int = 256, seed: int = 0) -> Tuple[float, float]:

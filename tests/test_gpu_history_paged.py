@@ -11,7 +11,7 @@ import numpy as np
 import pytest
 import torch
 
-from recommendation_model_sparse_amd import dlrm_bce_head, dlrm_dropout
+from recommendation_model_sparse_amd import binding, dlrm_bce_head, dlrm_dropout
 from recommendation_model_sparse_amd.history import HistoryEncoder, Shape
 
 from gpu_util import DEV, say
@@ -242,6 +242,68 @@ def test_what_does_not_fit_is_refused_before_anything_changes():
         cache.append(ids[:3])
     with pytest.raises(ValueError):
         HistoryEncoder(Shape(events=5, D=64, layers=1, linear=2), DEV)
+
+
+@pytest.mark.parametrize("call", ["prefill", "append"])
+@pytest.mark.parametrize("linear", [0, 1])
+@pytest.mark.parametrize("paged", [True, False])
+def test_a_visit_that_ends_half_way(monkeypatch, paged, linear, call):
+    """A layer that cannot go on: what has come to be part of a history is not served.  Over pages, users leave and begin anew, the
+    others go on; regions without linear layers hold what they held, and the visit can be made again."""
+    rng = np.random.default_rng(28)
+    enc = encoder(linear=linear)
+    make = lambda: enc.paged_cache(3, 64, 12, 16) if paged else enc.cache(3, 64)  # noqa: E731
+    cache, fresh = make(), make()
+    for c in (cache, fresh):
+        c.prefill(*visit(np.random.default_rng(1), [20, 0, 33]), 33)
+    counts = [5, 0, 7] if call == "prefill" else [1, 1, 1]
+    ids, off = visit(rng, counts)
+    go = (lambda c: c.prefill(ids, off, 7)) if call == "prefill" else (lambda c: c.append(ids))
+    calls = 0
+
+    def fails(*a, real=binding.dlrm_linear_fwd, **k):
+        nonlocal calls
+        calls += 1
+        if calls == 7:  # in the second layer, past its attention
+            raise MemoryError("of a test")
+        return real(*a, **k)
+
+    with monkeypatch.context() as m:
+        m.setattr(binding, "dlrm_linear_fwd", fails)
+        with pytest.raises(MemoryError):
+            go(cache)
+    say(f"[history] half way: paged {paged} linear {linear} {call}")
+    if not paged and not linear:
+        assert torch.equal(go(cache), go(fresh)) and torch.equal(cache.end, fresh.end)
+        return
+    for again in (go, lambda c: c.append(ids[:1].expand(3).contiguous()), lambda c: c.prefill(*visit(rng, [0, 0, 0]), 1)):
+        with pytest.raises(RuntimeError):
+            again(cache)
+    if not paged:
+        return
+    left = [i for i in range(3) if counts[i]]
+    cache.release(left[:-1])
+    with pytest.raises(RuntimeError):
+        go(cache)
+    cache.release(left[-1:])
+    fresh.release(left)
+    for c in (cache, fresh):
+        assert c.lengths.tolist() == [0 if n else h for n, h in zip(counts, [20, 0, 33])]
+    assert torch.equal(go(cache), go(fresh)) and torch.equal(cache.lengths, fresh.lengths) and cache.held.tolist() == fresh.held.tolist()
+
+
+@pytest.mark.parametrize("linear", [0, 1])
+@pytest.mark.parametrize("paged", [True, False])
+def test_what_is_refused_leaves_the_cache_as_it_is(paged, linear):
+    """Ids that cannot be, and too few of them: no history changes, and the next visit is served."""
+    enc, rng = encoder(linear=linear), np.random.default_rng(30)
+    cache = enc.paged_cache(3, 64, 12, 16) if paged else enc.cache(3, 64)
+    ids, off = visit(rng, [4, 2, 9])
+    for call in (lambda: cache.append(ids[:2]), lambda: cache.append(ids[:3].float()), lambda: cache.prefill(ids.float(), off, 9), lambda: cache.prefill(ids, off, 8)):
+        with pytest.raises((ValueError, TypeError)):
+            call()
+    other = enc.paged_cache(3, 64, 12, 16) if paged else enc.cache(3, 64)
+    assert torch.equal(cache.prefill(ids, off, 9), other.prefill(ids, off, 9)) and torch.equal(cache.append(ids[:3]), other.append(ids[:3]))
 
 
 def test_linear_layers_alone_keep_no_rows():
