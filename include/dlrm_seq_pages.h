@@ -50,8 +50,10 @@ size_t dlrm_seq_pages_update_workspace_size(int64_t B, int64_t N);
  *   slots    [N] int64: new event i of user b, row offsets[b] + i, gets the pool's row; -1 where the
  *            user is refused; rows outside every user's are not written
  *   refused  [1] int32: how many users were refused: those whose events do not fit their table, and those
- *            for whom, with all before them, there are not enough pages.  Nothing changes for such a user
- *            (who may have left), and none of the others waits for it.
+ *            for whom, with all that the users before them want, there are not enough pages: from the first
+ *            such user on everyone who wants a page, also where fewer would do and are there.  Those who want
+ *            none get their slots, and a user whose table is too short takes no part in the sum.  Nothing
+ *            changes for a refused user (who may have left).
  *
  * The order is that of the users: pages that come back are put on the stack first to last (a user's in
  * the table's order), pages are taken from its top, the first user's first page first.

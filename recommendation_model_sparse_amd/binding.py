@@ -1116,7 +1116,7 @@ def dlrm_seq_pages_update(table: torch.Tensor, lengths: torch.Tensor, free: torc
     """(slots [n] int64, refused [1] int32): users who leave give their pages back, new events get theirs
     (C: dlrm_seq_pages_update).  table [users, width], lengths [users], free [pages], free_count [1], all int32, are
     updated in place; offsets [users+1] of the new events, n at least their last; leave [users] bool.  A refused
-    user's slots are -1."""
+    user's slots are -1; behind one for whom the pool is too small everyone who wants a page is refused."""
     _offsets(offsets, "offsets")
     free = _need(free, "free", torch.int32)
     _is(free_count, "free_count", torch.int32, (1,))

@@ -73,6 +73,22 @@ def test_visits(B, page, width, pages, most, itype):
     assert total
 
 
+@pytest.mark.parametrize("others", [0, 1100])
+def test_whom_a_refused_user_refuses(others):
+    """By hand, of a pool of four pages of 8: one user gets its page, one's table is too short, one wants 13 pages; the next
+    wants one, which is there, and is refused with it; the last one's events fit the page that it holds."""
+    B = others + 5
+    held, counts = np.zeros(B, np.int64), np.zeros(B, np.int64)
+    held[-1], counts[-5:] = 3, [1, 200, 100, 8, 2]
+    say(f"[pages] whom a refused user refuses, {B} users")
+    pool, where = visit(new_pool(B, 16, 4), 8, offsets(held), 3, None)
+    assert pool[0][-1, 0] == 3 and pool[3] == 3
+    pool, where = visit(pool, 8, offsets(counts), 311, None, where)
+    table, lengths, _, count = (x.cpu().numpy() for x in where)
+    assert lengths[-5:].tolist() == [1, 0, 0, 0, 5] and not lengths[:-5].any() and count[0] == 2
+    assert table[-5:, 0].tolist() == [2, -1, -1, -1, 3]
+
+
 def test_slots_outside_the_users_are_left():
     """Offsets that begin past 0 and end before n."""
     pool = new_pool(3, 4, 12)
