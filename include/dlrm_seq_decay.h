@@ -13,8 +13,10 @@
  * Conventions: as dlrm_seq.h (jagged sequences laid end to end with CSR offsets; bf16 activations
  * as uint16_t; caller-owned buffers; nothing allocated; arguments validated before anything is
  * enqueued; bitwise reproducible).  States, decays, their gradients and all sums are fp32 (sums of
- * decays fp64).  Forward, backward and the single event hold the states' values to about 2^-22:
- * where a product takes them as bf16, it takes three such parts, unless a comment says otherwise.
+ * decays fp64), and state_out, the single event's state and dg are right to about 2^-22 of their terms: where a
+ * product takes bf16, it takes three such parts of a state.  Where only o, or dq, dk and dv of a call without dg, come of
+ * a state, two parts of what is added to it are taken (2^-16), and the state's product with a row from its values
+ * rounded to bf16 once (2^-8, as the outputs are).
  */
 #ifndef DLRM_SEQ_DECAY_H
 #define DLRM_SEQ_DECAY_H
@@ -70,7 +72,9 @@ size_t dlrm_seq_decay_fwd_workspace_size(const dlrm_seq_decay *a);
  *              A sequence without events leaves its state as it is.
  *   What an event holds has no effect on the outputs before it, NaN and infinities included; after it,
  *   what they reach is not finite.  o takes the products within 64 events, and the state's with q,
- *   from values rounded to bf16.
+ *   from values rounded to bf16.  (In place, the query heads of a group are not spread over workgroups while sequences
+ *   are whole, and their first states are copied where they are cut: 4 sequences of up to 60, 16 heads over 2 of 128, 25 us
+ *   where 14 apart.)
  */
 int dlrm_seq_decay_fwd(const dlrm_seq_decay *a, const float *state_in, float *state_out, uint16_t *o,
                        void *workspace, size_t workspace_bytes, dlrm_stream_t stream);
@@ -90,7 +94,9 @@ size_t dlrm_seq_decay_bwd_workspace_size(const dlrm_seq_decay *a);
  *   dg   [N][Hkv] fp32 (rows outside every sequence are not written), [Hkv] where g_row == 0, or NULL:
  *        not wanted
  *   Infinities and NaN in k and v have no effect on dq before them; those of q and dout reach dk and
- *   dv of the events near by; dg of a sequence that holds any means nothing (nor does that of a head).
+ *   dv of all events before them, and of up to 63 after them too; dg of a sequence that holds any means nothing (nor
+ *   does that of a head).
+ *   Without dg there is less to do, and dq, dk and dv come of less exact states (see above).
  */
 int dlrm_seq_decay_bwd(const dlrm_seq_decay *a, const uint16_t *dout, uint16_t *dq, uint16_t *dk,
                        uint16_t *dv, float *dg, void *workspace, size_t workspace_bytes,

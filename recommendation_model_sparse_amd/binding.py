@@ -1258,7 +1258,7 @@ def dlrm_seq_decay_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
                        dq: Optional[torch.Tensor] = None, dk: Optional[torch.Tensor] = None, dv: Optional[torch.Tensor] = None,
                        dg: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
     """(dq, dk, dv, dg or None) of dlrm_seq_decay_fwd without states (C: dlrm_seq_decay_bwd); dg has g's shape, and is
-    left out without want_dg, at less work."""
+    left out without want_dg, which takes 0.7 to 1 of the time (the most for heads above 64 cut into runs)."""
     _offsets(offsets, "offsets")
     B = offsets.numel() - 1
     a, dev, qs, Hkv = _seq_decay(q, k, v, g, offsets, B, scale, max_len)
