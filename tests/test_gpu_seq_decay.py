@@ -19,7 +19,7 @@ import pytest
 import torch
 
 from oracle import decay as oracle
-from recommendation_model_sparse_amd import (dlrm_seq_decay_bwd, dlrm_seq_decay_fwd, dlrm_seq_decay_step, synth)
+from recommendation_model_sparse_amd import (binding, dlrm_seq_decay_bwd, dlrm_seq_decay_fwd, dlrm_seq_decay_step, synth)
 
 from gpu_util import DEV, rel_err, say, to_dev
 
@@ -474,3 +474,57 @@ def test_offsets_that_are_out_of_order():
         dlrm_seq_decay_bwd(do, q, k, v, g, to_dev(np.array(off, np.int64)))
         torch.cuda.synchronize()
         assert (guard[:64] == 3).all() and (guard[N + 64:] == 3).all()
+
+
+def guarded(bytes_, fill):
+    """(a buffer's bytes between 4096 of `fill` on either side, what says whether those are as they were); 256-byte aligned."""
+    whole = torch.full((bytes_ + 2 * 4096,), fill, dtype=torch.uint8, device=DEV)
+    return whole[4096:4096 + bytes_], lambda: bool((whole[:4096] == fill).all() and (whole[4096 + bytes_:] == fill).all())
+
+
+@pytest.mark.parametrize("N,d,Hq,Hkv", [(200, 32, 1, 1), (200, 128, 4, 2), (3000, 32, 2, 1), (3000, 128, 2, 2)])
+@pytest.mark.parametrize("each", [True, False])
+def test_offsets_that_are_out_of_order_write_nothing_outside(N, d, Hq, Hkv, each):
+    """Of outputs, gradients, states and workspaces, whole sequences and runs of several chunks: each lies between guards."""
+    rng = rng_of("decay-guards", N, d)
+    q, k, v, do = (bf16(rng, N, h, d)[0] for h in (Hq, Hkv, Hkv, Hq))
+    g = to_dev(decays(rng, N, Hkv, each))
+    first = to_dev(rng.standard_normal((3, Hkv, d, d)).astype(np.float32))
+    say(f"[decay] guards N={N} d={d} each={each}")
+    for off in ([0, N + 100, N // 2, N], [-5, N // 4, 1 << 40, N // 3], [N, N // 2, 0, 0], [10, 10, 10, -1], [N // 2, N, 0, N - 1]):
+        off = to_dev(np.array(off, np.int64))
+        for longest in (1, None):
+            desc = binding._seq_decay(q, k, v, g, off, 3, None, longest)[0]
+            sizes = [binding.lib().dlrm_seq_decay_fwd_workspace_size(desc), binding.lib().dlrm_seq_decay_bwd_workspace_size(desc)]
+            assert (sizes[0] > 256) == (N > 200 and longest is None)  # cut into runs
+            spaces = [guarded(n, 0x11) for n in sizes]
+            outs = [guarded(2 * t.numel(), 0x22) for t in (q, q, k, v)] + [guarded(4 * g.numel(), 0x22), guarded(4 * first.numel(), 0x22)]
+            o, dq, dk, dv = (x[0].view(torch.bfloat16).view(t.shape) for x, t in zip(outs, (q, q, k, v)))
+            dg, state = outs[4][0].view(torch.float32).view(g.shape), outs[5][0].view(torch.float32).view(first.shape)
+            state.copy_(first)
+            dlrm_seq_decay_fwd(q, k, v, g, off, state=state, state_out=state, max_len=longest, out=o, workspace=spaces[0][0])
+            dlrm_seq_decay_bwd(do, q, k, v, g, off, max_len=longest, dq=dq, dk=dk, dv=dv, dg=dg, workspace=spaces[1][0])
+            torch.cuda.synchronize()
+            assert all(left() for _, left in spaces + outs), longest
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,d", [([0, 1500, 0, 5], 8, 2, 64), ([5, 0, 2000, 0, 700, 0], 2, 2, 128), ([0, 0, 4000], 4, 1, 32)])
+def test_states_in_place_where_sequences_are_cut(lens, Hq, Hkv, d):
+    """Empty ones among them keep their states; the rest as apart from the first states, bit by bit, and as in fp64."""
+    rng = rng_of("decay-in-place", *lens)
+    off, dev, (q, k, v), g, _ = problem(rng, lens, Hq, Hkv, d)
+    first = rng.standard_normal((len(lens), Hkv, d, d)).astype(np.float32)
+    ref = oracle.decay(q, k, v, g.astype(np.float64), off, float(np.float32(d ** -0.5)), first.astype(np.float64))
+    gate, own, off_d = gates(max(lens), d), to_dev(first), to_dev(off)
+    assert binding.lib().dlrm_seq_decay_fwd_workspace_size(binding._seq_decay(*dev, to_dev(g), off_d, len(lens), None, max(lens))[0]) > 4096
+    say(f"[decay] in place, cut: {lens} d={d}")
+    for _ in range(2):
+        apart = dlrm_seq_decay_fwd(*dev, to_dev(g), off_d, state=to_dev(first), want_state=True, max_len=max(lens))
+        own.copy_(to_dev(first))
+        o, last = dlrm_seq_decay_fwd(*dev, to_dev(g), off_d, state=own, state_out=own, max_len=max(lens))
+        torch.cuda.synchronize()
+        assert last is own and torch.equal(o, apart[0]) and torch.equal(own, apart[1])
+    assert rel_err(host(o), ref["o"], ref["o_s"]) <= gate["bf16"]
+    assert rel_err(own.cpu().numpy().astype(np.float64), ref["state"], ref["state_s"]) <= gate["state"]
+    for b, n in enumerate(lens):
+        assert n or np.array_equal(own[b].cpu().numpy(), first[b])
