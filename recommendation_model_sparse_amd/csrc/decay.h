@@ -20,11 +20,17 @@
 // 32x32x16, half as many wavefronts waited twice as long: a chunk of heads of 128 took 8100 cycles of a workgroup
 // by itself, of 64 7200.)
 //
-// A chunk takes 64 d (64 + 2 d) multiply-adds a head, so the rows' bytes are the floor: 291 MB forward and backward for 1024 sequences of 16 to 512, 2 heads of 64, 60 us at the rate of a large copy.  They take 178: o 38 (3.8 TB/s),
-// dq 61, dk and dv 94, with a gradient of each event's decay.  There the VALU is busy for half of the time (states
-// split into bf16 parts, pairs weighed and packed), LDS for 34 to 43 %, the matrix instructions for 11 to 18 %, at 2.3 to 2.9
-// wavefronts a SIMD.  4 sequences of 2000 to 4096, 8 heads of 128 over 2, take 163 of which 40 are the states at the
-// runs' starts; the walks have one or two workgroups a CU there and wait for their own barriers.
+// Pairs' weights, and states on their way to an output, are rounded to bf16, as the matrix instructions take it (three parts
+// of a weight would be three products): outputs are 2.3e-3 from the formula in 64 bits, of which their own rounding is 1.6e-3.
+//
+// A chunk takes 64 d (64 + 2 d) multiply-adds a head, so the rows' bytes are the floor: 291 MB forward and backward for 1024
+// sequences of 16 to 512, 2 heads of 64, 60 us at the rate of a large copy.  The two calls take 183 us.  Their kernels, by the
+// profiler, under which they take longer: o 38 (3.8 TB/s), dq 61, dk and dv 94, with a gradient of each event's decay, and
+// twice 5 for the order, 203.  There the VALU is busy for half of the time (states split into bf16 parts, pairs weighed and
+// packed, and scalar registers spilled to its own: 56 to 87 in the forward walks, 32 to 44 in those back with dg), LDS for 34 to
+// 43 %, the matrix instructions for 11 to 18 %, at 2.3 to 2.9 wavefronts a SIMD.  4 sequences of 2000 to 4096, 8 heads of 128 over 2,
+// take 167, by the profiler 173 of which 47 are the states at the runs' starts; the walks have one or two workgroups a CU there and
+// wait for their own barriers.
 #pragma once
 
 #include "dlrm_seq_decay.h"

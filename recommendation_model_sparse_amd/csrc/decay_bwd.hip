@@ -25,8 +25,9 @@ namespace {
 //
 // Both teams share the tiles of k, v, q and do (one read of each from memory), the decays and the ten tiles of pairs: each
 // <k, q> and <v, do> is worked out once.  LDS holds two workgroups a CU of heads of 64, one of 128, and registers four
-// wavefronts a SIMD.  UP, PR: as in the forward walk.
-// Measured: 1024 sequences of 16 to 512, 2 heads of 64, 94 us: VALU 54 %, LDS 37 %, MFMA 18 %, 2.4 TB/s; 4 of 2000 to 4096, 8
+// wavefronts a SIMD.  UP, PR: as in the forward walk.  Heads of 128 spill 4 vector registers with dg, 20 bytes of scratch a lane, and
+// 288 without, 388 bytes: 65 us where 55 with dg, for the 4 sequences below (the whole backward 117 and 124).
+// Measured, by the profiler: 1024 sequences of 16 to 512, 2 heads of 64, 94 us: VALU 54 %, LDS 37 %, MFMA 18 %, 2.4 TB/s; 4 of 2000 to 4096, 8
 // heads of 128 over 2 in runs of two chunks, 56 us: 28, 23, 18 %, one workgroup a CU.
 template <int LP, int UP, int PR, int GRAD>
 __global__ __launch_bounds__(Of<LP>::WAVES * 128, LP == 32 ? 3 : 4) void k_decay_back(const Walk a) {

@@ -68,7 +68,7 @@ static int splits_for(int64_t workgroups, int group, int places) {
 // the places wait for others, and the last of them ends three quarters of its own time after the mean; joining the states
 // takes 1 for each 16 runs of the longest sequence, and the two launches 2.  Of the runs of 1 to 8 and 16 chunks and none, on
 // 17 shapes forward and backward (1 to 1024 sequences of 1 to 8192, heads of 32, 64, 128, groups of 1 to 16), this choice
-// was 0.5 % slower than the best in the mean, 9 % at worst.
+// was 0.4 % slower than the best in the mean, 10 % at worst.
 // The states of the runs, one a sequence among them, are held to what the rows of q, k, v and o take, or to what the 256 MB behind
 // the L2s hold: with an unknown longest history the time alone would cut any batch, as one sequence might be all of it (20000
 // histories of 60 events, 4 heads of 128, are left whole, where runs would take 5.4 GB of states beside 4.9 GB of rows; of 1 to 120,
@@ -117,8 +117,8 @@ namespace {
 // outputs take it rounded (PR 1), but dg's terms are fp32's.  (Two parts with dg: 4 % faster, and dg 3e-6 off instead of 4e-7.)
 // A head is three steps between barriers: tiles to LDS; pairs, and what comes through the state, with the next rows under
 // way; what comes through the pairs.  The registers leave room for as many workgroups as LDS does: heads of 64 four a CU,
-// three with dg.
-// Measured: heads of 64, 1024 sequences of 16 to 512, 2 heads: o 38 us, 3.8 TB/s; dq 61.  Heads of 128, 64 sequences of 1 to 1500
+// three with dg.  (Heads of 128 without dg: five vector registers spilled, 24 bytes of scratch a lane.)
+// Measured, by the profiler: heads of 64, 1024 sequences of 16 to 512, 2 heads: o 38 us, 3.8 TB/s; dq 61.  Heads of 128, 64 sequences of 1 to 1500
 // with states, 8 heads over 2: 31 us, and 22 for the states at the runs' starts.
 template <int LP, int UP, int PR, int GRAD>
 __global__ __launch_bounds__(Of<LP>::WAVES * 64, LP == 128 ? (GRAD ? 2 : 4) : LP == 64 ? (GRAD ? 3 : 4) : GRAD ? 2 : 3) void k_decay_walk(const Walk a) {

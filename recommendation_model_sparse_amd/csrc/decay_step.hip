@@ -3,7 +3,7 @@
 // Bound by reading and writing the states once.  A workgroup takes one key head's state of one sequence: each
 // thread four neighbouring columns of some of its rows, which stay in registers for all query heads that share it.
 // Measured: 512 sequences, 4 states of 128 x 128 each, 41 us, 272 MB at 6.6 TB/s (part of the states is still in the
-// caches from the call before; with other states in between 59 us, 4.6); one sequence, 4 of 32 x 32, 3.5 us, a launch
+// caches from the call before; with other states in between 59 us, 4.6); one sequence, 4 of 32 x 32, 3.8 us, a launch
 // and three waits for memory.
 #include "decay.h"
 

@@ -87,9 +87,10 @@ namespace {
 // DP: the head's width rounded up (the products run over DP columns, those from d on are zeros);
 // LP: columns of a row in LDS.  WQ wavefronts of 32 queries each, by WK that share a tile's keys:
 // each then takes 32 of them, and their results are joined at the end.  PAGED: a key's row comes
-// from the table of its sequence's pages.  (Four histories of 3000 to 4096, heads of 128, all events new: 118 us, where reads
-// of wanted rows alone, with a branch each, took 134; a tile's reads begun while the one before is worked on, 115, but
-// 52.0 where 51.0 for 256 histories of up to 512: not kept.)
+// from the table of its sequence's pages, and rows are read without a branch: four histories of 3000 to 4096 with up to
+// 4000 new events, 8 heads of 128 over 2, took 118 us two by two wavefronts, where reads of wanted rows alone, with a branch each,
+// took 134 (two by four, which they have now, 80).  A tile's reads begun while the one before is worked on took 115, but
+// 52.0 where 51.0 for 256 histories of up to 512: not kept.
 template <int DP, int LP, int WQ, int WK, int OCC, int NEAR, bool PAGED>
 __global__ __launch_bounds__(WQ * WK * 64, OCC) void k_seq_attn_fwd(const Args a, const Pages pg, uint16_t *o_out, float *lse_out,
                                                                     int32_t *tiles_out) {
