@@ -38,7 +38,7 @@ extern "C" {
  *              outside are brought inside: no foreign memory is read.  Not read by the step.
  *   max_len    an upper bound of the sequences' lengths, by which a call chooses whether to cut
  *              sequences into runs that are worked on side by side, with a state for each in the workspace (up to
- *              256 MB, or as much as q, k, v and o take); N where it is not known: one sequence may then be
+ *              256 MB, or as much as q, k, v and o take; twice that in the backward); N where it is not known: one sequence may then be
  *              all of them, and batches of short ones are slower.  Longer sequences give results as exact, slower.  (The bits may differ with it, and with
  *              the number of sequences and rows.)
  *   q, k, v    bf16; element e of head h of row r at r * row_stride + h * head_stride + e, strides
@@ -79,7 +79,11 @@ size_t dlrm_seq_decay_fwd_workspace_size(const dlrm_seq_decay *a);
 int dlrm_seq_decay_fwd(const dlrm_seq_decay *a, const float *state_in, float *state_out, uint16_t *o,
                        void *workspace, size_t workspace_bytes, dlrm_stream_t stream);
 
-/* Bytes of workspace dlrm_seq_decay_bwd needs (0 on an invalid description). */
+/*
+ * Bytes of workspace dlrm_seq_decay_bwd needs, with dg or without (0 on an invalid description): beside the runs'
+ * states or an order, states at marks, d * d floats (d as 32, 64 or 128) for 512 rows and key head or, with one decay a head,
+ * 128 (for less where sequences are cut into runs of fewer), and two floats a row and key head.
+ */
 size_t dlrm_seq_decay_bwd_workspace_size(const dlrm_seq_decay *a);
 
 /*
